@@ -444,6 +444,62 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
                                  int64_t B, int64_t D, int64_t L, int64_t N, int64_t R,
                                  int dtype, int flags, void *stream);
 
+/* ---- gated delta rule ---------------------------------------------------------------------
+ * A selective scan whose state is a matrix: per sequence and value head h, with key head
+ * h / (H / HK), a state S (DK, DV) that starts at h0 (zero without one) and per token
+ *   S  <- exp(g_t) S                      (decay, g_t <= 0 a log; -inf forgets everything)
+ *   u_t = beta_t (v_t - S^T k_t),   S <- S + k_t u_t^T        (the delta rule)
+ *   o_t = scale S^T q_t.
+ * k is used as given: the rule is stable for |k_t|^2 beta_t <= 2, so callers normalise k.
+ *
+ *   q, k      (B, L, HK, DK)  dtype        g, beta  (B, L, H)          fp32
+ *   v, o      (B, L, H, DV)   dtype        h0, ht   (S, H, DK, DV)     fp32
+ * strides: 9 element strides, (batch, token, head) of q, of k and of v, whose last axis is
+ * contiguous (views into one fused projection, for instance; none negative); NULL for
+ * contiguous tensors.  Every other tensor is contiguous.  H is a multiple of HK,
+ * 1 <= DK <= 128 (SS2D_ERR_UNSUPPORTED above), any DV >= 1.
+ *
+ * cu_seqlens: NULL, and the B rows are S = B sequences of L tokens; or S + 1 ascending
+ * offsets (device memory) into the L tokens of B = 1: sequence n holds tokens
+ * cu_seqlens[n] .. cu_seqlens[n + 1] - 1, none for equal offsets.  Tokens outside of every
+ * sequence are neither read nor written.  The offsets are device data that no call checks
+ * on the host; the kernels cut them to [0, L], so that others than ascending ones give
+ * wrong values but touch no other memory.
+ *
+ * Arithmetic: S, the chunk's triangular solve and every sum are fp32 for both data types.
+ * For bfloat16 data a product's fp32 operand runs on the bf16 matrix cores as the sum of 3
+ * bfloat16 terms (24 bits), o's as 2 (17 bits) before its single rounding; fp32 data use the
+ * fp32 matrix instructions.
+ *
+ * ss1d_delta_forward writes o and, if ht is not NULL, the end states; ht may be h0 itself
+ * (in place).  saved (NULL, or ss1d_delta_saved_bytes bytes of device memory, aligned to 256)
+ * keeps what ss1d_delta_backward starts from: the states before every 64 tokens, and
+ * v_t - S^T k_t and o_t in fp32.
+ *
+ * ss1d_delta_step is the form for serving: T tokens (few) of each of B sequences, whose
+ * states are updated in place: row b's state is state[slots[b]], or state[b] with slots
+ * NULL.  A row whose slot is negative or >= S is padding: nothing of it is read or written,
+ * its rows of o included.  Rows that name the same slot are successive tokens of one
+ * sequence, in row order.
+ *
+ * The shared conventions hold, except that kernel timing does not cover these entry points.
+ * Scratch: the chunks' matrices, about 0.5 KB per token and value head (the step has none). */
+int ss1d_delta_forward(const void *q, const void *k, const void *v, const float *g,
+                       const float *beta, const float *h0, const int32_t *cu_seqlens, void *o,
+                       float *ht, void *saved, int64_t B, int64_t L, int64_t S, int64_t HK,
+                       int64_t H, int64_t DK, int64_t DV, const int64_t *strides, float scale,
+                       int dtype, void *stream);
+
+/* Bytes of `saved` (-1 for sizes that the operator rejects); packed: whether cu_seqlens is
+ * given. */
+int64_t ss1d_delta_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t H, int64_t DK, int64_t DV,
+                               int packed);
+
+int ss1d_delta_step(const void *q, const void *k, const void *v, const float *g,
+                    const float *beta, float *state, const int32_t *slots, void *o, int64_t B,
+                    int64_t T, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                    const int64_t *strides, float scale, int dtype, void *stream);
+
 /* ---- launch-plan override (testing and tuning, not part of the operator) ---------------
  * Sets, for calls made later from the calling host thread only, the lanes that share one
  * channel's states in the forward scan (split: 1, 2 or 4; 0 = automatic) and the chunk

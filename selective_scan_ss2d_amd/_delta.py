@@ -1,0 +1,181 @@
+"""Binding of the gated delta rule (``ss1d_delta_*`` of ``include/ss2d.h``).
+
+Argument checks and marshalling only; every step runs in the library's HIP kernels.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import _binding as bnd
+
+_CODES = {torch.float32: bnd.SS2D_F32, torch.bfloat16: bnd.SS2D_BF16}
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream or torch.cuda.current_stream(device)):
+        yield
+
+
+def _scope(device, stream, *inputs):
+    """The device and stream that a call's outputs and scratch belong to: a context only
+    where they are not the current ones already."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    if stream is not None:  # the inputs' memory is not to be reused before the call has run
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+    return _switched(device, stream)
+
+
+def _strided(name, t, shape, dtype, device):
+    """Checks a tensor whose last axis alone has to be contiguous; its outer strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st = t.stride()
+    if st[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return st[:3]
+
+
+def _inputs(q, k, v, g, beta):
+    """Checks the rule's inputs; (B, L, HK, DK, H, DV), the data type's code and the strides
+    (None for contiguous tensors)."""
+    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor):
+        raise TypeError("q and v must be torch.Tensors")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (B, L, HK, DK) and v (B, L, H, DV)")
+    dev, dtype = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("q must be a GPU tensor")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"q must be float32 or bfloat16, not {dtype}")
+    B, L, HK, DK = q.shape
+    H, DV = v.shape[2], v.shape[3]
+    if HK < 1 or H % HK:
+        raise ValueError(f"v has {H} heads, expected a multiple of q's {HK}")
+    sq = _strided("q", q, (B, L, HK, DK), dtype, dev)
+    sk = _strided("k", k, (B, L, HK, DK), dtype, dev)
+    sv = _strided("v", v, (B, L, H, DV), dtype, dev)
+    bnd._expect("g", g, (B, L, H), torch.float32, dev)
+    bnd._expect("beta", beta, (B, L, H), torch.float32, dev)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        strides = (ctypes.c_int64 * 9)(*sq, *sk, *sv)
+    return (B, L, HK, DK, H, DV), code, strides
+
+
+def _sequences(cu_seqlens, B, device):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must hold S + 1 offsets")
+    bnd._expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need a batch of 1")
+    return cu_seqlens.shape[0] - 1
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _output(name, t, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    bnd._expect(name, t, shape, dtype, device)
+    return t
+
+
+def _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o, stream, save):
+    lib = bnd.load_library()
+    (B, L, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
+    dev = q.device
+    S = _sequences(cu_seqlens, B, dev)
+    if initial_state is not None:
+        bnd._expect("initial_state", initial_state, (S, H, DK, DV), torch.float32, dev)
+    with _scope(dev, stream, q, k, v, g, beta, cu_seqlens, initial_state):
+        o = _output("o", o, (B, L, H, DV), q.dtype, dev)
+        ht = saved = None
+        if final_state is not False and final_state is not None:
+            ht = _output("final_state", None if final_state is True else final_state,
+                         (S, H, DK, DV), torch.float32, dev)
+        if save:
+            size = lib.ss1d_delta_saved_bytes(B, L, S, H, DK, DV, cu_seqlens is not None)
+            saved = torch.empty(max(0, size), dtype=torch.uint8, device=dev)
+        bnd._check(lib.ss1d_delta_forward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            _ptr(initial_state), _ptr(cu_seqlens), o.data_ptr(), _ptr(ht), _ptr(saved), B, L, S,
+            HK, H, DK, DV, strides, DK ** -0.5 if scale is None else scale, code,
+            bnd._stream_handle(dev, stream)))
+    return o, ht, saved
+
+
+def ss1d_delta_forward(q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
+                       final_state=False, o=None, stream=None):
+    """The gated delta rule over whole sequences.
+
+    Per sequence and value head, from a state S (DK, DV), zero or ``initial_state``:
+    S <- exp(g_t) S; u_t = beta_t (v_t - S^T k_t); S <- S + k_t u_t^T; o_t = scale S^T q_t.
+    q, k (B, L, HK, DK) and v (B, L, H, DV) float32 or bfloat16, last axis contiguous, H a
+    multiple of HK (value head h reads key head h // (H // HK)), DK <= 128; g (log decays)
+    and beta (B, L, H) float32.  scale defaults to DK ** -0.5.  k is expected normalised
+    (|k_t|^2 beta_t <= 2 keeps the rule stable).
+
+    cu_seqlens: int32 offsets (S + 1) of S sequences packed into the tokens of B = 1 (tokens
+    outside of them are left as they are in o).  initial_state (S, H, DK, DV) float32.
+    Returns o (B, L, H, DV); with final_state True (or a tensor to write, which may be
+    initial_state itself) the pair (o, end states (S, H, DK, DV) float32).
+    """
+    o, ht, _ = _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o,
+                        stream, False)
+    return o if ht is None else (o, ht)
+
+
+def ss1d_delta_forward_save(q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
+                            final_state=False, o=None, stream=None):
+    """The training forward: ss1d_delta_forward, and the buffer that ss1d_delta_backward starts
+    from.  Returns (o, saved), with final_state (o, end states, saved)."""
+    o, ht, saved = _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o,
+                            stream, True)
+    return (o, saved) if ht is None else (o, ht, saved)
+
+
+def ss1d_delta_step(q, k, v, g, beta, state, slots=None, scale=None, o=None, stream=None):
+    """The gated delta rule for T (few) tokens of each of B sequences, states in place.
+
+    q, k (B, T, HK, DK), v (B, T, H, DV), g and beta (B, T, H) as in ss1d_delta_forward; state
+    (S, H, DK, DV) float32, updated in place.  Row b's state is state[slots[b]] (int32 slots
+    (B)), or state[b].  Rows with a slot outside 0 .. S - 1 are padding and their rows of o
+    stay as they are; rows that name one slot are successive tokens of one sequence, in row
+    order.  Returns o (B, T, H, DV).
+    """
+    lib = bnd.load_library()
+    (B, T, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
+    dev = q.device
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be (S, H, DK, DV)")
+    S = state.shape[0]
+    bnd._expect("state", state, (S, H, DK, DV), torch.float32, dev)
+    if slots is not None:
+        bnd._expect("slots", slots, (B,), torch.int32, dev)
+    elif S != B:
+        raise ValueError(f"state holds {S} sequences, expected {B} without slots")
+    with _scope(dev, stream, q, k, v, g, beta, state, slots):
+        o = _output("o", o, (B, T, H, DV), q.dtype, dev)
+        bnd._check(lib.ss1d_delta_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            state.data_ptr(), _ptr(slots), o.data_ptr(), B, T, S, HK, H, DK, DV, strides,
+            DK ** -0.5 if scale is None else scale, code, bnd._stream_handle(dev, stream)))
+    return o

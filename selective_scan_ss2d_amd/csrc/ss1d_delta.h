@@ -1,0 +1,318 @@
+// Shared pieces of the gated delta rule's kernels (gfx950): the arguments, the matrix
+// operands and products, and the loads.
+//
+// The rule, per sequence and value head, with a (DK, DV) state S:
+//   S <- e^g_t S;  u_t = beta_t (v_t - S^T k_t);  S <- S + k_t u_t^T;  o_t = scale S^T q_t.
+// In chunks of 32 tokens, with G_i = g_1 + .. + g_i inside the chunk, S the state before it,
+//   L_ij = e^(G_i - G_j) k_i.k_j (j < i),   P_ij = scale e^(G_i - G_j) q_i.k_j (j <= i),
+//   r_i  = v_i - e^G_i S^T k_i,   (I + L diag(beta)) t = r,   u = beta t,
+//   o_i  = scale e^G_i S^T q_i + (P u)_i,
+//   S    <- e^G_32 S + sum_j e^(G_32 - G_j) k_j u_j^T.
+// With N = (I + L diag(beta))^-1 L (strictly lower triangular, free of beta on the outside)
+// t = r - N (beta r), and the backward's adjoint solve is w = y - N^T (beta y): the identity
+// part is never rounded, and beta = 0 needs no care.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ss2d_device.h"
+
+namespace ss2d {
+namespace delta {
+
+constexpr int kC = 32;      // tokens per chunk: one 32 x 32 matrix tile
+constexpr int kMaxDK = 128; // largest key width (the state's rows held by one wave)
+constexpr int kMark = 64;   // tokens between the states a training forward keeps
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct Strides {  // in elements; the last axis has stride 1
+  int64_t b, l, h;
+};
+
+struct Args {
+  const void *q, *k, *v;       // (B, L, HK, DK), (B, L, HK, DK), (B, L, H, DV)
+  const float *g, *beta;       // (B, L, H)
+  const float* h0;             // (S, H, DK, DV) or NULL
+  const int32_t* cu;           // (S + 1) offsets into the tokens of B = 1, or NULL
+  void* o;                     // (B, L, H, DV)
+  float* ht;                   // (S, H, DK, DV) or NULL
+  Strides sq, sk, sv;
+  int64_t S, L, T;             // sequences, tokens of a batch row, tokens in all
+  int H, HK, rep, DK, DV;      // rep = H / HK value heads share a key head
+  float scale;
+  // scratch, per (chunk slot, head): matrix fragments and gates
+  char *nf, *pf;               // N and P (backward: their transposes), per value head
+  char *ktf, *qtf;             // K^T and Q^T, per key head
+  float* gates;                // (slot, H, 3, 32): e^G, e^(G_32 - G), beta
+  int64_t slots;               // chunk slots
+  int p_planes;                // bf16 terms kept of P
+  // kept by a training forward
+  float *marks, *ts, *os;      // states before every 64 tokens, t and o in fp32
+};
+
+// ---- sequences and chunk slots -----------------------------------------------------------
+struct Seq {
+  int64_t row;   // first token among all tokens (rows of contiguous tensors)
+  int64_t len;
+};
+
+// Offsets out of order or out of range are cut to [0, T], so that no address leaves the
+// tensors whatever the offsets hold.
+__device__ __forceinline__ Seq sequence(const Args& a, int64_t n) {
+  if (!a.cu) return {n * a.L, a.L};
+  int64_t s = a.cu[n], e = a.cu[n + 1];
+  s = s < 0 ? 0 : (s > a.T ? a.T : s);
+  e = e < s ? s : (e > a.T ? a.T : e);
+  return {s, e - s};
+}
+
+// First slot of sequence n among slots of `unit` tokens, no two sequences sharing a slot:
+// dense, n ceil(L / unit); packed, floor(start / unit) + n.
+__device__ __forceinline__ int64_t first_slot(const Args& a, int64_t n, const Seq& s, int unit) {
+  return a.cu ? s.row / unit + n : n * ((a.L + unit - 1) / unit);
+}
+
+// The sequence and index inside it of a slot; false for a slot that no sequence uses.
+__device__ __forceinline__ bool find_slot(const Args& a, int64_t slot, int unit, int64_t* n,
+                                          int64_t* index, Seq* s) {
+  if (!a.cu) {
+    const int64_t per = (a.L + unit - 1) / unit;
+    *n = slot / per;
+    *index = slot - *n * per;
+    *s = sequence(a, *n);
+    return *n < a.S;
+  }
+  int64_t lo = 0, hi = a.S;  // the last sequence whose first slot is not past `slot`
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (first_slot(a, mid, sequence(a, mid), unit) <= slot) lo = mid; else hi = mid;
+  }
+  *n = lo;
+  *s = sequence(a, lo);
+  *index = slot - first_slot(a, lo, *s, unit);
+  return *index >= 0 && *index * unit < s->len;
+}
+
+// Element offset of token t of sequence n in a strided (B, L, H, .) tensor.
+__device__ __forceinline__ int64_t token_at(const Args& a, const Strides& st, int64_t n,
+                                            const Seq& s, int64_t t) {
+  return a.cu ? (s.row + t) * st.l : n * st.b + t * st.l;
+}
+
+// ---- matrix operands -----------------------------------------------------------------------
+// A tile of a product is 32 x 32 x 16.  Lane l holds 8 consecutive values of the contracted
+// axis, 8 (l / 32) + 0..7, of row (left operand) or column (right operand) l % 32.  The
+// result's lane holds column l % 32; its register r is row 8 (r / 4) + 4 (l / 32) + r % 4.
+// Left operands are loaded with their rows in the order swap23 (bits 2 and 3 exchanged):
+// then result register r is row 16 (r / 8) + 8 (l / 32) + r % 8 of the unpermuted order, and
+// registers 8 s .. 8 s + 7 are the right operand of the next product's step s as they
+// stand: states and solutions pass from one product to the next without leaving registers.
+__device__ __forceinline__ int swap23(int i) {
+  return (i & ~12) | ((i & 4) << 1) | ((i & 8) >> 1);
+}
+__device__ __forceinline__ int acc_row(int r, int half) { return 16 * (r >> 3) + 8 * half + (r & 7); }
+
+// An operand as the data type stores it.  fp32 data use the fp32 matrix instructions.
+template <typename T> struct Exact;
+template <> struct Exact<uint16_t> { bf16x8 v; };
+template <> struct Exact<float> { f32x8 v; };
+
+// An fp32 operand.  For bfloat16 data it is a sum of P bfloat16 terms, each the rounding of
+// what the terms before it leave: 3 terms hold 24 bits, i.e. the fp32 value, 2 terms 17.
+// A product with an operand that is exact in bfloat16 then takes P matrix instructions, one
+// of two fp32 operands the P (P + 1) / 2 pairs of terms that matter.
+template <typename T, int P> struct Wide;
+template <int P> struct Wide<uint16_t, P> { bf16x8 p[P]; };
+template <int P> struct Wide<float, P> { f32x8 v; };
+
+template <int P>
+__device__ __forceinline__ void set_wide(Wide<uint16_t, P>& w, f32x8 x) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    w.p[i] = __builtin_convertvector(x, bf16x8);
+    if (i + 1 < P) x -= __builtin_convertvector(w.p[i], f32x8);
+  }
+}
+template <int P>
+__device__ __forceinline__ void set_wide(Wide<float, P>& w, f32x8 x) { w.v = x; }
+
+__device__ __forceinline__ f32x8 part(const f32x16& x, int s) {
+  f32x8 y;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[8 * s + i];
+  return y;
+}
+
+__device__ __forceinline__ f32x16 mma16(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// fp32: one instruction contracts two values, one of each half of the wave.
+__device__ __forceinline__ f32x16 mma8(f32x8 a, f32x8 b, f32x16 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ f32x16 mma(const Exact<uint16_t>& a, const Exact<uint16_t>& b, f32x16 c) {
+  return mma16(a.v, b.v, c);
+}
+template <int P>
+__device__ __forceinline__ f32x16 mma(const Exact<uint16_t>& a, const Wide<uint16_t, P>& b, f32x16 c) {
+#pragma unroll
+  for (int j = P - 1; j >= 0; --j) c = mma16(a.v, b.p[j], c);
+  return c;
+}
+template <int P>
+__device__ __forceinline__ f32x16 mma(const Wide<uint16_t, P>& a, const Exact<uint16_t>& b, f32x16 c) {
+#pragma unroll
+  for (int j = P - 1; j >= 0; --j) c = mma16(a.p[j], b.v, c);
+  return c;
+}
+template <int P, int R>
+__device__ __forceinline__ f32x16 mma(const Wide<uint16_t, P>& a, const Wide<uint16_t, R>& b, f32x16 c) {
+  constexpr int M = P > R ? P : R;
+#pragma unroll
+  for (int i = P - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = R - 1; j >= 0; --j)
+      if (i + j < M) c = mma16(a.p[i], b.p[j], c);
+  return c;
+}
+__device__ __forceinline__ f32x16 mma(const Exact<float>& a, const Exact<float>& b, f32x16 c) {
+  return mma8(a.v, b.v, c);
+}
+template <int P>
+__device__ __forceinline__ f32x16 mma(const Exact<float>& a, const Wide<float, P>& b, f32x16 c) {
+  return mma8(a.v, b.v, c);
+}
+template <int P>
+__device__ __forceinline__ f32x16 mma(const Wide<float, P>& a, const Exact<float>& b, f32x16 c) {
+  return mma8(a.v, b.v, c);
+}
+template <int P, int R>
+__device__ __forceinline__ f32x16 mma(const Wide<float, P>& a, const Wide<float, R>& b, f32x16 c) {
+  return mma8(a.v, b.v, c);
+}
+
+// ---- loads ---------------------------------------------------------------------------------
+// 8 consecutive values of a row, columns c .. c + 7 of `width`; zero past the width or where
+// `on` is false.  kAligned: every row starts on 16 bytes and the width is a multiple of 8.
+template <bool kAligned>
+__device__ __forceinline__ void load8(Exact<uint16_t>& x, const uint16_t* row, int c, int width,
+                                      bool on) {
+  if constexpr (kAligned) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (on && c < width) u = *reinterpret_cast<const uint4*>(row + c);
+    x.v = __builtin_bit_cast(bf16x8, u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint16_t e = 0;
+      if (on && c + i < width) e = row[c + i];
+      x.v[i] = __builtin_bit_cast(__bf16, e);
+    }
+  }
+}
+template <bool kAligned>
+__device__ __forceinline__ void load8(Exact<float>& x, const float* row, int c, int width, bool on) {
+  if constexpr (kAligned) {
+    f32x4 u = {0, 0, 0, 0}, w = {0, 0, 0, 0};
+    if (on && c < width) {
+      u = *reinterpret_cast<const f32x4*>(row + c);
+      w = *reinterpret_cast<const f32x4*>(row + c + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x.v[i] = u[i]; x.v[4 + i] = w[i]; }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float e = 0.0f;
+      if (on && c + i < width) e = row[c + i];
+      x.v[i] = e;
+    }
+  }
+}
+
+// Fragments in scratch: 16 bytes a lane, one plane of 1 KB after another.
+constexpr int kPlane = 1024;
+template <typename T> constexpr int exact_planes() { return sizeof(T) == 4 ? 2 : 1; }
+template <typename T, int P> constexpr int wide_planes() { return sizeof(T) == 4 ? 2 : P; }
+
+__device__ __forceinline__ void put_planes(char* at, int lane, const f32x8& v) {
+  f32x4 u, w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { u[i] = v[i]; w[i] = v[4 + i]; }
+  reinterpret_cast<f32x4*>(at)[lane] = u;
+  reinterpret_cast<f32x4*>(at + kPlane)[lane] = w;
+}
+__device__ __forceinline__ f32x8 get_planes(const char* at, int lane) {
+  const f32x4 u = reinterpret_cast<const f32x4*>(at)[lane];
+  const f32x4 w = reinterpret_cast<const f32x4*>(at + kPlane)[lane];
+  f32x8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { v[i] = u[i]; v[4 + i] = w[i]; }
+  return v;
+}
+__device__ __forceinline__ void put(char* at, int lane, const Exact<uint16_t>& x) {
+  reinterpret_cast<uint4*>(at)[lane] = __builtin_bit_cast(uint4, x.v);
+}
+__device__ __forceinline__ void put(char* at, int lane, const Exact<float>& x) {
+  put_planes(at, lane, x.v);
+}
+__device__ __forceinline__ void get(Exact<uint16_t>& x, const char* at, int lane) {
+  x.v = __builtin_bit_cast(bf16x8, reinterpret_cast<const uint4*>(at)[lane]);
+}
+__device__ __forceinline__ void get(Exact<float>& x, const char* at, int lane) {
+  x.v = get_planes(at, lane);
+}
+template <int P>
+__device__ __forceinline__ void put(char* at, int lane, const Wide<uint16_t, P>& x) {
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    reinterpret_cast<uint4*>(at + i * kPlane)[lane] = __builtin_bit_cast(uint4, x.p[i]);
+}
+template <int P>
+__device__ __forceinline__ void put(char* at, int lane, const Wide<float, P>& x) {
+  put_planes(at, lane, x.v);
+}
+template <int P>
+__device__ __forceinline__ void get(Wide<uint16_t, P>& x, const char* at, int lane) {
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    x.p[i] = __builtin_bit_cast(bf16x8, reinterpret_cast<const uint4*>(at + i * kPlane)[lane]);
+}
+template <int P>
+__device__ __forceinline__ void get(Wide<float, P>& x, const char* at, int lane) {
+  x.v = get_planes(at, lane);
+}
+
+// Bytes of one chunk's fragments.
+template <typename T> constexpr int64_t n_bytes() { return 2 * wide_planes<T, 3>() * kPlane; }
+template <typename T> __host__ __device__ constexpr int64_t p_bytes(int planes) {
+  return 2 * int64_t(sizeof(T) == 4 ? 2 : planes) * kPlane;
+}
+template <typename T> __host__ __device__ constexpr int64_t t_bytes(int kt) {
+  return 2 * int64_t(kt) * exact_planes<T>() * kPlane;
+}
+
+// Orders a wave's own LDS accesses (its lanes exchange data; no other wave takes part).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Log decays below this are 0 in fp32 either way; the bound keeps -inf out of differences.
+constexpr float kMinLog = -1000.0f;
+
+int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);
+int launch_scan(const Args& a, int dtype, bool aligned, bool save, hipStream_t st);
+
+}  // namespace delta
+}  // namespace ss2d

@@ -1,0 +1,282 @@
+// C entry points of the gated delta rule: argument checks, scratch and the kernel sequence.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "ss1d_delta.h"
+#include "ss1d_delta_step.h"
+#include "ss2d.h"
+#include "ss2d_host.h"
+
+namespace {
+
+using ss2d::delta::Args;
+using ss2d::delta::Strides;
+
+constexpr int64_t kMaxTokens = int64_t(1) << 40;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of one launch
+
+struct Span {  // the memory of one argument
+  const void* p;
+  int64_t bytes;
+};
+
+// Bytes from the first to past the last element of a strided (B, L, H, D) tensor; -1 where
+// the strides or the size are out of range.
+int64_t strided_bytes(int64_t B, int64_t L, int64_t H, int64_t D, const Strides& s, int64_t e) {
+  if (s.b < 0 || s.l < 0 || s.h < 0) return -1;
+  if (B == 0 || L == 0 || H == 0 || D == 0) return 0;
+  int64_t tb, tl, th;
+  if (!ss2d::host_mul_ok(B - 1, s.b, &tb) || !ss2d::host_mul_ok(L - 1, s.l, &tl) ||
+      !ss2d::host_mul_ok(H - 1, s.h, &th))
+    return -1;
+  const int64_t last = tb + tl + th + D;  // each term is below 2^62; so is what is allowed
+  if (tb > ss2d::kHostMaxElems / 8 || tl > ss2d::kHostMaxElems / 8 ||
+      th > ss2d::kHostMaxElems / 8)
+    return -1;
+  return last * e;
+}
+
+void default_strides(int64_t L, int64_t H, int64_t D, Strides* s) { *s = {L * H * D, H * D, D}; }
+
+bool aligned_rows(const void* p, const Strides& s, int64_t D, int64_t e) {
+  const int64_t unit = 16 / e;
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && s.b % unit == 0 && s.l % unit == 0 &&
+         s.h % unit == 0 && D % 8 == 0;
+}
+
+int check_sizes(int64_t B, int64_t L, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                int dtype, bool packed) {
+  if (dtype != SS2D_F32 && dtype != SS2D_BF16) return SS2D_ERR_UNSUPPORTED;
+  if (B < 0 || L < 0 || S < 0 || HK < 1 || H < 0 || DK < 1 || DV < 1) return SS2D_ERR_SHAPE;
+  if (H % HK != 0) return SS2D_ERR_SHAPE;
+  if (packed ? B != 1 : S != B) return SS2D_ERR_SHAPE;
+  if (DK > ss2d::delta::kMaxDK) return SS2D_ERR_UNSUPPORTED;
+  if (B >= kMaxTokens || L >= kMaxTokens || S >= kMaxTokens || H >= (1 << 20) ||
+      DV >= (1 << 20))
+    return SS2D_ERR_SHAPE;
+  int64_t t, n;
+  if (!ss2d::host_mul_ok(B, L, &t) || t >= kMaxTokens) return SS2D_ERR_SHAPE;
+  if (!ss2d::host_mul_ok(t, H * DV, &n) || n > ss2d::kHostMaxElems / 64) return SS2D_ERR_SHAPE;
+  if (!ss2d::host_mul_ok(S, H * DK * DV, &n) || n > ss2d::kHostMaxElems / 64)
+    return SS2D_ERR_SHAPE;
+  return SS2D_OK;
+}
+
+int64_t slot_count(int64_t L, int64_t S, int64_t T, bool packed, int64_t unit) {
+  return packed ? T / unit + S : S * ((L + unit - 1) / unit);
+}
+
+// The state a training forward keeps: the marks, then t and o in fp32.
+struct Saved {
+  int64_t marks, rows, bytes;
+};
+Saved saved_layout(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DK, int64_t DV,
+                   bool packed) {
+  Saved s;
+  s.marks = static_cast<int64_t>(ss2d::host_align256(
+      size_t(slot_count(L, S, T, packed, ss2d::delta::kMark)) * H * DK * DV * 4));
+  s.rows = static_cast<int64_t>(ss2d::host_align256(size_t(T) * H * DV * 4));
+  s.bytes = s.marks + 2 * s.rows;
+  return s;
+}
+
+int check_pointers(const Span* ins, int n_in, const Span* outs, int n_out) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (ss2d::host_overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+        return SS2D_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (ss2d::host_overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return SS2D_ERR_ALIAS;
+  }
+  return SS2D_OK;
+}
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+struct Scratch {
+  size_t nf, pf, ktf, qtf, gates, bytes;
+};
+Scratch scratch_layout(const Args& a, int dtype, bool backward) {
+  using namespace ss2d::delta;
+  const size_t per = size_t(a.slots) * a.H, key = size_t(a.slots) * a.HK;
+  const int kt = a.DK <= 32 ? 1 : (a.DK <= 64 ? 2 : 4);
+  const bool f32 = dtype == SS2D_F32;
+  const size_t nb = f32 ? n_bytes<float>() : n_bytes<uint16_t>();
+  const size_t pb = f32 ? p_bytes<float>(a.p_planes) : p_bytes<uint16_t>(a.p_planes);
+  const size_t tb = f32 ? t_bytes<float>(kt) : t_bytes<uint16_t>(kt);
+  Scratch s{};
+  s.nf = 0;
+  s.pf = s.nf + ss2d::host_align256(per * nb);
+  s.ktf = s.pf + ss2d::host_align256(per * pb);
+  s.qtf = s.ktf + ss2d::host_align256(key * tb);
+  s.gates = s.qtf + (backward ? ss2d::host_align256(key * tb) : 0);
+  s.bytes = s.gates + ss2d::host_align256(per * 3 * kC * 4);
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t ss1d_delta_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t H, int64_t DK, int64_t DV,
+                               int packed) {
+  if (check_sizes(B, L, S, 1, H, DK, DV, SS2D_BF16, packed != 0) != SS2D_OK) return -1;
+  return saved_layout(L, S, B * L, H, DK, DV, packed != 0).bytes;
+}
+
+int ss1d_delta_forward(const void* q, const void* k, const void* v, const float* g,
+                       const float* beta, const float* h0, const int32_t* cu_seqlens, void* o,
+                       float* ht, void* saved, int64_t B, int64_t L, int64_t S, int64_t HK,
+                       int64_t H, int64_t DK, int64_t DV, const int64_t* strides, float scale,
+                       int dtype, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  int rc = check_sizes(B, L, S, HK, H, DK, DV, dtype, packed);
+  if (rc != SS2D_OK) return rc;
+  if (!std::isfinite(scale)) return SS2D_ERR_UNSUPPORTED;
+  if (S == 0 || H == 0) return SS2D_OK;
+  const int64_t T = B * L, e = dtype == SS2D_F32 ? 4 : 2;
+  if (T > 0 && (!q || !k || !v || !g || !beta || !o)) return SS2D_ERR_NULL;
+  if (T == 0 && !ht) return SS2D_OK;
+  Args a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.h0 = h0;
+  a.cu = cu_seqlens;
+  a.o = o;
+  a.ht = ht;
+  default_strides(L, HK, DK, &a.sq);
+  default_strides(L, HK, DK, &a.sk);
+  default_strides(L, H, DV, &a.sv);
+  if (strides) {
+    a.sq = {strides[0], strides[1], strides[2]};
+    a.sk = {strides[3], strides[4], strides[5]};
+    a.sv = {strides[6], strides[7], strides[8]};
+  }
+  a.S = S;
+  a.L = L;
+  a.T = T;
+  a.H = static_cast<int>(H);
+  a.HK = static_cast<int>(HK);
+  a.rep = static_cast<int>(H / HK);
+  a.DK = static_cast<int>(DK);
+  a.DV = static_cast<int>(DV);
+  a.scale = scale;
+  const int64_t qb = strided_bytes(B, L, HK, DK, a.sq, e), kb = strided_bytes(B, L, HK, DK, a.sk, e),
+                vb = strided_bytes(B, L, H, DV, a.sv, e);
+  if (qb < 0 || kb < 0 || vb < 0) return SS2D_ERR_SHAPE;
+  for (const void* p : {q, k, v, static_cast<const void*>(o)})
+    if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
+  for (const void* p : {static_cast<const void*>(g), static_cast<const void*>(beta),
+                        static_cast<const void*>(h0), static_cast<const void*>(ht),
+                        static_cast<const void*>(cu_seqlens)})
+    if (misaligned(p, 4)) return SS2D_ERR_ALIGN;
+  if (misaligned(saved, 256)) return SS2D_ERR_ALIGN;
+  const int64_t state = S * H * DK * DV * 4;
+  const Saved sv = saved_layout(L, S, T, H, DK, DV, packed);
+  const Span ins[] = {{q, qb}, {k, kb}, {v, vb}, {g, T * H * 4}, {beta, T * H * 4},
+                      {cu_seqlens, (S + 1) * 4}};
+  const Span outs[] = {{o, T * H * DV * e}, {ht, state}, {saved, sv.bytes}};
+  rc = check_pointers(ins, 6, outs, 3);
+  if (rc != SS2D_OK) return rc;
+  // the end states may replace the initial ones (each wave reads its columns first)
+  const Span first[] = {{h0, state}};
+  for (const Span& x : outs)
+    if (!(x.p == ht && ht == h0) && check_pointers(first, 1, &x, 1) != SS2D_OK)
+      return SS2D_ERR_ALIAS;
+
+  a.slots = slot_count(L, S, T, packed, ss2d::delta::kC);
+  a.p_planes = saved ? 3 : 2;
+  if ((a.slots * H / 4 + 1) * 256 > kMaxThreads || S * H * ((DV + 31) / 32) * 64 > kMaxThreads)
+    return SS2D_ERR_SHAPE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Scratch w = scratch_layout(a, dtype, false);
+  char* ws = nullptr;
+  rc = ss2d::host_scratch_alloc(&ws, w.bytes, st);
+  if (rc != SS2D_OK) return rc;
+  a.nf = ws + w.nf;
+  a.pf = ws + w.pf;
+  a.ktf = ws + w.ktf;
+  a.gates = reinterpret_cast<float*>(ws + w.gates);
+  if (saved) {
+    char* at = static_cast<char*>(saved);
+    a.marks = reinterpret_cast<float*>(at);
+    a.ts = reinterpret_cast<float*>(at + sv.marks);
+    a.os = reinterpret_cast<float*>(at + sv.marks + sv.rows);
+  }
+  const bool al = aligned_rows(q, a.sq, DK, e) && aligned_rows(k, a.sk, DK, e);
+  int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
+  if (!err) err = ss2d::delta::launch_scan(a, dtype, al, saved != nullptr, st);
+  const hipError_t fe = hipFreeAsync(ws, st);
+  if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
+  if (fe != hipSuccess) return ss2d::host_hip_fail(fe);
+  return SS2D_OK;
+}
+
+int ss1d_delta_step(const void* q, const void* k, const void* v, const float* g,
+                    const float* beta, float* state, const int32_t* slots, void* o, int64_t B,
+                    int64_t T, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                    const int64_t* strides, float scale, int dtype, void* stream) {
+  int rc = check_sizes(B, T, B, HK, H, DK, DV, dtype, false);
+  if (rc != SS2D_OK) return rc;
+  if (!std::isfinite(scale)) return SS2D_ERR_UNSUPPORTED;
+  int64_t n;
+  if (S < 0 || S >= kMaxTokens || !ss2d::host_mul_ok(S, H * DK * DV, &n) ||
+      n > ss2d::kHostMaxElems / 64)
+    return SS2D_ERR_SHAPE;
+  if (!slots && S < B) return SS2D_ERR_SHAPE;
+  if (B == 0 || T == 0 || H == 0 || S == 0) return SS2D_OK;
+  if (!q || !k || !v || !g || !beta || !state || !o) return SS2D_ERR_NULL;
+  const int64_t e = dtype == SS2D_F32 ? 4 : 2;
+  ss2d::delta::StepArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.slots = slots;
+  a.state = state;
+  a.o = o;
+  default_strides(T, HK, DK, &a.sq);
+  default_strides(T, HK, DK, &a.sk);
+  default_strides(T, H, DV, &a.sv);
+  if (strides) {
+    a.sq = {strides[0], strides[1], strides[2]};
+    a.sk = {strides[3], strides[4], strides[5]};
+    a.sv = {strides[6], strides[7], strides[8]};
+  }
+  a.B = B;
+  a.T = T;
+  a.S = S;
+  a.H = static_cast<int>(H);
+  a.HK = static_cast<int>(HK);
+  a.rep = static_cast<int>(H / HK);
+  a.DK = static_cast<int>(DK);
+  a.DV = static_cast<int>(DV);
+  a.scale = scale;
+  const int64_t qb = strided_bytes(B, T, HK, DK, a.sq, e), kb = strided_bytes(B, T, HK, DK, a.sk, e),
+                vb = strided_bytes(B, T, H, DV, a.sv, e);
+  if (qb < 0 || kb < 0 || vb < 0) return SS2D_ERR_SHAPE;
+  for (const void* p : {q, k, v, static_cast<const void*>(o)})
+    if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
+  for (const void* p : {static_cast<const void*>(g), static_cast<const void*>(beta),
+                        static_cast<const void*>(state), static_cast<const void*>(slots)})
+    if (misaligned(p, 4)) return SS2D_ERR_ALIGN;
+  const Span ins[] = {{q, qb}, {k, kb}, {v, vb}, {g, B * T * H * 4}, {beta, B * T * H * 4},
+                      {slots, B * 4}};
+  const Span outs[] = {{o, B * T * H * DV * e}, {state, S * H * DK * DV * 4}};
+  rc = check_pointers(ins, 6, outs, 2);
+  if (rc != SS2D_OK) return rc;
+  if (B * H * ((DV + 15) / 16) * 64 > kMaxThreads) return SS2D_ERR_SHAPE;
+  const bool vec = DV % 4 == 0 && !misaligned(state, 16);
+  const int err = ss2d::delta::launch_step(a, dtype, vec, static_cast<hipStream_t>(stream));
+  if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
+  return SS2D_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,203 @@
+// Chunk matrices of the gated delta rule, every chunk and value head on its own: the gates,
+// P (or P^T), N (or N^T) and, once per key head, K^T (and Q^T), all written as the matrix
+// fragments that the sequential kernels load with one 16-byte access per lane.
+#include "ss1d_delta.h"
+
+namespace ss2d {
+namespace delta {
+namespace {
+
+constexpr int kWaves = 4;
+
+struct Shared {
+  double G[kC];
+  float beta[kC];
+  float m[kC * kC];   // the triangular matrix of the solve, rows of 32
+  float t[kC * 36];   // a 32 x 32 tile on its way through a transpose
+};
+
+// Transposes one operand tile: lane (token swap23(l % 32)) holds 8 columns per step; the
+// result's lane holds column swap23(l % 32), tokens 16 s + 8 half + 0..7.
+template <typename T>
+__device__ __forceinline__ void transpose_tile(Shared& sh, const Exact<T>* x, Exact<T>* y, int own,
+                                               int half) {
+  T* t = reinterpret_cast<T*>(sh.t);
+  wave_sync();
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const auto v = x[s].v[e];
+      t[own * 36 + 16 * s + 8 * half + e] = __builtin_bit_cast(T, v);
+    }
+  wave_sync();
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const T v = t[(16 * s + 8 * half + e) * 36 + own];
+      if constexpr (sizeof(T) == 4) y[s].v[e] = v;
+      else y[s].v[e] = __builtin_bit_cast(__bf16, v);
+    }
+}
+
+template <typename T, int KT, bool kAligned, bool kBackward>
+__global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
+  __shared__ Shared shared[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Shared& sh = shared[wave];
+  const int64_t unit = int64_t(blockIdx.x) * kWaves + wave;
+  const int64_t slot = unit / a.H;
+  const int hv = static_cast<int>(unit - slot * a.H);
+  if (slot >= a.slots) return;
+  int64_t n, c;
+  Seq seq;
+  if (!find_slot(a, slot, kC, &n, &c, &seq)) return;
+  const int hk = hv / a.rep;
+  const int half = lane >> 5, col = lane & 31, own = swap23(col);
+  const int64_t t0 = c * kC;
+  const int valid = static_cast<int>(min<int64_t>(kC, seq.len - t0));
+
+  // K and Q rows of this lane's token; q.k and k.k of all pairs
+  const bool on = own < valid;
+  const int64_t tok = t0 + (on ? own : 0);
+  const T* krow = static_cast<const T*>(a.k) + token_at(a, a.sk, n, seq, tok) + hk * a.sk.h;
+  const T* qrow = static_cast<const T*>(a.q) + token_at(a, a.sq, n, seq, tok) + hk * a.sq.h;
+  f32x16 kk = {}, qk = {};
+  const bool keyed = hv % a.rep == 0;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    Exact<T> kx[2], qx[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      load8<kAligned>(kx[s], krow, 32 * kt + 16 * s + 8 * half, a.DK, on);
+      load8<kAligned>(qx[s], qrow, 32 * kt + 16 * s + 8 * half, a.DK, on);
+      kk = mma(kx[s], kx[s], kk);
+      // forward: rows k_j, columns q_i; backward: rows q_i, columns k_j
+      qk = kBackward ? mma(qx[s], kx[s], qk) : mma(kx[s], qx[s], qk);
+    }
+    if (keyed) {
+      Exact<T> y[2];
+      const int64_t per = int64_t(exact_planes<T>()) * kPlane;
+      const int64_t at = (slot * a.HK + hk) * t_bytes<T>(KT) + 2 * kt * per;
+      transpose_tile<T>(sh, kx, y, own, half);
+      put(a.ktf + at, lane, y[0]);
+      put(a.ktf + at + per, lane, y[1]);
+      if (kBackward) {
+        transpose_tile<T>(sh, qx, y, own, half);
+        put(a.qtf + at, lane, y[0]);
+        put(a.qtf + at + per, lane, y[1]);
+      }
+    }
+  }
+
+  // gates: prefix sums of the log decays in 64 bits, so that differences of far sums keep
+  // fp32 accuracy
+  const int64_t row = seq.row + t0 + (col < valid ? col : 0);
+  float gv = 0.0f, bv = 0.0f;
+  if (col < valid) {
+    gv = fmaxf(a.g[row * a.H + hv], kMinLog);
+    bv = a.beta[row * a.H + hv];
+  }
+  double G = gv;
+#pragma unroll
+  for (int d = 1; d < kC; d *= 2) {
+    const double up = __shfl_up(G, d, 32);
+    if (col >= d) G += up;
+  }
+  const double Gend = __shfl(G, 31, 32);
+  if (half == 0) {
+    sh.G[col] = G;
+    sh.beta[col] = bv;
+    float* gt = a.gates + (slot * a.H + hv) * (3 * kC);
+    gt[col] = expf(static_cast<float>(G));
+    gt[kC + col] = expf(static_cast<float>(Gend - G));
+    gt[2 * kC + col] = bv;
+  }
+  wave_sync();
+  const double Gown = sh.G[own];
+  const float bown = sh.beta[own];
+  float low[16];  // L: forward, row `own`, columns acc_row; backward, column `own`, rows acc_row
+  f32x16 p;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int other = acc_row(r, half);
+    const double diff = kBackward ? sh.G[other] - Gown : Gown - sh.G[other];
+    const bool below = kBackward ? other > own : other < own;
+    const float m = (below || other == own) ? expf(static_cast<float>(diff)) : 0.0f;
+    low[r] = below ? kk[r] * m : 0.0f;
+    p[r] = (below || other == own) ? qk[r] * m * a.scale : 0.0f;
+  }
+  // the solve's matrix: forward, row j holds beta_k L_kj over k (N row by row, from
+  // n (I + diag(beta) L) = l); backward, row i holds L_ij beta_j over j
+#pragma unroll
+  for (int r = 0; r < 16; ++r) sh.m[acc_row(r, half) * kC + own] = low[r] * bown;
+  float x[kC];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float mine = low[8 * s + e], theirs = __shfl_xor(mine, 32);
+      x[16 * s + e] = half == 0 ? mine : theirs;
+      x[16 * s + 8 + e] = half == 0 ? theirs : mine;
+    }
+  wave_sync();
+  if (kBackward) {
+#pragma unroll
+    for (int i = 1; i < kC; ++i)
+#pragma unroll
+      for (int j = 0; j < i; ++j) x[i] = fmaf(-sh.m[i * kC + j], x[j], x[i]);
+  } else {
+#pragma unroll
+    for (int j = kC - 2; j >= 0; --j)
+#pragma unroll
+      for (int k = kC - 1; k > j; --k) x[j] = fmaf(-sh.m[j * kC + k], x[k], x[j]);
+  }
+  char* nf = a.nf + (slot * a.H + hv) * n_bytes<T>();
+  char* pf = a.pf + (slot * a.H + hv) * p_bytes<T>(a.p_planes);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    f32x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = half == 0 ? x[16 * s + e] : x[16 * s + 8 + e];
+    Wide<T, 3> w;
+    set_wide(w, v);
+    put(nf + s * wide_planes<T, 3>() * kPlane, lane, w);
+    if (a.p_planes == 3) {
+      set_wide(w, part(p, s));
+      put(pf + s * wide_planes<T, 3>() * kPlane, lane, w);
+    } else {
+      Wide<T, 2> w2;
+      set_wide(w2, part(p, s));
+      put(pf + s * wide_planes<T, 2>() * kPlane, lane, w2);
+    }
+  }
+}
+
+template <typename T, int KT, bool kAligned>
+int launch_kt(const Args& a, bool backward, hipStream_t st) {
+  const int64_t waves = a.slots * a.H;
+  const dim3 grid(static_cast<unsigned>((waves + kWaves - 1) / kWaves)), block(64 * kWaves);
+  if (backward) hipLaunchKernelGGL((k_delta_prep<T, KT, kAligned, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_prep<T, KT, kAligned, false>), grid, block, 0, st, a);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <typename T, bool kAligned>
+int launch_t(const Args& a, bool backward, hipStream_t st) {
+  if (a.DK <= 32) return launch_kt<T, 1, kAligned>(a, backward, st);
+  if (a.DK <= 64) return launch_kt<T, 2, kAligned>(a, backward, st);
+  return launch_kt<T, 4, kAligned>(a, backward, st);
+}
+
+}  // namespace
+
+int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st) {
+  if (dtype == 0)
+    return aligned ? launch_t<float, true>(a, backward, st) : launch_t<float, false>(a, backward, st);
+  return aligned ? launch_t<uint16_t, true>(a, backward, st)
+                 : launch_t<uint16_t, false>(a, backward, st);
+}
+
+}  // namespace delta
+}  // namespace ss2d

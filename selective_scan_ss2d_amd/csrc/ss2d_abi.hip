@@ -10,6 +10,7 @@
 #include "ss2d.h"
 #include "ss2d_device.h"
 #include "ss2d_gate.h"
+#include "ss2d_host.h"
 
 namespace {
 
@@ -813,6 +814,11 @@ int project(int K, const void* x, const float* conv_w, const float* conv_b,
 }
 
 }  // namespace
+
+int ss2d::host_hip_fail(hipError_t e) { return hip_fail(e); }
+int ss2d::host_scratch_alloc(char** ws, size_t bytes, hipStream_t st) {
+  return scratch_alloc(ws, bytes, st);
+}
 
 extern "C" {
 
