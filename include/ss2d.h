@@ -473,8 +473,15 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  *
  * ss1d_delta_forward writes o and, if ht is not NULL, the end states; ht may be h0 itself
  * (in place).  saved (NULL, or ss1d_delta_saved_bytes bytes of device memory, aligned to 256)
- * keeps what ss1d_delta_backward starts from: the states before every 64 tokens, and
- * v_t - S^T k_t and o_t in fp32.
+ * keeps what ss1d_delta_backward starts from: the states before every 64 tokens and at the
+ * end, and v_t - S^T k_t and o_t in fp32.
+ *
+ * ss1d_delta_backward: the gradients of sum(dout * o) + sum(dht * ht) (dht NULL: none) with
+ * respect to q, k (summed over the value heads that share them) and v in dtype, g, beta and,
+ * if dh0 is not NULL, h0 in fp32; all contiguous.  saved: what ss1d_delta_forward kept for the
+ * same inputs (other contents give undefined gradients), or NULL to compute it again.  dout
+ * is contiguous.  Rows outside of every sequence are left as they are.  The gradient of a g
+ * below -1000, whose decay is 0, is 0.
  *
  * ss1d_delta_step is the form for serving: T tokens (few) of each of B sequences, whose
  * states are updated in place: row b's state is state[slots[b]], or state[b] with slots
@@ -483,7 +490,8 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * sequence, in row order.
  *
  * The shared conventions hold, except that kernel timing does not cover these entry points.
- * Scratch: the chunks' matrices, about 0.5 KB per token and value head (the step has none). */
+ * Scratch: the chunks' matrices, about 0.5 KB per token and value head (the step has none); the
+ * backward's gradients of the states, 1 / 64 of a state per token, and partial sums. */
 int ss1d_delta_forward(const void *q, const void *k, const void *v, const float *g,
                        const float *beta, const float *h0, const int32_t *cu_seqlens, void *o,
                        float *ht, void *saved, int64_t B, int64_t L, int64_t S, int64_t HK,
@@ -494,6 +502,13 @@ int ss1d_delta_forward(const void *q, const void *k, const void *v, const float 
  * given. */
 int64_t ss1d_delta_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t H, int64_t DK, int64_t DV,
                                int packed);
+
+int ss1d_delta_backward(const void *q, const void *k, const void *v, const float *g,
+                        const float *beta, const float *h0, const int32_t *cu_seqlens,
+                        const void *saved, const void *dout, const float *dht, void *dq, void *dk,
+                        void *dv, float *dg, float *dbeta, float *dh0, int64_t B, int64_t L,
+                        int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                        const int64_t *strides, float scale, int dtype, void *stream);
 
 int ss1d_delta_step(const void *q, const void *k, const void *v, const float *g,
                     const float *beta, float *state, const int32_t *slots, void *o, int64_t B,

@@ -35,7 +35,8 @@ def __getattr__(name):  # the sequence operators import torch; the rest of the p
 
 
 _LAZY = {
-    "_delta": ("ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_step"),
+    "_delta": ("ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_backward",
+               "ss1d_delta_step"),
 }
 
 __all__ = [
@@ -53,5 +54,6 @@ __all__ = [
     "ss2d_backward_saved", "ss1d_bidir_backward_saved", "ss2d_forward_routes_save",
     "ss1d_bidir_forward_routes_save", "ss2d_backward_routes_saved",
     "ss1d_bidir_backward_routes_saved", "scratch_trim",
-    "ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_step",
+    "ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_backward",
+    "ss1d_delta_step",
 ]

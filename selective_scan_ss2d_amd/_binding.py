@@ -70,6 +70,8 @@ SIGNATURES = {
                                          [_P] * 18 + [_I64] * 4 + [ctypes.c_int] * 2 + [_P]),
     "ss1d_delta_forward": (ctypes.c_int, [_P] * 10 + [_I64] * 7 + [_P, ctypes.c_float,
                                                                    ctypes.c_int, _P]),
+    "ss1d_delta_backward": (ctypes.c_int, [_P] * 16 + [_I64] * 7 + [_P, ctypes.c_float,
+                                                                    ctypes.c_int, _P]),
     "ss1d_delta_saved_bytes": (_I64, [_I64] * 6 + [ctypes.c_int]),
     "ss1d_delta_step": (ctypes.c_int, [_P] * 8 + [_I64] * 7 + [_P, ctypes.c_float, ctypes.c_int,
                                                                _P]),

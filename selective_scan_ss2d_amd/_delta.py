@@ -152,6 +152,42 @@ def ss1d_delta_forward_save(q, k, v, g, beta, scale=None, cu_seqlens=None, initi
     return (o, saved) if ht is None else (o, ht, saved)
 
 
+def ss1d_delta_backward(q, k, v, g, beta, do, scale=None, cu_seqlens=None, initial_state=None,
+                        dstate=None, saved=None, stream=None):
+    """Gradients of sum(do * o) + sum(dstate * end states) for ss1d_delta_forward's outputs on
+    the same inputs: a dict with those of q, k, v, g and beta, and of initial_state if it is
+    given.
+
+    do: contiguous, the shape and dtype of v's output; dstate: float32 (S, H, DK, DV) or None.
+    saved: the buffer of ss1d_delta_forward_save for the same inputs; None computes it again.
+    Rows outside of every packed sequence are zero.
+    """
+    lib = bnd.load_library()
+    (B, L, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
+    dev = q.device
+    S = _sequences(cu_seqlens, B, dev)
+    bnd._expect("do", do, (B, L, H, DV), q.dtype, dev)
+    for name, t in (("initial_state", initial_state), ("dstate", dstate)):
+        if t is not None:
+            bnd._expect(name, t, (S, H, DK, DV), torch.float32, dev)
+    if saved is not None:
+        size = lib.ss1d_delta_saved_bytes(B, L, S, H, DK, DV, cu_seqlens is not None)
+        bnd._expect("saved", saved, (max(0, size),), torch.uint8, dev)
+    with _scope(dev, stream, q, k, v, g, beta, do, cu_seqlens, initial_state, dstate, saved):
+        make = torch.empty if cu_seqlens is None else torch.zeros
+        d = {n: make(t.shape, dtype=t.dtype, device=dev)
+             for n, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta))}
+        if initial_state is not None:
+            d["initial_state"] = torch.empty_like(initial_state)
+        bnd._check(lib.ss1d_delta_backward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+            _ptr(initial_state), _ptr(cu_seqlens), _ptr(saved), do.data_ptr(), _ptr(dstate),
+            d["q"].data_ptr(), d["k"].data_ptr(), d["v"].data_ptr(), d["g"].data_ptr(),
+            d["beta"].data_ptr(), _ptr(d.get("initial_state")), B, L, S, HK, H, DK, DV, strides,
+            DK ** -0.5 if scale is None else scale, code, bnd._stream_handle(dev, stream)))
+    return d
+
+
 def ss1d_delta_step(q, k, v, g, beta, state, slots=None, scale=None, o=None, stream=None):
     """The gated delta rule for T (few) tokens of each of B sequences, states in place.
 

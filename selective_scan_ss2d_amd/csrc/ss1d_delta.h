@@ -53,7 +53,17 @@ struct Args {
   int64_t slots;               // chunk slots
   int p_planes;                // bf16 terms kept of P
   // kept by a training forward
-  float *marks, *ts, *os;      // states before every 64 tokens, t and o in fp32
+  float *marks, *ends;         // states before every 64 tokens and after the last
+  float *ts, *os;              // t and o in fp32, (T, H, DV)
+  // backward
+  const void* dout;            // gradient of o, contiguous
+  const float* dht;            // gradient of the end states, or NULL
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *dh0;     // dh0 may be NULL
+  void* dmarks;                // gradients of the states after every 64 tokens, data type
+  float *pbeta, *pgate;        // per tile of 32 columns: w.t and do.o - dv.v of every token
+  float* pdots;                // per 64 tokens, head and tile: <dS, S> after them
+  int64_t marks_n;             // slots of 64 tokens
 };
 
 // ---- sequences and chunk slots -----------------------------------------------------------
@@ -239,6 +249,32 @@ __device__ __forceinline__ void load8(Exact<float>& x, const float* row, int c, 
   }
 }
 
+// The 16 values of tokens acc_row(r, half) in column `col` of a strided tensor.
+template <typename T>
+__device__ __forceinline__ f32x16 load_columns(const T* base, int64_t stride, int half, int valid,
+                                               bool on) {
+  f32x16 x;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int t = acc_row(r, half);
+    x[r] = on && t < valid ? Elem<T>::load(base + t * stride) : 0.0f;
+  }
+  return x;
+}
+
+__device__ __forceinline__ f32x16 load_gate(const float* gate, int half) {
+  f32x16 x;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(gate + 16 * s + 8 * half + 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[8 * s + 4 * i + e] = u[e];
+    }
+  return x;
+}
+
 // Fragments in scratch: 16 bytes a lane, one plane of 1 KB after another.
 constexpr int kPlane = 1024;
 template <typename T> constexpr int exact_planes() { return sizeof(T) == 4 ? 2 : 1; }
@@ -313,6 +349,9 @@ constexpr float kMinLog = -1000.0f;
 
 int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);
 int launch_scan(const Args& a, int dtype, bool aligned, bool save, hipStream_t st);
+int launch_adjoint(const Args& a, int dtype, bool aligned, hipStream_t st);
+int launch_grads(const Args& a, int dtype, bool aligned, hipStream_t st);
+int launch_gate_grads(const Args& a, hipStream_t st);
 
 }  // namespace delta
 }  // namespace ss2d

@@ -68,18 +68,26 @@ int64_t slot_count(int64_t L, int64_t S, int64_t T, bool packed, int64_t unit) {
   return packed ? T / unit + S : S * ((L + unit - 1) / unit);
 }
 
-// The state a training forward keeps: the marks, then t and o in fp32.
+// The state a training forward keeps: the marks, the end states, then t and o in fp32.
 struct Saved {
-  int64_t marks, rows, bytes;
+  int64_t marks, ends, rows, bytes;
 };
 Saved saved_layout(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DK, int64_t DV,
                    bool packed) {
   Saved s;
   s.marks = static_cast<int64_t>(ss2d::host_align256(
       size_t(slot_count(L, S, T, packed, ss2d::delta::kMark)) * H * DK * DV * 4));
+  s.ends = static_cast<int64_t>(ss2d::host_align256(size_t(S) * H * DK * DV * 4));
   s.rows = static_cast<int64_t>(ss2d::host_align256(size_t(T) * H * DV * 4));
-  s.bytes = s.marks + 2 * s.rows;
+  s.bytes = s.marks + s.ends + 2 * s.rows;
   return s;
+}
+void set_saved(Args* a, void* saved, const Saved& s) {
+  char* at = static_cast<char*>(saved);
+  a->marks = reinterpret_cast<float*>(at);
+  a->ends = reinterpret_cast<float*>(at + s.marks);
+  a->ts = reinterpret_cast<float*>(at + s.marks + s.ends);
+  a->os = reinterpret_cast<float*>(at + s.marks + s.ends + s.rows);
 }
 
 int check_pointers(const Span* ins, int n_in, const Span* outs, int n_out) {
@@ -117,6 +125,80 @@ Scratch scratch_layout(const Args& a, int dtype, bool backward) {
   return s;
 }
 
+
+// The inputs of the forward and the backward: checks them and fills `a`; the spans of the
+// inputs go to ins[0..5].
+int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, const float* g,
+               const float* beta, const float* h0, const int32_t* cu, int64_t B, int64_t L,
+               int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV, const int64_t* strides,
+               float scale, int dtype) {
+  const int64_t T = B * L, e = dtype == SS2D_F32 ? 4 : 2;
+  a->q = q;
+  a->k = k;
+  a->v = v;
+  a->g = g;
+  a->beta = beta;
+  a->h0 = h0;
+  a->cu = cu;
+  default_strides(L, HK, DK, &a->sq);
+  default_strides(L, HK, DK, &a->sk);
+  default_strides(L, H, DV, &a->sv);
+  if (strides) {
+    a->sq = {strides[0], strides[1], strides[2]};
+    a->sk = {strides[3], strides[4], strides[5]};
+    a->sv = {strides[6], strides[7], strides[8]};
+  }
+  a->S = S;
+  a->L = L;
+  a->T = T;
+  a->H = static_cast<int>(H);
+  a->HK = static_cast<int>(HK);
+  a->rep = static_cast<int>(H / HK);
+  a->DK = static_cast<int>(DK);
+  a->DV = static_cast<int>(DV);
+  a->scale = scale;
+  a->slots = slot_count(L, S, T, cu != nullptr, ss2d::delta::kC);
+  a->marks_n = slot_count(L, S, T, cu != nullptr, ss2d::delta::kMark);
+  const int64_t qb = strided_bytes(B, L, HK, DK, a->sq, e),
+                kb = strided_bytes(B, L, HK, DK, a->sk, e),
+                vb = strided_bytes(B, L, H, DV, a->sv, e);
+  if (qb < 0 || kb < 0 || vb < 0) return SS2D_ERR_SHAPE;
+  for (const void* p : {q, k, v})
+    if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
+  for (const void* p : {static_cast<const void*>(g), static_cast<const void*>(beta),
+                        static_cast<const void*>(h0), static_cast<const void*>(cu)})
+    if (misaligned(p, 4)) return SS2D_ERR_ALIGN;
+  ins[0] = {q, qb};
+  ins[1] = {k, kb};
+  ins[2] = {v, vb};
+  ins[3] = {g, T * H * 4};
+  ins[4] = {beta, T * H * 4};
+  ins[5] = {cu, (S + 1) * 4};
+  const int64_t tiles = (DV + 31) / 32;
+  if ((a->slots * H / 4 + 1) * 256 > kMaxThreads || S * H * tiles * 64 > kMaxThreads ||
+      a->marks_n * HK * 256 > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
+    return SS2D_ERR_SHAPE;
+  return SS2D_OK;
+}
+
+bool aligned_keys(const Args& a, int64_t e) {
+  return aligned_rows(a.q, a.sq, a.DK, e) && aligned_rows(a.k, a.sk, a.DK, e);
+}
+
+void set_scratch(Args* a, char* ws, const Scratch& w) {
+  a->nf = ws + w.nf;
+  a->pf = ws + w.pf;
+  a->ktf = ws + w.ktf;
+  a->qtf = ws + w.qtf;
+  a->gates = reinterpret_cast<float*>(ws + w.gates);
+}
+
+int run_forward(const Args& a, int dtype, bool save, hipStream_t st) {
+  const bool al = aligned_keys(a, dtype == SS2D_F32 ? 4 : 2);
+  const int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
+  return err ? err : ss2d::delta::launch_scan(a, dtype, al, save, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -141,46 +223,16 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
   if (T > 0 && (!q || !k || !v || !g || !beta || !o)) return SS2D_ERR_NULL;
   if (T == 0 && !ht) return SS2D_OK;
   Args a{};
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.g = g;
-  a.beta = beta;
-  a.h0 = h0;
-  a.cu = cu_seqlens;
+  Span ins[6];
+  rc = set_inputs(&a, ins, q, k, v, g, beta, h0, cu_seqlens, B, L, S, HK, H, DK, DV, strides, scale,
+                  dtype);
+  if (rc != SS2D_OK) return rc;
   a.o = o;
   a.ht = ht;
-  default_strides(L, HK, DK, &a.sq);
-  default_strides(L, HK, DK, &a.sk);
-  default_strides(L, H, DV, &a.sv);
-  if (strides) {
-    a.sq = {strides[0], strides[1], strides[2]};
-    a.sk = {strides[3], strides[4], strides[5]};
-    a.sv = {strides[6], strides[7], strides[8]};
-  }
-  a.S = S;
-  a.L = L;
-  a.T = T;
-  a.H = static_cast<int>(H);
-  a.HK = static_cast<int>(HK);
-  a.rep = static_cast<int>(H / HK);
-  a.DK = static_cast<int>(DK);
-  a.DV = static_cast<int>(DV);
-  a.scale = scale;
-  const int64_t qb = strided_bytes(B, L, HK, DK, a.sq, e), kb = strided_bytes(B, L, HK, DK, a.sk, e),
-                vb = strided_bytes(B, L, H, DV, a.sv, e);
-  if (qb < 0 || kb < 0 || vb < 0) return SS2D_ERR_SHAPE;
-  for (const void* p : {q, k, v, static_cast<const void*>(o)})
-    if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
-  for (const void* p : {static_cast<const void*>(g), static_cast<const void*>(beta),
-                        static_cast<const void*>(h0), static_cast<const void*>(ht),
-                        static_cast<const void*>(cu_seqlens)})
-    if (misaligned(p, 4)) return SS2D_ERR_ALIGN;
-  if (misaligned(saved, 256)) return SS2D_ERR_ALIGN;
+  if (misaligned(o, static_cast<uintptr_t>(e)) || misaligned(ht, 4) || misaligned(saved, 256))
+    return SS2D_ERR_ALIGN;
   const int64_t state = S * H * DK * DV * 4;
   const Saved sv = saved_layout(L, S, T, H, DK, DV, packed);
-  const Span ins[] = {{q, qb}, {k, kb}, {v, vb}, {g, T * H * 4}, {beta, T * H * 4},
-                      {cu_seqlens, (S + 1) * 4}};
   const Span outs[] = {{o, T * H * DV * e}, {ht, state}, {saved, sv.bytes}};
   rc = check_pointers(ins, 6, outs, 3);
   if (rc != SS2D_OK) return rc;
@@ -190,28 +242,103 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
     if (!(x.p == ht && ht == h0) && check_pointers(first, 1, &x, 1) != SS2D_OK)
       return SS2D_ERR_ALIAS;
 
-  a.slots = slot_count(L, S, T, packed, ss2d::delta::kC);
   a.p_planes = saved ? 3 : 2;
-  if ((a.slots * H / 4 + 1) * 256 > kMaxThreads || S * H * ((DV + 31) / 32) * 64 > kMaxThreads)
-    return SS2D_ERR_SHAPE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Scratch w = scratch_layout(a, dtype, false);
   char* ws = nullptr;
   rc = ss2d::host_scratch_alloc(&ws, w.bytes, st);
   if (rc != SS2D_OK) return rc;
-  a.nf = ws + w.nf;
-  a.pf = ws + w.pf;
-  a.ktf = ws + w.ktf;
-  a.gates = reinterpret_cast<float*>(ws + w.gates);
+  set_scratch(&a, ws, w);
+  if (saved) set_saved(&a, saved, sv);
+  const int err = run_forward(a, dtype, saved != nullptr, st);
+  const hipError_t fe = hipFreeAsync(ws, st);
+  if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
+  if (fe != hipSuccess) return ss2d::host_hip_fail(fe);
+  return SS2D_OK;
+}
+
+int ss1d_delta_backward(const void* q, const void* k, const void* v, const float* g,
+                        const float* beta, const float* h0, const int32_t* cu_seqlens,
+                        const void* saved, const void* dout, const float* dht, void* dq, void* dk,
+                        void* dv, float* dg, float* dbeta, float* dh0, int64_t B, int64_t L,
+                        int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                        const int64_t* strides, float scale, int dtype, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  int rc = check_sizes(B, L, S, HK, H, DK, DV, dtype, packed);
+  if (rc != SS2D_OK) return rc;
+  if (!std::isfinite(scale)) return SS2D_ERR_UNSUPPORTED;
+  if (S == 0 || H == 0) return SS2D_OK;
+  const int64_t T = B * L, e = dtype == SS2D_F32 ? 4 : 2;
+  if (T == 0 && !dh0) return SS2D_OK;
+  if (T > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta))
+    return SS2D_ERR_NULL;
+  Args a{};
+  Span ins[10];
+  rc = set_inputs(&a, ins, q, k, v, g, beta, h0, cu_seqlens, B, L, S, HK, H, DK, DV, strides, scale,
+                  dtype);
+  if (rc != SS2D_OK) return rc;
+  for (const void* p : {dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                        static_cast<const void*>(dv)})
+    if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
+  for (const void* p : {static_cast<const void*>(dht), static_cast<const void*>(dg),
+                        static_cast<const void*>(dbeta), static_cast<const void*>(dh0)})
+    if (misaligned(p, 4)) return SS2D_ERR_ALIGN;
+  if (misaligned(saved, 256)) return SS2D_ERR_ALIGN;
+  const int64_t state = S * H * DK * DV * 4;
+  const Saved sv = saved_layout(L, S, T, H, DK, DV, packed);
+  ins[6] = {h0, state};
+  ins[7] = {saved, sv.bytes};
+  ins[8] = {dout, T * H * DV * e};
+  ins[9] = {dht, state};
+  const Span outs[] = {{dq, T * HK * DK * e}, {dk, T * HK * DK * e}, {dv, T * H * DV * e},
+                       {dg, T * H * 4}, {dbeta, T * H * 4}, {dh0, state}};
+  rc = check_pointers(ins, 10, outs, 6);
+  if (rc != SS2D_OK) return rc;
+  a.dout = dout;
+  a.dht = dht;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.dh0 = dh0;
+  a.p_planes = 3;
+
+  // scratch: the chunk matrices (first the forward's where nothing was kept, then the
+  // backward's in their place), the states' gradients, the gates' partial sums
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t tiles = (DV + 31) / 32;
+  const Scratch w = scratch_layout(a, dtype, true);
+  const size_t dmarks = w.bytes,
+               pbeta = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * e),
+               pgate = pbeta + ss2d::host_align256(size_t(tiles) * T * H * 4),
+               pdots = pgate + ss2d::host_align256(size_t(tiles) * T * H * 4),
+               keep = pdots + ss2d::host_align256(size_t(a.marks_n) * H * tiles * 4),
+               unused_o = keep + (saved ? 0 : size_t(sv.bytes)),
+               bytes = unused_o + (saved ? 0 : ss2d::host_align256(size_t(T) * H * DV * e));
+  char* ws = nullptr;
+  rc = ss2d::host_scratch_alloc(&ws, bytes, st);
+  if (rc != SS2D_OK) return rc;
+  set_scratch(&a, ws, w);
+  a.dmarks = ws + dmarks;
+  a.pbeta = reinterpret_cast<float*>(ws + pbeta);
+  a.pgate = reinterpret_cast<float*>(ws + pgate);
+  a.pdots = reinterpret_cast<float*>(ws + pdots);
+  int err = 0;
   if (saved) {
-    char* at = static_cast<char*>(saved);
-    a.marks = reinterpret_cast<float*>(at);
-    a.ts = reinterpret_cast<float*>(at + sv.marks);
-    a.os = reinterpret_cast<float*>(at + sv.marks + sv.rows);
+    set_saved(&a, const_cast<void*>(saved), sv);
+  } else {
+    set_saved(&a, ws + keep, sv);
+    a.o = ws + unused_o;
+    err = run_forward(a, dtype, true, st);
   }
-  const bool al = aligned_rows(q, a.sq, DK, e) && aligned_rows(k, a.sk, DK, e);
-  int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
-  if (!err) err = ss2d::delta::launch_scan(a, dtype, al, saved != nullptr, st);
+  const bool alk = aligned_keys(a, e);
+  const Strides rows = {L * H * DV, H * DV, DV};
+  const bool alv = aligned_rows(dout, rows, DV, e) && aligned_rows(dv, rows, DV, e);
+  if (!err && a.slots > 0) err = ss2d::delta::launch_prep(a, dtype, alk, true, st);
+  if (!err) err = ss2d::delta::launch_adjoint(a, dtype, alk, st);
+  if (!err && a.marks_n > 0) err = ss2d::delta::launch_grads(a, dtype, alv, st);
+  if (!err && a.marks_n > 0) err = ss2d::delta::launch_gate_grads(a, st);
   const hipError_t fe = hipFreeAsync(ws, st);
   if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
   if (fe != hipSuccess) return ss2d::host_hip_fail(fe);

@@ -6,32 +6,6 @@ namespace ss2d {
 namespace delta {
 namespace {
 
-// The 16 values of tokens acc_row(r, half) in column `col` of a strided tensor.
-template <typename T>
-__device__ __forceinline__ f32x16 load_columns(const T* base, int64_t stride, int half, int valid,
-                                               bool on) {
-  f32x16 x;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int t = acc_row(r, half);
-    x[r] = on && t < valid ? Elem<T>::load(base + t * stride) : 0.0f;
-  }
-  return x;
-}
-
-__device__ __forceinline__ f32x16 load_gate(const float* gate, int half) {
-  f32x16 x;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(gate + 16 * s + 8 * half + 4 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[8 * s + 4 * i + e] = u[e];
-    }
-  return x;
-}
-
 // kP: bf16 terms of the operands of o (2 leave o to its own rounding; 3 hold fp32, for the
 // training forward, whose backward forms the decays' gradient from o).
 template <typename T, int KT, bool kAligned, bool kSave>
@@ -154,13 +128,15 @@ __global__ __launch_bounds__(64) void k_delta_scan(Args a) {
       }
     }
   }
-  if (a.ht && in)
+  if (in)
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int d = 32 * kt + acc_row(r, half);
-        if (d < a.DK) a.ht[(head * a.DK + d) * a.DV + col] = S[kt][r];
+        if (d >= a.DK) continue;
+        if (a.ht) a.ht[(head * a.DK + d) * a.DV + col] = S[kt][r];
+        if (kSave) a.ends[(head * a.DK + d) * a.DV + col] = S[kt][r];
       }
 }
 

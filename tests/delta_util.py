@@ -85,3 +85,38 @@ def o_bounds(DK, ref, dtype):
     if dtype == torch.float32:
         return f32_bound(DK, ref), 0.0
     return f32_bound(DK, ref) + 16 * 2.0 ** -17 * float(ref.abs().max()), BF16_HALF
+
+
+def adjoint(t, scale, cu=None, dstate=None):
+    """The gradients of sum(do * o) + sum(dstate * end states) in float64, token by token."""
+    q, k, v, g, beta = (t[n].double() for n in NAMES)
+    H, DK, DV = v.shape[2], q.shape[3], v.shape[3]
+    rep = H // q.shape[2]
+    parts = [(b, 0, v.shape[1]) for b in range(v.shape[0])] if cu is None else \
+        [(0, int(a), int(e)) for a, e in zip(cu[:-1], cu[1:])]
+    d = {n: torch.zeros_like(x) for n, x in zip(NAMES, (q, k, v, g, beta))}
+    first = []
+    for i, (b, s, e) in enumerate(parts):
+        S = t["h0"][i].double() if t["h0"] is not None else torch.zeros(H, DK, DV).double()
+        _, _, states = rule(*[x[b, s:e] for x in (q, k, v, g, beta)], scale, S)
+        dS = dstate[i].double() if dstate is not None else torch.zeros(H, DK, DV).double()
+        for j in range(e - s - 1, -1, -1):
+            at = (b, s + j)
+            qt, kt = (x[at].repeat_interleave(rep, 0)[:, :, None] for x in (q, k))
+            before = states[j] * g[at].exp()[:, None, None]
+            r = v[at] - (kt * before).sum(1)
+            u = beta[at][:, None] * r
+            do = scale * t["do"][at].double()[:, None, :]
+            d["q"][at] = ((before + kt * u[:, None, :]) * do).sum(2).view(-1, rep, DK).sum(1)
+            dS = dS + qt * do
+            du = (dS * kt).sum(1)
+            d["beta"][at] = (du * r).sum(1)
+            dr = beta[at][:, None] * du
+            d["v"][at] = dr
+            dk = (dS * u[:, None, :]).sum(2) - (before * dr[:, None, :]).sum(2)
+            d["k"][at] = dk.view(-1, rep, DK).sum(1)
+            dS = dS - kt * dr[:, None, :]
+            d["g"][at] = (dS * before).sum((1, 2))
+            dS = dS * g[at].exp()[:, None, None]
+        first.append(dS)
+    return d, torch.stack(first)

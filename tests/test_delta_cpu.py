@@ -106,6 +106,32 @@ def test_outputs_over_inputs(lib):
                 assert step(lib, p) == bnd.SS2D_ERR_ALIAS, (out, i)
 
 
+def backward(lib, p, B=1, L=64, S=1, HK=2, H=4, DK=64, DV=64, strides=None, scale=1.0, dtype=1):
+    return lib.ss1d_delta_backward(*p, B, L, S, HK, H, DK, DV, strides, scale, dtype, None)
+
+
+def test_backward_refusals(lib):
+    for change, code in BAD:
+        assert backward(lib, ptrs(16), S=1, **dict(change)) != bnd.SS2D_OK
+    optional = (5, 6, 7, 9, 15)
+    dense = ptrs(16)
+    dense[6] = None
+    for i in range(16):
+        if i not in optional:
+            p = list(dense)
+            p[i] = None
+            assert backward(lib, p) == bnd.SS2D_ERR_NULL, i
+        p = ptrs(16)
+        p[i] += 1
+        assert backward(lib, p) == bnd.SS2D_ERR_ALIGN, i
+    for out in range(10, 16):
+        for i in range(16):
+            if i != out:
+                p = ptrs(16)
+                p[out] = p[i]
+                assert backward(lib, p) == bnd.SS2D_ERR_ALIAS, (out, i)
+
+
 def test_strides(lib):
     def st(*v):
         return (ctypes.c_int64 * 9)(*v)
@@ -137,9 +163,9 @@ def test_saved_bytes(lib):
     def aligned(x):
         return (x + 255) // 256 * 256
     n = lib.ss1d_delta_saved_bytes(3, 130, 3, 4, 64, 32, 0)
-    assert n == aligned(3 * 3 * 4 * 64 * 32 * 4) + 2 * aligned(3 * 130 * 4 * 32 * 4)
+    assert n == aligned(3 * 3 * 4 * 64 * 32 * 4) + aligned(3 * 4 * 64 * 32 * 4) + 2 * aligned(3 * 130 * 4 * 32 * 4)
     n = lib.ss1d_delta_saved_bytes(1, 130, 5, 4, 64, 32, 1)
-    assert n == aligned((2 + 5) * 4 * 64 * 32 * 4) + 2 * aligned(130 * 4 * 32 * 4)
+    assert n == aligned((2 + 5) * 4 * 64 * 32 * 4) + aligned(5 * 4 * 64 * 32 * 4) + 2 * aligned(130 * 4 * 32 * 4)
     assert lib.ss1d_delta_saved_bytes(1, 130, 2, 4, 64, 32, 0) == -1
     assert lib.ss1d_delta_saved_bytes(1, 130, 1, 4, 200, 32, 0) == -1
 
