@@ -515,6 +515,47 @@ int ss1d_delta_step(const void *q, const void *k, const void *v, const float *g,
                     int64_t T, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
                     const int64_t *strides, float scale, int dtype, void *stream);
 
+/* ---- block norm -----------------------------------------------------------------------------
+ * The norms before and after a block fused with its gate, residual scale and residual
+ * connection (the explainer's VMambaBlock, x + SS2D(norm x), with the gate y SiLU(z) of its
+ * SelectiveSSM):
+ *   p = Norm(h; w_post, b_post)        after the block (p = h with w_post NULL)
+ *   p <- p SiLU(z)                     gate (z NULL: none)
+ *   y = residual + res_scale p         residual NULL: y = res_scale p; res_scale NULL: 1
+ *   n = Norm(y; w_pre, b_pre)          before the next block (none with w_pre NULL)
+ * over D channels; layer 0: Norm(x) = x / sqrt(mean(x^2) + eps) w; layer 1: with x - mean(x) in
+ * place of x, plus b (a bias may be given with either kind, NULL for none).
+ *
+ *   channels_first 0: rows of D, (B * L, D);  1: (B, D, L), the layout of ss2d_forward's maps
+ *     with L = H * W (the norm over D at every position).
+ *   h, z, n: dtype; residual, y: ytype, which is dtype or SS2D_F32 (a residual stream kept
+ *     in fp32); the vectors fp32: w_*, b_* (D), res_scale (G, D): G runs of B * L / G
+ *     successive rows (channels first: of B / G images) each use their own row; G = 0 without.
+ * All contiguous.  D <= 8192, channels first D <= 1024 (SS2D_ERR_UNSUPPORTED above).  y may be
+ * the residual (in place) and may be NULL if n is given.  Everything is computed in fp32 from
+ * the inputs as stored; n from y before its rounding.
+ *
+ * ss2d_norm_backward: the gradients of sum(dy * y) + sum(dn * n), given y as it was stored (the
+ * second norm is recomputed from it) and the other inputs: dh, dz (given with z) in dtype,
+ * dresidual (NULL if there was none) in ytype, and in fp32 dres_scale (G, D), dw_post, db_post
+ * (given with b_post), dw_pre, db_pre (optional).  dy NULL: no gradient arrives at y.  y and
+ * dn are needed with w_pre.  The vectors' sums over rows run in a fixed order (no atomics);
+ * without rows they are 0.
+ *
+ * The shared conventions hold; kernel timing does not cover these entry points. */
+int ss2d_norm_forward(const void *h, const void *z, const void *residual, const float *res_scale,
+                      const float *w_post, const float *b_post, const float *w_pre,
+                      const float *b_pre, void *y, void *n, int64_t B, int64_t L, int64_t D,
+                      int64_t G, int channels_first, int layer, float eps, int dtype, int ytype,
+                      void *stream);
+
+int ss2d_norm_backward(const void *h, const void *z, const float *res_scale, const float *w_post,
+                       const float *b_post, const float *w_pre, const void *y, const void *dy,
+                       const void *dn, void *dh, void *dz, void *dresidual, float *dres_scale,
+                       float *dw_post, float *db_post, float *dw_pre, float *db_pre, int64_t B,
+                       int64_t L, int64_t D, int64_t G, int channels_first, int layer, float eps,
+                       int dtype, int ytype, void *stream);
+
 /* ---- launch-plan override (testing and tuning, not part of the operator) ---------------
  * Sets, for calls made later from the calling host thread only, the lanes that share one
  * channel's states in the forward scan (split: 1, 2 or 4; 0 = automatic) and the chunk

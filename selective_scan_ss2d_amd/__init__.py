@@ -37,6 +37,7 @@ def __getattr__(name):  # the sequence operators import torch; the rest of the p
 _LAZY = {
     "_delta": ("ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_backward",
                "ss1d_delta_step"),
+    "_norm": ("ss2d_norm_forward", "ss2d_norm_backward"),
 }
 
 __all__ = [
@@ -55,5 +56,5 @@ __all__ = [
     "ss1d_bidir_forward_routes_save", "ss2d_backward_routes_saved",
     "ss1d_bidir_backward_routes_saved", "scratch_trim",
     "ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_backward",
-    "ss1d_delta_step",
+    "ss1d_delta_step", "ss2d_norm_forward", "ss2d_norm_backward",
 ]

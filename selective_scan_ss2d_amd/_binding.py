@@ -75,6 +75,10 @@ SIGNATURES = {
     "ss1d_delta_saved_bytes": (_I64, [_I64] * 6 + [ctypes.c_int]),
     "ss1d_delta_step": (ctypes.c_int, [_P] * 8 + [_I64] * 7 + [_P, ctypes.c_float, ctypes.c_int,
                                                                _P]),
+    "ss2d_norm_forward": (ctypes.c_int, [_P] * 10 + [_I64] * 4 + [ctypes.c_int] * 2
+                          + [ctypes.c_float] + [ctypes.c_int] * 2 + [_P]),
+    "ss2d_norm_backward": (ctypes.c_int, [_P] * 17 + [_I64] * 4 + [ctypes.c_int] * 2
+                           + [ctypes.c_float] + [ctypes.c_int] * 2 + [_P]),
     "ss2d_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ss2d_abi_version": (ctypes.c_int, []),
     "ss2d_last_hip_error": (ctypes.c_int, []),

@@ -4,32 +4,13 @@ Argument checks and marshalling only; every step runs in the library's HIP kerne
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
 from . import _binding as bnd
+from ._call import CODES, output as _output, ptr as _ptr, scope as _scope
 
-_CODES = {torch.float32: bnd.SS2D_F32, torch.bfloat16: bnd.SS2D_BF16}
-
-
-@contextlib.contextmanager
-def _switched(device, stream):
-    with torch.cuda.device(device), torch.cuda.stream(stream or torch.cuda.current_stream(device)):
-        yield
-
-
-def _scope(device, stream, *inputs):
-    """The device and stream that a call's outputs and scratch belong to: a context only
-    where they are not the current ones already."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    if stream is not None:  # the inputs' memory is not to be reused before the call has run
-        for t in inputs:
-            if t is not None:
-                t.record_stream(stream)
-    return _switched(device, stream)
 
 
 def _strided(name, t, shape, dtype, device):
@@ -58,7 +39,7 @@ def _inputs(q, k, v, g, beta):
     dev, dtype = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("q must be a GPU tensor")
-    code = _CODES.get(dtype)
+    code = CODES.get(dtype)
     if code is None:
         raise TypeError(f"q must be float32 or bfloat16, not {dtype}")
     B, L, HK, DK = q.shape
@@ -85,17 +66,6 @@ def _sequences(cu_seqlens, B, device):
     if B != 1:
         raise ValueError("packed sequences (cu_seqlens) need a batch of 1")
     return cu_seqlens.shape[0] - 1
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _output(name, t, shape, dtype, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    bnd._expect(name, t, shape, dtype, device)
-    return t
 
 
 def _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o, stream, save):

@@ -1,0 +1,364 @@
+// The block norm with channels first, (B, D, L): a block takes a tile of adjacent positions
+// and all channels, 16 lanes across the positions and the other threads across the channels;
+// sums over the channels run in registers, across a wave and through LDS.  Every tensor is
+// read once and written once.  Bound by HBM.
+#include <algorithm>
+
+#include "ss2d_norm.h"
+
+namespace ss2d {
+namespace norm {
+namespace {
+
+constexpr int kP = 16;  // lanes across the positions
+
+template <typename T, int kN> struct alignas(sizeof(T) * kN) Pack { T v[kN]; };
+
+// A thread's kVec positions of a tile (adjacent with kWide: L a multiple of kVec, planes
+// aligned; else every 16th) and kC channels, every kGroups-th.
+template <int kThreads, int kC, int kVec, bool kWide>
+struct Tile {
+  static constexpr int kGroups = kThreads / kP;
+  int lane, group, D;
+  int64_t L, pos;  // first position of this thread
+  __device__ __forceinline__ int channel(int i) const { return group + kGroups * i; }
+  __device__ __forceinline__ int64_t at(int j) const { return pos + (kWide ? j : kP * j); }
+  __device__ __forceinline__ bool in(int j) const { return at(j) < L; }
+  template <typename T>
+  __device__ __forceinline__ void load(const void* base, int64_t image, int i, float* x) const {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = 0.0f;
+    if (channel(i) >= D) return;
+    const T* p = static_cast<const T*>(base) + (image * D + channel(i)) * L;
+    if constexpr (kWide) {
+      if (in(0)) {
+        const Pack<T, kVec> u = *reinterpret_cast<const Pack<T, kVec>*>(p + pos);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[j] = Elem<T>::to_f32(u.v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (in(j)) x[j] = Elem<T>::load(p + at(j));
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(void* base, int64_t image, int i, const float* x) const {
+    if (channel(i) >= D) return;
+    T* p = static_cast<T*>(base) + (image * D + channel(i)) * L;
+    if constexpr (kWide) {
+      if (!in(0)) return;
+      Pack<T, kVec> u;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) u.v[j] = Elem<T>::from_f32(x[j]);
+      *reinterpret_cast<Pack<T, kVec>*>(p + pos) = u;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (in(j)) p[at(j)] = Elem<T>::from_f32(x[j]);
+    }
+  }
+  __device__ __forceinline__ float channel_value(const float* w, int i) const {
+    return channel(i) < D ? w[channel(i)] : 0.0f;
+  }
+};
+
+// Sums a[j] and b[j] over the channel groups: across the wave's four, then the waves'.
+template <int kThreads, int kVec>
+__device__ __forceinline__ void channel_sum2(float* a, float* b, float2* shared) {
+  constexpr int kWaves = kThreads / 64;
+  const int lane = threadIdx.x & (kP - 1), wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = kP; d < 64; d *= 2)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      a[j] += __shfl_xor(a[j], d);
+      b[j] += __shfl_xor(b[j], d);
+    }
+  __syncthreads();  // the last use of `shared` is over
+  if ((threadIdx.x & 63) < kP)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) shared[(wave * kVec + j) * kP + lane] = make_float2(a[j], b[j]);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    a[j] = b[j] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float2 u = shared[(w * kVec + j) * kP + lane];
+      a[j] += u.x;
+      b[j] += u.y;
+    }
+  }
+}
+
+// x becomes (x - mean) r (layer) or x r along the channels; r of each position, 0 for
+// positions past the end (whose values are 0).
+template <int kThreads, int kC, int kVec, bool kWide>
+__device__ __forceinline__ void unit(const Tile<kThreads, kC, kVec, kWide>& t, float (*x)[kVec],
+                                     float* r, bool layer, float eps, float2* shared) {
+  const float inv = 1.0f / static_cast<float>(t.D);
+  float s[kVec] = {}, q[kVec] = {};
+  if (layer) {
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) s[j] += x[i][j];
+    channel_sum2<kThreads, kVec>(s, q, shared);
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) x[i][j] = t.channel(i) < t.D ? x[i][j] - s[j] * inv : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) s[j] = q[j] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) q[j] = fmaf(x[i][j], x[i][j], q[j]);
+  channel_sum2<kThreads, kVec>(q, s, shared);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) r[j] = t.in(j) ? 1.0f / sqrtf(fmaf(q[j], inv, eps)) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[i][j] *= r[j];
+}
+
+// From the gradient d at unit(x)'s output to the one at its input.
+template <int kThreads, int kC, int kVec, bool kWide>
+__device__ __forceinline__ void through(const Tile<kThreads, kC, kVec, kWide>& t, float (*d)[kVec],
+                                        const float (*x)[kVec], const float* r, bool layer,
+                                        float2* shared) {
+  const float inv = 1.0f / static_cast<float>(t.D);
+  float sx[kVec] = {}, s[kVec] = {};
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      sx[j] = fmaf(d[i][j], x[i][j], sx[j]);
+      s[j] += d[i][j];
+    }
+  channel_sum2<kThreads, kVec>(sx, s, shared);
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      d[i][j] = r[j] * (d[i][j] - fmaf(x[i][j], sx[j] * inv, layer ? s[j] * inv : 0.0f));
+}
+
+template <typename T, typename Y, int kThreads, int kC, int kVec, bool kWide>
+__global__ __launch_bounds__(kThreads) void k_norm_first(Args a) {
+  __shared__ float2 shared[kThreads / 64 * kVec * kP];
+  Tile<kThreads, kC, kVec, kWide> t;
+  t.lane = threadIdx.x & (kP - 1);
+  t.group = threadIdx.x / kP;
+  t.D = a.D;
+  t.L = a.L;
+  const int64_t per = (a.L + kP * kVec - 1) / (kP * kVec), tiles = a.B * per;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t image = tile / per;
+    t.pos = (tile - image * per) * (kP * kVec) + t.lane * (kWide ? kVec : 1);
+    float x[kC][kVec], r[kVec];
+#pragma unroll
+    for (int i = 0; i < kC; ++i) t.template load<T>(a.h, image, i, x[i]);
+    if (a.w_post) unit(t, x, r, a.layer, a.eps, shared);
+    const float* scale = a.scale ? a.scale + image / a.group * a.D : nullptr;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const float w = a.w_post ? t.channel_value(a.w_post, i) : 1.0f;
+      const float b = a.b_post ? t.channel_value(a.b_post, i) : 0.0f;
+      const float s = scale ? t.channel_value(scale, i) : 1.0f;
+      float z[kVec], res[kVec];
+      if (a.z) t.template load<T>(a.z, image, i, z);
+      if (a.residual) t.template load<Y>(a.residual, image, i, res);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        float p = a.w_post ? fmaf(x[i][j], w, b) : x[i][j];
+        if (a.z) p *= gate_value(z[j], sigmoid_f32(z[j]));
+        if (scale) p *= s;
+        if (a.residual) p += res[j];
+        x[i][j] = p;
+      }
+      if (a.y) t.template store<Y>(a.y, image, i, x[i]);
+    }
+    if (a.w_pre) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[i][j] = t.in(j) && t.channel(i) < a.D ? x[i][j] : 0.0f;
+      unit(t, x, r, a.layer, a.eps, shared);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const float w = t.channel_value(a.w_pre, i);
+        const float b = a.b_pre ? t.channel_value(a.b_pre, i) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[i][j] = fmaf(x[i][j], w, b);
+        t.template store<T>(a.n, image, i, x[i]);
+      }
+    }
+  }
+}
+
+// Adds a channel's sums over the 16 lanes of its positions and writes them.
+template <int kThreads, int kC, int kVec, bool kWide>
+__device__ __forceinline__ void write_sums(const Tile<kThreads, kC, kVec, kWide>& t, const float* x,
+                                           float* out) {
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    float s = x[i];
+#pragma unroll
+    for (int d = 1; d < kP; d *= 2) s += __shfl_xor(s, d);
+    if (t.lane == 0 && t.channel(i) < t.D) out[t.channel(i)] = s;
+  }
+}
+
+template <typename T, typename Y, int kThreads, int kC, int kVec, bool kWide>
+__global__ __launch_bounds__(kThreads) void k_norm_first_bwd(Args a) {
+  __shared__ float2 shared[kThreads / 64 * kVec * kP];
+  Tile<kThreads, kC, kVec, kWide> t;
+  t.lane = threadIdx.x & (kP - 1);
+  t.group = threadIdx.x / kP;
+  t.D = a.D;
+  t.L = a.L;
+  const int64_t per = (a.L + kP * kVec - 1) / (kP * kVec), tiles = a.group * per;
+  float dwp[kC] = {}, dbp[kC] = {}, dwn[kC] = {}, dbn[kC] = {};
+  const int64_t part = blockIdx.x % a.blocks_per_group;
+  const int64_t g0 = blockIdx.x / a.blocks_per_group * a.groups_per_block;
+  const int64_t g1 = min(a.G, g0 + a.groups_per_block);
+  for (int64_t g = g0; g < g1; ++g) {
+    float dsc[kC] = {};
+    const float* scale = a.scale ? a.scale + g * a.D : nullptr;
+    for (int64_t tile = part; tile < tiles; tile += a.blocks_per_group) {
+      const int64_t image = g * a.group + tile / per;
+      t.pos = tile % per * (kP * kVec) + t.lane * (kWide ? kVec : 1);
+      float x[kC][kVec], d[kC][kVec], r[kVec];
+      if (a.w_pre) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          t.template load<Y>(a.y, image, i, x[i]);
+          t.template load<T>(a.dn, image, i, d[i]);
+        }
+        unit(t, x, r, a.layer, a.eps, shared);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const float w = t.channel_value(a.w_pre, i);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            dwn[i] = fmaf(d[i][j], x[i][j], dwn[i]);
+            dbn[i] += d[i][j];
+            d[i][j] *= w;
+          }
+        }
+        through(t, d, x, r, a.layer, shared);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) d[i][j] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        if (a.dy) {
+          float y[kVec];
+          t.template load<Y>(a.dy, image, i, y);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) d[i][j] += y[j];
+        }
+        if (a.dres) t.template store<Y>(a.dres, image, i, d[i]);
+        t.template load<T>(a.h, image, i, x[i]);
+      }
+      if (a.w_post) unit(t, x, r, a.layer, a.eps, shared);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const float w = a.w_post ? t.channel_value(a.w_post, i) : 1.0f;
+        const float b = a.b_post ? t.channel_value(a.b_post, i) : 0.0f;
+        const float s = scale ? t.channel_value(scale, i) : 1.0f;
+        float z[kVec], dz[kVec];
+        if (a.z) t.template load<T>(a.z, image, i, z);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float p = a.w_post ? fmaf(x[i][j], w, b) : x[i][j];
+          float sg = 0.0f, gv = 1.0f;
+          if (a.z) {
+            sg = sigmoid_f32(z[j]);
+            gv = gate_value(z[j], sg);
+          }
+          if (scale) {
+            // positions past the end have d = 0
+            dsc[i] = fmaf(d[i][j], a.z ? p * gv : p, dsc[i]);
+            d[i][j] *= s;
+          }
+          if (a.z) {
+            dz[j] = d[i][j] * p * gate_slope(z[j], sg);
+            d[i][j] *= gv;
+          }
+          if (a.w_post) {
+            dwp[i] = fmaf(d[i][j], x[i][j], dwp[i]);
+            dbp[i] += d[i][j];
+            d[i][j] *= w;
+          }
+        }
+        if (a.z) t.template store<T>(a.dz, image, i, dz);
+      }
+      if (a.w_post) through(t, d, x, r, a.layer, shared);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) t.template store<T>(a.dh, image, i, d[i]);
+    }
+    if (a.scale) write_sums(t, dsc, a.scale_parts + (g * a.blocks_per_group + part) * a.D);
+  }
+  float* out = a.parts + int64_t(blockIdx.x) * kSums * a.D;
+  if (a.dw_post) write_sums(t, dwp, out);
+  if (a.db_post) write_sums(t, dbp, out + a.D);
+  if (a.dw_pre) write_sums(t, dwn, out + 2 * a.D);
+  if (a.db_pre) write_sums(t, dbn, out + 3 * a.D);
+}
+
+// Positions per tile: 64 up to 256 channels, then 32 and 16, so that a thread holds at most
+// 64 (backward: of three tensors) values and 16 channels.
+int vec_of(int D) { return D <= 256 ? 4 : (D <= 512 ? 2 : 1); }
+
+template <typename T, typename Y, int kThreads, int kC, int kVec, bool kWide>
+void launch(const Args& a, bool bwd, int64_t blocks, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  if (bwd)
+    hipLaunchKernelGGL((k_norm_first_bwd<T, Y, kThreads, kC, kVec, kWide>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_norm_first<T, Y, kThreads, kC, kVec, kWide>), grid, block, 0, st, a);
+}
+
+template <typename T, typename Y, bool kWide>
+int launch_channels(const Args& a, bool bwd, int64_t blocks, hipStream_t st) {
+  if (a.D <= 64) launch<T, Y, 256, 4, 4, kWide>(a, bwd, blocks, st);
+  else if (a.D <= 128) launch<T, Y, 256, 8, 4, kWide>(a, bwd, blocks, st);
+  else if (a.D <= 192) launch<T, Y, 256, 12, 4, kWide>(a, bwd, blocks, st);
+  else if (a.D <= 256) launch<T, Y, 256, 16, 4, kWide>(a, bwd, blocks, st);
+  else if (a.D <= 512) launch<T, Y, 512, 16, 2, kWide>(a, bwd, blocks, st);
+  else launch<T, Y, 1024, 16, 1, kWide>(a, bwd, blocks, st);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <bool kWide>
+int launch_types(const Args& a, int dtype, int ytype, bool bwd, int64_t blocks, hipStream_t st) {
+  if (dtype == 0) return launch_channels<float, float, kWide>(a, bwd, blocks, st);
+  if (ytype == 0) return launch_channels<uint16_t, float, kWide>(a, bwd, blocks, st);
+  return launch_channels<uint16_t, uint16_t, kWide>(a, bwd, blocks, st);
+}
+
+}  // namespace
+
+int64_t tiles_first(const Args& a) {  // of one group
+  const int64_t width = kP * vec_of(a.D);
+  return a.group * ((a.L + width - 1) / width);
+}
+
+int launch_norm_first(const Args& a, int dtype, int ytype, bool vec, bool bwd, int64_t blocks,
+                      hipStream_t st) {
+  if (!bwd) blocks = std::min<int64_t>(tiles_first(a) * a.G, 256 * 16);
+  const bool wide = vec && a.L % vec_of(a.D) == 0;
+  return wide ? launch_types<true>(a, dtype, ytype, bwd, blocks, st)
+              : launch_types<false>(a, dtype, ytype, bwd, blocks, st);
+}
+
+}  // namespace norm
+}  // namespace ss2d
