@@ -28,6 +28,7 @@ constexpr int kMark = 64;   // tokens between the states a training forward keep
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -47,9 +48,8 @@ struct Args {
   int H, HK, rep, DK, DV;      // rep = H / HK value heads share a key head
   float scale;
   // scratch, per (chunk slot, head): matrix fragments and gates
-  char *nf, *pf;               // N and P (backward: their transposes), per value head
-  char *ktf, *qtf;             // K^T and Q^T, per key head
-  float* gates;                // (slot, H, 3, 32): e^G, e^(G_32 - G), beta
+  char* keys;                  // (slot, HK) records, see KeyRecord
+  char* heads;                 // (slot, H) records, see HeadRecord
   int64_t slots;               // chunk slots
   int p_planes;                // bf16 terms kept of P
   // kept by a training forward
@@ -210,6 +210,10 @@ __device__ __forceinline__ f32x16 mma(const Wide<float, P>& a, const Wide<float,
   return mma8(a.v, b.v, c);
 }
 
+// Pointers into device memory, whose accesses need no look at the address space.
+template <typename T> using Global = __attribute__((address_space(1))) T*;
+template <typename T> __device__ __forceinline__ Global<T> global(T* p) { return (Global<T>)p; }
+
 // ---- loads ---------------------------------------------------------------------------------
 // 8 consecutive values of a row, columns c .. c + 7 of `width`; zero past the width or where
 // `on` is false.  kAligned: every row starts on 16 bytes and the width is a multiple of 8.
@@ -247,19 +251,6 @@ __device__ __forceinline__ void load8(Exact<float>& x, const float* row, int c, 
       x.v[i] = e;
     }
   }
-}
-
-// The 16 values of tokens acc_row(r, half) in column `col` of a strided tensor.
-template <typename T>
-__device__ __forceinline__ f32x16 load_columns(const T* base, int64_t stride, int half, int valid,
-                                               bool on) {
-  f32x16 x;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int t = acc_row(r, half);
-    x[r] = on && t < valid ? Elem<T>::load(base + t * stride) : 0.0f;
-  }
-  return x;
 }
 
 __device__ __forceinline__ f32x16 load_gate(const float* gate, int half) {
@@ -328,14 +319,65 @@ __device__ __forceinline__ void get(Wide<float, P>& x, const char* at, int lane)
   x.v = get_planes(at, lane);
 }
 
-// Bytes of one chunk's fragments.
-template <typename T> constexpr int64_t n_bytes() { return 2 * wide_planes<T, 3>() * kPlane; }
-template <typename T> __host__ __device__ constexpr int64_t p_bytes(int planes) {
-  return 2 * int64_t(sizeof(T) == 4 ? 2 : planes) * kPlane;
+// One chunk's operands in scratch, in the order in which the sequential kernels take them:
+// per key head K, K^T and Q (backward: Q^T), per value head N, P (backward: their transposes)
+// and a plane of gates (e^G, e^(G_32 - G), beta: 32 values each).
+template <typename T, int KT> struct KeyRecord {
+  static constexpr int kOperand = 2 * KT * exact_planes<T>();  // planes of one operand
+  static constexpr int kPlanes = 3 * kOperand;
+};
+template <typename T, int P> struct HeadRecord {
+  static constexpr int kN = 2 * wide_planes<T, 3>(), kP = 2 * wide_planes<T, P>();
+  static constexpr int kGates = kN + kP, kPlanes = kGates + 1;
+};
+__host__ __device__ constexpr int key_planes(bool f32, int kt) { return 3 * 2 * kt * (f32 ? 2 : 1); }
+__host__ __device__ constexpr int head_planes(bool f32, int p) {
+  return (f32 ? 4 : 6) + 2 * (f32 ? 2 : p) + 1;
 }
-template <typename T> __host__ __device__ constexpr int64_t t_bytes(int kt) {
-  return 2 * int64_t(kt) * exact_planes<T>() * kPlane;
-}
+
+// Brings the records of one chunk after another into LDS, two buffers in turn: fetch() starts
+// the next chunk's loads into registers, which the chunk's products overlap, commit() writes
+// them to the other buffer.  The block's kW waves share the planes.
+template <typename T, int KT, int P, int kW> struct Stage {
+  using Key = KeyRecord<T, KT>;
+  using Head = HeadRecord<T, P>;
+  static constexpr int kPlanes = Key::kPlanes + Head::kPlanes;
+  static constexpr int kEach = (kPlanes + kW - 1) / kW;
+  u32x4 x[kEach];
+  __device__ __forceinline__ void fetch(const Args& a, int64_t slot, int hv, int hk, int wave,
+                                        int lane) {
+    const char* key = a.keys + (slot * a.HK + hk) * (int64_t(Key::kPlanes) * kPlane);
+    const char* head = a.heads + (slot * a.H + hv) * (int64_t(Head::kPlanes) * kPlane);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int p = wave + kW * i;
+      if (p < kPlanes) {
+        const char* from = p < Key::kPlanes ? key + p * kPlane : head + (p - Key::kPlanes) * kPlane;
+        x[i] = *(Global<const u32x4>)(global(from) + 16 * lane);
+      }
+    }
+  }
+  __device__ __forceinline__ void commit(char* buffer, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int p = wave + kW * i;
+      if (p < kPlanes) reinterpret_cast<u32x4*>(buffer + p * kPlane)[lane] = x[i];
+    }
+  }
+  // operand `which` (0 K, 1 K^T, 2 Q or Q^T), tile kt, step s
+  static __device__ __forceinline__ const char* operand(const char* buffer, int which, int kt, int s) {
+    return buffer + (which * Key::kOperand + (2 * kt + s) * exact_planes<T>()) * kPlane;
+  }
+  static __device__ __forceinline__ const char* n(const char* buffer, int s) {
+    return buffer + (Key::kPlanes + s * wide_planes<T, 3>()) * kPlane;
+  }
+  static __device__ __forceinline__ const char* p(const char* buffer, int s) {
+    return buffer + (Key::kPlanes + Head::kN + s * wide_planes<T, P>()) * kPlane;
+  }
+  static __device__ __forceinline__ const float* gates(const char* buffer) {
+    return reinterpret_cast<const float*>(buffer + (Key::kPlanes + Head::kGates) * kPlane);
+  }
+};
 
 // Orders a wave's own LDS accesses (its lanes exchange data; no other wave takes part).
 __device__ __forceinline__ void wave_sync() {
@@ -344,12 +386,161 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// ---- 32 x 32 tiles of matrices in memory -----------------------------------------------------
+// A wave moves its tile in 16-byte pieces of rows and turns it in LDS of its own into the
+// product's layout (a column per lane) and back: there the rows' distance is a constant, so
+// the 16 accesses of a lane need no address arithmetic, which would otherwise cost more than
+// the products.  The row pitch keeps the wave's halves, 8 rows apart, on different banks.
+constexpr int row_base(int r) { return 16 * (r >> 3) + (r & 7); }  // acc_row of the lower half
+template <typename T> constexpr int tile_pitch() { return sizeof(T) == 4 ? 144 : 80; }
+constexpr int kTileBytes = 32 * 144;
+
+// Whole tiles of aligned rows go through registers, loaded ahead; others (a sequence's last
+// chunk, odd widths) element by element when they are wanted.
+template <typename T> struct Tile {
+  static constexpr int kPieces = sizeof(T);              // 16-byte pieces per lane: 2 or 4
+  static constexpr int kAcross = 2 * sizeof(T);          // pieces across a row
+  static constexpr int kStep = 64 / kAcross;             // rows per access of the wave
+  u32x4 x[kPieces];
+  const void* base;
+  uint32_t stride;
+  int rows, cols;
+
+  __device__ __forceinline__ static bool whole(const void* base, uint32_t stride, int rows, int cols) {
+    return ((reinterpret_cast<uintptr_t>(base) | stride) & 15) == 0 && rows >= 32 && cols >= 32;
+  }
+  // `rows` rows (others are 0) and `cols` columns (others repeat the last) of the tile whose
+  // first element is at `b`, rows `st` bytes apart (all uniform).
+  __device__ __forceinline__ void fetch(const void* b, uint32_t st, int lane, int r, int c) {
+    base = b;
+    stride = st;
+    rows = r;
+    cols = c;
+    if (!whole(b, st, r, c)) return;
+    const auto p = global(static_cast<const char*>(b));
+    const uint32_t off = lane / kAcross * st + lane % kAcross * 16;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      x[i] = *(Global<const u32x4>)(p + uint64_t(i * kStep) * st + off);
+  }
+  // The tile in the product's layout, by way of `lds`.
+  __device__ __forceinline__ f32x16 columns(char* lds, int lane) const {
+    wave_sync();
+    if (whole(base, stride, rows, cols)) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        *reinterpret_cast<u32x4*>(lds + (lane / kAcross + i * kStep) * tile_pitch<T>() +
+                                  lane % kAcross * 16) = x[i];
+    } else {
+      const auto p = global(static_cast<const char*>(base));
+      const uint32_t c = lane & 31;
+#pragma nounroll
+      for (int i = lane >> 5; i < 32; i += 2) {
+        T v = T(0);
+        if (i < rows) v = *(Global<const T>)(p + (uint64_t(i) * stride + min(int(c), cols - 1) * sizeof(T)));
+        *reinterpret_cast<T*>(lds + i * tile_pitch<T>() + c * sizeof(T)) = v;
+      }
+    }
+    wave_sync();
+    f32x16 v;
+    const char* at = lds + 8 * (lane >> 5) * tile_pitch<T>() + (lane & 31) * sizeof(T);
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      v[r] = Elem<T>::load(reinterpret_cast<const T*>(at + row_base(r) * tile_pitch<T>()));
+    return v;
+  }
+};
+
+// Stores `rows` rows and `cols` columns (0: none) of a tile in the product's layout.
+template <typename T>
+__device__ __forceinline__ void store_tile(const f32x16& v, void* base, uint32_t stride, char* lds,
+                                           int lane, int rows, int cols) {
+  using X = Tile<T>;
+  wave_sync();
+  char* to = lds + 8 * (lane >> 5) * tile_pitch<T>() + (lane & 31) * sizeof(T);
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    *reinterpret_cast<T*>(to + row_base(r) * tile_pitch<T>()) = Elem<T>::from_f32(v[r]);
+  wave_sync();
+  const auto p = global(static_cast<char*>(base));
+  if (X::whole(base, stride, rows, cols)) {
+    const uint32_t off = lane / X::kAcross * stride + lane % X::kAcross * 16;
+#pragma unroll
+    for (int i = 0; i < X::kPieces; ++i)
+      *(Global<u32x4>)(p + uint64_t(i * X::kStep) * stride + off) = *reinterpret_cast<const u32x4*>(
+          lds + (lane / X::kAcross + i * X::kStep) * tile_pitch<T>() + lane % X::kAcross * 16);
+  } else {
+    const int c = lane & 31, end = min(rows, 32);
+    if (c < cols)
+#pragma nounroll
+      for (int i = lane >> 5; i < end; i += 2)
+        *(Global<T>)(p + (uint64_t(i) * stride + c * sizeof(T))) =
+            *reinterpret_cast<const T*>(lds + i * tile_pitch<T>() + c * sizeof(T));
+  }
+}
+
+// A wave's place: 32 columns (`tile`) of one sequence and head.  Columns past the last one
+// repeat it, waves past the last tile repeat that tile: both compute and never store.
+struct Place {
+  int lane, wave, half, tile, hv, hk;
+  int cols, store_cols;  // columns of the tile; those that this wave stores (0: none)
+  int64_t n, head;
+  bool in;               // this lane's column is stored
+};
+template <int kW>
+__device__ __forceinline__ Place place(const Args& a, int64_t unit) {
+  Place p;
+  const int tiles = (a.DV + 31) / 32, per = (tiles + kW - 1) / kW;
+  p.lane = threadIdx.x & 63;
+  p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p.half = p.lane >> 5;
+  p.head = unit / per;
+  const int tile = static_cast<int>(unit - p.head * per) * kW + p.wave;
+  p.tile = min(tile, tiles - 1);
+  p.n = p.head / a.H;
+  p.hv = static_cast<int>(p.head - p.n * a.H);
+  p.hk = p.hv / a.rep;
+  p.cols = min(32, a.DV - 32 * p.tile);
+  p.store_cols = tile < tiles ? p.cols : 0;
+  p.in = (p.lane & 31) < p.store_cols;
+  return p;
+}
+
+// The state's (DK, DV) columns of a wave, from `base` (its first column; NULL: zeros).
+template <int KT>
+__device__ __forceinline__ void load_state(f32x16* S, const float* base, const Args& a, const Place& w,
+                                           char* lds) {
+  const uint32_t stride = a.DV * 4u;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    S[kt] = f32x16{};
+    const int rows = a.DK - 32 * kt;
+    if (base != nullptr && rows > 0) {
+      Tile<float> x;
+      x.fetch(base + int64_t(32) * kt * a.DV, stride, w.lane, rows, w.cols);
+      S[kt] = x.columns(lds, w.lane);
+    }
+  }
+}
+template <typename T, int KT>
+__device__ __forceinline__ void store_state(const f32x16* S, void* base, const Args& a, const Place& w,
+                                            char* lds) {
+  const uint32_t stride = a.DV * sizeof(T);
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) {
+    const int rows = a.DK - 32 * kt;
+    if (rows > 0)
+      store_tile<T>(S[kt], static_cast<char*>(base) + int64_t(32) * kt * stride, stride, lds, w.lane,
+                    rows, w.store_cols);
+  }
+}
+
 // Log decays below this are 0 in fp32 either way; the bound keeps -inf out of differences.
 constexpr float kMinLog = -1000.0f;
 
 int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);
-int launch_scan(const Args& a, int dtype, bool aligned, bool save, hipStream_t st);
-int launch_adjoint(const Args& a, int dtype, bool aligned, hipStream_t st);
+int launch_scan(const Args& a, int dtype, bool save, hipStream_t st);
+int launch_adjoint(const Args& a, int dtype, hipStream_t st);
 int launch_grads(const Args& a, int dtype, bool aligned, hipStream_t st);
 int launch_gate_grads(const Args& a, hipStream_t st);
 

@@ -15,6 +15,7 @@ using ss2d::delta::Args;
 using ss2d::delta::Strides;
 
 constexpr int64_t kMaxTokens = int64_t(1) << 40;
+constexpr int64_t kMaxLine = int64_t(1) << 24;    // elements from one token's row to the next
 constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of one launch
 
 struct Span {  // the memory of one argument
@@ -105,26 +106,18 @@ int check_pointers(const Span* ins, int n_in, const Span* outs, int n_out) {
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 struct Scratch {
-  size_t nf, pf, ktf, qtf, gates, bytes;
+  size_t keys, heads, bytes;
 };
-Scratch scratch_layout(const Args& a, int dtype, bool backward) {
+Scratch scratch_layout(const Args& a, int dtype) {
   using namespace ss2d::delta;
-  const size_t per = size_t(a.slots) * a.H, key = size_t(a.slots) * a.HK;
   const int kt = a.DK <= 32 ? 1 : (a.DK <= 64 ? 2 : 4);
   const bool f32 = dtype == SS2D_F32;
-  const size_t nb = f32 ? n_bytes<float>() : n_bytes<uint16_t>();
-  const size_t pb = f32 ? p_bytes<float>(a.p_planes) : p_bytes<uint16_t>(a.p_planes);
-  const size_t tb = f32 ? t_bytes<float>(kt) : t_bytes<uint16_t>(kt);
   Scratch s{};
-  s.nf = 0;
-  s.pf = s.nf + ss2d::host_align256(per * nb);
-  s.ktf = s.pf + ss2d::host_align256(per * pb);
-  s.qtf = s.ktf + ss2d::host_align256(key * tb);
-  s.gates = s.qtf + (backward ? ss2d::host_align256(key * tb) : 0);
-  s.bytes = s.gates + ss2d::host_align256(per * 3 * kC * 4);
+  s.keys = 0;
+  s.heads = size_t(a.slots) * a.HK * key_planes(f32, kt) * kPlane;
+  s.bytes = s.heads + size_t(a.slots) * a.H * head_planes(f32, a.p_planes) * kPlane;
   return s;
 }
-
 
 // The inputs of the forward and the backward: checks them and fills `a`; the spans of the
 // inputs go to ins[0..5].
@@ -163,6 +156,8 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
                 kb = strided_bytes(B, L, HK, DK, a->sk, e),
                 vb = strided_bytes(B, L, H, DV, a->sv, e);
   if (qb < 0 || kb < 0 || vb < 0) return SS2D_ERR_SHAPE;
+  // the kernels keep a chunk's row offsets in 32 bits
+  if (a->sv.l > kMaxLine || H * DV > kMaxLine) return SS2D_ERR_UNSUPPORTED;
   for (const void* p : {q, k, v})
     if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
   for (const void* p : {static_cast<const void*>(g), static_cast<const void*>(beta),
@@ -186,17 +181,14 @@ bool aligned_keys(const Args& a, int64_t e) {
 }
 
 void set_scratch(Args* a, char* ws, const Scratch& w) {
-  a->nf = ws + w.nf;
-  a->pf = ws + w.pf;
-  a->ktf = ws + w.ktf;
-  a->qtf = ws + w.qtf;
-  a->gates = reinterpret_cast<float*>(ws + w.gates);
+  a->keys = ws + w.keys;
+  a->heads = ws + w.heads;
 }
 
 int run_forward(const Args& a, int dtype, bool save, hipStream_t st) {
   const bool al = aligned_keys(a, dtype == SS2D_F32 ? 4 : 2);
   const int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
-  return err ? err : ss2d::delta::launch_scan(a, dtype, al, save, st);
+  return err ? err : ss2d::delta::launch_scan(a, dtype, save, st);
 }
 
 }  // namespace
@@ -244,7 +236,7 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
 
   a.p_planes = saved ? 3 : 2;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const Scratch w = scratch_layout(a, dtype, false);
+  const Scratch w = scratch_layout(a, dtype);
   char* ws = nullptr;
   rc = ss2d::host_scratch_alloc(&ws, w.bytes, st);
   if (rc != SS2D_OK) return rc;
@@ -308,7 +300,7 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   // backward's in their place), the states' gradients, the gates' partial sums
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t tiles = (DV + 31) / 32;
-  const Scratch w = scratch_layout(a, dtype, true);
+  const Scratch w = scratch_layout(a, dtype);
   const size_t dmarks = w.bytes,
                pbeta = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * e),
                pgate = pbeta + ss2d::host_align256(size_t(tiles) * T * H * 4),
@@ -336,7 +328,7 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   const Strides rows = {L * H * DV, H * DV, DV};
   const bool alv = aligned_rows(dout, rows, DV, e) && aligned_rows(dv, rows, DV, e);
   if (!err && a.slots > 0) err = ss2d::delta::launch_prep(a, dtype, alk, true, st);
-  if (!err) err = ss2d::delta::launch_adjoint(a, dtype, alk, st);
+  if (!err) err = ss2d::delta::launch_adjoint(a, dtype, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_grads(a, dtype, alv, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_gate_grads(a, st);
   const hipError_t fe = hipFreeAsync(ws, st);

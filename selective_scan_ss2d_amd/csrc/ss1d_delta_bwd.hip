@@ -21,94 +21,101 @@ namespace {
 // Sums each register over the 32 lanes of a half: lane l of the half gets the sum of
 // register row_of(l) (each twice).  Halving the registers at every exchange costs 16
 // exchanges for 16 sums.
-__device__ __forceinline__ float sum_columns(f32x16 x, int lane) {
+template <int kN> __device__ __forceinline__ void halve(float* x, int lane) {
+  const bool up = lane & (2 * kN);
 #pragma unroll
-  for (int n = 8, d = 16; n >= 1; n /= 2, d /= 2) {
-    const bool up = lane & d;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float keep = up ? x[n + i] : x[i], send = up ? x[i] : x[n + i];
-      x[i] = keep + __shfl_xor(send, d);
-    }
+  for (int i = 0; i < kN; ++i) {
+    const float keep = up ? x[kN + i] : x[i], send = up ? x[i] : x[kN + i];
+    x[i] = keep + __shfl_xor(send, 2 * kN);
   }
+  if constexpr (kN > 1) halve<kN / 2>(x, lane);
+}
+__device__ __forceinline__ float sum_columns(const f32x16& v, int lane) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = v[i];
+  halve<8>(x, lane);
   return x[0] + __shfl_xor(x[0], 1);
 }
 __device__ __forceinline__ int row_of(int lane) { return (lane & 31) >> 1; }
 
-// One wave per (sequence, head, 32 columns), chunks last to first.
-template <typename T, int KT, bool kAligned>
-__global__ __launch_bounds__(64) void k_delta_adjoint(Args a) {
-  const int lane = threadIdx.x, half = lane >> 5, own = swap23(lane & 31);
-  const int tiles = (a.DV + 31) / 32;
-  const int64_t unit = blockIdx.x;
-  const int64_t head = unit / tiles;
-  const int tile = static_cast<int>(unit - head * tiles);
-  const int64_t n = head / a.H;
-  const int hv = static_cast<int>(head - n * a.H), hk = hv / a.rep;
-  const int col = 32 * tile + (lane & 31);
-  const bool in = col < a.DV;
-  const Seq seq = sequence(a, n);
-  const int64_t slot0 = first_slot(a, n, seq, kC), mark0 = first_slot(a, n, seq, kMark);
+// One wave per (sequence, head, 32 columns), kW adjacent ones per block sharing the chunks'
+// operands through LDS, chunks last to first.
+template <typename T, int KT, int kW>
+__global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
+  using St = Stage<T, KT, 3, kW>;
+  __shared__ __align__(16) char buffers[2][St::kPlanes * kPlane];
+  __shared__ __align__(16) char spare[kW][kTileBytes];
+  const Place w = place<kW>(a, blockIdx.x);
+  const int lane = w.lane, half = w.half, tiles = (a.DV + 31) / 32;
+  char* const lds = spare[w.wave];
+  const Seq seq = sequence(a, w.n);
+  const int64_t slot0 = first_slot(a, w.n, seq, kC), mark0 = first_slot(a, w.n, seq, kMark);
+  const int64_t state = w.head * a.DK * a.DV + 32 * w.tile;
+  const uint32_t vline = static_cast<uint32_t>(a.sv.l) * sizeof(T), line = a.H * a.DV;
 
   f32x16 dS[KT];
-#pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int d = 32 * kt + acc_row(r, half);
-      dS[kt][r] = a.dht && in && d < a.DK ? a.dht[(head * a.DK + d) * a.DV + col] : 0.0f;
-    }
+  load_state<KT>(dS, a.dht ? a.dht + state : nullptr, a, w, lds);
   const int64_t chunks = (seq.len + kC - 1) / kC;
+  St stage;
+  Tile<T> vx, dx;
+  Tile<float> tx, ox;
+  auto row_of_chunk = [&](int64_t c) {
+    return (seq.row + c * kC) * line + w.hv * a.DV + 32 * w.tile;
+  };
+  auto fetch = [&](int64_t c) {  // what a chunk wants early: loaded a chunk ahead
+    stage.fetch(a, slot0 + c, w.hv, w.hk, w.wave, lane);
+    dx.fetch(static_cast<const T*>(a.dout) + row_of_chunk(c), line * sizeof(T), lane,
+             static_cast<int>(min<int64_t>(kC, seq.len - c * kC)), w.cols);
+  };
+  if (chunks > 0) {
+    fetch(chunks - 1);
+    stage.commit(buffers[(chunks - 1) & 1], w.wave, lane);
+    __syncthreads();
+  }
   for (int64_t c = chunks - 1; c >= 0; --c) {
-    const int64_t t0 = c * kC, slot = slot0 + c;
+    const int64_t t0 = c * kC, row0 = seq.row + t0;
     const int valid = static_cast<int>(min<int64_t>(kC, seq.len - t0));
-    if ((c & 1) || c == chunks - 1) {  // the end of a block of 64 tokens
-      const int64_t mark = mark0 + (c >> 1);
-      const float* after = c == chunks - 1 ? a.ends + head * a.DK * a.DV
-                                           : a.marks + ((mark + 1) * a.H + hv) * a.DK * a.DV;
-      T* at = static_cast<T*>(a.dmarks) + (mark * a.H + hv) * a.DK * a.DV;
-      float dot = 0.0f;
+    const char* buf = buffers[c & 1];
+    const f32x16 dout = dx.columns(lds, lane);
+    if (c > 0) fetch(c - 1);
+    // what it wants at its end
+    const T* vat = static_cast<const T*>(a.v) + token_at(a, a.sv, w.n, seq, t0) + w.hv * a.sv.h;
+    vx.fetch(vat + 32 * w.tile, vline, lane, valid, w.cols);
+    tx.fetch(a.ts + row_of_chunk(c), line * 4, lane, valid, w.cols);
+    ox.fetch(a.os + row_of_chunk(c), line * 4, lane, valid, w.cols);
+    const bool ends = (c & 1) || c == chunks - 1;  // the end of a block of 64 tokens
+    const int64_t mark = mark0 + (c >> 1);
+    Tile<float> after[KT];
+    if (ends) {
+      const float* from = c == chunks - 1
+                              ? a.ends + state
+                              : a.marks + ((mark + 1) * a.H + w.hv) * a.DK * a.DV + 32 * w.tile;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int d = 32 * kt + acc_row(r, half);
-          if (in && d < a.DK) {
-            dot = fmaf(dS[kt][r], after[int64_t(d) * a.DV + col], dot);
-            at[int64_t(d) * a.DV + col] = Elem<T>::from_f32(dS[kt][r]);
-          }
-        }
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
-      if (lane == 0) a.pdots[(mark * a.H + hv) * tiles + tile] = dot;
+        if (a.DK > 32 * kt)
+          after[kt].fetch(from + int64_t(32) * kt * a.DV, a.DV * 4u, lane, a.DK - 32 * kt, w.cols);
     }
-    const bool on = own < valid;
-    const int64_t tok = t0 + (on ? own : 0);
-    const T* krow = static_cast<const T*>(a.k) + token_at(a, a.sk, n, seq, tok) + hk * a.sk.h;
+    __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the products
     f32x16 ks = {};
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Exact<T> kx;
-        load8<kAligned>(kx, krow, 32 * kt + 16 * s + 8 * half, a.DK, on);
-        Wide<T, 3> w;
-        set_wide(w, part(dS[kt], s));
-        ks = mma(kx, w, ks);
+        get(kx, St::operand(buf, 0, kt, s), lane);
+        Wide<T, 3> sw;
+        set_wide(sw, part(dS[kt], s));
+        ks = mma(kx, sw, ks);
       }
-    const float* gate = a.gates + (slot * a.H + hv) * (3 * kC);
+    const float* gate = St::gates(buf);
     const f32x16 gam = load_gate(gate, half), beta = load_gate(gate + 2 * kC, half);
-    const int64_t row0 = seq.row + t0;
-    const int64_t line = int64_t(a.H) * a.DV, at = row0 * line + hv * a.DV + col;
-    const f32x16 dout = load_columns<T>(static_cast<const T*>(a.dout) + at, line, half, valid, in);
-    const char* nf = a.nf + (slot * a.H + hv) * n_bytes<T>();
-    const char* pf = a.pf + (slot * a.H + hv) * p_bytes<T>(3);
     f32x16 du = load_gate(gate + kC, half) * ks;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       Wide<T, 3> pw;
       Wide<T, 1> dw;  // exact: do is in the data type
-      get(pw, pf + s * wide_planes<T, 3>() * kPlane, lane);
+      get(pw, St::p(buf, s), lane);
       set_wide(dw, part(dout, s));
       if constexpr (sizeof(T) == 4) {
         du = mma(pw, dw, du);
@@ -121,33 +128,29 @@ __global__ __launch_bounds__(64) void k_delta_adjoint(Args a) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       Wide<T, 3> nw, rw;
-      get(nw, nf + s * wide_planes<T, 3>() * kPlane, lane);
+      get(nw, St::n(buf, s), lane);
       set_wide(rw, part(bu, s));
       nr = mma(nw, rw, nr);
     }
-    const f32x16 w = du - nr, dv = beta * w;
-    // what the gates' gradients take from these 32 columns
-    f32x16 ts, os;
+    const f32x16 y = du - nr, dv = beta * y;
+    if (ends) {
+      store_state<T, KT>(
+          dS, static_cast<T*>(a.dmarks) + (mark * a.H + w.hv) * a.DK * a.DV + 32 * w.tile, a, w, lds);
+      float dot = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = acc_row(r, half);
-      const bool ok = in && i < valid;
-      ts[r] = ok ? a.ts[at + i * line] : 0.0f;
-      os[r] = ok ? a.os[at + i * line] : 0.0f;
-      if (ok) static_cast<T*>(a.dv)[at + i * line] = Elem<T>::from_f32(dv[r]);
-    }
-    const T* vat = static_cast<const T*>(a.v) + token_at(a, a.sv, n, seq, t0) + hv * a.sv.h + col;
-    const f32x16 v = load_columns<T>(vat, a.sv.l, half, valid, in);
-    const float sb = sum_columns(w * ts, lane), sg = sum_columns(dout * os - dv * v, lane);
-    const int i = acc_row(row_of(lane), half);
-    if ((lane & 1) == 0 && i < valid) {
-      const int64_t p = (tile * a.T + row0 + i) * a.H + hv;
-      a.pbeta[p] = sb;
-      a.pgate[p] = sg;
+      for (int kt = 0; kt < KT; ++kt)
+        if (a.DK > 32 * kt) {
+          const f32x16 S = after[kt].columns(lds, lane);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) dot = fmaf(dS[kt][r], S[r], dot);
+        }
+      dot = w.in ? dot : 0.0f;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
+      if (lane == 0 && w.store_cols > 0) a.pdots[(mark * a.H + w.hv) * tiles + w.tile] = dot;
     }
     const f32x16 gdo = (a.scale * gam) * dout, gdv = -(gam * dv);
     const float whole = gate[kC - 1];
-    const int64_t keyed = (slot * a.HK + hk) * t_bytes<T>(KT);
     Wide<T, 3> ow[2], vw[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -160,22 +163,35 @@ __global__ __launch_bounds__(64) void k_delta_adjoint(Args a) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Exact<T> qx, kx;
-        const int64_t f = keyed + (2 * kt + s) * exact_planes<T>() * kPlane;
-        get(qx, a.qtf + f, lane);
-        get(kx, a.ktf + f, lane);
+        get(qx, St::operand(buf, 2, kt, s), lane);
+        get(kx, St::operand(buf, 1, kt, s), lane);
         dS[kt] = mma(qx, ow[s], dS[kt]);
         dS[kt] = mma(kx, vw[s], dS[kt]);
       }
     }
-  }
-  if (a.dh0 && in)
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    // dv, and what the gates' gradients take from these 32 columns
+    store_tile<T>(dv, static_cast<T*>(a.dv) + row_of_chunk(c), line * sizeof(T), lds, lane, valid,
+                  w.store_cols);
+    f32x16 sb = y * tx.columns(lds, lane);
+    f32x16 sg = dout * ox.columns(lds, lane) - dv * vx.columns(lds, lane);
+    if (w.store_cols < 32) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int d = 32 * kt + acc_row(r, half);
-        if (d < a.DK) a.dh0[(head * a.DK + d) * a.DV + col] = dS[kt][r];
+        sb[r] = w.in ? sb[r] : 0.0f;
+        sg[r] = w.in ? sg[r] : 0.0f;
       }
+    }
+    const float beta_sum = sum_columns(sb, lane), gate_sum = sum_columns(sg, lane);
+    const int i = acc_row(row_of(lane), half);
+    if ((lane & 1) == 0 && i < valid && w.store_cols > 0) {
+      const int64_t p = (w.tile * a.T + row0 + i) * a.H + w.hv;
+      a.pbeta[p] = beta_sum;
+      a.pgate[p] = gate_sum;
+    }
+    if (c > 0) stage.commit(buffers[(c - 1) & 1], w.wave, lane);
+    __syncthreads();
+  }
+  if (a.dh0) store_state<float, KT>(dS, a.dh0 + state, a, w, lds);
 }
 
 // dq and dk of one block of 64 tokens and key head, summed over the value heads that share
@@ -197,7 +213,8 @@ __global__ __launch_bounds__(256) void k_delta_grads(Args a) {
   const int valid = static_cast<int>(min<int64_t>(kMark, seq.len - t0));
   const int64_t slot = first_slot(a, n, seq, kC) + 2 * b;  // of the first 32 tokens
   const int64_t line = int64_t(a.H) * a.DV;
-  const int64_t frag = exact_planes<T>() * kPlane;
+  constexpr int64_t frag = exact_planes<T>() * kPlane;
+  constexpr int64_t operand = KeyRecord<T, KT>::kOperand * kPlane;
   const bool live = 32 * mine < valid;
 
   f32x16 total[KT];
@@ -326,7 +343,8 @@ __global__ __launch_bounds__(256) void k_delta_grads(Args a) {
           l1[r] = o < row ? -f * l1[r] : (o > row ? -f * l2[r] : 0.0f);
         }
       }
-      const int64_t keyed = ((slot + other) * a.HK + hk) * t_bytes<T>(KT);
+      const char* record = a.keys + ((slot + other) * a.HK + hk) *
+                                        (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Wide<T, 2> pw, lw;
@@ -334,16 +352,16 @@ __global__ __launch_bounds__(256) void k_delta_grads(Args a) {
         if (keys) set_wide(lw, part(l1, s));
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-          const int64_t f = keyed + (2 * kt + s) * frag;
+          const char* f = record + operand + (2 * kt + s) * frag;
           Exact<T> kx;
-          get(kx, a.ktf + f, lane);
+          get(kx, f, lane);
           if (!keys) {
             total[kt] = mma(pw, kx, total[kt]);
           } else {
             total[kt] = mma(lw, kx, total[kt]);
             if (causal) {
               Exact<T> qx;
-              get(qx, a.qtf + f, lane);
+              get(qx, f + operand, lane);
               total[kt] = mma(pw, qx, total[kt]);
             }
           }
@@ -397,11 +415,18 @@ __global__ __launch_bounds__(256) void k_delta_gate_grads(Args a) {
   a.dg[at] = a.g[at] < kMinLog ? 0.0f : static_cast<float>(dg + dot);
 }
 
-template <typename T, int KT, bool kAligned>
-int adjoint_kt(const Args& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.S * a.H * ((a.DV + 31) / 32))), block(64);
-  hipLaunchKernelGGL((k_delta_adjoint<T, KT, kAligned>), grid, block, 0, st, a);
+template <typename T, int KT, int kW>
+int adjoint_w(const Args& a, hipStream_t st) {
+  const int64_t blocks = a.S * a.H * (((a.DV + 31) / 32 + kW - 1) / kW);
+  hipLaunchKernelGGL((k_delta_adjoint<T, KT, kW>), dim3(static_cast<unsigned>(blocks)), dim3(64 * kW),
+                     0, st, a);
   return static_cast<int>(hipGetLastError());
+}
+template <typename T, int KT>
+int adjoint_kt(const Args& a, hipStream_t st) {
+  if (a.DV <= 32) return adjoint_w<T, KT, 1>(a, st);
+  if (a.DV <= 64) return adjoint_w<T, KT, 2>(a, st);
+  return adjoint_w<T, KT, 4>(a, st);
 }
 template <typename T, int KT, bool kAligned>
 int grads_kt(const Args& a, hipStream_t st) {
@@ -410,11 +435,11 @@ int grads_kt(const Args& a, hipStream_t st) {
   return static_cast<int>(hipGetLastError());
 }
 
-template <typename T, bool kAligned>
+template <typename T>
 int adjoint_t(const Args& a, hipStream_t st) {
-  if (a.DK <= 32) return adjoint_kt<T, 1, kAligned>(a, st);
-  if (a.DK <= 64) return adjoint_kt<T, 2, kAligned>(a, st);
-  return adjoint_kt<T, 4, kAligned>(a, st);
+  if (a.DK <= 32) return adjoint_kt<T, 1>(a, st);
+  if (a.DK <= 64) return adjoint_kt<T, 2>(a, st);
+  return adjoint_kt<T, 4>(a, st);
 }
 template <typename T, bool kAligned>
 int grads_t(const Args& a, hipStream_t st) {
@@ -425,9 +450,8 @@ int grads_t(const Args& a, hipStream_t st) {
 
 }  // namespace
 
-int launch_adjoint(const Args& a, int dtype, bool aligned, hipStream_t st) {
-  if (dtype == 0) return aligned ? adjoint_t<float, true>(a, st) : adjoint_t<float, false>(a, st);
-  return aligned ? adjoint_t<uint16_t, true>(a, st) : adjoint_t<uint16_t, false>(a, st);
+int launch_adjoint(const Args& a, int dtype, hipStream_t st) {
+  return dtype == 0 ? adjoint_t<float>(a, st) : adjoint_t<uint16_t>(a, st);
 }
 int launch_grads(const Args& a, int dtype, bool aligned, hipStream_t st) {
   if (dtype == 0) return aligned ? grads_t<float, true>(a, st) : grads_t<float, false>(a, st);

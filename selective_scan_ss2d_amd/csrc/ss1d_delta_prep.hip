@@ -65,6 +65,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
   const T* qrow = static_cast<const T*>(a.q) + token_at(a, a.sq, n, seq, tok) + hk * a.sq.h;
   f32x16 kk = {}, qk = {};
   const bool keyed = hv % a.rep == 0;
+  constexpr int64_t frag = exact_planes<T>() * kPlane;
+  constexpr int64_t operand = KeyRecord<T, KT>::kOperand * kPlane;
+  char* const head = a.heads + (slot * a.H + hv) *
+                                   (int64_t(head_planes(sizeof(T) == 4, a.p_planes)) * kPlane);
+  char* const pf = head + HeadRecord<T, 3>::kN * kPlane;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     Exact<T> kx[2], qx[2];
@@ -77,17 +82,18 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
       qk = kBackward ? mma(qx[s], kx[s], qk) : mma(kx[s], qx[s], qk);
     }
     if (keyed) {
+      char* at = a.keys + (slot * a.HK + hk) * (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane) +
+                 2 * kt * frag;
       Exact<T> y[2];
-      const int64_t per = int64_t(exact_planes<T>()) * kPlane;
-      const int64_t at = (slot * a.HK + hk) * t_bytes<T>(KT) + 2 * kt * per;
       transpose_tile<T>(sh, kx, y, own, half);
-      put(a.ktf + at, lane, y[0]);
-      put(a.ktf + at + per, lane, y[1]);
-      if (kBackward) {
-        transpose_tile<T>(sh, qx, y, own, half);
-        put(a.qtf + at, lane, y[0]);
-        put(a.qtf + at + per, lane, y[1]);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        put(at + s * frag, lane, kx[s]);
+        put(at + operand + s * frag, lane, y[s]);
       }
+      if (kBackward) transpose_tile<T>(sh, qx, y, own, half);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) put(at + 2 * operand + s * frag, lane, kBackward ? y[s] : qx[s]);
     }
   }
 
@@ -109,7 +115,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
   if (half == 0) {
     sh.G[col] = G;
     sh.beta[col] = bv;
-    float* gt = a.gates + (slot * a.H + hv) * (3 * kC);
+    float* gt = reinterpret_cast<float*>(
+        head + (head_planes(sizeof(T) == 4, a.p_planes) - 1) * int64_t(kPlane));
     gt[col] = expf(static_cast<float>(G));
     gt[kC + col] = expf(static_cast<float>(Gend - G));
     gt[2 * kC + col] = bv;
@@ -153,8 +160,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
 #pragma unroll
       for (int k = kC - 1; k > j; --k) x[j] = fmaf(-sh.m[j * kC + k], x[k], x[j]);
   }
-  char* nf = a.nf + (slot * a.H + hv) * n_bytes<T>();
-  char* pf = a.pf + (slot * a.H + hv) * p_bytes<T>(a.p_planes);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     f32x8 v;
@@ -162,7 +167,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
     for (int e = 0; e < 8; ++e) v[e] = half == 0 ? x[16 * s + e] : x[16 * s + 8 + e];
     Wide<T, 3> w;
     set_wide(w, v);
-    put(nf + s * wide_planes<T, 3>() * kPlane, lane, w);
+    put(head + s * wide_planes<T, 3>() * kPlane, lane, w);
     if (a.p_planes == 3) {
       set_wide(w, part(p, s));
       put(pf + s * wide_planes<T, 3>() * kPlane, lane, w);
