@@ -141,16 +141,42 @@ template <typename T, int P> struct Wide;
 template <int P> struct Wide<uint16_t, P> { bf16x8 p[P]; };
 template <int P> struct Wide<float, P> { f32x8 v; };
 
+// Two values rounded to nearest bfloat16 and packed.  Written out because the compiler
+// otherwise converts each value once more, alone, to get at the rounded value.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(r) : "v"(lo), "v"(hi));
+  return r;
+}
 template <int P>
 __device__ __forceinline__ void set_wide(Wide<uint16_t, P>& w, f32x8 x) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    w.p[i] = __builtin_convertvector(x, bf16x8);
-    if (i + 1 < P) x -= __builtin_convertvector(w.p[i], f32x8);
+    u32x4 u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t both = pack_bf16(x[2 * j], x[2 * j + 1]);
+      u[j] = both;
+      if (i + 1 < P) {
+        x[2 * j] -= __uint_as_float(both << 16);
+        x[2 * j + 1] -= __uint_as_float(both & 0xffff0000u);
+      }
+    }
+    w.p[i] = __builtin_bit_cast(bf16x8, u);
   }
 }
 template <int P>
 __device__ __forceinline__ void set_wide(Wide<float, P>& w, f32x8 x) { w.v = x; }
+
+template <int P>
+__device__ __forceinline__ Wide<uint16_t, P> first_terms(const Wide<uint16_t, 3>& w) {
+  Wide<uint16_t, P> x;
+#pragma unroll
+  for (int i = 0; i < P; ++i) x.p[i] = w.p[i];
+  return x;
+}
+template <int P>
+__device__ __forceinline__ Wide<float, P> first_terms(const Wide<float, 3>& w) { return {w.v}; }
 
 __device__ __forceinline__ f32x8 part(const f32x16& x, int s) {
   f32x8 y;
@@ -268,6 +294,7 @@ __device__ __forceinline__ f32x16 load_gate(const float* gate, int half) {
 
 // Fragments in scratch: 16 bytes a lane, one plane of 1 KB after another.
 constexpr int kPlane = 1024;
+constexpr int kReadPast = 4 * kPlane;  // what Stage reads behind the last record at most
 template <typename T> constexpr int exact_planes() { return sizeof(T) == 4 ? 2 : 1; }
 template <typename T, int P> constexpr int wide_planes() { return sizeof(T) == 4 ? 2 : P; }
 
@@ -337,32 +364,47 @@ __host__ __device__ constexpr int head_planes(bool f32, int p) {
 
 // Brings the records of one chunk after another into LDS, two buffers in turn: fetch() starts
 // the next chunk's loads into registers, which the chunk's products overlap, commit() writes
-// them to the other buffer.  The block's kW waves share the planes.
+// them to the other buffer.  The block's kW waves share the planes; where those do not divide
+// evenly the last ones are read (from the scratch behind the record) and not written.
 template <typename T, int KT, int P, int kW> struct Stage {
   using Key = KeyRecord<T, KT>;
   using Head = HeadRecord<T, P>;
   static constexpr int kPlanes = Key::kPlanes + Head::kPlanes;
-  static constexpr int kEach = (kPlanes + kW - 1) / kW;
-  u32x4 x[kEach];
-  __device__ __forceinline__ void fetch(const Args& a, int64_t slot, int hv, int hk, int wave,
-                                        int lane) {
-    const char* key = a.keys + (slot * a.HK + hk) * (int64_t(Key::kPlanes) * kPlane);
-    const char* head = a.heads + (slot * a.H + hv) * (int64_t(Head::kPlanes) * kPlane);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int p = wave + kW * i;
-      if (p < kPlanes) {
-        const char* from = p < Key::kPlanes ? key + p * kPlane : head + (p - Key::kPlanes) * kPlane;
-        x[i] = *(Global<const u32x4>)(global(from) + 16 * lane);
-      }
-    }
+  static constexpr int kKeys = (Key::kPlanes + kW - 1) / kW, kHeads = (Head::kPlanes + kW - 1) / kW;
+  u32x4 x[kKeys + kHeads];
+  Global<const char> key, head;       // this wave's first plane of the next chunk's records
+  int64_t key_step, head_step;        // to the next chunk's (backward: the one before)
+  int wave, lane;
+  __device__ __forceinline__ void start(const Args& a, int64_t slot, int hv, int hk, int w, int l,
+                                        int direction) {
+    wave = w;
+    lane = l;
+    const int64_t kb = int64_t(Key::kPlanes) * kPlane, hb = int64_t(Head::kPlanes) * kPlane;
+    key = global(static_cast<const char*>(a.keys)) + (slot * a.HK + hk) * kb + w * kPlane;
+    head = global(static_cast<const char*>(a.heads)) + (slot * a.H + hv) * hb + w * kPlane;
+    key_step = direction * a.HK * kb;
+    head_step = direction * a.H * hb;
   }
-  __device__ __forceinline__ void commit(char* buffer, int wave, int lane) const {
+  __device__ __forceinline__ void fetch() {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int p = wave + kW * i;
-      if (p < kPlanes) reinterpret_cast<u32x4*>(buffer + p * kPlane)[lane] = x[i];
-    }
+    for (int i = 0; i < kKeys; ++i) x[i] = *(Global<const u32x4>)(key + i * kW * kPlane + 16u * lane);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      x[kKeys + i] = *(Global<const u32x4>)(head + i * kW * kPlane + 16u * lane);
+    key += key_step;
+    head += head_step;
+  }
+  __device__ __forceinline__ void commit(char* buffer) const {
+    char* to = buffer + wave * kPlane + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if ((i + 1) * kW <= Key::kPlanes || wave + i * kW < Key::kPlanes)
+        *reinterpret_cast<u32x4*>(to + i * kW * kPlane) = x[i];
+    to += Key::kPlanes * kPlane;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      if ((i + 1) * kW <= Head::kPlanes || wave + i * kW < Head::kPlanes)
+        *reinterpret_cast<u32x4*>(to + i * kW * kPlane) = x[kKeys + i];
   }
   // operand `which` (0 K, 1 K^T, 2 Q or Q^T), tile kt, step s
   static __device__ __forceinline__ const char* operand(const char* buffer, int which, int kt, int s) {
@@ -397,47 +439,45 @@ constexpr int kTileBytes = 32 * 144;
 
 // Whole tiles of aligned rows go through registers, loaded ahead; others (a sequence's last
 // chunk, odd widths) element by element when they are wanted.
+__device__ __forceinline__ bool aligned16(const void* base, uint32_t stride, int cols) {
+  return ((reinterpret_cast<uintptr_t>(base) | stride) & 15) == 0 && cols >= 32;
+}
+
 template <typename T> struct Tile {
   static constexpr int kPieces = sizeof(T);              // 16-byte pieces per lane: 2 or 4
   static constexpr int kAcross = 2 * sizeof(T);          // pieces across a row
   static constexpr int kStep = 64 / kAcross;             // rows per access of the wave
   u32x4 x[kPieces];
-  const void* base;
-  uint32_t stride;
-  int rows, cols;
 
-  __device__ __forceinline__ static bool whole(const void* base, uint32_t stride, int rows, int cols) {
-    return ((reinterpret_cast<uintptr_t>(base) | stride) & 15) == 0 && rows >= 32 && cols >= 32;
-  }
-  // `rows` rows (others are 0) and `cols` columns (others repeat the last) of the tile whose
-  // first element is at `b`, rows `st` bytes apart (all uniform).
-  __device__ __forceinline__ void fetch(const void* b, uint32_t st, int lane, int r, int c) {
-    base = b;
-    stride = st;
-    rows = r;
-    cols = c;
-    if (!whole(b, st, r, c)) return;
-    const auto p = global(static_cast<const char*>(b));
-    const uint32_t off = lane / kAcross * st + lane % kAcross * 16;
+  // Starts the loads of a whole tile, its rows `stride` bytes apart (base and stride uniform).
+  __device__ __forceinline__ void fetch(const void* base, uint32_t stride, int lane) {
+    const auto p = global(static_cast<const char*>(base));
+    const uint32_t off = lane / kAcross * stride + lane % kAcross * 16;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
-      x[i] = *(Global<const u32x4>)(p + uint64_t(i * kStep) * st + off);
+      x[i] = *(Global<const u32x4>)(p + (uint64_t(i * kStep) * stride + off));
   }
-  // The tile in the product's layout, by way of `lds`.
-  __device__ __forceinline__ f32x16 columns(char* lds, int lane) const {
-    wave_sync();
-    if (whole(base, stride, rows, cols)) {
+  __device__ __forceinline__ void put(char* lds, int lane) const {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        *reinterpret_cast<u32x4*>(lds + (lane / kAcross + i * kStep) * tile_pitch<T>() +
-                                  lane % kAcross * 16) = x[i];
+    for (int i = 0; i < kPieces; ++i)
+      *reinterpret_cast<u32x4*>(lds + (lane / kAcross + i * kStep) * tile_pitch<T>() +
+                                lane % kAcross * 16) = x[i];
+  }
+  // The tile in the product's layout by way of `lds`: what fetch() brought where `whole`, else
+  // `rows` rows (others are 0) and `cols` columns (others repeat the last) from `base`.
+  __device__ __forceinline__ f32x16 columns(bool whole, const void* base, uint32_t stride, int rows,
+                                            int cols, char* lds, int lane) const {
+    wave_sync();
+    if (whole) {
+      put(lds, lane);
     } else {
       const auto p = global(static_cast<const char*>(base));
       const uint32_t c = lane & 31;
 #pragma nounroll
       for (int i = lane >> 5; i < 32; i += 2) {
         T v = T(0);
-        if (i < rows) v = *(Global<const T>)(p + (uint64_t(i) * stride + min(int(c), cols - 1) * sizeof(T)));
+        if (i < rows)
+          v = *(Global<const T>)(p + (uint64_t(i) * stride + min(int(c), cols - 1) * sizeof(T)));
         *reinterpret_cast<T*>(lds + i * tile_pitch<T>() + c * sizeof(T)) = v;
       }
     }
@@ -451,10 +491,11 @@ template <typename T> struct Tile {
   }
 };
 
-// Stores `rows` rows and `cols` columns (0: none) of a tile in the product's layout.
+// Stores a tile in the product's layout: all of it where `whole`, else `rows` rows and `cols`
+// columns (0: none).
 template <typename T>
-__device__ __forceinline__ void store_tile(const f32x16& v, void* base, uint32_t stride, char* lds,
-                                           int lane, int rows, int cols) {
+__device__ __forceinline__ void store_tile(const f32x16& v, void* base, uint32_t stride, bool whole,
+                                           int rows, int cols, char* lds, int lane) {
   using X = Tile<T>;
   wave_sync();
   char* to = lds + 8 * (lane >> 5) * tile_pitch<T>() + (lane & 31) * sizeof(T);
@@ -463,12 +504,13 @@ __device__ __forceinline__ void store_tile(const f32x16& v, void* base, uint32_t
     *reinterpret_cast<T*>(to + row_base(r) * tile_pitch<T>()) = Elem<T>::from_f32(v[r]);
   wave_sync();
   const auto p = global(static_cast<char*>(base));
-  if (X::whole(base, stride, rows, cols)) {
+  if (whole) {
     const uint32_t off = lane / X::kAcross * stride + lane % X::kAcross * 16;
 #pragma unroll
     for (int i = 0; i < X::kPieces; ++i)
-      *(Global<u32x4>)(p + uint64_t(i * X::kStep) * stride + off) = *reinterpret_cast<const u32x4*>(
-          lds + (lane / X::kAcross + i * X::kStep) * tile_pitch<T>() + lane % X::kAcross * 16);
+      *(Global<u32x4>)(p + (uint64_t(i * X::kStep) * stride + off)) =
+          *reinterpret_cast<const u32x4*>(lds + (lane / X::kAcross + i * X::kStep) * tile_pitch<T>() +
+                                          lane % X::kAcross * 16);
   } else {
     const int c = lane & 31, end = min(rows, 32);
     if (c < cols)
@@ -515,24 +557,40 @@ __device__ __forceinline__ void load_state(f32x16* S, const float* base, const A
   for (int kt = 0; kt < KT; ++kt) {
     S[kt] = f32x16{};
     const int rows = a.DK - 32 * kt;
-    if (base != nullptr && rows > 0) {
-      Tile<float> x;
-      x.fetch(base + int64_t(32) * kt * a.DV, stride, w.lane, rows, w.cols);
-      S[kt] = x.columns(lds, w.lane);
-    }
+    if (base == nullptr || rows <= 0) continue;
+    const float* at = base + int64_t(32) * kt * a.DV;
+    Tile<float> x;
+    const bool whole = aligned16(at, stride, w.cols) && rows >= 32;
+    if (whole) x.fetch(at, stride, w.lane);
+    S[kt] = x.columns(whole, at, stride, rows, w.cols, lds, w.lane);
   }
 }
 template <typename T, int KT>
-__device__ __forceinline__ void store_state(const f32x16* S, void* base, const Args& a, const Place& w,
-                                            char* lds) {
+__device__ __forceinline__ void store_state(const f32x16* S, void* base, float factor, const Args& a,
+                                            const Place& w, char* lds) {
   const uint32_t stride = a.DV * sizeof(T);
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     const int rows = a.DK - 32 * kt;
-    if (rows > 0)
-      store_tile<T>(S[kt], static_cast<char*>(base) + int64_t(32) * kt * stride, stride, lds, w.lane,
-                    rows, w.store_cols);
+    if (rows <= 0) continue;
+    void* at = static_cast<char*>(base) + int64_t(32) * kt * stride;
+    store_tile<T>(S[kt] * factor, at, stride, aligned16(at, stride, w.store_cols) && rows >= 32, rows,
+                  w.store_cols, lds, w.lane);
   }
+}
+
+// A state under decay is held as S = factor * X with a common factor, so that a chunk's decay
+// costs one multiplication instead of one per value; what is added to S is divided by the
+// factor.  Before the factor falls under 2^-16 (growing decays: exceeds 1) it goes into X.
+template <int KT>
+__device__ __forceinline__ float decay_state(f32x16* X, float factor, float decay) {
+  factor *= decay;
+  if (!(factor >= 0x1p-16f && factor <= 1.0f)) {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) X[kt] *= factor;
+    factor = 1.0f;
+  }
+  return factor;
 }
 
 // Log decays below this are 0 in fp32 either way; the bound keeps -inf out of differences.

@@ -115,7 +115,7 @@ Scratch scratch_layout(const Args& a, int dtype) {
   Scratch s{};
   s.keys = 0;
   s.heads = size_t(a.slots) * a.HK * key_planes(f32, kt) * kPlane;
-  s.bytes = s.heads + size_t(a.slots) * a.H * head_planes(f32, a.p_planes) * kPlane;
+  s.bytes = s.heads + size_t(a.slots) * a.H * head_planes(f32, a.p_planes) * kPlane + kReadPast;
   return s;
 }
 

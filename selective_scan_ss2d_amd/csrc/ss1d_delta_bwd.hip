@@ -56,45 +56,52 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
 
   f32x16 dS[KT];
   load_state<KT>(dS, a.dht ? a.dht + state : nullptr, a, w, lds);
+  float factor = 1.0f;
   const int64_t chunks = (seq.len + kC - 1) / kC;
+  const int64_t first = seq.row * line + w.hv * a.DV + 32 * w.tile;
+  const T* v0 = static_cast<const T*>(a.v) + token_at(a, a.sv, w.n, seq, 0) + w.hv * a.sv.h + 32 * w.tile;
+  const T* d0 = static_cast<const T*>(a.dout) + first;
+  T* out0 = static_cast<T*>(a.dv) + first;
+  const bool valign = aligned16(v0, vline, w.cols), dalign = aligned16(d0, line * sizeof(T), w.cols);
+  const bool oalign = aligned16(out0, line * sizeof(T), w.store_cols);
+  const bool salign = aligned16(nullptr, line * 4, w.cols);
+  const bool malign = aligned16(nullptr, a.DV * 4, w.cols) && a.DK % 32 == 0;
   St stage;
   Tile<T> vx, dx;
-  Tile<float> tx, ox;
-  auto row_of_chunk = [&](int64_t c) {
-    return (seq.row + c * kC) * line + w.hv * a.DV + 32 * w.tile;
-  };
-  auto fetch = [&](int64_t c) {  // what a chunk wants early: loaded a chunk ahead
-    stage.fetch(a, slot0 + c, w.hv, w.hk, w.wave, lane);
-    dx.fetch(static_cast<const T*>(a.dout) + row_of_chunk(c), line * sizeof(T), lane,
-             static_cast<int>(min<int64_t>(kC, seq.len - c * kC)), w.cols);
-  };
+  Tile<float> tx, ox, after[KT];
   if (chunks > 0) {
-    fetch(chunks - 1);
-    stage.commit(buffers[(chunks - 1) & 1], w.wave, lane);
+    stage.start(a, slot0 + chunks - 1, w.hv, w.hk, w.wave, lane, -1);
+    stage.fetch();
+    if (dalign && seq.len % kC == 0) dx.fetch(d0 + (chunks - 1) * kC * line, line * sizeof(T), lane);
+    stage.commit(buffers[(chunks - 1) & 1]);
     __syncthreads();
   }
   for (int64_t c = chunks - 1; c >= 0; --c) {
-    const int64_t t0 = c * kC, row0 = seq.row + t0;
+    const int64_t t0 = c * kC, row0 = seq.row + t0, at = t0 * line;
     const int valid = static_cast<int>(min<int64_t>(kC, seq.len - t0));
+    const bool whole = valid == kC;
     const char* buf = buffers[c & 1];
-    const f32x16 dout = dx.columns(lds, lane);
-    if (c > 0) fetch(c - 1);
-    // what it wants at its end
-    const T* vat = static_cast<const T*>(a.v) + token_at(a, a.sv, w.n, seq, t0) + w.hv * a.sv.h;
-    vx.fetch(vat + 32 * w.tile, vline, lane, valid, w.cols);
-    tx.fetch(a.ts + row_of_chunk(c), line * 4, lane, valid, w.cols);
-    ox.fetch(a.os + row_of_chunk(c), line * 4, lane, valid, w.cols);
+    const f32x16 dout =
+        dx.columns(dalign && whole, d0 + at, line * sizeof(T), valid, w.cols, lds, lane);
+    if (c > 0) {  // what the next chunk wants early
+      stage.fetch();
+      if (dalign) dx.fetch(d0 + at - kC * int64_t(line), line * sizeof(T), lane);
+    }
+    // what this one wants at its end
+    if (valign && whole) vx.fetch(v0 + t0 * a.sv.l, vline, lane);
+    if (salign && whole) {
+      tx.fetch(a.ts + first + at, line * 4, lane);
+      ox.fetch(a.os + first + at, line * 4, lane);
+    }
     const bool ends = (c & 1) || c == chunks - 1;  // the end of a block of 64 tokens
     const int64_t mark = mark0 + (c >> 1);
-    Tile<float> after[KT];
-    if (ends) {
-      const float* from = c == chunks - 1
-                              ? a.ends + state
-                              : a.marks + ((mark + 1) * a.H + w.hv) * a.DK * a.DV + 32 * w.tile;
+    const float* from = c == chunks - 1
+                            ? a.ends + state
+                            : a.marks + ((mark + 1) * a.H + w.hv) * a.DK * a.DV + 32 * w.tile;
+    if (ends && malign) {
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
-        if (a.DK > 32 * kt)
-          after[kt].fetch(from + int64_t(32) * kt * a.DV, a.DV * 4u, lane, a.DK - 32 * kt, w.cols);
+        if (a.DK > 32 * kt) after[kt].fetch(from + int64_t(32) * kt * a.DV, a.DV * 4u, lane);
     }
     __builtin_amdgcn_sched_barrier(0);  // the loads above go out before the products
     f32x16 ks = {};
@@ -110,7 +117,7 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
       }
     const float* gate = St::gates(buf);
     const f32x16 gam = load_gate(gate, half), beta = load_gate(gate + 2 * kC, half);
-    f32x16 du = load_gate(gate + kC, half) * ks;
+    f32x16 du = load_gate(gate + kC, half) * factor * ks;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       Wide<T, 3> pw;
@@ -134,23 +141,25 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
     }
     const f32x16 y = du - nr, dv = beta * y;
     if (ends) {
-      store_state<T, KT>(
-          dS, static_cast<T*>(a.dmarks) + (mark * a.H + w.hv) * a.DK * a.DV + 32 * w.tile, a, w, lds);
+      store_state<T, KT>(dS, static_cast<T*>(a.dmarks) + (mark * a.H + w.hv) * a.DK * a.DV + 32 * w.tile,
+                         factor, a, w, lds);
       float dot = 0.0f;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
         if (a.DK > 32 * kt) {
-          const f32x16 S = after[kt].columns(lds, lane);
+          const f32x16 S = after[kt].columns(malign, from + int64_t(32) * kt * a.DV, a.DV * 4u,
+                                             a.DK - 32 * kt, w.cols, lds, lane);
 #pragma unroll
           for (int r = 0; r < 16; ++r) dot = fmaf(dS[kt][r], S[r], dot);
         }
-      dot = w.in ? dot : 0.0f;
+      dot = w.in ? dot * factor : 0.0f;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
       if (lane == 0 && w.store_cols > 0) a.pdots[(mark * a.H + w.hv) * tiles + w.tile] = dot;
     }
-    const f32x16 gdo = (a.scale * gam) * dout, gdv = -(gam * dv);
-    const float whole = gate[kC - 1];
+    factor = decay_state<KT>(dS, factor, gate[kC - 1]);
+    const f32x16 over = gam * (1.0f / factor);
+    const f32x16 gdo = a.scale * over * dout, gdv = -(over * dv);
     Wide<T, 3> ow[2], vw[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -159,7 +168,6 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
     }
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
-      dS[kt] *= whole;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Exact<T> qx, kx;
@@ -170,10 +178,10 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
       }
     }
     // dv, and what the gates' gradients take from these 32 columns
-    store_tile<T>(dv, static_cast<T*>(a.dv) + row_of_chunk(c), line * sizeof(T), lds, lane, valid,
-                  w.store_cols);
-    f32x16 sb = y * tx.columns(lds, lane);
-    f32x16 sg = dout * ox.columns(lds, lane) - dv * vx.columns(lds, lane);
+    store_tile<T>(dv, out0 + at, line * sizeof(T), oalign && whole, valid, w.store_cols, lds, lane);
+    f32x16 sb = y * tx.columns(salign && whole, a.ts + first + at, line * 4, valid, w.cols, lds, lane);
+    f32x16 sg = dout * ox.columns(salign && whole, a.os + first + at, line * 4, valid, w.cols, lds, lane) -
+                dv * vx.columns(valign && whole, v0 + t0 * a.sv.l, vline, valid, w.cols, lds, lane);
     if (w.store_cols < 32) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -188,10 +196,10 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
       a.pbeta[p] = beta_sum;
       a.pgate[p] = gate_sum;
     }
-    if (c > 0) stage.commit(buffers[(c - 1) & 1], w.wave, lane);
+    if (c > 0) stage.commit(buffers[(c - 1) & 1]);
     __syncthreads();
   }
-  if (a.dh0) store_state<float, KT>(dS, a.dh0 + state, a, w, lds);
+  if (a.dh0) store_state<float, KT>(dS, a.dh0 + state, factor, a, w, lds);
 }
 
 // dq and dk of one block of 64 tokens and key head, summed over the value heads that share

@@ -128,18 +128,18 @@ def test_strided_views_of_one_projection(dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 def test_continuing_from_a_state(dtype):
-    """Two halves, the second from the first's end state (in place), against the whole: the
-    split falls on a chunk's edge, so that the sums are the same."""
+    """Two parts, the second from the first's end state (in place): the whole's values, to the
+    rounding of where the sums and the states' factors are cut."""
     t = du.make_inputs(2, 160, 1, 2, 64, 64, dtype, seed=11, h0=2)
-    o, ht = run(t, final_state=True)
     d = du.to_gpu(t)
-    first = [d[n][:, :96].contiguous() for n in du.NAMES]
-    second = [d[n][:, 96:].contiguous() for n in du.NAMES]
-    state = d["h0"].clone()
-    oa, back = ss.ss1d_delta_forward(*first, initial_state=state, final_state=state)
-    assert back is state
-    ob, _ = ss.ss1d_delta_forward(*second, initial_state=state, final_state=state)
-    assert torch.equal(torch.cat([oa, ob], 1), o) and torch.equal(state, ht)
+    for cut in (1, 50, 96):
+        first = [d[n][:, :cut].contiguous() for n in du.NAMES]
+        second = [d[n][:, cut:].contiguous() for n in du.NAMES]
+        state = d["h0"].clone()
+        oa, back = ss.ss1d_delta_forward(*first, initial_state=state, final_state=state)
+        assert back is state
+        ob, _ = ss.ss1d_delta_forward(*second, initial_state=state, final_state=state)
+        check_forward(t, dtype, torch.cat([oa, ob], 1), state, 64 ** -0.5)
 
 
 def test_values_in_masked_places():
