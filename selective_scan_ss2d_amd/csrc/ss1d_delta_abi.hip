@@ -171,7 +171,7 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
   ins[5] = {cu, (S + 1) * 4};
   const int64_t tiles = (DV + 31) / 32;
   if ((a->slots * H / 4 + 1) * 256 > kMaxThreads || S * H * tiles * 64 > kMaxThreads ||
-      a->marks_n * HK * 256 > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
+      a->marks_n * HK * 384 > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
     return SS2D_ERR_SHAPE;
   return SS2D_OK;
 }

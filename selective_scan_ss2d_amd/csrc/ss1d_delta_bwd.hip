@@ -203,190 +203,302 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
 }
 
 // dq and dk of one block of 64 tokens and key head, summed over the value heads that share
-// it: four waves, one for each of (dq, dk) x (first, second 32 tokens).  For bfloat16 data
-// one operand of every product has 2 terms (or is exact), so each product carries at most
-// one operand rounding besides the output's own.
-template <typename T, int KT, bool kAligned>
-__global__ __launch_bounds__(256) void k_delta_grads(Args a) {
-  __shared__ double G[kMark];
-  const int lane = threadIdx.x & 63, half = lane >> 5, own = swap23(lane & 31);
-  const int wave = threadIdx.x >> 6, mine = wave & 1;  // this wave's 32 tokens
-  const bool keys = wave >> 1;
-  const int64_t mark = blockIdx.x / a.HK;
-  const int hk = static_cast<int>(blockIdx.x - mark * a.HK);
-  int64_t n, b;
-  Seq seq;
-  if (!find_slot(a, mark, kMark, &n, &b, &seq)) return;
-  const int64_t t0 = b * kMark, row0 = seq.row + t0;
-  const int valid = static_cast<int>(min<int64_t>(kMark, seq.len - t0));
-  const int64_t slot = first_slot(a, n, seq, kC) + 2 * b;  // of the first 32 tokens
-  const int64_t line = int64_t(a.H) * a.DV;
-  constexpr int64_t frag = exact_planes<T>() * kPlane;
+// it, by six waves: for the first and second 32 tokens each, one wave for dq, one for dk's
+// part from the states and one for dk's part from the block itself (added to the former at
+// the end).  The matrices whose columns (DV) are contracted pass through LDS 32 columns at a
+// time, split into bfloat16 terms once for all waves, the next 32 already on their way.  For
+// bfloat16 data one operand of every product has 2 terms (or is exact), so each product
+// carries at most one operand rounding besides the output's own.
+template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows by 16 columns
+  static constexpr int kU = 0;                                     // u = beta t: 64 rows, 2 terms
+  static constexpr int kDo = kU + 4 * wide_planes<T, 2>();         // do: 64 rows
+  static constexpr int kDv = kDo + 4 * exact_planes<T>();          // dv: 64 rows
+  static constexpr int kS = kDv + 4 * exact_planes<T>();           // S: DK rows, 2 terms
+  static constexpr int kDs = kS + 2 * KT * wide_planes<T, 2>();    // dS: DK rows
+  static constexpr int kPlanes = kDs + 2 * KT * exact_planes<T>();
+  static constexpr int kTasks = 12 + 4 * KT;                       // one per 32 x 16 part
+};
+
+constexpr int kGradWaves = 6;
+
+// A 16- or 32-byte piece of a row: 8 values from column c, 0 past the width or where !on.
+template <bool kAligned, typename T>
+__device__ __forceinline__ f32x8 piece(const T* row, int c, int width, bool on) {
+  f32x8 v;
+  const bool any = on && c < width;
+  const auto p = global(row) + (any ? c : 0);
+  if constexpr (kAligned) {
+    constexpr int kN = sizeof(T) / 2;
+    u32x4 u[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      u[i] = ((Global<const u32x4>)p)[i];
+      if (!any) u[i] = u32x4{0, 0, 0, 0};
+    }
+    T e[8];
+    __builtin_memcpy(e, u, sizeof(e));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool ok = on && c + i < width;
+      const T e = p[ok ? i : 0];
+      v[i] = ok ? Elem<T>::to_f32(e) : 0.0f;
+    }
+  }
+  return v;
+}
+
+__device__ __forceinline__ void put_exact(char* at, int lane, f32x8 v, uint16_t) {
+  Wide<uint16_t, 1> w;  // the values are bfloat16 ones: nothing is rounded
+  set_wide(w, v);
+  put(at, lane, w);
+}
+__device__ __forceinline__ void put_exact(char* at, int lane, f32x8 v, float) {
+  put_planes(at, lane, v);
+}
+
+// The block's place and the LDS that its waves share.
+struct GradBlock {
+  const Args& a;
+  char* panels;
+  float* sums;   // dk's part from the block: (2, 16 KT, 64)
+  double* G;     // prefix sums of the log decays
+  float* betas;
+  int lane, half, own, wave, mine, hk, valid;
+  int64_t mark, row0, slot;
+};
+
+// One wave's work; kKind: 0 dq, 1 dk's part from the states, 2 dk's part from the block.  The
+// three run the same sequence of barriers.
+template <typename T, int KT, bool kAligned, int kKind>
+__device__ __forceinline__ void grad_wave(const GradBlock& g) {
+  using Pn = Panels<T, KT>;
+  constexpr int kEach = (Pn::kTasks + kGradWaves - 1) / kGradWaves;
+  constexpr int kW2 = wide_planes<T, 2>() * kPlane, kEx = exact_planes<T>() * kPlane;
   constexpr int64_t operand = KeyRecord<T, KT>::kOperand * kPlane;
-  const bool live = 32 * mine < valid;
+  const Args& a = g.a;
+  const int lane = g.lane, half = g.half, own = g.own, mine = g.mine, valid = g.valid;
+  char* const panels = g.panels;
+  const int64_t line = int64_t(a.H) * a.DV;
 
   f32x16 total[KT];
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) total[kt] = f32x16{};
 
-  for (int hv = hk * a.rep; hv < (hk + 1) * a.rep; ++hv) {
+  for (int hv = g.hk * a.rep; hv < (g.hk + 1) * a.rep; ++hv) {
     __syncthreads();
-    if (wave == 0) {
-      double x = lane < valid ? fmaxf(a.g[(row0 + lane) * a.H + hv], kMinLog) : 0.0;
+    if (g.wave == 0) {
+      double x = 0.0;
+      float be = 0.0f;
+      if (lane < valid) {
+        x = fmaxf(a.g[(g.row0 + lane) * a.H + hv], kMinLog);
+        be = a.beta[(g.row0 + lane) * a.H + hv];
+      }
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const double up = __shfl_up(x, d);
         if (lane >= d) x += up;
       }
-      G[lane] = x;
+      g.G[lane] = x;
+      g.betas[lane] = be;
     }
     __syncthreads();
-    if (!live) continue;
-    const int64_t head_at = row0 * line + int64_t(hv) * a.DV;
-    const T* dout = static_cast<const T*>(a.dout) + head_at;
-    const T* dv = static_cast<const T*>(a.dv) + head_at;
-    const float* ts = a.ts + head_at;
-    const float* S = a.marks + (mark * a.H + hv) * a.DK * a.DV;
-    const T* dS = static_cast<const T*>(a.dmarks) + (mark * a.H + hv) * a.DK * a.DV;
-    const int row = 32 * mine + own;             // this lane's token as a row of its tile
-    const bool on = row < valid;
-    const int64_t at = int64_t(on ? row : 0) * line;
-    const float beta_own = on ? a.beta[(row0 + row) * a.H + hv] : 0.0f;
-    const double Gown = G[row], Gend = G[kMark - 1];
-
-    // the states' part: rows of this wave's tokens against the states' rows
-    f32x16 x[KT], y[KT];
+    const int64_t head_at = g.row0 * line + int64_t(hv) * a.DV;
+    const int64_t state_at = (g.mark * a.H + hv) * a.DK * a.DV;
+    // this wave's tasks of the next 32 columns
+    f32x8 x[kEach];
+    auto fetch = [&](int c0) {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) x[kt] = y[kt] = f32x16{};
-    for (int c = 0; c < a.DV; c += 16) {
-      const int c8 = c + 8 * half;
-      if (!keys) {
-        Exact<T> d;
-        load8<kAligned>(d, dout + at, c8, a.DV, on);
+      for (int i = 0; i < kEach; ++i) {
+        const int task = g.wave + kGradWaves * i;
+        const int c = c0 + 16 * (task & 1) + 8 * half;
+        if (task < 12) {  // rows of tokens
+          const int row = 32 * (task >> 1 & 1) + own;
+          const bool on = row < valid;
+          const int64_t at = head_at + int64_t(on ? row : 0) * line;
+          if (task < 4) x[i] = piece<kAligned>(a.ts + at, c, a.DV, on) * g.betas[row];
+          else if (task < 8) x[i] = piece<kAligned>(static_cast<const T*>(a.dout) + at, c, a.DV, on);
+          else x[i] = piece<kAligned>(static_cast<const T*>(a.dv) + at, c, a.DV, on);
+        } else if (task < Pn::kTasks) {  // rows of the states
+          const int k = 32 * ((task - 12) >> 1) % (32 * KT) + own;
+          const bool on = k < a.DK;
+          const int64_t at = state_at + int64_t(on ? k : 0) * a.DV;
+          if (task < 12 + 2 * KT) x[i] = piece<kAligned>(a.marks + at, c, a.DV, on);
+          else x[i] = piece<kAligned>(static_cast<const T*>(a.dmarks) + at, c, a.DV, on);
+        }
+      }
+    };
+    auto commit = [&]() {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          const int k = 32 * kt + own;
-          Exact<float> s;
-          load8<kAligned>(s, S + int64_t(k < a.DK ? k : 0) * a.DV, c8, a.DV, k < a.DK);
+      for (int i = 0; i < kEach; ++i) {
+        const int task = g.wave + kGradWaves * i;
+        if (task < 4 || (task >= 12 && task < 12 + 2 * KT)) {
+          const int plane = task < 4 ? Pn::kU + task * wide_planes<T, 2>()
+                                     : Pn::kS + (task - 12) * wide_planes<T, 2>();
           Wide<T, 2> w;
-          set_wide(w, s.v);
-          x[kt] = mma(d, w, x[kt]);
-        }
-      } else {
-        Exact<T> d;
-        load8<kAligned>(d, dv + at, c8, a.DV, on);
-        Exact<float> t;
-        load8<kAligned>(t, ts + at, c8, a.DV, on);
-        Wide<T, 2> u;
-        set_wide(u, t.v * beta_own);
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-          const int k = 32 * kt + own;
-          const int64_t r = int64_t(k < a.DK ? k : 0) * a.DV;
-          Exact<float> s;
-          load8<kAligned>(s, S + r, c8, a.DV, k < a.DK);
-          Wide<T, 2> w;
-          set_wide(w, s.v);
-          y[kt] = mma(d, w, y[kt]);
-          Exact<T> g;
-          load8<kAligned>(g, dS + r, c8, a.DV, k < a.DK);
-          x[kt] = mma(u, g, x[kt]);
+          set_wide(w, x[i]);
+          put(panels + plane * kPlane, lane, w);
+        } else if (task < Pn::kTasks) {
+          const int plane = task < 12 ? Pn::kDo + (task - 4) * exact_planes<T>()
+                                      : Pn::kDs + (task - 12 - 2 * KT) * exact_planes<T>();
+          put_exact(panels + plane * kPlane, lane, x[i], T(0));
         }
       }
-    }
+    };
+    // kind 0: x = do S^T, p[o] = u_o . do;  kind 1: x = u dS^T, y = dv S^T;
+    // kind 2: p[o] = do_o . u, l[o] = u_o . dv (earlier tokens o) or dv_o . u (later ones): o runs
+    // over the block's halves in registers' rows, the lanes hold this wave's tokens; own is l
+    // of the other sense within this wave's 32 tokens
+    constexpr int kY = kKind == 0 ? KT : (kKind == 1 ? 2 * KT : 1);
+    f32x16 y[kY], p[2], l[2], other_sense = {};
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const double g = G[32 * mine + acc_row(r, half)];
-      const float in = expf(static_cast<float>(g)), out = expf(static_cast<float>(Gend - g));
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-        total[kt][r] += keys ? out * x[kt][r] - in * y[kt][r] : a.scale * in * x[kt][r];
-    }
-    // the block's own part: 32 x 32 tiles with the other tokens in registers' rows and this
-    // wave's tokens in lanes, which are left operands as they stand
-    for (int other = 0; other < 2; ++other) {
-      if (32 * other >= valid) break;
-      const bool causal = keys ? other >= mine : other <= mine;
-      if (!keys && !causal) continue;
-      const int row2 = 32 * other + own;
-      const bool on2 = row2 < valid;
-      const int64_t at2 = int64_t(on2 ? row2 : 0) * line;
-      const float beta2 = on2 ? a.beta[(row0 + row2) * a.H + hv] : 0.0f;
-      f32x16 p = {}, l1 = {}, l2 = {};
-      for (int c = 0; c < a.DV; c += 16) {
-        const int c8 = c + 8 * half;
-        Exact<float> t, t2;
-        Wide<T, 2> u, u2;
-        load8<kAligned>(t, ts + at, c8, a.DV, on);
-        load8<kAligned>(t2, ts + at2, c8, a.DV, on2);
-        set_wide(u, t.v * beta_own);
-        set_wide(u2, t2.v * beta2);
-        Exact<T> d;
-        if (!keys) {  // u_j . do_i, tokens i in lanes
-          load8<kAligned>(d, dout + at, c8, a.DV, on);
-          p = mma(u2, d, p);
-        } else {
-          if (causal) {  // do_i . u_j, tokens j in lanes
-            load8<kAligned>(d, dout + at2, c8, a.DV, on2);
-            p = mma(d, u, p);
-          }
-          if (other <= mine) {  // u . dv of this wave's tokens: the later ones
-            load8<kAligned>(d, dv + at, c8, a.DV, on);
-            l1 = mma(u2, d, l1);
-          }
-          if (other >= mine) {
-            load8<kAligned>(d, dv + at2, c8, a.DV, on2);
-            l2 = mma(d, u, l2);
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int o = 32 * other + acc_row(r, half);
-        const float f = expf(static_cast<float>(o <= row ? Gown - G[o] : G[o] - Gown));
-        if (!keys) {
-          p[r] = o <= row ? a.scale * f * p[r] : 0.0f;
-        } else {
-          p[r] = o >= row ? a.scale * f * p[r] : 0.0f;
-          l1[r] = o < row ? -f * l1[r] : (o > row ? -f * l2[r] : 0.0f);
-        }
-      }
-      const char* record = a.keys + ((slot + other) * a.HK + hk) *
-                                        (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane);
+    for (int kt = 0; kt < kY; ++kt) y[kt] = f32x16{};
+    p[0] = p[1] = l[0] = l[1] = f32x16{};
+    fetch(0);
+    for (int c0 = 0; c0 < a.DV; c0 += 32) {
+      commit();
+      __syncthreads();
+      if (c0 + 32 < a.DV) fetch(c0 + 32);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        Wide<T, 2> pw, lw;
-        set_wide(pw, part(p, s));
-        if (keys) set_wide(lw, part(l1, s));
+        auto wide = [&](int first, int o) {
+          Wide<T, 2> w;
+          get(w, panels + first * kPlane + (2 * o + s) * kW2, lane);
+          return w;
+        };
+        auto exact = [&](int first, int o) {
+          Exact<T> w;
+          get(w, panels + first * kPlane + (2 * o + s) * kEx, lane);
+          return w;
+        };
+        if constexpr (kKind == 0) {
+          const Exact<T> d = exact(Pn::kDo, mine);
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) y[kt] = mma(d, wide(Pn::kS, kt), y[kt]);
+          p[0] = mma(wide(Pn::kU, 0), d, p[0]);
+          if (mine == 1) p[1] = mma(wide(Pn::kU, 1), d, p[1]);
+        } else if constexpr (kKind == 1) {
+          const Exact<T> d = exact(Pn::kDv, mine);
+          const Wide<T, 2> u = wide(Pn::kU, mine);
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            y[KT + kt] = mma(d, wide(Pn::kS, kt), y[KT + kt]);
+            y[kt] = mma(u, exact(Pn::kDs, kt), y[kt]);
+          }
+        } else {
+          const Wide<T, 2> u = wide(Pn::kU, mine);
+          const Exact<T> d = exact(Pn::kDv, mine);
+          if (mine == 0) p[0] = mma(exact(Pn::kDo, 0), u, p[0]);
+          p[1] = mma(exact(Pn::kDo, 1), u, p[1]);
+          l[0] = mma(mine == 0 ? u : wide(Pn::kU, 0), d, l[0]);
+          if (mine == 0) l[1] = mma(exact(Pn::kDv, 1), u, l[1]);
+          else l[1] = mma(u, d, l[1]);
+          other_sense = mma(d, u, other_sense);
+        }
+      }
+      __syncthreads();
+    }
+    if (32 * mine >= valid) continue;
+    const int row = 32 * mine + own;
+    const double Gown = g.G[row], Gend = g.G[kMark - 1];
+    if constexpr (kKind < 2) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const double at = g.G[32 * mine + acc_row(r, half)];
+        const float in = expf(static_cast<float>(at)), out = expf(static_cast<float>(Gend - at));
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-          const char* f = record + operand + (2 * kt + s) * frag;
-          Exact<T> kx;
-          get(kx, f, lane);
-          if (!keys) {
-            total[kt] = mma(pw, kx, total[kt]);
+          if constexpr (kKind == 0) total[kt][r] += a.scale * in * y[kt][r];
+          else total[kt][r] += out * y[kt][r] - in * y[KT + kt][r];
+        }
+      }
+    }
+    if constexpr (kKind != 1) {
+#pragma unroll
+      for (int other = 0; other < 2; ++other) {
+        if (32 * other >= valid) break;
+        if (kKind == 0 && other > mine) break;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int o = 32 * other + acc_row(r, half);
+          const double at = g.G[o];
+          const float f = expf(static_cast<float>(o <= row ? Gown - at : at - Gown));
+          if constexpr (kKind == 0) {
+            p[other][r] = o <= row ? a.scale * f * p[other][r] : 0.0f;
           } else {
-            total[kt] = mma(lw, kx, total[kt]);
-            if (causal) {
-              Exact<T> qx;
-              get(qx, f + operand, lane);
-              total[kt] = mma(pw, qx, total[kt]);
+            p[other][r] = o >= row ? a.scale * f * p[other][r] : 0.0f;
+            const float v = other == mine && o > row ? other_sense[r] : l[other][r];
+            l[other][r] = o == row ? 0.0f : -f * v;
+          }
+        }
+        const char* record = a.keys + ((g.slot + other) * a.HK + g.hk) *
+                                          (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane) + operand;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          Wide<T, 2> pw, lw;
+          set_wide(pw, part(p[other], s));
+          if constexpr (kKind == 2) set_wide(lw, part(l[other], s));
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            const char* f = record + (2 * kt + s) * kEx;
+            Exact<T> kx;
+            get(kx, f, lane);
+            if constexpr (kKind == 0) {
+              total[kt] = mma(pw, kx, total[kt]);
+            } else {
+              total[kt] = mma(lw, kx, total[kt]);
+              if (other >= mine) {
+                Exact<T> qx;
+                get(qx, f + operand, lane);
+                total[kt] = mma(pw, qx, total[kt]);
+              }
             }
           }
         }
       }
     }
   }
-  if (!live) return;
-  T* out = static_cast<T*>(keys ? a.dk : a.dq);
+  float* const sums = g.sums + mine * KT * 16 * 64 + lane;
+  if constexpr (kKind == 2)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sums[(16 * kt + r) * 64] = total[kt][r];
+  __syncthreads();
+  if (kKind == 2 || 32 * mine >= valid) return;
+  T* out = static_cast<T*>(kKind ? a.dk : a.dq);
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int i = 32 * mine + acc_row(r, half), k = 32 * kt + own;
+      const float v = kKind ? total[kt][r] + sums[(16 * kt + r) * 64] : total[kt][r];
       if (i < valid && k < a.DK)
-        out[((row0 + i) * a.HK + hk) * a.DK + k] = Elem<T>::from_f32(total[kt][r]);
+        out[((g.row0 + i) * a.HK + g.hk) * a.DK + k] = Elem<T>::from_f32(v);
     }
+}
+
+template <typename T, int KT, bool kAligned>
+__global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(Args a) {
+  __shared__ __align__(16) char panels[Panels<T, KT>::kPlanes * kPlane];
+  __shared__ float sums[2 * KT * 16 * 64];
+  __shared__ double G[kMark];
+  __shared__ float betas[kMark];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t mark = blockIdx.x / a.HK;
+  int64_t n, b;
+  Seq seq;
+  if (!find_slot(a, mark, kMark, &n, &b, &seq)) return;
+  const GradBlock g{a, panels, sums, G, betas, lane, lane >> 5, swap23(lane & 31), wave, wave & 1,
+                    static_cast<int>(blockIdx.x - mark * a.HK),
+                    static_cast<int>(min<int64_t>(kMark, seq.len - b * kMark)), mark,
+                    seq.row + b * kMark, first_slot(a, n, seq, kC) + 2 * b};
+  if (wave < 2) grad_wave<T, KT, kAligned, 0>(g);
+  else if (wave < 4) grad_wave<T, KT, kAligned, 1>(g);
+  else grad_wave<T, KT, kAligned, 2>(g);
 }
 
 // dbeta and dg of one block of 64 tokens and head: sums over the column tiles, then the sum
@@ -438,7 +550,7 @@ int adjoint_kt(const Args& a, hipStream_t st) {
 }
 template <typename T, int KT, bool kAligned>
 int grads_kt(const Args& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.marks_n * a.HK)), block(256);
+  const dim3 grid(static_cast<unsigned>(a.marks_n * a.HK)), block(64 * kGradWaves);
   hipLaunchKernelGGL((k_delta_grads<T, KT, kAligned>), grid, block, 0, st, a);
   return static_cast<int>(hipGetLastError());
 }
