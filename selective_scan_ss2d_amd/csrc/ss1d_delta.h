@@ -492,13 +492,13 @@ template <typename T> struct Tile {
 };
 
 // Stores a tile in the product's layout: all of it where `whole`, else `rows` rows and `cols`
-// columns (0: none).
+// columns (0: none).  column: that of this lane's values (lane % 32 by default).
 template <typename T>
 __device__ __forceinline__ void store_tile(const f32x16& v, void* base, uint32_t stride, bool whole,
-                                           int rows, int cols, char* lds, int lane) {
+                                           int rows, int cols, char* lds, int lane, int column = -1) {
   using X = Tile<T>;
   wave_sync();
-  char* to = lds + 8 * (lane >> 5) * tile_pitch<T>() + (lane & 31) * sizeof(T);
+  char* to = lds + 8 * (lane >> 5) * tile_pitch<T>() + (column < 0 ? lane & 31 : column) * sizeof(T);
 #pragma unroll
   for (int r = 0; r < 16; ++r)
     *reinterpret_cast<T*>(to + row_base(r) * tile_pitch<T>()) = Elem<T>::from_f32(v[r]);
@@ -594,7 +594,11 @@ __device__ __forceinline__ float decay_state(f32x16* X, float factor, float deca
 }
 
 // Log decays below this are 0 in fp32 either way; the bound keeps -inf out of differences.
+// Prefix sums are kept in 64 bits and in units of log 2: a difference of far sums then is
+// exact to fp32, and one v_exp_f32 (1 ulp) makes it a factor.
 constexpr float kMinLog = -1000.0f;
+constexpr double kLog2eWide = 1.4426950408889634074;
+__device__ __forceinline__ float decay_of(double diff) { return exp2_hw(static_cast<float>(diff)); }
 
 int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);
 int launch_scan(const Args& a, int dtype, bool save, hipStream_t st);

@@ -215,7 +215,9 @@ template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows 
   static constexpr int kDv = kDo + 4 * exact_planes<T>();          // dv: 64 rows
   static constexpr int kS = kDv + 4 * exact_planes<T>();           // S: DK rows, 2 terms
   static constexpr int kDs = kS + 2 * KT * wide_planes<T, 2>();    // dS: DK rows
-  static constexpr int kPlanes = kDs + 2 * KT * exact_planes<T>();
+  static constexpr int kKeys = kDs + 2 * KT * exact_planes<T>();   // K^T and Q^T of both halves
+  static constexpr int kKeyPlanes = 8 * KT * exact_planes<T>();
+  static constexpr int kPlanes = kKeys + kKeyPlanes;
   static constexpr int kTasks = 12 + 4 * KT;                       // one per 32 x 16 part
 };
 
@@ -263,9 +265,8 @@ __device__ __forceinline__ void put_exact(char* at, int lane, f32x8 v, float) {
 struct GradBlock {
   const Args& a;
   char* panels;
-  float* sums;   // dk's part from the block: (2, 16 KT, 64)
-  double* G;     // prefix sums of the log decays
-  float* betas;
+  char* spare;   // a tile of each wave, dk's part from the block in place of the panels
+  double* G;     // prefix sums of the log decays, of two heads in turn
   int lane, half, own, wave, mine, hk, valid;
   int64_t mark, row0, slot;
 };
@@ -287,28 +288,25 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) total[kt] = f32x16{};
 
-  for (int hv = g.hk * a.rep; hv < (g.hk + 1) * a.rep; ++hv) {
-    __syncthreads();
-    if (g.wave == 0) {
-      double x = 0.0;
-      float be = 0.0f;
-      if (lane < valid) {
-        x = fmaxf(a.g[(g.row0 + lane) * a.H + hv], kMinLog);
-        be = a.beta[(g.row0 + lane) * a.H + hv];
-      }
+  // K^T and Q^T of the block's two chunks, for all heads
+  u32x4 keys[(Pn::kKeyPlanes + kGradWaves - 1) / kGradWaves];
+  constexpr int kHalf = Pn::kKeyPlanes / 2;
 #pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const double up = __shfl_up(x, d);
-        if (lane >= d) x += up;
-      }
-      g.G[lane] = x;
-      g.betas[lane] = be;
+  for (int i = 0; i * kGradWaves < Pn::kKeyPlanes; ++i) {
+    const int p = g.wave + kGradWaves * i, o = p >= kHalf;
+    if (p < Pn::kKeyPlanes && 32 * o < valid) {
+      const char* record = a.keys + ((g.slot + o) * a.HK + g.hk) *
+                                        (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane) + operand;
+      keys[i] = *(Global<const u32x4>)(global(record) + (p - o * kHalf) * kPlane + 16u * lane);
     }
-    __syncthreads();
+  }
+  for (int hv = g.hk * a.rep; hv < (g.hk + 1) * a.rep; ++hv) {
+    double* const G = g.G + (hv & 1) * kMark;
     const int64_t head_at = g.row0 * line + int64_t(hv) * a.DV;
     const int64_t state_at = (g.mark * a.H + hv) * a.DK * a.DV;
     // this wave's tasks of the next 32 columns
     f32x8 x[kEach];
+    float bt[kEach] = {};
     auto fetch = [&](int c0) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -318,7 +316,10 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
           const int row = 32 * (task >> 1 & 1) + own;
           const bool on = row < valid;
           const int64_t at = head_at + int64_t(on ? row : 0) * line;
-          if (task < 4) x[i] = piece<kAligned>(a.ts + at, c, a.DV, on) * g.betas[row];
+          if (task < 4) {
+            x[i] = piece<kAligned>(a.ts + at, c, a.DV, on);
+            bt[i] = on ? a.beta[(g.row0 + row) * a.H + hv] : 0.0f;
+          }
           else if (task < 8) x[i] = piece<kAligned>(static_cast<const T*>(a.dout) + at, c, a.DV, on);
           else x[i] = piece<kAligned>(static_cast<const T*>(a.dv) + at, c, a.DV, on);
         } else if (task < Pn::kTasks) {  // rows of the states
@@ -338,7 +339,7 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
           const int plane = task < 4 ? Pn::kU + task * wide_planes<T, 2>()
                                      : Pn::kS + (task - 12) * wide_planes<T, 2>();
           Wide<T, 2> w;
-          set_wide(w, x[i]);
+          set_wide(w, task < 4 ? x[i] * bt[i] : x[i]);
           put(panels + plane * kPlane, lane, w);
         } else if (task < Pn::kTasks) {
           const int plane = task < 12 ? Pn::kDo + (task - 4) * exact_planes<T>()
@@ -357,7 +358,23 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
     for (int kt = 0; kt < kY; ++kt) y[kt] = f32x16{};
     p[0] = p[1] = l[0] = l[1] = f32x16{};
     fetch(0);
+    if (g.wave == 5) {  // read after the barriers below
+      double x = lane < valid ? fmaxf(a.g[(g.row0 + lane) * a.H + hv], kMinLog) * kLog2eWide : 0.0;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double up = __shfl_up(x, d);
+        if (lane >= d) x += up;
+      }
+      G[lane] = x;
+    }
     for (int c0 = 0; c0 < a.DV; c0 += 32) {
+      if (c0 == 0 && hv == g.hk * a.rep)
+#pragma unroll
+        for (int i = 0; i * kGradWaves < Pn::kKeyPlanes; ++i) {
+          const int p = g.wave + kGradWaves * i;
+          if (p < Pn::kKeyPlanes)
+            *reinterpret_cast<u32x4*>(panels + (Pn::kKeys + p) * kPlane + 16 * lane) = keys[i];
+        }
       commit();
       __syncthreads();
       if (c0 + 32 < a.DV) fetch(c0 + 32);
@@ -402,12 +419,12 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
     }
     if (32 * mine >= valid) continue;
     const int row = 32 * mine + own;
-    const double Gown = g.G[row], Gend = g.G[kMark - 1];
+    const double Gown = G[row], Gend = G[kMark - 1];
     if constexpr (kKind < 2) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const double at = g.G[32 * mine + acc_row(r, half)];
-        const float in = expf(static_cast<float>(at)), out = expf(static_cast<float>(Gend - at));
+        const double at = G[32 * mine + acc_row(r, half)];
+        const float in = decay_of(at), out = decay_of(Gend - at);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
           if constexpr (kKind == 0) total[kt][r] += a.scale * in * y[kt][r];
@@ -423,8 +440,8 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int o = 32 * other + acc_row(r, half);
-          const double at = g.G[o];
-          const float f = expf(static_cast<float>(o <= row ? Gown - at : at - Gown));
+          const double at = G[o];
+          const float f = decay_of(o <= row ? Gown - at : at - Gown);
           if constexpr (kKind == 0) {
             p[other][r] = o <= row ? a.scale * f * p[other][r] : 0.0f;
           } else {
@@ -433,8 +450,7 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
             l[other][r] = o == row ? 0.0f : -f * v;
           }
         }
-        const char* record = a.keys + ((g.slot + other) * a.HK + g.hk) *
-                                          (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane) + operand;
+        const char* record = panels + (Pn::kKeys + other * kHalf) * kPlane;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           Wide<T, 2> pw, lw;
@@ -460,7 +476,9 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       }
     }
   }
-  float* const sums = g.sums + mine * KT * 16 * 64 + lane;
+  // the last readers of the panels' first part are past the loop's barrier
+  float* const sums = reinterpret_cast<float*>(panels) + mine * KT * 16 * 64 + lane;
+  static_assert(2 * KT * 16 * 64 * 4 <= Pn::kKeys * kPlane, "the sums take the panels' place");
   if constexpr (kKind == 2)
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
@@ -468,31 +486,34 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       for (int r = 0; r < 16; ++r) sums[(16 * kt + r) * 64] = total[kt][r];
   __syncthreads();
   if (kKind == 2 || 32 * mine >= valid) return;
-  T* out = static_cast<T*>(kKind ? a.dk : a.dq);
+  T* out = static_cast<T*>(kKind ? a.dk : a.dq) +
+           ((g.row0 + 32 * mine) * a.HK + g.hk) * int64_t(a.DK);
+  const uint32_t stride = a.HK * a.DK * sizeof(T);
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt)
+  for (int kt = 0; kt < KT; ++kt) {
+    if constexpr (kKind == 1)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = 32 * mine + acc_row(r, half), k = 32 * kt + own;
-      const float v = kKind ? total[kt][r] + sums[(16 * kt + r) * 64] : total[kt][r];
-      if (i < valid && k < a.DK)
-        out[((g.row0 + i) * a.HK + g.hk) * a.DK + k] = Elem<T>::from_f32(v);
-    }
+      for (int r = 0; r < 16; ++r) total[kt][r] += sums[(16 * kt + r) * 64];
+    const int rows = valid - 32 * mine, cols = min(32, a.DK - 32 * kt);
+    if (cols > 0)
+      store_tile<T>(total[kt], out + 32 * kt, stride,
+                    aligned16(out + 32 * kt, stride, cols) && rows >= 32, rows, cols,
+                    g.spare + g.wave * kTileBytes, lane, own);
+  }
 }
 
 template <typename T, int KT, bool kAligned>
 __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(Args a) {
   __shared__ __align__(16) char panels[Panels<T, KT>::kPlanes * kPlane];
-  __shared__ float sums[2 * KT * 16 * 64];
-  __shared__ double G[kMark];
-  __shared__ float betas[kMark];
+  __shared__ __align__(16) char spare[4 * kTileBytes];
+  __shared__ double G[2 * kMark];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t mark = blockIdx.x / a.HK;
   int64_t n, b;
   Seq seq;
   if (!find_slot(a, mark, kMark, &n, &b, &seq)) return;
-  const GradBlock g{a, panels, sums, G, betas, lane, lane >> 5, swap23(lane & 31), wave, wave & 1,
+  const GradBlock g{a, panels, spare, G, lane, lane >> 5, swap23(lane & 31), wave, wave & 1,
                     static_cast<int>(blockIdx.x - mark * a.HK),
                     static_cast<int>(min<int64_t>(kMark, seq.len - b * kMark)), mark,
                     seq.row + b * kMark, first_slot(a, n, seq, kC) + 2 * b};

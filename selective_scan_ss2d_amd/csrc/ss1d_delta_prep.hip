@@ -97,15 +97,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
     }
   }
 
-  // gates: prefix sums of the log decays in 64 bits, so that differences of far sums keep
-  // fp32 accuracy
+  // gates
   const int64_t row = seq.row + t0 + (col < valid ? col : 0);
   float gv = 0.0f, bv = 0.0f;
   if (col < valid) {
     gv = fmaxf(a.g[row * a.H + hv], kMinLog);
     bv = a.beta[row * a.H + hv];
   }
-  double G = gv;
+  double G = gv * kLog2eWide;
 #pragma unroll
   for (int d = 1; d < kC; d *= 2) {
     const double up = __shfl_up(G, d, 32);
@@ -117,8 +116,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
     sh.beta[col] = bv;
     float* gt = reinterpret_cast<float*>(
         head + (head_planes(sizeof(T) == 4, a.p_planes) - 1) * int64_t(kPlane));
-    gt[col] = expf(static_cast<float>(G));
-    gt[kC + col] = expf(static_cast<float>(Gend - G));
+    gt[col] = decay_of(G);
+    gt[kC + col] = decay_of(Gend - G);
     gt[2 * kC + col] = bv;
   }
   wave_sync();
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
     const int other = acc_row(r, half);
     const double diff = kBackward ? sh.G[other] - Gown : Gown - sh.G[other];
     const bool below = kBackward ? other > own : other < own;
-    const float m = (below || other == own) ? expf(static_cast<float>(diff)) : 0.0f;
+    const float m = (below || other == own) ? decay_of(diff) : 0.0f;
     low[r] = below ? kk[r] * m : 0.0f;
     p[r] = (below || other == own) ? qk[r] * m * a.scale : 0.0f;
   }
