@@ -511,6 +511,12 @@ int ss1d_delta_backward(const void *q, const void *k, const void *v, const float
                         int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
                         const int64_t *strides, float scale, int dtype, void *stream);
 
+/* Testing and tuning, as ss2d_set_launch_plan: for later calls from this host thread, the
+ * chunks of 32 tokens per segment (even; 0: whole sequences, -1: automatic) that the forward
+ * and the backward cut sequences into.  A saved state belongs to the setting it was made
+ * with.  Returns SS2D_OK or SS2D_ERR_SHAPE. */
+int ss1d_delta_set_segment(int64_t chunks);
+
 int ss1d_delta_step(const void *q, const void *k, const void *v, const float *g,
                     const float *beta, float *state, const int32_t *slots, void *o, int64_t B,
                     int64_t T, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,

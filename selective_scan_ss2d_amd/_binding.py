@@ -72,6 +72,7 @@ SIGNATURES = {
                                                                    ctypes.c_int, _P]),
     "ss1d_delta_backward": (ctypes.c_int, [_P] * 16 + [_I64] * 7 + [_P, ctypes.c_float,
                                                                     ctypes.c_int, _P]),
+    "ss1d_delta_set_segment": (ctypes.c_int, [_I64]),
     "ss1d_delta_saved_bytes": (_I64, [_I64] * 6 + [ctypes.c_int]),
     "ss1d_delta_step": (ctypes.c_int, [_P] * 8 + [_I64] * 7 + [_P, ctypes.c_float, ctypes.c_int,
                                                                _P]),

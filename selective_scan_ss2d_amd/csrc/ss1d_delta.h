@@ -52,6 +52,11 @@ struct Args {
   char* heads;                 // (slot, H) records, see HeadRecord
   int64_t slots;               // chunk slots
   int p_planes;                // bf16 terms kept of P
+  // sequences cut into segments of `seglen` chunks (0: not cut), see span kernels; per
+  // (segment slot, head): the state after the segment from a zero one (DK, DV), what the
+  // segment makes of the state before it (DK, DK), and the state before it (DK, DV)
+  int64_t seglen, seg_slots;
+  float *span_z, *span_m, *starts;
   // kept by a training forward
   float *marks, *ends;         // states before every 64 tokens and after the last
   float *ts, *os;              // t and o in fp32, (T, H, DV)
@@ -107,6 +112,34 @@ __device__ __forceinline__ bool find_slot(const Args& a, int64_t slot, int unit,
   *s = sequence(a, lo);
   *index = slot - first_slot(a, lo, *s, unit);
   return *index >= 0 && *index * unit < s->len;
+}
+
+// Part of a sequence: all of it, or segment `index` of it (slots of seglen chunks; segment 0
+// exists for an empty sequence too).
+struct Segment {
+  int64_t n, index, slot;
+  Seq seq;
+  int64_t begin, end;  // chunks
+  bool last;
+};
+__device__ __forceinline__ bool find_segment(const Args& a, int64_t slot, Segment* g) {
+  if (a.seglen == 0) {
+    g->n = slot;
+    g->index = 0;
+    g->slot = slot;
+    g->seq = sequence(a, slot);
+    g->begin = 0;
+    g->end = (g->seq.len + kC - 1) / kC;
+    g->last = true;
+    return true;
+  }
+  const bool used = find_slot(a, slot, static_cast<int>(a.seglen * kC), &g->n, &g->index, &g->seq);
+  const int64_t chunks = (g->seq.len + kC - 1) / kC;
+  g->slot = slot;
+  g->begin = g->index * a.seglen;
+  g->end = min(chunks, g->begin + a.seglen);
+  g->last = g->end == chunks;
+  return used || (g->index == 0 && g->n < a.S);
 }
 
 // Element offset of token t of sequence n in a strided (B, L, H, .) tensor.
@@ -347,15 +380,15 @@ __device__ __forceinline__ void get(Wide<float, P>& x, const char* at, int lane)
 }
 
 // One chunk's operands in scratch, in the order in which the sequential kernels take them:
-// per key head K, K^T and Q (backward: Q^T), per value head N, P (backward: their transposes)
-// and a plane of gates (e^G, e^(G_32 - G), beta: 32 values each).
+// per key head K, K^T and Q (backward: Q^T), per value head N, a plane of gates (e^G,
+// e^(G_32 - G), beta: 32 values each) and P (backward: N^T and P^T).
 template <typename T, int KT> struct KeyRecord {
   static constexpr int kOperand = 2 * KT * exact_planes<T>();  // planes of one operand
   static constexpr int kPlanes = 3 * kOperand;
 };
 template <typename T, int P> struct HeadRecord {
   static constexpr int kN = 2 * wide_planes<T, 3>(), kP = 2 * wide_planes<T, P>();
-  static constexpr int kGates = kN + kP, kPlanes = kGates + 1;
+  static constexpr int kGates = kN, kPStart = kN + 1, kPlanes = kN + 1 + kP;
 };
 __host__ __device__ constexpr int key_planes(bool f32, int kt) { return 3 * 2 * kt * (f32 ? 2 : 1); }
 __host__ __device__ constexpr int head_planes(bool f32, int p) {
@@ -366,11 +399,14 @@ __host__ __device__ constexpr int head_planes(bool f32, int p) {
 // the next chunk's loads into registers, which the chunk's products overlap, commit() writes
 // them to the other buffer.  The block's kW waves share the planes; where those do not divide
 // evenly the last ones are read (from the scratch behind the record) and not written.
-template <typename T, int KT, int P, int kW> struct Stage {
+// kState: only what the state's own recurrence takes (K, K^T, N and the gates).
+template <typename T, int KT, int P, int kW, bool kState = false> struct Stage {
   using Key = KeyRecord<T, KT>;
   using Head = HeadRecord<T, P>;
-  static constexpr int kPlanes = Key::kPlanes + Head::kPlanes;
-  static constexpr int kKeys = (Key::kPlanes + kW - 1) / kW, kHeads = (Head::kPlanes + kW - 1) / kW;
+  static constexpr int kKeyRead = kState ? 2 * Key::kOperand : Key::kPlanes;
+  static constexpr int kHeadRead = kState ? Head::kN + 1 : Head::kPlanes;
+  static constexpr int kPlanes = kKeyRead + kHeadRead;
+  static constexpr int kKeys = (kKeyRead + kW - 1) / kW, kHeads = (kHeadRead + kW - 1) / kW;
   u32x4 x[kKeys + kHeads];
   Global<const char> key, head;       // this wave's first plane of the next chunk's records
   int64_t key_step, head_step;        // to the next chunk's (backward: the one before)
@@ -379,7 +415,8 @@ template <typename T, int KT, int P, int kW> struct Stage {
                                         int direction) {
     wave = w;
     lane = l;
-    const int64_t kb = int64_t(Key::kPlanes) * kPlane, hb = int64_t(Head::kPlanes) * kPlane;
+    const int64_t kb = int64_t(Key::kPlanes) * kPlane,
+                  hb = int64_t(head_planes(sizeof(T) == 4, a.p_planes)) * kPlane;
     key = global(static_cast<const char*>(a.keys)) + (slot * a.HK + hk) * kb + w * kPlane;
     head = global(static_cast<const char*>(a.heads)) + (slot * a.H + hv) * hb + w * kPlane;
     key_step = direction * a.HK * kb;
@@ -398,12 +435,12 @@ template <typename T, int KT, int P, int kW> struct Stage {
     char* to = buffer + wave * kPlane + 16 * lane;
 #pragma unroll
     for (int i = 0; i < kKeys; ++i)
-      if ((i + 1) * kW <= Key::kPlanes || wave + i * kW < Key::kPlanes)
+      if ((i + 1) * kW <= kKeyRead || wave + i * kW < kKeyRead)
         *reinterpret_cast<u32x4*>(to + i * kW * kPlane) = x[i];
-    to += Key::kPlanes * kPlane;
+    to += kKeyRead * kPlane;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
-      if ((i + 1) * kW <= Head::kPlanes || wave + i * kW < Head::kPlanes)
+      if ((i + 1) * kW <= kHeadRead || wave + i * kW < kHeadRead)
         *reinterpret_cast<u32x4*>(to + i * kW * kPlane) = x[kKeys + i];
   }
   // operand `which` (0 K, 1 K^T, 2 Q or Q^T), tile kt, step s
@@ -411,13 +448,13 @@ template <typename T, int KT, int P, int kW> struct Stage {
     return buffer + (which * Key::kOperand + (2 * kt + s) * exact_planes<T>()) * kPlane;
   }
   static __device__ __forceinline__ const char* n(const char* buffer, int s) {
-    return buffer + (Key::kPlanes + s * wide_planes<T, 3>()) * kPlane;
+    return buffer + (kKeyRead + s * wide_planes<T, 3>()) * kPlane;
   }
   static __device__ __forceinline__ const char* p(const char* buffer, int s) {
-    return buffer + (Key::kPlanes + Head::kN + s * wide_planes<T, P>()) * kPlane;
+    return buffer + (kKeyRead + Head::kPStart + s * wide_planes<T, P>()) * kPlane;
   }
   static __device__ __forceinline__ const float* gates(const char* buffer) {
-    return reinterpret_cast<const float*>(buffer + (Key::kPlanes + Head::kGates) * kPlane);
+    return reinterpret_cast<const float*>(buffer + (kKeyRead + Head::kGates) * kPlane);
   }
 };
 
@@ -526,26 +563,28 @@ __device__ __forceinline__ void store_tile(const f32x16& v, void* base, uint32_t
 struct Place {
   int lane, wave, half, tile, hv, hk;
   int cols, store_cols;  // columns of the tile; those that this wave stores (0: none)
-  int64_t n, head;
+  int64_t head;          // of the state's tensors: n * H + hv
   bool in;               // this lane's column is stored
+  Segment g;
 };
+// The block's unit is (segment, head, kW tiles); `width` columns make the tiles.
 template <int kW>
-__device__ __forceinline__ Place place(const Args& a, int64_t unit) {
-  Place p;
-  const int tiles = (a.DV + 31) / 32, per = (tiles + kW - 1) / kW;
-  p.lane = threadIdx.x & 63;
-  p.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  p.half = p.lane >> 5;
-  p.head = unit / per;
-  const int tile = static_cast<int>(unit - p.head * per) * kW + p.wave;
-  p.tile = min(tile, tiles - 1);
-  p.n = p.head / a.H;
-  p.hv = static_cast<int>(p.head - p.n * a.H);
-  p.hk = p.hv / a.rep;
-  p.cols = min(32, a.DV - 32 * p.tile);
-  p.store_cols = tile < tiles ? p.cols : 0;
-  p.in = (p.lane & 31) < p.store_cols;
-  return p;
+__device__ __forceinline__ bool place(Place* p, const Args& a, int64_t unit, int width) {
+  const int tiles = (width + 31) / 32, per = (tiles + kW - 1) / kW;
+  p->lane = threadIdx.x & 63;
+  p->wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p->half = p->lane >> 5;
+  const int64_t sh = unit / per, slot = sh / a.H;
+  p->hv = static_cast<int>(sh - slot * a.H);
+  p->hk = p->hv / a.rep;
+  if (!find_segment(a, slot, &p->g)) return false;
+  p->head = p->g.n * a.H + p->hv;
+  const int tile = static_cast<int>(unit - sh * per) * kW + p->wave;
+  p->tile = min(tile, tiles - 1);
+  p->cols = min(32, width - 32 * p->tile);
+  p->store_cols = tile < tiles ? p->cols : 0;
+  p->in = (p->lane & 31) < p->store_cols;
+  return true;
 }
 
 // The state's (DK, DV) columns of a wave, from `base` (its first column; NULL: zeros).
@@ -567,8 +606,8 @@ __device__ __forceinline__ void load_state(f32x16* S, const float* base, const A
 }
 template <typename T, int KT>
 __device__ __forceinline__ void store_state(const f32x16* S, void* base, float factor, const Args& a,
-                                            const Place& w, char* lds) {
-  const uint32_t stride = a.DV * sizeof(T);
+                                            const Place& w, char* lds, int width = 0) {
+  const uint32_t stride = (width ? width : a.DV) * sizeof(T);  // values of a row
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     const int rows = a.DK - 32 * kt;
@@ -602,7 +641,9 @@ __device__ __forceinline__ float decay_of(double diff) { return exp2_hw(static_c
 
 int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);
 int launch_scan(const Args& a, int dtype, bool save, hipStream_t st);
-int launch_adjoint(const Args& a, int dtype, hipStream_t st);
+int launch_span(const Args& a, int dtype, hipStream_t st);
+int launch_join(const Args& a, int dtype, bool backward, hipStream_t st);
+int launch_adjoint(const Args& a, int dtype, bool span, hipStream_t st);
 int launch_grads(const Args& a, int dtype, bool aligned, hipStream_t st);
 int launch_gate_grads(const Args& a, hipStream_t st);
 

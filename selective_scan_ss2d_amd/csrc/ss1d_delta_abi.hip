@@ -1,6 +1,7 @@
 // C entry points of the gated delta rule: argument checks, scratch and the kernel sequence.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -13,6 +14,9 @@ namespace {
 
 using ss2d::delta::Args;
 using ss2d::delta::Strides;
+
+// Segment length that a test forces on its own thread (ss1d_delta_set_segment); -1: the rule's.
+thread_local int64_t g_segment_override = -1;
 
 constexpr int64_t kMaxTokens = int64_t(1) << 40;
 constexpr int64_t kMaxLine = int64_t(1) << 24;    // elements from one token's row to the next
@@ -69,9 +73,28 @@ int64_t slot_count(int64_t L, int64_t S, int64_t T, bool packed, int64_t unit) {
   return packed ? T / unit + S : S * ((L + unit - 1) / unit);
 }
 
-// The state a training forward keeps: the marks, the end states, then t and o in fp32.
+// Chunks per segment, 0 for whole sequences.  A segmented forward does the state's recurrence
+// about 2.5 times (M and Z, then the run), so it pays where the chip is otherwise idle: the
+// segments are made long enough for about 2 waves on every SIMD (2048), and no shorter than 8
+// chunks or sqrt(C / 4) of the C chunks of a row, because the join runs through them one by
+// one (about a quarter of a chunk's time each).  Even, so that blocks of 64 tokens do not
+// straddle them.
+int64_t segment_chunks(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DV, bool packed) {
+  using ss2d::delta::kC;
+  if (g_segment_override >= 0) return g_segment_override;
+  const int64_t chunks = (L + kC - 1) / kC, tiles = (DV + 31) / 32;
+  const int64_t waves = S * H * tiles, total = (T / kC + (packed ? S : 0)) * H * tiles;
+  if (waves >= 1024) return 0;
+  int64_t len = std::max<int64_t>(8, (total + 2047) / 2048);
+  len = std::max<int64_t>(len, static_cast<int64_t>(std::ceil(std::sqrt(static_cast<double>(chunks) / 4))));
+  len += len & 1;
+  return 2 * len <= chunks ? len : 0;
+}
+
+// The state a training forward keeps: the marks, the end states, t and o in fp32, and the
+// segments' matrices M, which the backward's join takes transposed.
 struct Saved {
-  int64_t marks, ends, rows, bytes;
+  int64_t marks, ends, rows, spans, bytes;
 };
 Saved saved_layout(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DK, int64_t DV,
                    bool packed) {
@@ -80,7 +103,11 @@ Saved saved_layout(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DK, int64
       size_t(slot_count(L, S, T, packed, ss2d::delta::kMark)) * H * DK * DV * 4));
   s.ends = static_cast<int64_t>(ss2d::host_align256(size_t(S) * H * DK * DV * 4));
   s.rows = static_cast<int64_t>(ss2d::host_align256(size_t(T) * H * DV * 4));
-  s.bytes = s.marks + s.ends + 2 * s.rows;
+  const int64_t len = segment_chunks(L, S, T, H, DV, packed);
+  s.spans = len ? static_cast<int64_t>(ss2d::host_align256(
+                      size_t(slot_count(L, S, T, packed, len * ss2d::delta::kC)) * H * DK * DK * 4))
+                : 0;
+  s.bytes = s.marks + s.ends + 2 * s.rows + s.spans;
   return s;
 }
 void set_saved(Args* a, void* saved, const Saved& s) {
@@ -89,6 +116,7 @@ void set_saved(Args* a, void* saved, const Saved& s) {
   a->ends = reinterpret_cast<float*>(at + s.marks);
   a->ts = reinterpret_cast<float*>(at + s.marks + s.ends);
   a->os = reinterpret_cast<float*>(at + s.marks + s.ends + s.rows);
+  a->span_m = reinterpret_cast<float*>(at + s.marks + s.ends + 2 * s.rows);
 }
 
 int check_pointers(const Span* ins, int n_in, const Span* outs, int n_out) {
@@ -106,16 +134,22 @@ int check_pointers(const Span* ins, int n_in, const Span* outs, int n_out) {
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 struct Scratch {
-  size_t keys, heads, bytes;
+  size_t keys, heads, z, starts, m, bytes;
 };
-Scratch scratch_layout(const Args& a, int dtype) {
+// kept: the segments' matrices M are not in scratch but in what the training forward keeps.
+Scratch scratch_layout(const Args& a, int dtype, bool kept) {
   using namespace ss2d::delta;
   const int kt = a.DK <= 32 ? 1 : (a.DK <= 64 ? 2 : 4);
   const bool f32 = dtype == SS2D_F32;
   Scratch s{};
   s.keys = 0;
   s.heads = size_t(a.slots) * a.HK * key_planes(f32, kt) * kPlane;
-  s.bytes = s.heads + size_t(a.slots) * a.H * head_planes(f32, a.p_planes) * kPlane + kReadPast;
+  s.z = ss2d::host_align256(s.heads + size_t(a.slots) * a.H * head_planes(f32, a.p_planes) * kPlane +
+                            kReadPast);
+  const size_t segments = size_t(a.seg_slots) * a.H * a.DK * 4;
+  s.starts = s.z + ss2d::host_align256(segments * a.DV);
+  s.m = s.starts + ss2d::host_align256(segments * a.DV);
+  s.bytes = s.m + (kept ? 0 : ss2d::host_align256(segments * a.DK));
   return s;
 }
 
@@ -152,6 +186,8 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
   a->scale = scale;
   a->slots = slot_count(L, S, T, cu != nullptr, ss2d::delta::kC);
   a->marks_n = slot_count(L, S, T, cu != nullptr, ss2d::delta::kMark);
+  a->seglen = segment_chunks(L, S, T, H, DV, cu != nullptr);
+  a->seg_slots = a->seglen ? slot_count(L, S, T, cu != nullptr, a->seglen * ss2d::delta::kC) : 0;
   const int64_t qb = strided_bytes(B, L, HK, DK, a->sq, e),
                 kb = strided_bytes(B, L, HK, DK, a->sk, e),
                 vb = strided_bytes(B, L, H, DV, a->sv, e);
@@ -170,7 +206,9 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
   ins[4] = {beta, T * H * 4};
   ins[5] = {cu, (S + 1) * 4};
   const int64_t tiles = (DV + 31) / 32;
-  if ((a->slots * H / 4 + 1) * 256 > kMaxThreads || S * H * tiles * 64 > kMaxThreads ||
+  const int64_t units = a->seglen ? a->seg_slots : S;
+  if ((a->slots * H / 4 + 1) * 256 > kMaxThreads ||
+      std::max(units, S) * H * (tiles + 8) * 64 > kMaxThreads ||
       a->marks_n * HK * 384 > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
     return SS2D_ERR_SHAPE;
   return SS2D_OK;
@@ -183,17 +221,28 @@ bool aligned_keys(const Args& a, int64_t e) {
 void set_scratch(Args* a, char* ws, const Scratch& w) {
   a->keys = ws + w.keys;
   a->heads = ws + w.heads;
+  a->span_z = reinterpret_cast<float*>(ws + w.z);
+  a->starts = reinterpret_cast<float*>(ws + w.starts);
+  a->span_m = reinterpret_cast<float*>(ws + w.m);
 }
 
 int run_forward(const Args& a, int dtype, bool save, hipStream_t st) {
   const bool al = aligned_keys(a, dtype == SS2D_F32 ? 4 : 2);
-  const int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
+  int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
+  if (!err && a.seglen) err = ss2d::delta::launch_span(a, dtype, st);
+  if (!err && a.seglen) err = ss2d::delta::launch_join(a, dtype, false, st);
   return err ? err : ss2d::delta::launch_scan(a, dtype, save, st);
 }
 
 }  // namespace
 
 extern "C" {
+
+int ss1d_delta_set_segment(int64_t chunks) {
+  if (chunks < -1 || chunks > (1 << 20) || (chunks > 0 && chunks % 2 != 0)) return SS2D_ERR_SHAPE;
+  g_segment_override = chunks;
+  return SS2D_OK;
+}
 
 int64_t ss1d_delta_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t H, int64_t DK, int64_t DV,
                                int packed) {
@@ -236,7 +285,7 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
 
   a.p_planes = saved ? 3 : 2;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const Scratch w = scratch_layout(a, dtype);
+  const Scratch w = scratch_layout(a, dtype, saved != nullptr);
   char* ws = nullptr;
   rc = ss2d::host_scratch_alloc(&ws, w.bytes, st);
   if (rc != SS2D_OK) return rc;
@@ -300,7 +349,7 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   // backward's in their place), the states' gradients, the gates' partial sums
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t tiles = (DV + 31) / 32;
-  const Scratch w = scratch_layout(a, dtype);
+  const Scratch w = scratch_layout(a, dtype, true);
   const size_t dmarks = w.bytes,
                pbeta = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * e),
                pgate = pbeta + ss2d::host_align256(size_t(tiles) * T * H * 4),
@@ -328,7 +377,9 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   const Strides rows = {L * H * DV, H * DV, DV};
   const bool alv = aligned_rows(dout, rows, DV, e) && aligned_rows(dv, rows, DV, e);
   if (!err && a.slots > 0) err = ss2d::delta::launch_prep(a, dtype, alk, true, st);
-  if (!err) err = ss2d::delta::launch_adjoint(a, dtype, st);
+  if (!err && a.seglen) err = ss2d::delta::launch_adjoint(a, dtype, true, st);
+  if (!err && a.seglen) err = ss2d::delta::launch_join(a, dtype, true, st);
+  if (!err) err = ss2d::delta::launch_adjoint(a, dtype, false, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_grads(a, dtype, alv, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_gate_grads(a, st);
   const hipError_t fe = hipFreeAsync(ws, st);

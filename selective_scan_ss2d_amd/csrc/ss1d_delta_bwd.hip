@@ -41,25 +41,32 @@ __device__ __forceinline__ int row_of(int lane) { return (lane & 31) >> 1; }
 
 // One wave per (sequence, head, 32 columns), kW adjacent ones per block sharing the chunks'
 // operands through LDS, chunks last to first.
-template <typename T, int KT, int kW>
+// kSpan: the span pass over segments (see the forward): only the gradient before a segment,
+// from zero after it, is kept.
+template <typename T, int KT, int kW, bool kSpan>
 __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
   using St = Stage<T, KT, 3, kW>;
   __shared__ __align__(16) char buffers[2][St::kPlanes * kPlane];
   __shared__ __align__(16) char spare[kW][kTileBytes];
-  const Place w = place<kW>(a, blockIdx.x);
+  Place w;
+  if (!place<kW>(&w, a, blockIdx.x, a.DV)) return;
+  const Segment& g = w.g;
+  if (kSpan && (g.index == 0 || g.end == g.begin)) return;  // nothing comes before the first one
   const int lane = w.lane, half = w.half, tiles = (a.DV + 31) / 32;
   char* const lds = spare[w.wave];
-  const Seq seq = sequence(a, w.n);
-  const int64_t slot0 = first_slot(a, w.n, seq, kC), mark0 = first_slot(a, w.n, seq, kMark);
+  const Seq& seq = g.seq;
+  const int64_t mark0 = first_slot(a, g.n, seq, kMark);
   const int64_t state = w.head * a.DK * a.DV + 32 * w.tile;
+  const int64_t start = (g.slot * a.H + w.hv) * a.DK * a.DV + 32 * w.tile;
   const uint32_t vline = static_cast<uint32_t>(a.sv.l) * sizeof(T), line = a.H * a.DV;
 
   f32x16 dS[KT];
-  load_state<KT>(dS, a.dht ? a.dht + state : nullptr, a, w, lds);
+  const float* after_all = g.last ? (a.dht ? a.dht + state : nullptr) : a.starts + start;
+  load_state<KT>(dS, kSpan ? nullptr : after_all, a, w, lds);
   float factor = 1.0f;
-  const int64_t chunks = (seq.len + kC - 1) / kC;
+  const int64_t chunks = (seq.len + kC - 1) / kC;  // of the sequence
   const int64_t first = seq.row * line + w.hv * a.DV + 32 * w.tile;
-  const T* v0 = static_cast<const T*>(a.v) + token_at(a, a.sv, w.n, seq, 0) + w.hv * a.sv.h + 32 * w.tile;
+  const T* v0 = static_cast<const T*>(a.v) + token_at(a, a.sv, g.n, seq, 0) + w.hv * a.sv.h + 32 * w.tile;
   const T* d0 = static_cast<const T*>(a.dout) + first;
   T* out0 = static_cast<T*>(a.dv) + first;
   const bool valign = aligned16(v0, vline, w.cols), dalign = aligned16(d0, line * sizeof(T), w.cols);
@@ -69,31 +76,31 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
   St stage;
   Tile<T> vx, dx;
   Tile<float> tx, ox, after[KT];
-  if (chunks > 0) {
-    stage.start(a, slot0 + chunks - 1, w.hv, w.hk, w.wave, lane, -1);
+  if (g.begin < g.end) {
+    stage.start(a, first_slot(a, g.n, seq, kC) + g.end - 1, w.hv, w.hk, w.wave, lane, -1);
     stage.fetch();
-    if (dalign && seq.len % kC == 0) dx.fetch(d0 + (chunks - 1) * kC * line, line * sizeof(T), lane);
-    stage.commit(buffers[(chunks - 1) & 1]);
+    if (dalign && g.end * kC <= seq.len) dx.fetch(d0 + (g.end - 1) * kC * line, line * sizeof(T), lane);
+    stage.commit(buffers[(g.end - 1) & 1]);
     __syncthreads();
   }
-  for (int64_t c = chunks - 1; c >= 0; --c) {
+  for (int64_t c = g.end - 1; c >= g.begin; --c) {
     const int64_t t0 = c * kC, row0 = seq.row + t0, at = t0 * line;
     const int valid = static_cast<int>(min<int64_t>(kC, seq.len - t0));
     const bool whole = valid == kC;
     const char* buf = buffers[c & 1];
     const f32x16 dout =
         dx.columns(dalign && whole, d0 + at, line * sizeof(T), valid, w.cols, lds, lane);
-    if (c > 0) {  // what the next chunk wants early
+    if (c > g.begin) {  // what the next chunk wants early
       stage.fetch();
       if (dalign) dx.fetch(d0 + at - kC * int64_t(line), line * sizeof(T), lane);
     }
     // what this one wants at its end
-    if (valign && whole) vx.fetch(v0 + t0 * a.sv.l, vline, lane);
-    if (salign && whole) {
+    if (!kSpan && valign && whole) vx.fetch(v0 + t0 * a.sv.l, vline, lane);
+    if (!kSpan && salign && whole) {
       tx.fetch(a.ts + first + at, line * 4, lane);
       ox.fetch(a.os + first + at, line * 4, lane);
     }
-    const bool ends = (c & 1) || c == chunks - 1;  // the end of a block of 64 tokens
+    const bool ends = !kSpan && ((c & 1) || c == chunks - 1);  // the end of a block of 64 tokens
     const int64_t mark = mark0 + (c >> 1);
     const float* from = c == chunks - 1
                             ? a.ends + state
@@ -177,29 +184,32 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
         dS[kt] = mma(kx, vw[s], dS[kt]);
       }
     }
-    // dv, and what the gates' gradients take from these 32 columns
-    store_tile<T>(dv, out0 + at, line * sizeof(T), oalign && whole, valid, w.store_cols, lds, lane);
-    f32x16 sb = y * tx.columns(salign && whole, a.ts + first + at, line * 4, valid, w.cols, lds, lane);
-    f32x16 sg = dout * ox.columns(salign && whole, a.os + first + at, line * 4, valid, w.cols, lds, lane) -
-                dv * vx.columns(valign && whole, v0 + t0 * a.sv.l, vline, valid, w.cols, lds, lane);
-    if (w.store_cols < 32) {
+    if constexpr (!kSpan) {
+      // dv, and what the gates' gradients take from these 32 columns
+      store_tile<T>(dv, out0 + at, line * sizeof(T), oalign && whole, valid, w.store_cols, lds, lane);
+      f32x16 sb = y * tx.columns(salign && whole, a.ts + first + at, line * 4, valid, w.cols, lds, lane);
+      f32x16 sg = dout * ox.columns(salign && whole, a.os + first + at, line * 4, valid, w.cols, lds, lane) -
+                  dv * vx.columns(valign && whole, v0 + t0 * a.sv.l, vline, valid, w.cols, lds, lane);
+      if (w.store_cols < 32) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        sb[r] = w.in ? sb[r] : 0.0f;
-        sg[r] = w.in ? sg[r] : 0.0f;
+        for (int r = 0; r < 16; ++r) {
+          sb[r] = w.in ? sb[r] : 0.0f;
+          sg[r] = w.in ? sg[r] : 0.0f;
+        }
+      }
+      const float beta_sum = sum_columns(sb, lane), gate_sum = sum_columns(sg, lane);
+      const int i = acc_row(row_of(lane), half);
+      if ((lane & 1) == 0 && i < valid && w.store_cols > 0) {
+        const int64_t p = (w.tile * a.T + row0 + i) * a.H + w.hv;
+        a.pbeta[p] = beta_sum;
+        a.pgate[p] = gate_sum;
       }
     }
-    const float beta_sum = sum_columns(sb, lane), gate_sum = sum_columns(sg, lane);
-    const int i = acc_row(row_of(lane), half);
-    if ((lane & 1) == 0 && i < valid && w.store_cols > 0) {
-      const int64_t p = (w.tile * a.T + row0 + i) * a.H + w.hv;
-      a.pbeta[p] = beta_sum;
-      a.pgate[p] = gate_sum;
-    }
-    if (c > 0) stage.commit(buffers[(c - 1) & 1]);
+    if (c > g.begin) stage.commit(buffers[(c - 1) & 1]);
     __syncthreads();
   }
-  if (a.dh0) store_state<float, KT>(dS, a.dh0 + state, factor, a, w, lds);
+  if (kSpan) store_state<float, KT>(dS, a.span_z + start, factor, a, w, lds);
+  else if (a.dh0 && g.index == 0) store_state<float, KT>(dS, a.dh0 + state, factor, a, w, lds);
 }
 
 // dq and dk of one block of 64 tokens and key head, summed over the value heads that share
@@ -557,17 +567,19 @@ __global__ __launch_bounds__(256) void k_delta_gate_grads(Args a) {
 }
 
 template <typename T, int KT, int kW>
-int adjoint_w(const Args& a, hipStream_t st) {
-  const int64_t blocks = a.S * a.H * (((a.DV + 31) / 32 + kW - 1) / kW);
-  hipLaunchKernelGGL((k_delta_adjoint<T, KT, kW>), dim3(static_cast<unsigned>(blocks)), dim3(64 * kW),
-                     0, st, a);
+int adjoint_w(const Args& a, bool span, hipStream_t st) {
+  const int64_t units = a.seglen > 0 ? a.seg_slots : a.S;
+  const int64_t blocks = units * a.H * (((a.DV + 31) / 32 + kW - 1) / kW);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kW);
+  if (span) hipLaunchKernelGGL((k_delta_adjoint<T, KT, kW, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_adjoint<T, KT, kW, false>), grid, block, 0, st, a);
   return static_cast<int>(hipGetLastError());
 }
 template <typename T, int KT>
-int adjoint_kt(const Args& a, hipStream_t st) {
-  if (a.DV <= 32) return adjoint_w<T, KT, 1>(a, st);
-  if (a.DV <= 64) return adjoint_w<T, KT, 2>(a, st);
-  return adjoint_w<T, KT, 4>(a, st);
+int adjoint_kt(const Args& a, bool span, hipStream_t st) {
+  if (a.DV <= 32) return adjoint_w<T, KT, 1>(a, span, st);
+  if (a.DV <= 64) return adjoint_w<T, KT, 2>(a, span, st);
+  return adjoint_w<T, KT, 4>(a, span, st);
 }
 template <typename T, int KT, bool kAligned>
 int grads_kt(const Args& a, hipStream_t st) {
@@ -577,10 +589,10 @@ int grads_kt(const Args& a, hipStream_t st) {
 }
 
 template <typename T>
-int adjoint_t(const Args& a, hipStream_t st) {
-  if (a.DK <= 32) return adjoint_kt<T, 1>(a, st);
-  if (a.DK <= 64) return adjoint_kt<T, 2>(a, st);
-  return adjoint_kt<T, 4>(a, st);
+int adjoint_t(const Args& a, bool span, hipStream_t st) {
+  if (a.DK <= 32) return adjoint_kt<T, 1>(a, span, st);
+  if (a.DK <= 64) return adjoint_kt<T, 2>(a, span, st);
+  return adjoint_kt<T, 4>(a, span, st);
 }
 template <typename T, bool kAligned>
 int grads_t(const Args& a, hipStream_t st) {
@@ -591,8 +603,8 @@ int grads_t(const Args& a, hipStream_t st) {
 
 }  // namespace
 
-int launch_adjoint(const Args& a, int dtype, hipStream_t st) {
-  return dtype == 0 ? adjoint_t<float>(a, st) : adjoint_t<uint16_t>(a, st);
+int launch_adjoint(const Args& a, int dtype, bool span, hipStream_t st) {
+  return dtype == 0 ? adjoint_t<float>(a, span, st) : adjoint_t<uint16_t>(a, span, st);
 }
 int launch_grads(const Args& a, int dtype, bool aligned, hipStream_t st) {
   if (dtype == 0) return aligned ? grads_t<float, true>(a, st) : grads_t<float, false>(a, st);

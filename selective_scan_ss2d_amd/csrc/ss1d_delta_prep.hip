@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
   constexpr int64_t operand = KeyRecord<T, KT>::kOperand * kPlane;
   char* const head = a.heads + (slot * a.H + hv) *
                                    (int64_t(head_planes(sizeof(T) == 4, a.p_planes)) * kPlane);
-  char* const pf = head + HeadRecord<T, 3>::kN * kPlane;
+  char* const pf = head + HeadRecord<T, 3>::kPStart * kPlane;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) {
     Exact<T> kx[2], qx[2];
@@ -114,8 +114,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
   if (half == 0) {
     sh.G[col] = G;
     sh.beta[col] = bv;
-    float* gt = reinterpret_cast<float*>(
-        head + (head_planes(sizeof(T) == 4, a.p_planes) - 1) * int64_t(kPlane));
+    float* gt = reinterpret_cast<float*>(head + HeadRecord<T, 3>::kGates * kPlane);
     gt[col] = decay_of(G);
     gt[kC + col] = decay_of(Gend - G);
     gt[2 * kC + col] = bv;

@@ -1,6 +1,12 @@
 // The sequential pass of the gated delta rule's forward: one wave carries 32 columns of one
 // sequence and head's state through its chunks, the state in registers, the chunk's operands
 // in LDS, where the block's waves (adjacent columns) share them, loaded a chunk ahead.
+//
+// With few sequences and heads the chunks' chain leaves most of the chip idle.  Then the
+// sequences are cut into segments: what a segment makes of the state before it is affine,
+// S -> M S + Z, and the span pass computes M (from the identity's columns, no v) and Z (from
+// zero) of all segments at once with the same recurrence, the join pass runs S through them,
+// and the forward then starts every segment from its state.
 #include "ss1d_delta.h"
 
 namespace ss2d {
@@ -9,53 +15,77 @@ namespace {
 
 // Operands hold 24 bits (3 bf16 terms), those of o 17 (2 terms, which leaves o to its own
 // rounding); with kSave, the training forward, o's hold 24 as well, because the backward
-// forms the decays' gradient from o.
-template <typename T, int KT, int kW, bool kSave>
-__global__ __launch_bounds__(64 * kW) __attribute__((amdgpu_waves_per_eu(kSave ? 1 : 2)))
-void k_delta_scan(Args a) {
+// forms the decays' gradient from o.  kSpan: the span pass, no o; the tiles are those of Z,
+// then those of M.
+enum Mode { kForward, kSaving, kSpanning };
+template <typename T, int KT, int kW, Mode kMode>
+__global__ __launch_bounds__(64 * kW) void k_delta_scan(Args a) {
+  constexpr bool kSave = kMode == kSaving, kSpan = kMode == kSpanning;
   constexpr int kP = kSave ? 3 : 2;
-  using St = Stage<T, KT, kP, kW>;
+  using St = Stage<T, KT, kP, kW, kSpan>;
   __shared__ __align__(16) char buffers[2][St::kPlanes * kPlane];
   __shared__ __align__(16) char spare[kW][kTileBytes];
-  const Place w = place<kW>(a, blockIdx.x);
+  Place w;
+  // the span pass counts whole tiles: DV's first, then DK's
+  const int vtiles = (a.DV + 31) / 32;
+  if (!place<kW>(&w, a, blockIdx.x, kSpan ? 32 * (vtiles + KT) : a.DV)) return;
+  const Segment& g = w.g;
+  // nothing starts from the last segment's end; the backward takes its M all the same
+  if (kSpan && (g.end == g.begin || (g.last && a.marks == nullptr))) return;
+  const bool matrix = kSpan && w.tile >= vtiles;
+  if (kSpan) {
+    w.cols = matrix ? max(0, min(32, a.DK - 32 * (w.tile - vtiles))) : min(32, a.DV - 32 * w.tile);
+    w.store_cols = min(w.cols, w.store_cols);
+    w.in = (w.lane & 31) < w.store_cols;
+  }
   const int lane = w.lane, half = w.half;
   char* const lds = spare[w.wave];
-  const Seq seq = sequence(a, w.n);
-  const int64_t slot0 = first_slot(a, w.n, seq, kC);
+  const Seq& seq = g.seq;
   const int64_t state = w.head * a.DK * a.DV + 32 * w.tile;
-  const int64_t chunks = (seq.len + kC - 1) / kC;
+  const int64_t start = (g.slot * a.H + w.hv) * a.DK * a.DV + 32 * w.tile;
+  const int64_t chunks = g.end, t0 = g.begin * kC;
 
   f32x16 S[KT];
-  load_state<KT>(S, a.h0 ? a.h0 + state : nullptr, a, w, lds);
+  if constexpr (kSpan) {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        S[kt][r] = matrix && 32 * kt + acc_row(r, half) == 32 * (w.tile - vtiles) + (lane & 31) ? 1.0f : 0.0f;
+  } else {
+    load_state<KT>(S, g.index > 0 ? a.starts + start : (a.h0 ? a.h0 + state : nullptr), a, w, lds);
+  }
   float factor = 1.0f;
 
-  const int64_t first = seq.row * a.H * a.DV + w.hv * a.DV + 32 * w.tile;
+  const int64_t first = (seq.row + t0) * a.H * a.DV + w.hv * a.DV + 32 * w.tile;
   const uint32_t vline = static_cast<uint32_t>(a.sv.l) * sizeof(T), line = a.H * a.DV;
-  const T* vat = static_cast<const T*>(a.v) + token_at(a, a.sv, w.n, seq, 0) + w.hv * a.sv.h + 32 * w.tile;
+  const T* vat = static_cast<const T*>(a.v) + token_at(a, a.sv, g.n, seq, t0) + w.hv * a.sv.h + 32 * w.tile;
   T* oat = static_cast<T*>(a.o) + first;
-  const bool valign = aligned16(vat, vline, w.cols);
+  const bool valign = !matrix && aligned16(vat, vline, w.cols);
   const bool oalign = aligned16(oat, line * sizeof(T), w.store_cols);
   const bool salign = aligned16(nullptr, line * 4, w.store_cols);
   float* tat = kSave ? a.ts + first : nullptr;
   float* pat = kSave ? a.os + first : nullptr;
-  float* mat = kSave ? a.marks + (first_slot(a, w.n, seq, kMark) * a.H + w.hv) * a.DK * a.DV + 32 * w.tile
+  float* mat = kSave ? a.marks + ((first_slot(a, g.n, seq, kMark) + g.begin / 2) * a.H + w.hv) * a.DK * a.DV +
+                           32 * w.tile
                      : nullptr;
-  int left = static_cast<int>(min<int64_t>(seq.len, 1 << 30));  // tokens of this and later chunks
+  int left = static_cast<int>(min<int64_t>(seq.len - t0, 1 << 30));  // tokens from this chunk on
 
   St stage;
   Tile<T> vx;
-  if (chunks > 0) {
-    stage.start(a, slot0, w.hv, w.hk, w.wave, lane, 1);
+  if (g.begin < g.end) {
+    stage.start(a, first_slot(a, g.n, seq, kC) + g.begin, w.hv, w.hk, w.wave, lane, 1);
     stage.fetch();
     if (valign && left >= kC) vx.fetch(vat, vline, lane);
-    stage.commit(buffers[0]);
+    stage.commit(buffers[g.begin & 1]);
     __syncthreads();
   }
-  for (int64_t c = 0; c < chunks; ++c) {
+  for (int64_t c = g.begin; c < chunks; ++c) {
     left = static_cast<int>(min<int64_t>(seq.len - c * kC, 1 << 30));
     const bool whole = left >= kC;
     const char* buf = buffers[c & 1];
-    const f32x16 v = vx.columns(valign && whole, vat, vline, left, w.cols, lds, lane);
+    f32x16 v = {};
+    if (!matrix) v = vx.columns(valign && whole, vat, vline, left, w.cols, lds, lane);
     vat += kC * a.sv.l;
     if (c + 1 < chunks) {
       stage.fetch();
@@ -72,12 +102,14 @@ void k_delta_scan(Args a) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Exact<T> kx, qx;
-        get(kx, St::operand(buf, 0, kt, s), lane);
-        get(qx, St::operand(buf, 2, kt, s), lane);
         Wide<T, 3> sw;
         set_wide(sw, part(S[kt], s));
+        get(kx, St::operand(buf, 0, kt, s), lane);
         ks = mma(kx, sw, ks);
-        qs = mma(qx, first_terms<kP>(sw), qs);
+        if constexpr (!kSpan) {
+          get(qx, St::operand(buf, 2, kt, s), lane);
+          qs = mma(qx, first_terms<kP>(sw), qs);
+        }
       }
     const float* gate = St::gates(buf);
     const f32x16 gam = load_gate(gate, half) * factor, beta = load_gate(gate + 2 * kC, half);
@@ -105,57 +137,175 @@ void k_delta_scan(Args a) {
         get(kx, St::operand(buf, 1, kt, s), lane);
         S[kt] = mma(kx, ew[s], S[kt]);
       }
-    f32x16 pu = {};
+    if constexpr (!kSpan) {
+      f32x16 pu = {};
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Wide<T, kP> pw, uw;
-      get(pw, St::p(buf, s), lane);
-      set_wide(uw, part(u, s));
-      pu = mma(pw, uw, pu);
-    }
-    const f32x16 o = a.scale * gam * qs + pu;
-    store_tile<T>(o, oat, line * sizeof(T), oalign && whole, left, w.store_cols, lds, lane);
-    oat += kC * int64_t(line);
-    if (kSave) {
-      store_tile<float>(t, tat, line * 4, salign && whole, left, w.store_cols, lds, lane);
-      store_tile<float>(o, pat, line * 4, salign && whole, left, w.store_cols, lds, lane);
-      tat += kC * int64_t(line);
-      pat += kC * int64_t(line);
+      for (int s = 0; s < 2; ++s) {
+        Wide<T, kP> pw, uw;
+        get(pw, St::p(buf, s), lane);
+        set_wide(uw, part(u, s));
+        pu = mma(pw, uw, pu);
+      }
+      const f32x16 o = a.scale * gam * qs + pu;
+      store_tile<T>(o, oat, line * sizeof(T), oalign && whole, left, w.store_cols, lds, lane);
+      oat += kC * int64_t(line);
+      if (kSave) {
+        store_tile<float>(t, tat, line * 4, salign && whole, left, w.store_cols, lds, lane);
+        store_tile<float>(o, pat, line * 4, salign && whole, left, w.store_cols, lds, lane);
+        tat += kC * int64_t(line);
+        pat += kC * int64_t(line);
+      }
     }
     if (c + 1 < chunks) stage.commit(buffers[(c + 1) & 1]);
     __syncthreads();
   }
-  if (a.ht) store_state<float, KT>(S, a.ht + state, factor, a, w, lds);
-  if (kSave) store_state<float, KT>(S, a.ends + state, factor, a, w, lds);
+  if constexpr (kSpan) {
+    const int64_t sh = g.slot * a.H + w.hv;
+    if (matrix)
+      store_state<float, KT>(S, a.span_m + sh * a.DK * a.DK + 32 * (w.tile - vtiles), factor, a, w, lds,
+                             a.DK);
+    else store_state<float, KT>(S, a.span_z + start, factor, a, w, lds);
+  } else if (g.last) {
+    if (a.ht) store_state<float, KT>(S, a.ht + state, factor, a, w, lds);
+    if (kSave) store_state<float, KT>(S, a.ends + state, factor, a, w, lds);
+  }
 }
 
+// Runs the state of 32 columns through its sequence's segments, S <- M S + Z (forward; the
+// state before every segment but the first goes to `starts`) or, last to first, dS <- M^T dS + Z
+// (backward; the gradient after every segment but the last).  One wave per 32 of the state's
+// rows: each publishes its rows as operand terms in LDS and multiplies its rows of M with all.
+template <typename T, int KT, bool kBackward>
+__global__ __launch_bounds__(64 * KT) void k_delta_join(Args a) {
+  __shared__ __align__(16) char operand[2 * KT * wide_planes<T, 3>() * kPlane];
+  __shared__ __align__(16) char spare[KT][kTileBytes];
+  const int lane = threadIdx.x & 63, half = lane >> 5, own = swap23(lane & 31);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* const lds = spare[wave];
+  const int tiles = (a.DV + 31) / 32;
+  const int64_t head = blockIdx.x / tiles, n = head / a.H;
+  const int tile = static_cast<int>(blockIdx.x - head * tiles), hv = static_cast<int>(head - n * a.H);
+  const Seq seq = sequence(a, n);
+  const int64_t chunks = (seq.len + kC - 1) / kC, count = (chunks + a.seglen - 1) / a.seglen;
+  if (count < 2) return;
+  const int64_t slot0 = first_slot(a, n, seq, static_cast<int>(a.seglen * kC));
+  const int cols = min(32, a.DV - 32 * tile), rows = a.DK - 32 * wave;  // of this wave's tile
+  const uint32_t stride = a.DV * 4u;
+  const int64_t at = int64_t(32) * wave * a.DV + 32 * tile;
+  const int64_t size = int64_t(a.DK) * a.DV, matrix = int64_t(a.DK) * a.DK;
+  const bool whole = aligned16(nullptr, stride, cols) && rows >= 32;
+  const int64_t first = kBackward ? count - 1 : 0, step = kBackward ? -1 : 1;
+
+  const float* from = kBackward ? a.dht : a.h0;
+  Tile<float> z;
+  f32x16 S = {};
+  if (from != nullptr && rows > 0) {
+    from += head * size + at;
+    const bool w0 = whole && aligned16(from, stride, cols);
+    if (w0) z.fetch(from, stride, lane);
+    S = z.columns(w0, from, stride, rows, cols, lds, lane);
+  }
+  // this wave's rows of M (or M^T): 8 values per operand step, loaded a segment ahead
+  f32x8 m[2 * KT];
+  const int k1 = min(32 * wave + own, a.DK - 1);
+  const bool kin = 32 * wave + own < a.DK;
+  auto fetch = [&](int64_t i) {
+    const auto p = global(a.span_m) + ((slot0 + i) * a.H + hv) * matrix;
+#pragma unroll
+    for (int s = 0; s < 2 * KT; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k2 = 16 * s + 8 * half + e, c = min(k2, a.DK - 1);
+        const float v = kBackward ? p[c * a.DK + k1] : p[k1 * a.DK + c];
+        m[s][e] = kin && k2 < a.DK ? v : 0.0f;
+      }
+    if (whole) z.fetch(a.span_z + ((slot0 + i) * a.H + hv) * size + at, stride, lane);
+  };
+  fetch(first);
+  for (int64_t i = first, left = count - 1; left > 0; i += step, --left) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      Wide<T, 3> w;
+      set_wide(w, part(S, s));
+      put(operand + (2 * wave + s) * wide_planes<T, 3>() * kPlane, lane, w);
+    }
+    Wide<T, 3> mw[2 * KT];
+#pragma unroll
+    for (int s = 0; s < 2 * KT; ++s) set_wide(mw[s], m[s]);
+    f32x16 next = {};
+    if (rows > 0)
+      next = z.columns(whole, a.span_z + ((slot0 + i) * a.H + hv) * size + at, stride, rows, cols, lds,
+                       lane);
+    if (left > 1) fetch(i + step);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2 * KT; ++s) {
+      Wide<T, 3> w;
+      get(w, operand + s * wide_planes<T, 3>() * kPlane, lane);
+      next = mma(mw[s], w, next);
+    }
+    S = next;
+    if (rows > 0)
+      store_tile<float>(S, a.starts + ((slot0 + i + step) * a.H + hv) * size + at, stride, whole, rows, cols,
+                        lds, lane);
+    __syncthreads();
+  }
+}
+
+int64_t units(const Args& a) { return a.seglen > 0 ? a.seg_slots : a.S; }
+
 template <typename T, int KT, int kW>
-int launch_w(const Args& a, bool save, hipStream_t st) {
-  const int64_t blocks = a.S * a.H * (((a.DV + 31) / 32 + kW - 1) / kW);
+int launch_w(const Args& a, Mode mode, hipStream_t st) {
+  const int tiles = (a.DV + 31) / 32 + (mode == kSpanning ? KT : 0);
+  const int64_t blocks = units(a) * a.H * ((tiles + kW - 1) / kW);
   const dim3 grid(static_cast<unsigned>(blocks)), block(64 * kW);
-  if (save) hipLaunchKernelGGL((k_delta_scan<T, KT, kW, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_delta_scan<T, KT, kW, false>), grid, block, 0, st, a);
+  if (mode == kSaving) hipLaunchKernelGGL((k_delta_scan<T, KT, kW, kSaving>), grid, block, 0, st, a);
+  else if (mode == kSpanning)
+    hipLaunchKernelGGL((k_delta_scan<T, KT, kW, kSpanning>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_scan<T, KT, kW, kForward>), grid, block, 0, st, a);
   return static_cast<int>(hipGetLastError());
 }
 
 template <typename T, int KT>
-int launch_kt(const Args& a, bool save, hipStream_t st) {
-  if (a.DV <= 32) return launch_w<T, KT, 1>(a, save, st);
-  if (a.DV <= 64) return launch_w<T, KT, 2>(a, save, st);
-  return launch_w<T, KT, 4>(a, save, st);
+int launch_kt(const Args& a, Mode mode, hipStream_t st) {
+  const int width = a.DV + (mode == kSpanning ? 32 * KT : 0);
+  if (width <= 32) return launch_w<T, KT, 1>(a, mode, st);
+  if (width <= 64) return launch_w<T, KT, 2>(a, mode, st);
+  return launch_w<T, KT, 4>(a, mode, st);
 }
 
 template <typename T>
-int launch_t(const Args& a, bool save, hipStream_t st) {
-  if (a.DK <= 32) return launch_kt<T, 1>(a, save, st);
-  if (a.DK <= 64) return launch_kt<T, 2>(a, save, st);
-  return launch_kt<T, 4>(a, save, st);
+int launch_t(const Args& a, Mode mode, hipStream_t st) {
+  if (a.DK <= 32) return launch_kt<T, 1>(a, mode, st);
+  if (a.DK <= 64) return launch_kt<T, 2>(a, mode, st);
+  return launch_kt<T, 4>(a, mode, st);
+}
+
+template <typename T, int KT>
+int join_kt(const Args& a, bool backward, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.S * a.H * ((a.DV + 31) / 32))), block(64 * KT);
+  if (backward) hipLaunchKernelGGL((k_delta_join<T, KT, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_join<T, KT, false>), grid, block, 0, st, a);
+  return static_cast<int>(hipGetLastError());
+}
+template <typename T>
+int join_t(const Args& a, bool backward, hipStream_t st) {
+  if (a.DK <= 32) return join_kt<T, 1>(a, backward, st);
+  if (a.DK <= 64) return join_kt<T, 2>(a, backward, st);
+  return join_kt<T, 4>(a, backward, st);
 }
 
 }  // namespace
 
 int launch_scan(const Args& a, int dtype, bool save, hipStream_t st) {
-  return dtype == 0 ? launch_t<float>(a, save, st) : launch_t<uint16_t>(a, save, st);
+  const Mode mode = save ? kSaving : kForward;
+  return dtype == 0 ? launch_t<float>(a, mode, st) : launch_t<uint16_t>(a, mode, st);
+}
+int launch_span(const Args& a, int dtype, hipStream_t st) {
+  return dtype == 0 ? launch_t<float>(a, kSpanning, st) : launch_t<uint16_t>(a, kSpanning, st);
+}
+int launch_join(const Args& a, int dtype, bool backward, hipStream_t st) {
+  return dtype == 0 ? join_t<float>(a, backward, st) : join_t<uint16_t>(a, backward, st);
 }
 
 }  // namespace delta

@@ -120,3 +120,19 @@ def adjoint(t, scale, cu=None, dstate=None):
             dS = dS * g[at].exp()[:, None, None]
         first.append(dS)
     return d, torch.stack(first)
+
+
+class segments:
+    """Forces the forward's and backward's segment length (chunks of 32 tokens, even; 0: whole
+    sequences) for this thread's calls inside the block."""
+
+    def __init__(self, chunks):
+        self.chunks = chunks
+
+    def __enter__(self):
+        from selective_scan_ss2d_amd import _binding as bnd
+        assert bnd.load_library().ss1d_delta_set_segment(self.chunks) == 0
+
+    def __exit__(self, *exc):
+        from selective_scan_ss2d_amd import _binding as bnd
+        bnd.load_library().ss1d_delta_set_segment(-1)

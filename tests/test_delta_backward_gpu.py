@@ -76,6 +76,34 @@ def test_decays(dtype, decay):
     check_grads(t, run(t, 0.3, True), dtype, 0.3)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 8), (2, 130, 1, 2, 64, 48), (1, 257, 2, 2, 127, 33),
+                                   (1, 320, 1, 2, 128, 64), (1, 129, 1, 1, 30, 100)])
+def test_segments(shape, dtype):
+    """Sequences cut into segments of 2 chunks, kept and recomputed."""
+    B, L, HK, H, DK, DV = shape
+    t = du.make_inputs(*shape, dtype, seed=L, h0=B if L % 2 else 0)
+    dstate = 0.1 * torch.randn(B, H, DK, DV, generator=torch.Generator().manual_seed(1))
+    with du.segments(2):
+        d = run(t, DK ** -0.5, True, dstate=dstate.cuda())
+        again = run(t, DK ** -0.5, False, dstate=dstate.cuda())
+    check_grads(t, d, dtype, DK ** -0.5, dstate=dstate)
+    for n in d:
+        assert torch.equal(d[n], again[n]), n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_segments_of_packed_sequences(dtype):
+    lens = [0, 1, 31, 200, 0, 65, 128]
+    cu = torch.tensor([3] + [0] * len(lens), dtype=torch.int32)
+    for i, n in enumerate(lens):
+        cu[i + 1] = cu[i] + n
+    t = du.make_inputs(1, int(cu[-1]) + 5, 1, 2, 64, 48, dtype, seed=8, h0=len(lens))
+    with du.segments(2):
+        d = run(t, 0.5, True, cu_seqlens=cu.cuda())
+    check_grads(t, d, dtype, 0.5, cu)
+
+
 def test_training_forward_is_the_forward():
     """o of the training forward differs from the forward's by its operands' terms only."""
     t = du.make_inputs(2, 100, 1, 2, 64, 64, torch.float32, seed=6)

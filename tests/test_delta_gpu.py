@@ -142,6 +142,57 @@ def test_continuing_from_a_state(dtype):
         check_forward(t, dtype, torch.cat([oa, ob], 1), state, 64 ** -0.5)
 
 
+SEGMENTED = [(1, 1, 1, 1, 8, 8), (2, 130, 1, 2, 64, 48), (1, 257, 2, 2, 127, 33),
+             (1, 400, 1, 2, 128, 128), (3, 192, 1, 1, 32, 64), (1, 129, 1, 1, 30, 100)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("chunks", [2, 4])
+@pytest.mark.parametrize("shape", SEGMENTED)
+def test_segments(shape, chunks, dtype):
+    """Sequences cut into segments that run at once, joined by their matrices."""
+    B, L, HK, H, DK, DV = shape
+    t = du.make_inputs(*shape, dtype, seed=L, h0=B if L % 2 else 0)
+    with du.segments(chunks):
+        o, ht = run(t, final_state=True)
+        check_forward(t, dtype, o, ht, DK ** -0.5)
+        state = t["h0"].cuda() if t["h0"] is not None else None
+        if state is not None:  # in place
+            d = du.to_gpu(t)
+            p, _ = ss.ss1d_delta_forward(*[d[n] for n in du.NAMES], initial_state=state,
+                                         final_state=state)
+            assert torch.equal(p, o) and torch.equal(state, ht)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_segments_of_packed_sequences(dtype):
+    lens = [0, 1, 31, 300, 0, 33, 64, 65, 128, 129, 0]
+    cu = torch.tensor([5] + [0] * len(lens), dtype=torch.int32)
+    for i, n in enumerate(lens):
+        cu[i + 1] = cu[i] + n
+    t = du.make_inputs(1, int(cu[-1]) + 9, 2, 4, 64, 48, dtype, seed=8, h0=len(lens))
+    d = du.to_gpu(t)
+    o = torch.zeros_like(d["v"])
+    with du.segments(2):
+        o, ht = ss.ss1d_delta_forward(*[d[n] for n in du.NAMES], scale=0.5, cu_seqlens=cu.cuda(),
+                                      initial_state=d["h0"], final_state=True, o=o)
+    check_forward(t, dtype, o, ht, 0.5, cu)
+    assert torch.equal(ht[0], d["h0"][0])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_long_sequence_cuts_itself(dtype):
+    """One head and 2,100 tokens: the rule's own segments, against the uncut run."""
+    t = du.make_inputs(1, 2100, 1, 1, 64, 64, dtype, seed=3, decay=0.02)
+    o, ht = run(t, final_state=True)
+    with du.segments(0):
+        p, pht = run(t, final_state=True)
+    assert not torch.equal(ht, pht)
+    big = p.double().cpu()
+    du.check(o, big, "o", *[2 * x for x in du.o_bounds(64, big, dtype)])
+    du.check(ht, pht.double().cpu(), "end state", 2 * du.f32_bound(64, pht.double().cpu()))
+
+
 def test_values_in_masked_places():
     """NaN and infinities in tokens that belong to no sequence reach nothing."""
     t = du.make_inputs(1, 100, 1, 1, 64, 64, torch.bfloat16, seed=12)
