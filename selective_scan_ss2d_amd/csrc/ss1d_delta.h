@@ -26,6 +26,8 @@ constexpr int kC = 32;      // tokens per chunk: one 32 x 32 matrix tile
 constexpr int kMaxDK = 128; // largest key width (the state's rows held by one wave)
 constexpr int kMark = 64;   // tokens between the states a training forward keeps
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -53,10 +55,12 @@ struct Args {
   int64_t slots;               // chunk slots
   int p_planes;                // bf16 terms kept of P
   // sequences cut into segments of `seglen` chunks (0: not cut), see span kernels; per
-  // (segment slot, head): the state after the segment from a zero one (DK, DV), what the
-  // segment makes of the state before it (DK, DK), and the state before it (DK, DV)
+  // (segment slot, head): the state after the segment from a zero one (DK, DV), the state
+  // before it (DK, DV), and the matrix that the segment applies to it, with its transpose if
+  // a backward is to come (operand fragments, see matrix_plane)
   int64_t seglen, seg_slots;
-  float *span_z, *span_m, *starts;
+  float *span_z, *starts;
+  char *span_m, *span_t;
   // kept by a training forward
   float *marks, *ends;         // states before every 64 tokens and after the last
   float *ts, *os;              // t and o in fp32, (T, H, DV)
@@ -174,11 +178,13 @@ template <typename T, int P> struct Wide;
 template <int P> struct Wide<uint16_t, P> { bf16x8 p[P]; };
 template <int P> struct Wide<float, P> { f32x8 v; };
 
-// Two values rounded to nearest bfloat16 and packed.  Written out because the compiler
-// otherwise converts each value once more, alone, to get at the rounded value.
+// Two values rounded to nearest bfloat16 and packed by one v_cvt_pk_bf16_f32.  The empty asm
+// hides where the bits come from: the compiler otherwise converts each value once more, alone,
+// to get at the rounded value.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(r) : "v"(lo), "v"(hi));
+  const f32x2 x = {lo, hi};
+  uint32_t r = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+  asm("" : "+v"(r));
   return r;
 }
 template <int P>
@@ -379,6 +385,12 @@ __device__ __forceinline__ void get(Wide<float, P>& x, const char* at, int lane)
   x.v = get_planes(at, lane);
 }
 
+// A segment's (DK, DK) matrix in fp32: for each 32 rows the operands of 2 KT steps.
+__host__ __device__ constexpr int64_t matrix_bytes(int kt) { return int64_t(4) * kt * kt * kPlane; }
+__device__ __forceinline__ int64_t matrix_plane(int kt, int rows, int step) {
+  return (int64_t(rows) * 2 * kt + step) * 2 * kPlane;
+}
+
 // One chunk's operands in scratch, in the order in which the sequential kernels take them:
 // per key head K, K^T and Q (backward: Q^T), per value head N, a plane of gates (e^G,
 // e^(G_32 - G), beta: 32 values each) and P (backward: N^T and P^T).
@@ -395,9 +407,10 @@ __host__ __device__ constexpr int head_planes(bool f32, int p) {
   return (f32 ? 4 : 6) + 2 * (f32 ? 2 : p) + 1;
 }
 
-// Brings the records of one chunk after another into LDS, two buffers in turn: fetch() starts
-// the next chunk's loads into registers, which the chunk's products overlap, commit() writes
-// them to the other buffer.  The block's kW waves share the planes; where those do not divide
+// Brings the records of one chunk after another into LDS: fetch() starts the next chunk's loads
+// into registers, which the chunk's products overlap; after the products and a barrier,
+// commit() writes them.  (One buffer and two barriers: a second buffer would save one, but
+// the LDS it takes keeps a second block off the CU, whose waves fill the first one's gaps.)  The block's kW waves share the planes; where those do not divide
 // evenly the last ones are read (from the scratch behind the record) and not written.
 // kState: only what the state's own recurrence takes (K, K^T, N and the gates).
 template <typename T, int KT, int P, int kW, bool kState = false> struct Stage {
@@ -621,6 +634,11 @@ __device__ __forceinline__ void store_state(const f32x16* S, void* base, float f
 // A state under decay is held as S = factor * X with a common factor, so that a chunk's decay
 // costs one multiplication instead of one per value; what is added to S is divided by the
 // factor.  Before the factor falls under 2^-16 (growing decays: exceeds 1) it goes into X.
+//
+// The products before it have to be used up by then (`settled`): where a value that a matrix
+// instruction wrote is first read behind a short conditional block, the compiler counts the wait
+// states along that block alone and not along the jump past it, and the read comes too early.
+__device__ __forceinline__ void settled(f32x16& x) { asm volatile("" : "+v"(x)); }
 template <int KT>
 __device__ __forceinline__ float decay_state(f32x16* X, float factor, float decay) {
   factor *= decay;
@@ -642,7 +660,7 @@ __device__ __forceinline__ float decay_of(double diff) { return exp2_hw(static_c
 int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);
 int launch_scan(const Args& a, int dtype, bool save, hipStream_t st);
 int launch_span(const Args& a, int dtype, hipStream_t st);
-int launch_join(const Args& a, int dtype, bool backward, hipStream_t st);
+int launch_join(const Args& a, bool backward, hipStream_t st);
 int launch_adjoint(const Args& a, int dtype, bool span, hipStream_t st);
 int launch_grads(const Args& a, int dtype, bool aligned, hipStream_t st);
 int launch_gate_grads(const Args& a, hipStream_t st);

@@ -91,8 +91,10 @@ int64_t segment_chunks(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DV, b
   return 2 * len <= chunks ? len : 0;
 }
 
+int key_tiles(int64_t DK) { return DK <= 32 ? 1 : (DK <= 64 ? 2 : 4); }
+
 // The state a training forward keeps: the marks, the end states, t and o in fp32, and the
-// segments' matrices M, which the backward's join takes transposed.
+// segments' transposed matrices.
 struct Saved {
   int64_t marks, ends, rows, spans, bytes;
 };
@@ -105,7 +107,8 @@ Saved saved_layout(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DK, int64
   s.rows = static_cast<int64_t>(ss2d::host_align256(size_t(T) * H * DV * 4));
   const int64_t len = segment_chunks(L, S, T, H, DV, packed);
   s.spans = len ? static_cast<int64_t>(ss2d::host_align256(
-                      size_t(slot_count(L, S, T, packed, len * ss2d::delta::kC)) * H * DK * DK * 4))
+                      size_t(slot_count(L, S, T, packed, len * ss2d::delta::kC)) * H *
+                      ss2d::delta::matrix_bytes(key_tiles(DK))))
                 : 0;
   s.bytes = s.marks + s.ends + 2 * s.rows + s.spans;
   return s;
@@ -116,7 +119,7 @@ void set_saved(Args* a, void* saved, const Saved& s) {
   a->ends = reinterpret_cast<float*>(at + s.marks);
   a->ts = reinterpret_cast<float*>(at + s.marks + s.ends);
   a->os = reinterpret_cast<float*>(at + s.marks + s.ends + s.rows);
-  a->span_m = reinterpret_cast<float*>(at + s.marks + s.ends + 2 * s.rows);
+  a->span_t = at + s.marks + s.ends + 2 * s.rows;
 }
 
 int check_pointers(const Span* ins, int n_in, const Span* outs, int n_out) {
@@ -136,10 +139,9 @@ bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 struct Scratch {
   size_t keys, heads, z, starts, m, bytes;
 };
-// kept: the segments' matrices M are not in scratch but in what the training forward keeps.
-Scratch scratch_layout(const Args& a, int dtype, bool kept) {
+Scratch scratch_layout(const Args& a, int dtype) {
   using namespace ss2d::delta;
-  const int kt = a.DK <= 32 ? 1 : (a.DK <= 64 ? 2 : 4);
+  const int kt = key_tiles(a.DK);
   const bool f32 = dtype == SS2D_F32;
   Scratch s{};
   s.keys = 0;
@@ -149,7 +151,7 @@ Scratch scratch_layout(const Args& a, int dtype, bool kept) {
   const size_t segments = size_t(a.seg_slots) * a.H * a.DK * 4;
   s.starts = s.z + ss2d::host_align256(segments * a.DV);
   s.m = s.starts + ss2d::host_align256(segments * a.DV);
-  s.bytes = s.m + (kept ? 0 : ss2d::host_align256(segments * a.DK));
+  s.bytes = s.m + size_t(a.seg_slots) * a.H * matrix_bytes(kt);
   return s;
 }
 
@@ -223,14 +225,14 @@ void set_scratch(Args* a, char* ws, const Scratch& w) {
   a->heads = ws + w.heads;
   a->span_z = reinterpret_cast<float*>(ws + w.z);
   a->starts = reinterpret_cast<float*>(ws + w.starts);
-  a->span_m = reinterpret_cast<float*>(ws + w.m);
+  a->span_m = ws + w.m;
 }
 
 int run_forward(const Args& a, int dtype, bool save, hipStream_t st) {
   const bool al = aligned_keys(a, dtype == SS2D_F32 ? 4 : 2);
   int err = a.slots > 0 ? ss2d::delta::launch_prep(a, dtype, al, false, st) : 0;
   if (!err && a.seglen) err = ss2d::delta::launch_span(a, dtype, st);
-  if (!err && a.seglen) err = ss2d::delta::launch_join(a, dtype, false, st);
+  if (!err && a.seglen) err = ss2d::delta::launch_join(a, false, st);
   return err ? err : ss2d::delta::launch_scan(a, dtype, save, st);
 }
 
@@ -285,7 +287,7 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
 
   a.p_planes = saved ? 3 : 2;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const Scratch w = scratch_layout(a, dtype, saved != nullptr);
+  const Scratch w = scratch_layout(a, dtype);
   char* ws = nullptr;
   rc = ss2d::host_scratch_alloc(&ws, w.bytes, st);
   if (rc != SS2D_OK) return rc;
@@ -349,7 +351,7 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   // backward's in their place), the states' gradients, the gates' partial sums
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t tiles = (DV + 31) / 32;
-  const Scratch w = scratch_layout(a, dtype, true);
+  const Scratch w = scratch_layout(a, dtype);
   const size_t dmarks = w.bytes,
                pbeta = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * e),
                pgate = pbeta + ss2d::host_align256(size_t(tiles) * T * H * 4),
@@ -378,7 +380,7 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   const bool alv = aligned_rows(dout, rows, DV, e) && aligned_rows(dv, rows, DV, e);
   if (!err && a.slots > 0) err = ss2d::delta::launch_prep(a, dtype, alk, true, st);
   if (!err && a.seglen) err = ss2d::delta::launch_adjoint(a, dtype, true, st);
-  if (!err && a.seglen) err = ss2d::delta::launch_join(a, dtype, true, st);
+  if (!err && a.seglen) err = ss2d::delta::launch_join(a, true, st);
   if (!err) err = ss2d::delta::launch_adjoint(a, dtype, false, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_grads(a, dtype, alv, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_gate_grads(a, st);

@@ -44,9 +44,10 @@ __device__ __forceinline__ int row_of(int lane) { return (lane & 31) >> 1; }
 // kSpan: the span pass over segments (see the forward): only the gradient before a segment,
 // from zero after it, is kept.
 template <typename T, int KT, int kW, bool kSpan>
-__global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
+__global__ __launch_bounds__(64 * kW)
+__attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a) {
   using St = Stage<T, KT, 3, kW>;
-  __shared__ __align__(16) char buffers[2][St::kPlanes * kPlane];
+  __shared__ __align__(16) char buf[St::kPlanes * kPlane];
   __shared__ __align__(16) char spare[kW][kTileBytes];
   Place w;
   if (!place<kW>(&w, a, blockIdx.x, a.DV)) return;
@@ -80,25 +81,18 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
     stage.start(a, first_slot(a, g.n, seq, kC) + g.end - 1, w.hv, w.hk, w.wave, lane, -1);
     stage.fetch();
     if (dalign && g.end * kC <= seq.len) dx.fetch(d0 + (g.end - 1) * kC * line, line * sizeof(T), lane);
-    stage.commit(buffers[(g.end - 1) & 1]);
+    stage.commit(buf);
     __syncthreads();
   }
   for (int64_t c = g.end - 1; c >= g.begin; --c) {
     const int64_t t0 = c * kC, row0 = seq.row + t0, at = t0 * line;
     const int valid = static_cast<int>(min<int64_t>(kC, seq.len - t0));
     const bool whole = valid == kC;
-    const char* buf = buffers[c & 1];
     const f32x16 dout =
         dx.columns(dalign && whole, d0 + at, line * sizeof(T), valid, w.cols, lds, lane);
     if (c > g.begin) {  // what the next chunk wants early
       stage.fetch();
       if (dalign) dx.fetch(d0 + at - kC * int64_t(line), line * sizeof(T), lane);
-    }
-    // what this one wants at its end
-    if (!kSpan && valign && whole) vx.fetch(v0 + t0 * a.sv.l, vline, lane);
-    if (!kSpan && salign && whole) {
-      tx.fetch(a.ts + first + at, line * 4, lane);
-      ox.fetch(a.os + first + at, line * 4, lane);
     }
     const bool ends = !kSpan && ((c & 1) || c == chunks - 1);  // the end of a block of 64 tokens
     const int64_t mark = mark0 + (c >> 1);
@@ -137,6 +131,13 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
         du = mma(pw, Exact<T>{dw.p[0]}, du);
       }
     }
+    // what this one wants at its end
+    if (!kSpan && valign && whole) vx.fetch(v0 + t0 * a.sv.l, vline, lane);
+    if (!kSpan && salign && whole) {
+      tx.fetch(a.ts + first + at, line * 4, lane);
+      ox.fetch(a.os + first + at, line * 4, lane);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     const f32x16 bu = beta * du;
     f32x16 nr = {};
 #pragma unroll
@@ -146,7 +147,9 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
       set_wide(rw, part(bu, s));
       nr = mma(nw, rw, nr);
     }
-    const f32x16 y = du - nr, dv = beta * y;
+    f32x16 y = du - nr, dv = beta * y;
+    settled(y);
+    settled(dv);
     if (ends) {
       store_state<T, KT>(dS, static_cast<T*>(a.dmarks) + (mark * a.H + w.hv) * a.DK * a.DV + 32 * w.tile,
                          factor, a, w, lds);
@@ -205,8 +208,11 @@ __global__ __launch_bounds__(64 * kW) void k_delta_adjoint(Args a) {
         a.pgate[p] = gate_sum;
       }
     }
-    if (c > g.begin) stage.commit(buffers[(c - 1) & 1]);
-    __syncthreads();
+    if (c > g.begin) {
+      __syncthreads();
+      stage.commit(buf);
+      __syncthreads();
+    }
   }
   if (kSpan) store_state<float, KT>(dS, a.span_z + start, factor, a, w, lds);
   else if (a.dh0 && g.index == 0) store_state<float, KT>(dS, a.dh0 + state, factor, a, w, lds);

@@ -19,11 +19,12 @@ namespace {
 // then those of M.
 enum Mode { kForward, kSaving, kSpanning };
 template <typename T, int KT, int kW, Mode kMode>
-__global__ __launch_bounds__(64 * kW) void k_delta_scan(Args a) {
+__global__ __launch_bounds__(64 * kW)
+__attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k_delta_scan(Args a) {
   constexpr bool kSave = kMode == kSaving, kSpan = kMode == kSpanning;
   constexpr int kP = kSave ? 3 : 2;
   using St = Stage<T, KT, kP, kW, kSpan>;
-  __shared__ __align__(16) char buffers[2][St::kPlanes * kPlane];
+  __shared__ __align__(16) char buf[St::kPlanes * kPlane];
   __shared__ __align__(16) char spare[kW][kTileBytes];
   Place w;
   // the span pass counts whole tiles: DV's first, then DK's
@@ -77,13 +78,12 @@ __global__ __launch_bounds__(64 * kW) void k_delta_scan(Args a) {
     stage.start(a, first_slot(a, g.n, seq, kC) + g.begin, w.hv, w.hk, w.wave, lane, 1);
     stage.fetch();
     if (valign && left >= kC) vx.fetch(vat, vline, lane);
-    stage.commit(buffers[g.begin & 1]);
+    stage.commit(buf);
     __syncthreads();
   }
   for (int64_t c = g.begin; c < chunks; ++c) {
     left = static_cast<int>(min<int64_t>(seq.len - c * kC, 1 << 30));
     const bool whole = left >= kC;
-    const char* buf = buffers[c & 1];
     f32x16 v = {};
     if (!matrix) v = vx.columns(valign && whole, vat, vline, left, w.cols, lds, lane);
     vat += kC * a.sv.l;
@@ -123,7 +123,9 @@ __global__ __launch_bounds__(64 * kW) void k_delta_scan(Args a) {
       nr = mma(nw, rw, nr);
     }
     t -= nr;
-    const f32x16 u = beta * t;
+    f32x16 u = beta * t;
+    settled(t);
+    settled(u);
     factor = decay_state<KT>(S, factor, gate[kC - 1]);
     const f32x16 eu = load_gate(gate + kC, half) * (1.0f / factor) * u;
     Wide<T, 3> ew[2];
@@ -156,15 +158,41 @@ __global__ __launch_bounds__(64 * kW) void k_delta_scan(Args a) {
         pat += kC * int64_t(line);
       }
     }
-    if (c + 1 < chunks) stage.commit(buffers[(c + 1) & 1]);
-    __syncthreads();
+    if (c + 1 < chunks) {
+      __syncthreads();
+      stage.commit(buf);
+      __syncthreads();
+    }
   }
   if constexpr (kSpan) {
-    const int64_t sh = g.slot * a.H + w.hv;
-    if (matrix)
-      store_state<float, KT>(S, a.span_m + sh * a.DK * a.DK + 32 * (w.tile - vtiles), factor, a, w, lds,
-                             a.DK);
-    else store_state<float, KT>(S, a.span_z + start, factor, a, w, lds);
+    if (!matrix) {
+      store_state<float, KT>(S, a.span_z + start, factor, a, w, lds);
+    } else {
+      // M in the join's operand order, fp32: this tile's columns are two steps of every 32 rows;
+      // for the backward M^T, whose operands the registers hold as they are
+      const int mt = w.tile - vtiles;
+      const int64_t at = (g.slot * a.H + w.hv) * matrix_bytes(KT);
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const f32x16 x = S[kt] * factor;
+        wave_sync();
+        char* to = lds + 8 * half * tile_pitch<float>() + (lane & 31) * 4;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          *reinterpret_cast<float*>(to + row_base(r) * tile_pitch<float>()) = x[r];
+        wave_sync();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const char* from = lds + swap23(lane & 31) * tile_pitch<float>() + (16 * s + 8 * half) * 4;
+          f32x8 v;
+          __builtin_memcpy(&v, from, 32);
+          put_planes(a.span_m + at + matrix_plane(KT, kt, 2 * mt + s), lane, v);
+          if (a.span_t != nullptr)  // lane l holds column l: row swap23 of the operand
+            put_planes(a.span_t + at + matrix_plane(KT, mt, 2 * kt + s), 32 * half + swap23(lane & 31),
+                       part(x, s));
+        }
+      }
+    }
   } else if (g.last) {
     if (a.ht) store_state<float, KT>(S, a.ht + state, factor, a, w, lds);
     if (kSave) store_state<float, KT>(S, a.ends + state, factor, a, w, lds);
@@ -175,11 +203,12 @@ __global__ __launch_bounds__(64 * kW) void k_delta_scan(Args a) {
 // state before every segment but the first goes to `starts`) or, last to first, dS <- M^T dS + Z
 // (backward; the gradient after every segment but the last).  One wave per 32 of the state's
 // rows: each publishes its rows as operand terms in LDS and multiplies its rows of M with all.
-template <typename T, int KT, bool kBackward>
+template <int KT, bool kBackward>
 __global__ __launch_bounds__(64 * KT) void k_delta_join(Args a) {
+  using T = uint16_t;  // fp32 operands as 3 bfloat16 terms, whatever the data
   __shared__ __align__(16) char operand[2 * KT * wide_planes<T, 3>() * kPlane];
   __shared__ __align__(16) char spare[KT][kTileBytes];
-  const int lane = threadIdx.x & 63, half = lane >> 5, own = swap23(lane & 31);
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char* const lds = spare[wave];
   const int tiles = (a.DV + 31) / 32;
@@ -192,7 +221,7 @@ __global__ __launch_bounds__(64 * KT) void k_delta_join(Args a) {
   const int cols = min(32, a.DV - 32 * tile), rows = a.DK - 32 * wave;  // of this wave's tile
   const uint32_t stride = a.DV * 4u;
   const int64_t at = int64_t(32) * wave * a.DV + 32 * tile;
-  const int64_t size = int64_t(a.DK) * a.DV, matrix = int64_t(a.DK) * a.DK;
+  const int64_t size = int64_t(a.DK) * a.DV;
   const bool whole = aligned16(nullptr, stride, cols) && rows >= 32;
   const int64_t first = kBackward ? count - 1 : 0, step = kBackward ? -1 : 1;
 
@@ -205,20 +234,18 @@ __global__ __launch_bounds__(64 * KT) void k_delta_join(Args a) {
     if (w0) z.fetch(from, stride, lane);
     S = z.columns(w0, from, stride, rows, cols, lds, lane);
   }
-  // this wave's rows of M (or M^T): 8 values per operand step, loaded a segment ahead
+  // this wave's rows of M (or M^T), loaded a segment ahead
   f32x8 m[2 * KT];
-  const int k1 = min(32 * wave + own, a.DK - 1);
-  const bool kin = 32 * wave + own < a.DK;
+  const char* const matrices = kBackward ? a.span_t : a.span_m;
   auto fetch = [&](int64_t i) {
-    const auto p = global(a.span_m) + ((slot0 + i) * a.H + hv) * matrix;
+    const char* p = matrices + ((slot0 + i) * a.H + hv) * matrix_bytes(KT);
 #pragma unroll
-    for (int s = 0; s < 2 * KT; ++s)
+    for (int s = 0; s < 2 * KT; ++s) {
+      const auto q = (Global<const f32x4>)global(p + matrix_plane(KT, wave, s)) + lane;
+      const f32x4 u = q[0], v = q[64];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int k2 = 16 * s + 8 * half + e, c = min(k2, a.DK - 1);
-        const float v = kBackward ? p[c * a.DK + k1] : p[k1 * a.DK + c];
-        m[s][e] = kin && k2 < a.DK ? v : 0.0f;
-      }
+      for (int e = 0; e < 4; ++e) { m[s][e] = u[e]; m[s][4 + e] = v[e]; }
+    }
     if (whole) z.fetch(a.span_z + ((slot0 + i) * a.H + hv) * size + at, stride, lane);
   };
   fetch(first);
@@ -281,20 +308,13 @@ int launch_t(const Args& a, Mode mode, hipStream_t st) {
   return launch_kt<T, 4>(a, mode, st);
 }
 
-template <typename T, int KT>
+template <int KT>
 int join_kt(const Args& a, bool backward, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(a.S * a.H * ((a.DV + 31) / 32))), block(64 * KT);
-  if (backward) hipLaunchKernelGGL((k_delta_join<T, KT, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_delta_join<T, KT, false>), grid, block, 0, st, a);
+  if (backward) hipLaunchKernelGGL((k_delta_join<KT, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_join<KT, false>), grid, block, 0, st, a);
   return static_cast<int>(hipGetLastError());
 }
-template <typename T>
-int join_t(const Args& a, bool backward, hipStream_t st) {
-  if (a.DK <= 32) return join_kt<T, 1>(a, backward, st);
-  if (a.DK <= 64) return join_kt<T, 2>(a, backward, st);
-  return join_kt<T, 4>(a, backward, st);
-}
-
 }  // namespace
 
 int launch_scan(const Args& a, int dtype, bool save, hipStream_t st) {
@@ -304,8 +324,10 @@ int launch_scan(const Args& a, int dtype, bool save, hipStream_t st) {
 int launch_span(const Args& a, int dtype, hipStream_t st) {
   return dtype == 0 ? launch_t<float>(a, kSpanning, st) : launch_t<uint16_t>(a, kSpanning, st);
 }
-int launch_join(const Args& a, int dtype, bool backward, hipStream_t st) {
-  return dtype == 0 ? join_t<float>(a, backward, st) : join_t<uint16_t>(a, backward, st);
+int launch_join(const Args& a, bool backward, hipStream_t st) {
+  if (a.DK <= 32) return join_kt<1>(a, backward, st);
+  if (a.DK <= 64) return join_kt<2>(a, backward, st);
+  return join_kt<4>(a, backward, st);
 }
 
 }  // namespace delta
