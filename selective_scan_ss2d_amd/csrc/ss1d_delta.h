@@ -227,6 +227,13 @@ __device__ __forceinline__ f32x8 part(const f32x16& x, int s) {
 __device__ __forceinline__ f32x16 mma16(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+// Waits until the matrix instructions before it have written their results (at most 18 states):
+// stands where the compiler counts short, see `settled`.
+__device__ __forceinline__ void drained() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 1");
+  __builtin_amdgcn_sched_barrier(0);
+}
 // fp32: one instruction contracts two values, one of each half of the wave.
 __device__ __forceinline__ f32x16 mma8(f32x8 a, f32x8 b, f32x16 c) {
 #pragma unroll

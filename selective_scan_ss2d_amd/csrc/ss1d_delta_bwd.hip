@@ -289,7 +289,7 @@ struct GradBlock {
 
 // One wave's work; kKind: 0 dq, 1 dk's part from the states, 2 dk's part from the block.  The
 // three run the same sequence of barriers.
-template <typename T, int KT, bool kAligned, int kKind>
+template <typename T, int KT, bool kAligned, bool kShared, int kKind>
 __device__ __forceinline__ void grad_wave(const GradBlock& g) {
   using Pn = Panels<T, KT>;
   constexpr int kEach = (Pn::kTasks + kGradWaves - 1) / kGradWaves;
@@ -300,9 +300,10 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
   char* const panels = g.panels;
   const int64_t line = int64_t(a.H) * a.DV;
 
-  f32x16 total[KT];
+  f32x16 total[KT];  // over the key head's value heads
+  if constexpr (kShared)
 #pragma unroll
-  for (int kt = 0; kt < KT; ++kt) total[kt] = f32x16{};
+    for (int kt = 0; kt < KT; ++kt) total[kt] = f32x16{};
 
   // K^T and Q^T of the block's two chunks, for all heads
   u32x4 keys[(Pn::kKeyPlanes + kGradWaves - 1) / kGradWaves];
@@ -316,7 +317,8 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       keys[i] = *(Global<const u32x4>)(global(record) + (p - o * kHalf) * kPlane + 16u * lane);
     }
   }
-  for (int hv = g.hk * a.rep; hv < (g.hk + 1) * a.rep; ++hv) {
+  const int rep = kShared ? a.rep : 1;
+  for (int hv = g.hk * rep; hv < (g.hk + 1) * rep; ++hv) {
     double* const G = g.G + (hv & 1) * kMark;
     const int64_t head_at = g.row0 * line + int64_t(hv) * a.DV;
     const int64_t state_at = (g.mark * a.H + hv) * a.DK * a.DV;
@@ -384,7 +386,7 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       G[lane] = x;
     }
     for (int c0 = 0; c0 < a.DV; c0 += 32) {
-      if (c0 == 0 && hv == g.hk * a.rep)
+      if (c0 == 0 && hv == g.hk * rep)
 #pragma unroll
         for (int i = 0; i * kGradWaves < Pn::kKeyPlanes; ++i) {
           const int p = g.wave + kGradWaves * i;
@@ -431,8 +433,12 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
           other_sense = mma(d, u, other_sense);
         }
       }
+      if constexpr (sizeof(T) == 4) drained();
       __syncthreads();
     }
+    if constexpr (!kShared)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) total[kt] = f32x16{};
     if (32 * mine >= valid) continue;
     const int row = 32 * mine + own;
     const double Gown = G[row], Gend = G[kMark - 1];
@@ -518,8 +524,10 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
   }
 }
 
-template <typename T, int KT, bool kAligned>
-__global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(Args a) {
+template <typename T, int KT, bool kAligned, bool kShared>
+__global__ __launch_bounds__(64 * kGradWaves)
+__attribute__((amdgpu_waves_per_eu(KT * sizeof(T) <= 4 && !kShared ? 3 : 2)))
+void k_delta_grads(Args a) {
   __shared__ __align__(16) char panels[Panels<T, KT>::kPlanes * kPlane];
   __shared__ __align__(16) char spare[4 * kTileBytes];
   __shared__ double G[2 * kMark];
@@ -533,9 +541,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(Args a) {
                     static_cast<int>(blockIdx.x - mark * a.HK),
                     static_cast<int>(min<int64_t>(kMark, seq.len - b * kMark)), mark,
                     seq.row + b * kMark, first_slot(a, n, seq, kC) + 2 * b};
-  if (wave < 2) grad_wave<T, KT, kAligned, 0>(g);
-  else if (wave < 4) grad_wave<T, KT, kAligned, 1>(g);
-  else grad_wave<T, KT, kAligned, 2>(g);
+  if (wave < 2) grad_wave<T, KT, kAligned, kShared, 0>(g);
+  else if (wave < 4) grad_wave<T, KT, kAligned, kShared, 1>(g);
+  else grad_wave<T, KT, kAligned, kShared, 2>(g);
 }
 
 // dbeta and dg of one block of 64 tokens and head: sums over the column tiles, then the sum
@@ -590,7 +598,8 @@ int adjoint_kt(const Args& a, bool span, hipStream_t st) {
 template <typename T, int KT, bool kAligned>
 int grads_kt(const Args& a, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(a.marks_n * a.HK)), block(64 * kGradWaves);
-  hipLaunchKernelGGL((k_delta_grads<T, KT, kAligned>), grid, block, 0, st, a);
+  if (a.rep > 1) hipLaunchKernelGGL((k_delta_grads<T, KT, kAligned, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_delta_grads<T, KT, kAligned, false>), grid, block, 0, st, a);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -42,7 +42,8 @@ __device__ __forceinline__ void transpose_tile(Shared& sh, const Exact<T>* x, Ex
 }
 
 template <typename T, int KT, bool kAligned, bool kBackward>
-__global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4)))
+void k_delta_prep(Args a) {
   __shared__ Shared shared[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Shared& sh = shared[wave];
@@ -134,35 +135,30 @@ __global__ __launch_bounds__(64 * kWaves) void k_delta_prep(Args a) {
     p[r] = (below || other == own) ? qk[r] * m * a.scale : 0.0f;
   }
   // the solve's matrix: forward, row j holds beta_k L_kj over k (N row by row, from
-  // n (I + diag(beta) L) = l); backward, row i holds L_ij beta_j over j
+  // n (I + diag(beta) L) = l); backward, row i holds L_ij beta_j over j, with rows, columns and
+  // the unknowns in reverse order, so that both are solved from the last to the first
+  auto at = [](int i) { return kBackward ? kC - 1 - i : i; };
 #pragma unroll
-  for (int r = 0; r < 16; ++r) sh.m[acc_row(r, half) * kC + own] = low[r] * bown;
+  for (int r = 0; r < 16; ++r) sh.m[at(acc_row(r, half)) * kC + at(own)] = low[r] * bown;
   float x[kC];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float mine = low[8 * s + e], theirs = __shfl_xor(mine, 32);
-      x[16 * s + e] = half == 0 ? mine : theirs;
-      x[16 * s + 8 + e] = half == 0 ? theirs : mine;
+      x[at(16 * s + e)] = half == 0 ? mine : theirs;
+      x[at(16 * s + 8 + e)] = half == 0 ? theirs : mine;
     }
   wave_sync();
-  if (kBackward) {
 #pragma unroll
-    for (int i = 1; i < kC; ++i)
+  for (int j = kC - 2; j >= 0; --j)
 #pragma unroll
-      for (int j = 0; j < i; ++j) x[i] = fmaf(-sh.m[i * kC + j], x[j], x[i]);
-  } else {
-#pragma unroll
-    for (int j = kC - 2; j >= 0; --j)
-#pragma unroll
-      for (int k = kC - 1; k > j; --k) x[j] = fmaf(-sh.m[j * kC + k], x[k], x[j]);
-  }
+    for (int k = kC - 1; k > j; --k) x[j] = fmaf(-sh.m[j * kC + k], x[k], x[j]);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     f32x8 v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = half == 0 ? x[16 * s + e] : x[16 * s + 8 + e];
+    for (int e = 0; e < 8; ++e) v[e] = half == 0 ? x[at(16 * s + e)] : x[at(16 * s + 8 + e)];
     Wide<T, 3> w;
     set_wide(w, v);
     put(head + s * wide_planes<T, 3>() * kPlane, lane, w);
