@@ -219,80 +219,88 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
 }
 
 // dq and dk of one block of 64 tokens and key head, summed over the value heads that share
-// it, by six waves: for the first and second 32 tokens each, one wave for dq, one for dk's
-// part from the states and one for dk's part from the block itself (added to the former at
+// it, by eight waves: for the first and second 32 tokens each, one wave for dq, one for dk's
+// part from the states and two for dk's part from the block itself (added to the former at
 // the end).  The matrices whose columns (DV) are contracted pass through LDS 32 columns at a
 // time, split into bfloat16 terms once for all waves, the next 32 already on their way.  For
 // bfloat16 data one operand of every product has 2 terms (or is exact), so each product
 // carries at most one operand rounding besides the output's own.
 template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows by 16 columns
-  static constexpr int kU = 0;                                     // u = beta t: 64 rows, 2 terms
-  static constexpr int kDo = kU + 4 * wide_planes<T, 2>();         // do: 64 rows
-  static constexpr int kDv = kDo + 4 * exact_planes<T>();          // dv: 64 rows
-  static constexpr int kS = kDv + 4 * exact_planes<T>();           // S: DK rows, 2 terms
-  static constexpr int kDs = kS + 2 * KT * wide_planes<T, 2>();    // dS: DK rows
-  static constexpr int kKeys = kDs + 2 * KT * exact_planes<T>();   // K^T and Q^T of both halves
+  // parts of 32 rows by 16 columns: u = beta t and the state in 2 terms; do, dv and dS exact
+  static constexpr int kWide = 4 + 2 * KT, kNarrow = 8 + 2 * KT;
+  static constexpr int kU = 0;                                   // 64 rows
+  static constexpr int kS = kU + 4 * wide_planes<T, 2>();        // DK rows
+  static constexpr int kDo = kS + 2 * KT * wide_planes<T, 2>();  // 64 rows
+  static constexpr int kDv = kDo + 4 * exact_planes<T>();        // 64 rows
+  static constexpr int kDs = kDv + 4 * exact_planes<T>();        // DK rows
+  static constexpr int kKeys = kDs + 2 * KT * exact_planes<T>(); // K^T and Q^T of both halves
   static constexpr int kKeyPlanes = 8 * KT * exact_planes<T>();
   static constexpr int kPlanes = kKeys + kKeyPlanes;
-  static constexpr int kTasks = 12 + 4 * KT;                       // one per 32 x 16 part
 };
 
-constexpr int kGradWaves = 6;
+constexpr int kGradWaves = 8;
 
-// A 16- or 32-byte piece of a row: 8 values from column c, 0 past the width or where !on.
-template <bool kAligned, typename T>
-__device__ __forceinline__ f32x8 piece(const T* row, int c, int width, bool on) {
-  f32x8 v;
-  const bool any = on && c < width;
-  const auto p = global(row) + (any ? c : 0);
-  if constexpr (kAligned) {
-    constexpr int kN = sizeof(T) / 2;
-    u32x4 u[kN];
+// A 16- or 32-byte piece of a row, as it comes from memory: 8 values from column c on, of
+// which those past the width (and all where !on) are 0 once taken.
+template <typename T> struct Piece {
+  u32x4 u[sizeof(T) / 2];
+
+  template <bool kAligned>
+  __device__ __forceinline__ void load(const T* row, int c, int width) {
+    const auto p = global(row);
+    if constexpr (kAligned) {
+      const auto q = (Global<const u32x4>)(p + (c < width ? c : 0));
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      u[i] = ((Global<const u32x4>)p)[i];
-      if (!any) u[i] = u32x4{0, 0, 0, 0};
-    }
-    T e[8];
-    __builtin_memcpy(e, u, sizeof(e));
+      for (int i = 0; i < int(sizeof(T) / 2); ++i) u[i] = q[i];
+    } else {
+      T e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to_f32(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool ok = on && c + i < width;
-      const T e = p[ok ? i : 0];
-      v[i] = ok ? Elem<T>::to_f32(e) : 0.0f;
+      for (int i = 0; i < 8; ++i) e[i] = p[c + i < width ? c + i : 0];
+      __builtin_memcpy(u, e, sizeof(e));
     }
   }
-  return v;
-}
-
-__device__ __forceinline__ void put_exact(char* at, int lane, f32x8 v, uint16_t) {
-  Wide<uint16_t, 1> w;  // the values are bfloat16 ones: nothing is rounded
-  set_wide(w, v);
-  put(at, lane, w);
-}
-__device__ __forceinline__ void put_exact(char* at, int lane, f32x8 v, float) {
-  put_planes(at, lane, v);
-}
+  template <bool kAligned>
+  __device__ __forceinline__ Piece taken(int c, int width, bool on) const {
+    Piece y = *this;
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int i = 0; i < int(sizeof(T) / 2); ++i)
+        if (!on || c >= width) y.u[i] = u32x4{0, 0, 0, 0};
+    } else {
+      T e[8];
+      __builtin_memcpy(e, u, sizeof(e));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!on || c + i >= width) e[i] = T(0);
+      __builtin_memcpy(y.u, e, sizeof(e));
+    }
+    return y;
+  }
+  __device__ __forceinline__ void put(char* at, int lane) const {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i)
+      reinterpret_cast<u32x4*>(at + i * kPlane)[lane] = u[i];
+  }
+};
 
 // The block's place and the LDS that its waves share.
 struct GradBlock {
   const Args& a;
   char* panels;
-  char* spare;   // a tile of each wave, dk's part from the block in place of the panels
+  char* spare;   // a tile of each storing wave
   double* G;     // prefix sums of the log decays, of two heads in turn
   int lane, half, own, wave, mine, hk, valid;
   int64_t mark, row0, slot;
 };
 
-// One wave's work; kKind: 0 dq, 1 dk's part from the states, 2 dk's part from the block.  The
-// three run the same sequence of barriers.
+// One wave's work; kKind: 0 dq, 1 dk's part from the states, 2 dk's part from later outputs of
+// the block, 3 dk's part from its other values.  All run the same sequence of barriers.
 template <typename T, int KT, bool kAligned, bool kShared, int kKind>
 __device__ __forceinline__ void grad_wave(const GradBlock& g) {
   using Pn = Panels<T, KT>;
-  constexpr int kEach = (Pn::kTasks + kGradWaves - 1) / kGradWaves;
+  constexpr int kNs = (Pn::kNarrow + kGradWaves - 1) / kGradWaves;
+  constexpr int kWs = (Pn::kWide + kGradWaves - 1) / kGradWaves;
+  constexpr int kKs = (Pn::kKeyPlanes + kGradWaves - 1) / kGradWaves;
   constexpr int kW2 = wide_planes<T, 2>() * kPlane, kEx = exact_planes<T>() * kPlane;
   constexpr int64_t operand = KeyRecord<T, KT>::kOperand * kPlane;
   const Args& a = g.a;
@@ -305,79 +313,90 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) total[kt] = f32x16{};
 
-  // K^T and Q^T of the block's two chunks, for all heads
-  u32x4 keys[(Pn::kKeyPlanes + kGradWaves - 1) / kGradWaves];
-  constexpr int kHalf = Pn::kKeyPlanes / 2;
-#pragma unroll
-  for (int i = 0; i * kGradWaves < Pn::kKeyPlanes; ++i) {
-    const int p = g.wave + kGradWaves * i, o = p >= kHalf;
-    if (p < Pn::kKeyPlanes && 32 * o < valid) {
-      const char* record = a.keys + ((g.slot + o) * a.HK + g.hk) *
-                                        (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane) + operand;
-      keys[i] = *(Global<const u32x4>)(global(record) + (p - o * kHalf) * kPlane + 16u * lane);
-    }
-  }
   const int rep = kShared ? a.rep : 1;
   for (int hv = g.hk * rep; hv < (g.hk + 1) * rep; ++hv) {
+    const bool first = hv == g.hk * rep;
     double* const G = g.G + (hv & 1) * kMark;
     const int64_t head_at = g.row0 * line + int64_t(hv) * a.DV;
     const int64_t state_at = (g.mark * a.H + hv) * a.DK * a.DV;
-    // this wave's tasks of the next 32 columns
-    f32x8 x[kEach];
-    float bt[kEach] = {};
+    float gate = 0.0f;
+    if (g.wave == kGradWaves - 1) gate = a.g[(g.row0 + (lane < valid ? lane : 0)) * a.H + hv];
+
+    // This wave's parts of the next 32 columns: two lanes per row.  The loads depend on nothing
+    // but addresses, so that all are on their way at once; what is out of range is left out
+    // when the parts are written to LDS.
+    Piece<T> narrow[kNs];
+    Piece<float> wide[kWs];
+    float beta[kWs];
+    const int prow = lane >> 1, pcol = 8 * (lane & 1), to = 32 * (lane & 1) + swap23(prow);
     auto fetch = [&](int c0) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int task = g.wave + kGradWaves * i;
-        const int c = c0 + 16 * (task & 1) + 8 * half;
-        if (task < 12) {  // rows of tokens
-          const int row = 32 * (task >> 1 & 1) + own;
-          const bool on = row < valid;
-          const int64_t at = head_at + int64_t(on ? row : 0) * line;
-          if (task < 4) {
-            x[i] = piece<kAligned>(a.ts + at, c, a.DV, on);
-            bt[i] = on ? a.beta[(g.row0 + row) * a.H + hv] : 0.0f;
-          }
-          else if (task < 8) x[i] = piece<kAligned>(static_cast<const T*>(a.dout) + at, c, a.DV, on);
-          else x[i] = piece<kAligned>(static_cast<const T*>(a.dv) + at, c, a.DV, on);
-        } else if (task < Pn::kTasks) {  // rows of the states
-          const int k = 32 * ((task - 12) >> 1) % (32 * KT) + own;
-          const bool on = k < a.DK;
-          const int64_t at = state_at + int64_t(on ? k : 0) * a.DV;
-          if (task < 12 + 2 * KT) x[i] = piece<kAligned>(a.marks + at, c, a.DV, on);
-          else x[i] = piece<kAligned>(static_cast<const T*>(a.dmarks) + at, c, a.DV, on);
-        }
+      for (int i = 0; i < kWs; ++i) {
+        const int part = min(g.wave + kGradWaves * i, Pn::kWide - 1);
+        const bool tokens = part < 4;
+        const int row = 32 * ((tokens ? part : part - 4) >> 1) + prow;
+        const int at = row < (tokens ? valid : a.DK) ? row : 0;
+        const float* base = tokens ? a.ts + head_at : a.marks + state_at;
+        wide[i].template load<kAligned>(base + at * (tokens ? line : a.DV), c0 + 16 * (part & 1) + pcol, a.DV);
+        beta[i] = a.beta[(g.row0 + (tokens ? at : 0)) * a.H + hv];
+      }
+#pragma unroll
+      for (int i = 0; i < kNs; ++i) {
+        const int part = min(g.wave + kGradWaves * i, Pn::kNarrow - 1);
+        const bool tokens = part < 8;
+        const int row = 32 * ((tokens ? part & 3 : part - 8) >> 1) + prow;
+        const int at = row < (tokens ? valid : a.DK) ? row : 0;
+        const T* base = static_cast<const T*>(part < 4 ? a.dout : tokens ? a.dv : a.dmarks) +
+                        (tokens ? head_at : state_at);
+        narrow[i].template load<kAligned>(base + at * (tokens ? line : a.DV), c0 + 16 * (part & 1) + pcol, a.DV);
       }
     };
-    auto commit = [&]() {
+    auto commit = [&](int c0) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int task = g.wave + kGradWaves * i;
-        if (task < 4 || (task >= 12 && task < 12 + 2 * KT)) {
-          const int plane = task < 4 ? Pn::kU + task * wide_planes<T, 2>()
-                                     : Pn::kS + (task - 12) * wide_planes<T, 2>();
-          Wide<T, 2> w;
-          set_wide(w, task < 4 ? x[i] * bt[i] : x[i]);
-          put(panels + plane * kPlane, lane, w);
-        } else if (task < Pn::kTasks) {
-          const int plane = task < 12 ? Pn::kDo + (task - 4) * exact_planes<T>()
-                                      : Pn::kDs + (task - 12 - 2 * KT) * exact_planes<T>();
-          put_exact(panels + plane * kPlane, lane, x[i], T(0));
-        }
+      for (int i = 0; i < kWs; ++i) {
+        const int part = g.wave + kGradWaves * i;
+        if (part >= Pn::kWide) break;
+        const bool tokens = part < 4;
+        const int row = 32 * ((tokens ? part : part - 4) >> 1) + prow;
+        const Piece<float> x = wide[i].template taken<kAligned>(c0 + 16 * (part & 1) + pcol, a.DV,
+                                                                row < (tokens ? valid : a.DK));
+        f32x8 v;
+        __builtin_memcpy(&v, x.u, 32);
+        Wide<T, 2> w;
+        set_wide(w, tokens ? v * beta[i] : v);
+        put(panels + (Pn::kU + part * wide_planes<T, 2>()) * kPlane, to, w);
+      }
+#pragma unroll
+      for (int i = 0; i < kNs; ++i) {
+        const int part = g.wave + kGradWaves * i;
+        if (part >= Pn::kNarrow) break;
+        const bool tokens = part < 8;
+        const int row = 32 * ((tokens ? part & 3 : part - 8) >> 1) + prow;
+        narrow[i].template taken<kAligned>(c0 + 16 * (part & 1) + pcol, a.DV,
+                                           row < (tokens ? valid : a.DK))
+            .put(panels + (Pn::kDo + part * exact_planes<T>()) * kPlane, to);
       }
     };
-    // kind 0: x = do S^T, p[o] = u_o . do;  kind 1: x = u dS^T, y = dv S^T;
-    // kind 2: p[o] = do_o . u, l[o] = u_o . dv (earlier tokens o) or dv_o . u (later ones): o runs
-    // over the block's halves in registers' rows, the lanes hold this wave's tokens; own is l
-    // of the other sense within this wave's 32 tokens
-    constexpr int kY = kKind == 0 ? KT : (kKind == 1 ? 2 * KT : 1);
-    f32x16 y[kY], p[2], l[2], other_sense = {};
-#pragma unroll
-    for (int kt = 0; kt < kY; ++kt) y[kt] = f32x16{};
-    p[0] = p[1] = l[0] = l[1] = f32x16{};
     fetch(0);
-    if (g.wave == 5) {  // read after the barriers below
-      double x = lane < valid ? fmaxf(a.g[(g.row0 + lane) * a.H + hv], kMinLog) * kLog2eWide : 0.0;
+    if (first) {  // K^T and Q^T of the block's two chunks, for all heads
+      constexpr int kHalf = Pn::kKeyPlanes / 2;
+      u32x4 keys[kKs];
+#pragma unroll
+      for (int i = 0; i < kKs; ++i) {
+        const int p = min(g.wave + kGradWaves * i, Pn::kKeyPlanes - 1), o = p >= kHalf && 32 < valid;
+        const char* record = a.keys + ((g.slot + o) * a.HK + g.hk) *
+                                          (int64_t(KeyRecord<T, KT>::kPlanes) * kPlane) + operand;
+        keys[i] = *(Global<const u32x4>)(global(record) + p % kHalf * kPlane + 16u * lane);
+      }
+#pragma unroll
+      for (int i = 0; i < kKs; ++i) {
+        const int p = g.wave + kGradWaves * i;
+        if (p < Pn::kKeyPlanes)
+          *reinterpret_cast<u32x4*>(panels + (Pn::kKeys + p) * kPlane + 16 * lane) = keys[i];
+      }
+    }
+    if (g.wave == kGradWaves - 1) {  // read after the barriers below
+      double x = lane < valid ? fmaxf(gate, kMinLog) * kLog2eWide : 0.0;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const double up = __shfl_up(x, d);
@@ -385,55 +404,63 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       }
       G[lane] = x;
     }
-    for (int c0 = 0; c0 < a.DV; c0 += 32) {
-      if (c0 == 0 && hv == g.hk * rep)
+    // kind 0: y = do S^T, p[o] = u_o . do;  kind 1: y = u dS^T and dv S^T;  kind 2: p[o] = do_o . u;
+    // kind 3: p[o] = u_o . dv (earlier tokens o) or dv_o . u (later ones): o runs over the block's
+    // halves in registers' rows, the lanes hold this wave's tokens; q is p of the other sense
+    // within this wave's 32 tokens
+    constexpr int kY = kKind == 0 ? KT : (kKind == 1 ? 2 * KT : 1);
+    f32x16 y[kY], p[2], q = {};
 #pragma unroll
-        for (int i = 0; i * kGradWaves < Pn::kKeyPlanes; ++i) {
-          const int p = g.wave + kGradWaves * i;
-          if (p < Pn::kKeyPlanes)
-            *reinterpret_cast<u32x4*>(panels + (Pn::kKeys + p) * kPlane + 16 * lane) = keys[i];
-        }
-      commit();
+    for (int kt = 0; kt < kY; ++kt) y[kt] = f32x16{};
+    p[0] = p[1] = f32x16{};
+    for (int c0 = 0; c0 < a.DV; c0 += 32) {
+      commit(c0);
       __syncthreads();
       if (c0 + 32 < a.DV) fetch(c0 + 32);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        auto wide = [&](int first, int o) {
+        auto wide_of = [&](int first_plane, int o) {
           Wide<T, 2> w;
-          get(w, panels + first * kPlane + (2 * o + s) * kW2, lane);
+          get(w, panels + first_plane * kPlane + (2 * o + s) * kW2, lane);
           return w;
         };
-        auto exact = [&](int first, int o) {
+        auto exact_of = [&](int first_plane, int o) {
           Exact<T> w;
-          get(w, panels + first * kPlane + (2 * o + s) * kEx, lane);
+          get(w, panels + first_plane * kPlane + (2 * o + s) * kEx, lane);
           return w;
         };
         if constexpr (kKind == 0) {
-          const Exact<T> d = exact(Pn::kDo, mine);
+          const Exact<T> d = exact_of(Pn::kDo, mine);
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt) y[kt] = mma(d, wide(Pn::kS, kt), y[kt]);
-          p[0] = mma(wide(Pn::kU, 0), d, p[0]);
-          if (mine == 1) p[1] = mma(wide(Pn::kU, 1), d, p[1]);
+          for (int kt = 0; kt < KT; ++kt) y[kt] = mma(d, wide_of(Pn::kS, kt), y[kt]);
+          p[0] = mma(wide_of(Pn::kU, 0), d, p[0]);
+          if (mine == 1) p[1] = mma(wide_of(Pn::kU, 1), d, p[1]);
         } else if constexpr (kKind == 1) {
-          const Exact<T> d = exact(Pn::kDv, mine);
-          const Wide<T, 2> u = wide(Pn::kU, mine);
+          const Exact<T> d = exact_of(Pn::kDv, mine);
+          const Wide<T, 2> u = wide_of(Pn::kU, mine);
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
-            y[KT + kt] = mma(d, wide(Pn::kS, kt), y[KT + kt]);
-            y[kt] = mma(u, exact(Pn::kDs, kt), y[kt]);
+            y[KT + kt] = mma(d, wide_of(Pn::kS, kt), y[KT + kt]);
+            y[kt] = mma(u, exact_of(Pn::kDs, kt), y[kt]);
           }
+        } else if constexpr (kKind == 2) {
+          const Wide<T, 2> u = wide_of(Pn::kU, mine);
+          p[0] = mma(exact_of(Pn::kDo, 0), u, p[0]);  // not used by the later 32 tokens
+          p[1] = mma(exact_of(Pn::kDo, 1), u, p[1]);
         } else {
-          const Wide<T, 2> u = wide(Pn::kU, mine);
-          const Exact<T> d = exact(Pn::kDv, mine);
-          if (mine == 0) p[0] = mma(exact(Pn::kDo, 0), u, p[0]);
-          p[1] = mma(exact(Pn::kDo, 1), u, p[1]);
-          l[0] = mma(mine == 0 ? u : wide(Pn::kU, 0), d, l[0]);
-          if (mine == 0) l[1] = mma(exact(Pn::kDv, 1), u, l[1]);
-          else l[1] = mma(u, d, l[1]);
-          other_sense = mma(d, u, other_sense);
+          const Wide<T, 2> u = wide_of(Pn::kU, mine);
+          const Exact<T> d = exact_of(Pn::kDv, mine);
+          if (mine == 0) {
+            p[0] = mma(u, d, p[0]);
+            p[1] = mma(exact_of(Pn::kDv, 1), u, p[1]);
+          } else {
+            p[0] = mma(wide_of(Pn::kU, 0), d, p[0]);
+            p[1] = mma(u, d, p[1]);
+          }
+          q = mma(d, u, q);
         }
       }
-      if constexpr (sizeof(T) == 4) drained();
+      drained();
       __syncthreads();
     }
     if constexpr (!kShared)
@@ -455,46 +482,33 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       }
     }
     if constexpr (kKind != 1) {
+      constexpr int kHalf = Pn::kKeyPlanes / 2;
 #pragma unroll
       for (int other = 0; other < 2; ++other) {
         if (32 * other >= valid) break;
-        if (kKind == 0 && other > mine) break;
+        if ((kKind == 0 && other > mine) || (kKind == 2 && other < mine)) continue;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int o = 32 * other + acc_row(r, half);
           const double at = G[o];
           const float f = decay_of(o <= row ? Gown - at : at - Gown);
-          if constexpr (kKind == 0) {
-            p[other][r] = o <= row ? a.scale * f * p[other][r] : 0.0f;
-          } else {
-            p[other][r] = o >= row ? a.scale * f * p[other][r] : 0.0f;
-            const float v = other == mine && o > row ? other_sense[r] : l[other][r];
-            l[other][r] = o == row ? 0.0f : -f * v;
-          }
+          if constexpr (kKind == 0) p[other][r] = o <= row ? a.scale * f * p[other][r] : 0.0f;
+          else if constexpr (kKind == 2) p[other][r] = o >= row ? a.scale * f * p[other][r] : 0.0f;
+          else p[other][r] = o == row ? 0.0f : -f * (other == mine && o > row ? q[r] : p[other][r]);
         }
-        const char* record = panels + (Pn::kKeys + other * kHalf) * kPlane;
+        const char* keys = panels + (Pn::kKeys + other * kHalf) * kPlane + (kKind == 2 ? operand : 0);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          Wide<T, 2> pw, lw;
+          Wide<T, 2> pw;
           set_wide(pw, part(p[other], s));
-          if constexpr (kKind == 2) set_wide(lw, part(l[other], s));
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
-            const char* f = record + (2 * kt + s) * kEx;
-            Exact<T> kx;
-            get(kx, f, lane);
-            if constexpr (kKind == 0) {
-              total[kt] = mma(pw, kx, total[kt]);
-            } else {
-              total[kt] = mma(lw, kx, total[kt]);
-              if (other >= mine) {
-                Exact<T> qx;
-                get(qx, f + operand, lane);
-                total[kt] = mma(pw, qx, total[kt]);
-              }
-            }
+            Exact<T> x;
+            get(x, keys + (2 * kt + s) * kEx, lane);
+            total[kt] = mma(pw, x, total[kt]);
           }
         }
+        drained();
       }
     }
   }
@@ -507,7 +521,13 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) sums[(16 * kt + r) * 64] = total[kt][r];
   __syncthreads();
-  if (kKind == 2 || 32 * mine >= valid) return;
+  if constexpr (kKind == 3)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sums[(16 * kt + r) * 64] += total[kt][r];
+  __syncthreads();
+  if (kKind > 1 || 32 * mine >= valid) return;
   T* out = static_cast<T*>(kKind ? a.dk : a.dq) +
            ((g.row0 + 32 * mine) * a.HK + g.hk) * int64_t(a.DK);
   const uint32_t stride = a.HK * a.DK * sizeof(T);
@@ -526,7 +546,7 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
 
 template <typename T, int KT, bool kAligned, bool kShared>
 __global__ __launch_bounds__(64 * kGradWaves)
-__attribute__((amdgpu_waves_per_eu(KT * sizeof(T) <= 4 && !kShared ? 3 : 2)))
+__attribute__((amdgpu_waves_per_eu(KT * sizeof(T) <= 4 && !kShared ? 4 : 2)))
 void k_delta_grads(Args a) {
   __shared__ __align__(16) char panels[Panels<T, KT>::kPlanes * kPlane];
   __shared__ __align__(16) char spare[4 * kTileBytes];
@@ -543,7 +563,8 @@ void k_delta_grads(Args a) {
                     seq.row + b * kMark, first_slot(a, n, seq, kC) + 2 * b};
   if (wave < 2) grad_wave<T, KT, kAligned, kShared, 0>(g);
   else if (wave < 4) grad_wave<T, KT, kAligned, kShared, 1>(g);
-  else grad_wave<T, KT, kAligned, kShared, 2>(g);
+  else if (wave < 6) grad_wave<T, KT, kAligned, kShared, 2>(g);
+  else grad_wave<T, KT, kAligned, kShared, 3>(g);
 }
 
 // dbeta and dg of one block of 64 tokens and head: sums over the column tiles, then the sum
