@@ -35,6 +35,7 @@ struct Args {
 
 constexpr int kMaxD = 8192;        // channels last: 8 values a thread, 1024 threads
 constexpr int kMaxDFirst = 1024;   // channels first
+constexpr int64_t kMaxLFirst = int64_t(1) << 24;  // 64 planes of fp32 within 32-bit offsets
 constexpr int kSums = 4;           // dw_post, db_post, dw_pre, db_pre
 
 // SiLU and its derivative sigmoid(z) (1 + z (1 - sigmoid(z))).

@@ -11,28 +11,32 @@ namespace {
 
 constexpr int kV = 8;  // values per thread
 
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4* p, float* x);
-template <>
-__device__ __forceinline__ void unpack<uint16_t>(const uint4* p, float* x) {
-  const uint4 u = *p;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A thread's 8 values of a row as they come from memory.  Loading and converting are apart, so
+// that all loads of a row are on their way before the first is waited for.
+template <typename T, bool kVec> struct Raw { T v[kV]; };
+template <typename T> struct Raw<T, true> { uint4 u[sizeof(T) / 2]; };
+
+__device__ __forceinline__ void unpack(const Raw<uint16_t, true>& r, float* x) {
+  const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-template <>
-__device__ __forceinline__ void unpack<float>(const uint4* p, float* x) {
+__device__ __forceinline__ void unpack(const Raw<float, true>& r, float* x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 u = reinterpret_cast<const float4*>(p)[i];
-    x[4 * i] = u.x;
-    x[4 * i + 1] = u.y;
-    x[4 * i + 2] = u.z;
-    x[4 * i + 3] = u.w;
+    x[4 * i] = __uint_as_float(r.u[i].x);
+    x[4 * i + 1] = __uint_as_float(r.u[i].y);
+    x[4 * i + 2] = __uint_as_float(r.u[i].z);
+    x[4 * i + 3] = __uint_as_float(r.u[i].w);
   }
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T, false>& r, float* x) {
+#pragma unroll
+  for (int i = 0; i < kV; ++i) x[i] = Elem<T>::to_f32(r.v[i]);
 }
 
 // A thread's columns of a row: kVec, 8 adjacent ones (rows on 16 bytes, D a multiple of 8);
@@ -41,21 +45,30 @@ template <int kLanes, bool kVec>
 struct Row {
   int lane, D;
   __device__ __forceinline__ int col(int i) const { return kVec ? lane * kV + i : lane + kLanes * i; }
-  __device__ __forceinline__ bool in(int i) const { return col(i) < D; }
+  __device__ __forceinline__ bool in(int i) const { return col(kVec ? 0 : i) < D; }
   template <typename T>
-  __device__ __forceinline__ void load(const void* base, int64_t row, float* x) const {
+  __device__ __forceinline__ void fetch(const void* base, int64_t row, Raw<T, kVec>& r) const {
     const T* p = static_cast<const T*>(base) + row * D;
     if constexpr (kVec) {
-      if (in(0)) {
-        unpack<T>(reinterpret_cast<const uint4*>(p + lane * kV), x);
-      } else {
+      const uint4* q = reinterpret_cast<const uint4*>(p + (in(0) ? lane * kV : 0));
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = 0.0f;
-      }
+      for (int i = 0; i < int(sizeof(T) / 2); ++i) r.u[i] = q[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < kV; ++i) x[i] = in(i) ? Elem<T>::load(p + col(i)) : 0.0f;
+      for (int i = 0; i < kV; ++i) r.v[i] = p[in(i) ? col(i) : 0];
     }
+  }
+  template <typename T>
+  __device__ __forceinline__ void take(const Raw<T, kVec>& r, float* x) const {
+    unpack(r, x);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) x[i] = in(i) ? x[i] : 0.0f;
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(const void* base, int64_t row, float* x) const {
+    Raw<T, kVec> r;
+    fetch<T>(base, row, r);
+    take<T>(r, x);
   }
   template <typename T>
   __device__ __forceinline__ void store(void* base, int64_t row, const float* x) const {
@@ -76,47 +89,53 @@ struct Row {
   }
 };
 
-// Sums two values over the kLanes threads of a row.
+// Sums two values over the kLanes threads of a row.  Rows on several waves meet in LDS, in two
+// buffers in turn: one barrier then is enough.
 template <int kLanes>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float2* shared) {
+struct RowSum {
+  static constexpr int kThreads = kLanes > 256 ? kLanes : 256, kW = kLanes > 64 ? kLanes / 64 : 1;
+  float2 (*shared)[kThreads / 64];
+  int turn = 0;
+  __device__ __forceinline__ void operator()(float& a, float& b) {
 #pragma unroll
-  for (int d = 1; d < (kLanes < 64 ? kLanes : 64); d *= 2) {
-    a += __shfl_xor(a, d);
-    b += __shfl_xor(b, d);
-  }
-  if constexpr (kLanes > 64) {
-    constexpr int kW = kLanes / 64;
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();  // the last use of `shared` is over
-    if ((threadIdx.x & 63) == 0) shared[wave] = make_float2(a, b);
-    __syncthreads();
-    const int first = wave / kW * kW;
-    a = b = 0.0f;
+    for (int d = 1; d < (kLanes < 64 ? kLanes : 64); d *= 2) {
+      a += __shfl_xor(a, d);
+      b += __shfl_xor(b, d);
+    }
+    if constexpr (kLanes > 64) {
+      const int wave = threadIdx.x >> 6;
+      float2* buffer = shared[turn];
+      turn ^= 1;
+      if ((threadIdx.x & 63) == 0) buffer[wave] = make_float2(a, b);
+      __syncthreads();
+      const int first = wave / kW * kW;
+      a = b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      a += shared[first + i].x;
-      b += shared[first + i].y;
+      for (int i = 0; i < kW; ++i) {
+        a += buffer[first + i].x;
+        b += buffer[first + i].y;
+      }
     }
   }
-}
+};
 
 // x becomes (x - mean) r (layer) or x r; returns r.  Two passes over the registers.
 template <int kLanes, bool kVec>
 __device__ __forceinline__ float unit(const Row<kLanes, kVec>& row, float* x, bool layer, float eps,
-                                      float2* shared) {
+                                      RowSum<kLanes>& sum) {
   const float inv = 1.0f / static_cast<float>(row.D);
   float s = 0.0f, q = 0.0f, none = 0.0f;
   if (layer) {
 #pragma unroll
     for (int i = 0; i < kV; ++i) s += x[i];
-    row_sum2<kLanes>(s, none, shared);
+    sum(s, none);
     s *= inv;
 #pragma unroll
     for (int i = 0; i < kV; ++i) x[i] = row.in(i) ? x[i] - s : 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < kV; ++i) q = fmaf(x[i], x[i], q);
-  row_sum2<kLanes>(q, none, shared);
+  sum(q, none);
   const float r = 1.0f / sqrtf(fmaf(q, inv, eps));
 #pragma unroll
   for (int i = 0; i < kV; ++i) x[i] *= r;
@@ -126,7 +145,7 @@ __device__ __forceinline__ float unit(const Row<kLanes, kVec>& row, float* x, bo
 // From the gradient d at unit(x)'s output to the one at its input.
 template <int kLanes, bool kVec>
 __device__ __forceinline__ void through(const Row<kLanes, kVec>& row, float* d, const float* x,
-                                        float r, bool layer, float2* shared) {
+                                        float r, bool layer, RowSum<kLanes>& sum) {
   const float inv = 1.0f / static_cast<float>(row.D);
   float sx = 0.0f, s = 0.0f;
 #pragma unroll
@@ -134,7 +153,7 @@ __device__ __forceinline__ void through(const Row<kLanes, kVec>& row, float* d, 
     sx = fmaf(d[i], x[i], sx);
     s += d[i];
   }
-  row_sum2<kLanes>(sx, s, shared);
+  sum(sx, s);
   sx *= inv;
   s = layer ? s * inv : 0.0f;
 #pragma unroll
@@ -144,7 +163,8 @@ __device__ __forceinline__ void through(const Row<kLanes, kVec>& row, float* d, 
 template <typename T, typename Y, int kLanes, bool kVec>
 __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm(Args a) {
   constexpr int kThreads = kLanes > 256 ? kLanes : 256, kRows = kThreads / kLanes;
-  __shared__ float2 shared[kThreads / 64];
+  __shared__ float2 shared[2][kThreads / 64];
+  RowSum<kLanes> sum{shared};
   const Row<kLanes, kVec> row{static_cast<int>(threadIdx.x % kLanes), a.D};
   float wp[kV], bp[kV], wn[kV], bn[kV], sc[kV];
   if (a.w_post) row.template load<float>(a.w_post, 0, wp);
@@ -157,14 +177,18 @@ __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm(Args a) {
     const int64_t at = base + threadIdx.x / kLanes;
     const bool on = at < rows;            // rows past the end run along for the barriers
     const int64_t i0 = on ? at : rows - 1;
-    float x[kV];
-    row.template load<T>(a.h, i0, x);
-    float z[kV], res[kV];
-    if (a.z) row.template load<T>(a.z, i0, z);
-    if (a.residual) row.template load<Y>(a.residual, i0, res);
+    Raw<T, kVec> rh, rz;
+    Raw<Y, kVec> rr;
+    row.template fetch<T>(a.h, i0, rh);
+    if (a.z) row.template fetch<T>(a.z, i0, rz);
+    if (a.residual) row.template fetch<Y>(a.residual, i0, rr);
     if (a.scale && a.G > 1) row.template load<float>(a.scale, i0 / a.group, sc);
+    float x[kV], z[kV], res[kV];
+    row.template take<T>(rh, x);
+    if (a.z) row.template take<T>(rz, z);
+    if (a.residual) row.template take<Y>(rr, res);
     if (a.w_post) {
-      unit(row, x, a.layer, a.eps, shared);
+      unit(row, x, a.layer, a.eps, sum);
 #pragma unroll
       for (int i = 0; i < kV; ++i) x[i] = a.b_post ? fmaf(x[i], wp[i], bp[i]) : x[i] * wp[i];
     }
@@ -184,7 +208,7 @@ __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm(Args a) {
     if (a.w_pre) {
 #pragma unroll
       for (int i = 0; i < kV; ++i) x[i] = row.in(i) ? x[i] : 0.0f;
-      unit(row, x, a.layer, a.eps, shared);
+      unit(row, x, a.layer, a.eps, sum);
 #pragma unroll
       for (int i = 0; i < kV; ++i) x[i] = a.b_pre ? fmaf(x[i], wn[i], bn[i]) : x[i] * wn[i];
       if (on) row.template store<T>(a.n, at, x);
@@ -220,7 +244,8 @@ __device__ __forceinline__ void write_sums(const Row<kLanes, kVec>& row, const f
 template <typename T, typename Y, int kLanes, bool kVec>
 __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm_bwd(Args a) {
   constexpr int kThreads = kLanes > 256 ? kLanes : 256, kRows = kThreads / kLanes;
-  __shared__ float2 shared[kThreads / 64];
+  __shared__ float2 shared[2][kThreads / 64];
+  RowSum<kLanes> sum{shared};
   __shared__ float buffer[kRows == 1 ? 1 : kThreads * kV];
   const Row<kLanes, kVec> row{static_cast<int>(threadIdx.x % kLanes), a.D};
   float wp[kV], bp[kV], wn[kV], sc[kV];
@@ -235,23 +260,35 @@ __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm_bwd(Args a
     float dsc[kV] = {};
     if (a.scale) row.template load<float>(a.scale, g, sc);
     const int64_t end = (g + 1) * a.group;
-    for (int64_t base = g * a.group + part * kRows; base < end; base += a.blocks_per_group * kRows) {
-      const int64_t at = base + threadIdx.x / kLanes;
-      const bool on = at < end;
-      const int64_t i0 = on ? at : end - 1;
-      float d[kV], x[kV], e[kV], hx[kV], z[kV];
-      row.template load<T>(a.h, i0, hx);
-      if (a.z) row.template load<T>(a.z, i0, z);
-      if (a.dy) {
-        row.template load<Y>(a.dy, i0, d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) d[i] = 0.0f;
-      }
+    const int64_t step = a.blocks_per_group * kRows;
+    Raw<T, kVec> rh, rz, rn;
+    Raw<Y, kVec> rd, ry;
+    auto fetch = [&](int64_t base) {
+      const int64_t i = min(base + threadIdx.x / kLanes, end - 1);
+      row.template fetch<T>(a.h, i, rh);
+      if (a.z) row.template fetch<T>(a.z, i, rz);
+      if (a.dy) row.template fetch<Y>(a.dy, i, rd);
       if (a.w_pre) {
-        row.template load<Y>(a.y, i0, x);
-        row.template load<T>(a.dn, i0, e);
-        const float r = unit(row, x, a.layer, a.eps, shared);
+        row.template fetch<Y>(a.y, i, ry);
+        row.template fetch<T>(a.dn, i, rn);
+      }
+    };
+    int64_t base = g * a.group + part * kRows;
+    if (base < end) fetch(base);
+    for (; base < end; base += step) {
+      const int64_t at = base + threadIdx.x / kLanes;
+      const bool on = at < end;  // rows past the end run along for the barriers
+      float d[kV] = {}, x[kV], e[kV], hx[kV], z[kV];
+      row.template take<T>(rh, hx);
+      if (a.z) row.template take<T>(rz, z);
+      if (a.dy) row.template take<Y>(rd, d);
+      if (a.w_pre) {
+        row.template take<Y>(ry, x);
+        row.template take<T>(rn, e);
+      }
+      fetch(base + step);  // the next row's values come in meanwhile
+      if (a.w_pre) {
+        const float r = unit(row, x, a.layer, a.eps, sum);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
           if (on) {
@@ -260,13 +297,13 @@ __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm_bwd(Args a
           }
           e[i] *= wn[i];
         }
-        through(row, e, x, r, a.layer, shared);
+        through(row, e, x, r, a.layer, sum);
 #pragma unroll
         for (int i = 0; i < kV; ++i) d[i] += e[i];
       }
       if (a.dres && on) row.template store<Y>(a.dres, at, d);
       float r = 0.0f;
-      if (a.w_post) r = unit(row, hx, a.layer, a.eps, shared);
+      if (a.w_post) r = unit(row, hx, a.layer, a.eps, sum);
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
         float p = hx[i];
@@ -297,7 +334,7 @@ __global__ __launch_bounds__(kLanes > 256 ? kLanes : 256) void k_norm_bwd(Args a
       if (a.w_post) {
 #pragma unroll
         for (int i = 0; i < kV; ++i) d[i] = row.in(i) ? d[i] : 0.0f;
-        through(row, d, hx, r, a.layer, shared);
+        through(row, d, hx, r, a.layer, sum);
       }
       if (on) row.template store<T>(a.dh, at, d);
     }
@@ -328,15 +365,15 @@ __global__ __launch_bounds__(1024) void k_norm_sums(Sums s) {
   if (!out) return;
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
   const float* p = s.parts + blockIdx.y * s.first + c;
-  float x[4] = {};
+  float x[8] = {};
   if (c < s.D) {
     int64_t b = g;
-    for (; b + 48 < s.count; b += 64)
+    for (; b + 112 < s.count; b += 128)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] += p[(b + 16 * i) * s.stride];
+      for (int i = 0; i < 8; ++i) x[i] += p[(b + 16 * i) * s.stride];
     for (; b < s.count; b += 16) x[0] += p[b * s.stride];
   }
-  buffer[g][threadIdx.x & 63] = (x[0] + x[1]) + (x[2] + x[3]);
+  buffer[g][threadIdx.x & 63] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
   __syncthreads();
   if (g == 0 && c < s.D) {
     float t = 0.0f;
@@ -346,20 +383,27 @@ __global__ __launch_bounds__(1024) void k_norm_sums(Sums s) {
   }
 }
 
-// The same per group of res_scale: out[g][c] = sum over its parts.
+// The same per group of res_scale: out[g][c] = sum over its parts, 64 columns and 4 groups of
+// parts per block.
 __global__ __launch_bounds__(256) void k_norm_group_sums(const float* parts, float* out, int64_t count,
                                                          int D) {
-  const int c = blockIdx.y * 256 + threadIdx.x;
-  if (c >= D) return;
+  __shared__ float buffer[4][64];
+  const int c = blockIdx.y * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
   const int64_t g = blockIdx.x;
   const float* p = parts + g * count * D + c;
-  float x[4] = {};
-  int64_t b = 0;
-  for (; b + 3 < count; b += 4)
+  float x[8] = {};
+  if (c < D) {
+    int64_t b = w;
+    for (; b + 28 < count; b += 32)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] += p[(b + i) * D];
-  for (; b < count; ++b) x[0] += p[b * D];
-  out[g * D + c] = (x[0] + x[1]) + (x[2] + x[3]);
+      for (int i = 0; i < 8; ++i) x[i] += p[(b + 4 * i) * D];
+    for (; b < count; b += 4) x[0] += p[b * D];
+  }
+  buffer[w][threadIdx.x & 63] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  __syncthreads();
+  if (w == 0 && c < D)
+    out[g * D + c] = (buffer[0][threadIdx.x] + buffer[1][threadIdx.x]) +
+                     (buffer[2][threadIdx.x] + buffer[3][threadIdx.x]);
 }
 
 int lanes_of(int D) {
@@ -406,7 +450,7 @@ int64_t rows_of_block(int D) {
 
 int launch_norm_first(const Args& a, int dtype, int ytype, bool vec, bool bwd, int64_t blocks,
                       hipStream_t st);
-int64_t tiles_first(const Args& a);
+int64_t tiles_first(const Args& a, bool bwd);
 
 int launch_norm(const Args& a, int dtype, int ytype, bool first, bool vec, hipStream_t st) {
   if (first) return launch_norm_first(a, dtype, ytype, vec, false, 0, st);
@@ -421,7 +465,7 @@ int launch_norm(const Args& a, int dtype, int ytype, bool first, bool vec, hipSt
 int64_t plan_norm_bwd(Args* a, bool first) {
   constexpr int64_t kBlocks = 1024;
   const int64_t per = first ? 1 : rows_of_block(a->D);
-  const int64_t rounds = first ? tiles_first(*a) : (a->group + per - 1) / per;  // of a group
+  const int64_t rounds = first ? tiles_first(*a, true) : (a->group + per - 1) / per;  // of a group
   a->groups_per_block = 1;
   a->blocks_per_group = std::max<int64_t>(1, std::min((rounds + 3) / 4, kBlocks / a->G));
   if (a->G > kBlocks) a->groups_per_block = (a->G + kBlocks - 1) / kBlocks;
@@ -442,7 +486,7 @@ int launch_norm_sums(const Args& a, int64_t blocks, hipStream_t st) {
     hipLaunchKernelGGL(k_norm_sums, dim3((a.D + 63) / 64, kSums), dim3(1024), 0, st, s);
   }
   if (a.dscale && a.scale_parts != a.dscale)
-    hipLaunchKernelGGL(k_norm_group_sums, dim3(static_cast<unsigned>(a.G), (a.D + 255) / 256), dim3(256),
+    hipLaunchKernelGGL(k_norm_group_sums, dim3(static_cast<unsigned>(a.G), (a.D + 63) / 64), dim3(256),
                        0, st, a.scale_parts, a.dscale, a.blocks_per_group, a.D);
   return static_cast<int>(hipGetLastError());
 }

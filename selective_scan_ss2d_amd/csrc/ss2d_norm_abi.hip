@@ -23,6 +23,7 @@ int check(int64_t B, int64_t L, int64_t D, int64_t G, int first, float eps, int 
   if (B < 0 || L < 0 || D < 1 || G < 0) return SS2D_ERR_SHAPE;
   if (!std::isfinite(eps) || eps < 0.0f) return SS2D_ERR_UNSUPPORTED;
   if (D > (first ? ss2d::norm::kMaxDFirst : ss2d::norm::kMaxD)) return SS2D_ERR_UNSUPPORTED;
+  if (first && L > ss2d::norm::kMaxLFirst) return SS2D_ERR_UNSUPPORTED;
   int64_t rows, n;
   if (!ss2d::host_mul_ok(B, L, &rows) || !ss2d::host_mul_ok(rows, D, &n) ||
       n > ss2d::kHostMaxElems / 64)

@@ -13,49 +13,68 @@ namespace {
 constexpr int kP = 16;  // lanes across the positions
 
 template <typename T, int kN> struct alignas(sizeof(T) * kN) Pack { T v[kN]; };
+// A pack as one word of memory.
+template <int kBytes> struct WordOf { using type = uint32_t __attribute__((ext_vector_type(kBytes / 4))); };
+template <> struct WordOf<2> { using type = uint16_t; };
+template <> struct WordOf<4> { using type = uint32_t; };
+template <typename T, int kN> using Word = typename WordOf<sizeof(T) * kN>::type;
+
+template <typename T>
+using Global = __attribute__((address_space(1))) T*;
 
 // A thread's kVec positions of a tile (adjacent with kWide: L a multiple of kVec, planes
-// aligned; else every 16th) and kC channels, every kGroups-th.
+// aligned; else every 16th) and kC channels, every kGroups-th.  Addresses are a base that all
+// threads share, per channel, and a 32-bit offset of the thread (kGroups L 4 bytes fit).
 template <int kThreads, int kC, int kVec, bool kWide>
 struct Tile {
   static constexpr int kGroups = kThreads / kP;
   int lane, group, D;
-  int64_t L, pos;  // first position of this thread
+  int64_t L;
+  int pos;  // first position of this thread
   __device__ __forceinline__ int channel(int i) const { return group + kGroups * i; }
-  __device__ __forceinline__ int64_t at(int j) const { return pos + (kWide ? j : kP * j); }
+  __device__ __forceinline__ int at(int j) const { return pos + (kWide ? j : kP * j); }
   __device__ __forceinline__ bool in(int j) const { return at(j) < L; }
   template <typename T>
-  __device__ __forceinline__ void load(const void* base, int64_t image, int i, float* x) const {
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) x[j] = 0.0f;
-    if (channel(i) >= D) return;
-    const T* p = static_cast<const T*>(base) + (image * D + channel(i)) * L;
+  __device__ __forceinline__ Global<T> base_of(T* base, int64_t image, int i) const {
+    return (Global<T>)(base + (image * D + (kGroups * i < D ? kGroups * i : 0)) * L);
+  }
+  __device__ __forceinline__ uint32_t offset(int p) const {
+    return static_cast<uint32_t>(group) * static_cast<uint32_t>(L) + static_cast<uint32_t>(p);
+  }
+  // Loading and converting are apart and free of conditions, so that all loads of a tile are on
+  // their way before the first is waited for; what is out of range reads the base's first value.
+  template <typename T>
+  __device__ __forceinline__ void fetch(const void* base, int64_t image, int i, Pack<T, kVec>& r) const {
+    const Global<const T> p = base_of(static_cast<const T*>(base), image, i);
+    const bool on = channel(i) < D;
     if constexpr (kWide) {
-      if (in(0)) {
-        const Pack<T, kVec> u = *reinterpret_cast<const Pack<T, kVec>*>(p + pos);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) x[j] = Elem<T>::to_f32(u.v[j]);
-      }
+      const Word<T, kVec> u = *(Global<const Word<T, kVec>>)(p + (on && in(0) ? offset(pos) : 0u));
+      __builtin_memcpy(&r, &u, sizeof(r));
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (in(j)) x[j] = Elem<T>::load(p + at(j));
+      for (int j = 0; j < kVec; ++j) r.v[j] = p[on && in(j) ? offset(at(j)) : 0u];
     }
+  }
+  template <typename T>
+  __device__ __forceinline__ void take(const Pack<T, kVec>& r, int i, float* x) const {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      x[j] = channel(i) < D && in(kWide ? 0 : j) ? Elem<T>::to_f32(r.v[j]) : 0.0f;
   }
   template <typename T>
   __device__ __forceinline__ void store(void* base, int64_t image, int i, const float* x) const {
     if (channel(i) >= D) return;
-    T* p = static_cast<T*>(base) + (image * D + channel(i)) * L;
+    const Global<T> p = base_of(static_cast<T*>(base), image, i);
     if constexpr (kWide) {
       if (!in(0)) return;
       Pack<T, kVec> u;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) u.v[j] = Elem<T>::from_f32(x[j]);
-      *reinterpret_cast<Pack<T, kVec>*>(p + pos) = u;
+      *(Global<Word<T, kVec>>)(p + offset(pos)) = __builtin_bit_cast(Word<T, kVec>, u);
     } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
-        if (in(j)) p[at(j)] = Elem<T>::from_f32(x[j]);
+        if (in(j)) p[offset(at(j))] = Elem<T>::from_f32(x[j]);
     }
   }
   __device__ __forceinline__ float channel_value(const float* w, int i) const {
@@ -148,7 +167,8 @@ __device__ __forceinline__ void through(const Tile<kThreads, kC, kVec, kWide>& t
 }
 
 template <typename T, typename Y, int kThreads, int kC, int kVec, bool kWide>
-__global__ __launch_bounds__(kThreads) void k_norm_first(Args a) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kC * kVec <= 24 ? 4 : 2)))
+void k_norm_first(Args a) {
   __shared__ float2 shared[kThreads / 64 * kVec * kP];
   Tile<kThreads, kC, kVec, kWide> t;
   t.lane = threadIdx.x & (kP - 1);
@@ -158,10 +178,20 @@ __global__ __launch_bounds__(kThreads) void k_norm_first(Args a) {
   const int64_t per = (a.L + kP * kVec - 1) / (kP * kVec), tiles = a.B * per;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t image = tile / per;
-    t.pos = (tile - image * per) * (kP * kVec) + t.lane * (kWide ? kVec : 1);
+    t.pos = static_cast<int>(tile - image * per) * (kP * kVec) + t.lane * (kWide ? kVec : 1);
     float x[kC][kVec], r[kVec];
+    Pack<T, kVec> rh[kC], rz[kC];
+    Pack<Y, kVec> rr[kC];
 #pragma unroll
-    for (int i = 0; i < kC; ++i) t.template load<T>(a.h, image, i, x[i]);
+    for (int i = 0; i < kC; ++i) t.template fetch<T>(a.h, image, i, rh[i]);
+    if (a.z)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) t.template fetch<T>(a.z, image, i, rz[i]);
+    if (a.residual)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) t.template fetch<Y>(a.residual, image, i, rr[i]);
+#pragma unroll
+    for (int i = 0; i < kC; ++i) t.template take<T>(rh[i], i, x[i]);
     if (a.w_post) unit(t, x, r, a.layer, a.eps, shared);
     const float* scale = a.scale ? a.scale + image / a.group * a.D : nullptr;
 #pragma unroll
@@ -170,8 +200,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_first(Args a) {
       const float b = a.b_post ? t.channel_value(a.b_post, i) : 0.0f;
       const float s = scale ? t.channel_value(scale, i) : 1.0f;
       float z[kVec], res[kVec];
-      if (a.z) t.template load<T>(a.z, image, i, z);
-      if (a.residual) t.template load<Y>(a.residual, image, i, res);
+      if (a.z) t.template take<T>(rz[i], i, z);
+      if (a.residual) t.template take<Y>(rr[i], i, res);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         float p = a.w_post ? fmaf(x[i][j], w, b) : x[i][j];
@@ -231,14 +261,29 @@ __global__ __launch_bounds__(kThreads) void k_norm_first_bwd(Args a) {
     const float* scale = a.scale ? a.scale + g * a.D : nullptr;
     for (int64_t tile = part; tile < tiles; tile += a.blocks_per_group) {
       const int64_t image = g * a.group + tile / per;
-      t.pos = tile % per * (kP * kVec) + t.lane * (kWide ? kVec : 1);
+      t.pos = static_cast<int>(tile % per) * (kP * kVec) + t.lane * (kWide ? kVec : 1);
       float x[kC][kVec], d[kC][kVec], r[kVec];
+      Pack<T, kVec> rh[kC], rz[kC];
+      Pack<Y, kVec> rd[kC];
       if (a.w_pre) {
+        Pack<Y, kVec> ry[kC];
+        Pack<T, kVec> rn[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) t.template fetch<Y>(a.y, image, i, ry[i]);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) t.template fetch<T>(a.dn, image, i, rn[i]);
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
-          t.template load<Y>(a.y, image, i, x[i]);
-          t.template load<T>(a.dn, image, i, d[i]);
+          t.template take<Y>(ry[i], i, x[i]);
+          t.template take<T>(rn[i], i, d[i]);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) d[i][j] = 0.0f;
+      }
+      if (a.w_pre) {
         unit(t, x, r, a.layer, a.eps, shared);
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
@@ -251,22 +296,26 @@ __global__ __launch_bounds__(kThreads) void k_norm_first_bwd(Args a) {
           }
         }
         through(t, d, x, r, a.layer, shared);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) d[i][j] = 0.0f;
       }
+      // only now, for the registers' sake
+      if (a.dy)
+#pragma unroll
+        for (int i = 0; i < kC; ++i) t.template fetch<Y>(a.dy, image, i, rd[i]);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) t.template fetch<T>(a.h, image, i, rh[i]);
+      if (a.z)
+#pragma unroll
+        for (int i = 0; i < kC; ++i) t.template fetch<T>(a.z, image, i, rz[i]);
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
         if (a.dy) {
           float y[kVec];
-          t.template load<Y>(a.dy, image, i, y);
+          t.template take<Y>(rd[i], i, y);
 #pragma unroll
           for (int j = 0; j < kVec; ++j) d[i][j] += y[j];
         }
         if (a.dres) t.template store<Y>(a.dres, image, i, d[i]);
-        t.template load<T>(a.h, image, i, x[i]);
+        t.template take<T>(rh[i], i, x[i]);
       }
       if (a.w_post) unit(t, x, r, a.layer, a.eps, shared);
 #pragma unroll
@@ -275,7 +324,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_first_bwd(Args a) {
         const float b = a.b_post ? t.channel_value(a.b_post, i) : 0.0f;
         const float s = scale ? t.channel_value(scale, i) : 1.0f;
         float z[kVec], dz[kVec];
-        if (a.z) t.template load<T>(a.z, image, i, z);
+        if (a.z) t.template take<T>(rz[i], i, z);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
           const float p = a.w_post ? fmaf(x[i][j], w, b) : x[i][j];
@@ -314,27 +363,41 @@ __global__ __launch_bounds__(kThreads) void k_norm_first_bwd(Args a) {
   if (a.db_pre) write_sums(t, dbn, out + 3 * a.D);
 }
 
-// Positions per tile: 64 up to 256 channels, then 32 and 16, so that a thread holds at most
-// 64 (backward: of three tensors) values and 16 channels.
-int vec_of(int D) { return D <= 256 ? 4 : (D <= 512 ? 2 : 1); }
+// Positions of a thread; tiles are 16 times as wide.  A thread holds at most 32 values of a
+// tensor (backward, with two tensors and the sums of its channels: 16) and 16 channels.
+int vec_of(int D, bool bwd) {
+  if (bwd) return D <= 128 ? 4 : (D <= 256 ? 2 : 1);
+  return D <= 256 ? 4 : (D <= 512 ? 2 : 1);
+}
 
 template <typename T, typename Y, int kThreads, int kC, int kVec, bool kWide>
-void launch(const Args& a, bool bwd, int64_t blocks, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
-  if (bwd)
-    hipLaunchKernelGGL((k_norm_first_bwd<T, Y, kThreads, kC, kVec, kWide>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_norm_first<T, Y, kThreads, kC, kVec, kWide>), grid, block, 0, st, a);
+void forward(const Args& a, int64_t blocks, hipStream_t st) {
+  hipLaunchKernelGGL((k_norm_first<T, Y, kThreads, kC, kVec, kWide>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(kThreads), 0, st, a);
+}
+template <typename T, typename Y, int kThreads, int kC, int kVec, bool kWide>
+void backward(const Args& a, int64_t blocks, hipStream_t st) {
+  hipLaunchKernelGGL((k_norm_first_bwd<T, Y, kThreads, kC, kVec, kWide>),
+                     dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, a);
 }
 
 template <typename T, typename Y, bool kWide>
 int launch_channels(const Args& a, bool bwd, int64_t blocks, hipStream_t st) {
-  if (a.D <= 64) launch<T, Y, 256, 4, 4, kWide>(a, bwd, blocks, st);
-  else if (a.D <= 128) launch<T, Y, 256, 8, 4, kWide>(a, bwd, blocks, st);
-  else if (a.D <= 192) launch<T, Y, 256, 12, 4, kWide>(a, bwd, blocks, st);
-  else if (a.D <= 256) launch<T, Y, 256, 16, 4, kWide>(a, bwd, blocks, st);
-  else if (a.D <= 512) launch<T, Y, 512, 16, 2, kWide>(a, bwd, blocks, st);
-  else launch<T, Y, 1024, 16, 1, kWide>(a, bwd, blocks, st);
+  if (bwd) {
+    if (a.D <= 64) backward<T, Y, 256, 4, 4, kWide>(a, blocks, st);
+    else if (a.D <= 128) backward<T, Y, 512, 4, 4, kWide>(a, blocks, st);
+    else if (a.D <= 192) backward<T, Y, 512, 6, 2, kWide>(a, blocks, st);
+    else if (a.D <= 256) backward<T, Y, 512, 8, 2, kWide>(a, blocks, st);
+    else if (a.D <= 512) backward<T, Y, 1024, 8, 1, kWide>(a, blocks, st);
+    else backward<T, Y, 1024, 16, 1, kWide>(a, blocks, st);
+  } else {
+    if (a.D <= 64) forward<T, Y, 256, 4, 4, kWide>(a, blocks, st);
+    else if (a.D <= 128) forward<T, Y, 512, 4, 4, kWide>(a, blocks, st);
+    else if (a.D <= 192) forward<T, Y, 512, 6, 4, kWide>(a, blocks, st);
+    else if (a.D <= 256) forward<T, Y, 512, 8, 4, kWide>(a, blocks, st);
+    else if (a.D <= 512) forward<T, Y, 1024, 8, 2, kWide>(a, blocks, st);
+    else forward<T, Y, 1024, 16, 1, kWide>(a, blocks, st);
+  }
   return static_cast<int>(hipGetLastError());
 }
 
@@ -347,15 +410,15 @@ int launch_types(const Args& a, int dtype, int ytype, bool bwd, int64_t blocks, 
 
 }  // namespace
 
-int64_t tiles_first(const Args& a) {  // of one group
-  const int64_t width = kP * vec_of(a.D);
+int64_t tiles_first(const Args& a, bool bwd) {  // of one group
+  const int64_t width = kP * vec_of(a.D, bwd);
   return a.group * ((a.L + width - 1) / width);
 }
 
 int launch_norm_first(const Args& a, int dtype, int ytype, bool vec, bool bwd, int64_t blocks,
                       hipStream_t st) {
-  if (!bwd) blocks = std::min<int64_t>(tiles_first(a) * a.G, 256 * 16);
-  const bool wide = vec && a.L % vec_of(a.D) == 0;
+  if (!bwd) blocks = std::min<int64_t>(tiles_first(a, false) * a.G, 256 * 16);
+  const bool wide = vec && a.L % vec_of(a.D, bwd) == 0;
   return wide ? launch_types<true>(a, dtype, ytype, bwd, blocks, st)
               : launch_types<false>(a, dtype, ytype, bwd, blocks, st);
 }
