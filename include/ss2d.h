@@ -470,7 +470,9 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * Arithmetic: S, the chunk's triangular solve and every sum are fp32 for both data types.
  * For bfloat16 data a product's fp32 operand runs on the bf16 matrix cores as the sum of 3
  * bfloat16 terms (24 bits), o's as 2 (17 bits) before its single rounding; fp32 data use the
- * fp32 matrix instructions.
+ * fp32 matrix instructions.  Few or long sequences are cut into segments that run at once: each
+ * gives its end state from a zero start, Z, and its matrix M, and the states between them follow
+ * from S <- M S + Z, on operands of 3 terms for either type.
  *
  * ss1d_delta_forward writes o and, if ht is not NULL, the end states; ht may be h0 itself
  * (in place).  saved (NULL, or ss1d_delta_saved_bytes bytes of device memory, aligned to 256)
@@ -491,8 +493,10 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * sequence, in row order.
  *
  * The shared conventions hold, except that kernel timing does not cover these entry points.
- * Scratch: the chunks' matrices, about 0.5 KB per token and value head (the step has none); the
- * backward's gradients of the states, 1 / 64 of a state per token, and partial sums. */
+ * Scratch (the step has none): per token, the chunks' matrices, about 0.4 KB per value head and
+ * 6 DK (fp32: 12 DK) bytes per key head, DK rounded up to 32, 64 or 128; per segment and head,
+ * M, Z and a state; the backward's gradients of the states, one per 64 tokens and head, and
+ * partial sums. */
 int ss1d_delta_forward(const void *q, const void *k, const void *v, const float *g,
                        const float *beta, const float *h0, const int32_t *cu_seqlens, void *o,
                        float *ht, void *saved, int64_t B, int64_t L, int64_t S, int64_t HK,
@@ -538,7 +542,8 @@ int ss1d_delta_step(const void *q, const void *k, const void *v, const float *g,
  *   h, z, n: dtype; residual, y: ytype, which is dtype or SS2D_F32 (a residual stream kept
  *     in fp32); the vectors fp32: w_*, b_* (D), res_scale (G, D): G runs of B * L / G
  *     successive rows (channels first: of B / G images) each use their own row; G = 0 without.
- * All contiguous.  D <= 8192, channels first D <= 1024 (SS2D_ERR_UNSUPPORTED above).  y may be
+ * All contiguous.  D <= 8192, channels first D <= 1024 and L <= 2^24 (SS2D_ERR_UNSUPPORTED
+ * above).  y may be
  * the residual (in place) and may be NULL if n is given.  Everything is computed in fp32 from
  * the inputs as stored; n from y before its rounding.
  *

@@ -25,6 +25,7 @@ namespace delta {
 constexpr int kC = 32;      // tokens per chunk: one 32 x 32 matrix tile
 constexpr int kMaxDK = 128; // largest key width (the state's rows held by one wave)
 constexpr int kMark = 64;   // tokens between the states a training forward keeps
+constexpr int kGradWaves = 8;   // of a block that forms dq and dk
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

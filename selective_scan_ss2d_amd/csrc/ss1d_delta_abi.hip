@@ -216,7 +216,7 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
   const int64_t units = a->seglen ? a->seg_slots : S;
   if ((a->slots * H / 4 + 1) * 256 > kMaxThreads ||
       std::max(units, S) * H * (tiles + 8) * 64 > kMaxThreads ||
-      a->marks_n * HK * 384 > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
+      a->marks_n * HK * 64 * ss2d::delta::kGradWaves > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
     return SS2D_ERR_SHAPE;
   return SS2D_OK;
 }
@@ -284,7 +284,8 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
   const Span outs[] = {{o, T * H * DV * e}, {ht, state}, {saved, sv.bytes}};
   rc = check_pointers(ins, 6, outs, 3);
   if (rc != SS2D_OK) return rc;
-  // the end states may replace the initial ones (each wave reads its columns first)
+  // the end states may replace the initial ones: each wave reads its columns first, several
+  // segments of a sequence read the join's copy
   const Span first[] = {{h0, state}};
   for (const Span& x : outs)
     if (!(x.p == ht && ht == h0) && check_pointers(first, 1, &x, 1) != SS2D_OK)

@@ -238,8 +238,6 @@ template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows 
   static constexpr int kPlanes = kKeys + kKeyPlanes;
 };
 
-constexpr int kGradWaves = 8;
-
 // A 16- or 32-byte piece of a row, as it comes from memory: 8 values from column c on, of
 // which those past the width (and all where !on) are 0 once taken.
 template <typename T> struct Piece {

@@ -54,7 +54,11 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
       for (int r = 0; r < 16; ++r)
         S[kt][r] = matrix && 32 * kt + acc_row(r, half) == 32 * (w.tile - vtiles) + (lane & 31) ? 1.0f : 0.0f;
   } else {
-    load_state<KT>(S, g.index > 0 ? a.starts + start : (a.h0 ? a.h0 + state : nullptr), a, w, lds);
+    // a sequence of several segments starts from the join's copy of h0: its last segment, another
+    // wave, may write the end state over h0 itself
+    const bool copied = g.index > 0 || !g.last;
+    load_state<KT>(S, a.h0 == nullptr && g.index == 0 ? nullptr : (copied ? a.starts + start : a.h0 + state),
+                   a, w, lds);
   }
   float factor = 1.0f;
 
@@ -200,7 +204,7 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
 }
 
 // Runs the state of 32 columns through its sequence's segments, S <- M S + Z (forward; the
-// state before every segment but the first goes to `starts`) or, last to first, dS <- M^T dS + Z
+// state before every segment goes to `starts`, a zero one before the first does not) or, last to first, dS <- M^T dS + Z
 // (backward; the gradient after every segment but the last).  One wave per 32 of the state's
 // rows: each publishes its rows as operand terms in LDS and multiplies its rows of M with all.
 template <int KT, bool kBackward>
@@ -233,6 +237,8 @@ __global__ __launch_bounds__(64 * KT) void k_delta_join(Args a) {
     const bool w0 = whole && aligned16(from, stride, cols);
     if (w0) z.fetch(from, stride, lane);
     S = z.columns(w0, from, stride, rows, cols, lds, lane);
+    if (!kBackward)
+      store_tile<float>(S, a.starts + (slot0 * a.H + hv) * size + at, stride, whole, rows, cols, lds, lane);
   }
   // this wave's rows of M (or M^T), loaded a segment ahead
   f32x8 m[2 * KT];

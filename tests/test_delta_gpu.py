@@ -164,6 +164,19 @@ def test_segments(shape, chunks, dtype):
             assert torch.equal(p, o) and torch.equal(state, ht)
 
 
+def test_end_states_over_initial_states_of_many_segments():
+    """In place, the last segment's waves write where the first one's start is kept."""
+    t = du.make_inputs(12, 1500, 2, 8, 64, 64, torch.bfloat16, seed=5, h0=12)
+    d = du.to_gpu(t)
+    with du.segments(2):
+        o, ht = run(t, final_state=True)
+        for _ in range(5):
+            state = t["h0"].cuda()
+            p, _ = ss.ss1d_delta_forward(*[d[n] for n in du.NAMES], initial_state=state,
+                                         final_state=state)
+            assert torch.equal(p, o) and torch.equal(state, ht)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_segments_of_packed_sequences(dtype):
     lens = [0, 1, 31, 300, 0, 33, 64, 65, 128, 129, 0]

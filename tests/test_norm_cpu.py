@@ -27,6 +27,7 @@ def backward(lib, p, B=4, L=16, D=64, G=2, first=0, layer=1, eps=1e-6, dtype=1, 
 @pytest.mark.parametrize("change, code", [
     (dict(dtype=2), "UNSUPPORTED"), (dict(dtype=0, ytype=1), "UNSUPPORTED"),
     (dict(D=8193), "UNSUPPORTED"), (dict(D=1025, first=1), "UNSUPPORTED"), (dict(D=0), "SHAPE"),
+    (dict(B=2, L=(1 << 24) + 1, D=4, first=1), "UNSUPPORTED"),
     (dict(B=-1), "SHAPE"), (dict(L=-1), "SHAPE"), (dict(G=-1), "SHAPE"), (dict(G=3), "SHAPE"),
     (dict(G=8, first=1), "SHAPE"), (dict(eps=-1.0), "UNSUPPORTED"),
     (dict(eps=float("nan")), "UNSUPPORTED"), (dict(B=1 << 40, L=1 << 30), "SHAPE")])
