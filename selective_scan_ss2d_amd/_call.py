@@ -17,16 +17,30 @@ def _switched(device, stream):
         yield
 
 
-def scope(device, stream, *inputs):
+def scope(device, stream, *tensors):
     """The device and stream that a call's outputs and scratch belong to: a context only
-    where they are not the current ones already."""
+    where they are not the current ones already.  tensors: the caller's, None among them."""
     if stream is None and device.index == torch.cuda.current_device():
         return contextlib.nullcontext()
-    if stream is not None:  # the inputs' memory is not to be reused before the call has run
-        for t in inputs:
-            if t is not None:
+    if stream is not None:  # their memory is not to be reused before the call has run
+        for t in tensors:
+            if isinstance(t, torch.Tensor):
                 t.record_stream(stream)
     return _switched(device, stream)
+
+
+def handle(device, stream):
+    """The HIP stream that a call runs on (without making a torch.cuda.Stream, 2 us)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
+
+
+def expect(name, t, shape, dtype, device):
+    """Checks a contiguous tensor."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == device and t.is_contiguous()):
+        bnd._expect(name, t, shape, dtype, device)  # says what is wrong
 
 
 def ptr(t):
@@ -36,5 +50,5 @@ def ptr(t):
 def output(name, t, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    bnd._expect(name, t, shape, dtype, device)
+    expect(name, t, shape, dtype, device)
     return t

@@ -9,24 +9,22 @@ import ctypes
 import torch
 
 from . import _binding as bnd
-from ._call import CODES, output as _output, ptr as _ptr, scope as _scope
-
+from ._call import (CODES, expect as _expect, handle as _handle, output as _output, ptr as _ptr,
+                    scope as _scope)
 
 
 def _strided(name, t, shape, dtype, device):
-    """Checks a tensor whose last axis alone has to be contiguous; its outer strides."""
+    """Checks a tensor whose last axis alone has to be contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    st = t.stride()
-    if st[3] != 1 and shape[3] > 1:
+    if t.stride(3) != 1 and shape[3] > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return st[:3]
 
 
 def _inputs(q, k, v, g, beta):
@@ -46,14 +44,14 @@ def _inputs(q, k, v, g, beta):
     H, DV = v.shape[2], v.shape[3]
     if HK < 1 or H % HK:
         raise ValueError(f"v has {H} heads, expected a multiple of q's {HK}")
-    sq = _strided("q", q, (B, L, HK, DK), dtype, dev)
-    sk = _strided("k", k, (B, L, HK, DK), dtype, dev)
-    sv = _strided("v", v, (B, L, H, DV), dtype, dev)
-    bnd._expect("g", g, (B, L, H), torch.float32, dev)
-    bnd._expect("beta", beta, (B, L, H), torch.float32, dev)
+    _strided("q", q, (B, L, HK, DK), dtype, dev)
+    _strided("k", k, (B, L, HK, DK), dtype, dev)
+    _strided("v", v, (B, L, H, DV), dtype, dev)
+    _expect("g", g, (B, L, H), torch.float32, dev)
+    _expect("beta", beta, (B, L, H), torch.float32, dev)
     strides = None
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
-        strides = (ctypes.c_int64 * 9)(*sq, *sk, *sv)
+        strides = (ctypes.c_int64 * 9)(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
     return (B, L, HK, DK, H, DV), code, strides
 
 
@@ -62,7 +60,7 @@ def _sequences(cu_seqlens, B, device):
         return B
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must hold S + 1 offsets")
-    bnd._expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
     if B != 1:
         raise ValueError("packed sequences (cu_seqlens) need a batch of 1")
     return cu_seqlens.shape[0] - 1
@@ -74,8 +72,9 @@ def _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o,
     dev = q.device
     S = _sequences(cu_seqlens, B, dev)
     if initial_state is not None:
-        bnd._expect("initial_state", initial_state, (S, H, DK, DV), torch.float32, dev)
-    with _scope(dev, stream, q, k, v, g, beta, cu_seqlens, initial_state):
+        _expect("initial_state", initial_state, (S, H, DK, DV), torch.float32, dev)
+    given = final_state if isinstance(final_state, torch.Tensor) else None
+    with _scope(dev, stream, q, k, v, g, beta, cu_seqlens, initial_state, o, given):
         o = _output("o", o, (B, L, H, DV), q.dtype, dev)
         ht = saved = None
         if final_state is not False and final_state is not None:
@@ -88,7 +87,7 @@ def _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o,
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
             _ptr(initial_state), _ptr(cu_seqlens), o.data_ptr(), _ptr(ht), _ptr(saved), B, L, S,
             HK, H, DK, DV, strides, DK ** -0.5 if scale is None else scale, code,
-            bnd._stream_handle(dev, stream)))
+            _handle(dev, stream)))
     return o, ht, saved
 
 
@@ -136,13 +135,13 @@ def ss1d_delta_backward(q, k, v, g, beta, do, scale=None, cu_seqlens=None, initi
     (B, L, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
     dev = q.device
     S = _sequences(cu_seqlens, B, dev)
-    bnd._expect("do", do, (B, L, H, DV), q.dtype, dev)
+    _expect("do", do, (B, L, H, DV), q.dtype, dev)
     for name, t in (("initial_state", initial_state), ("dstate", dstate)):
         if t is not None:
-            bnd._expect(name, t, (S, H, DK, DV), torch.float32, dev)
+            _expect(name, t, (S, H, DK, DV), torch.float32, dev)
     if saved is not None:
         size = lib.ss1d_delta_saved_bytes(B, L, S, H, DK, DV, cu_seqlens is not None)
-        bnd._expect("saved", saved, (max(0, size),), torch.uint8, dev)
+        _expect("saved", saved, (max(0, size),), torch.uint8, dev)
     with _scope(dev, stream, q, k, v, g, beta, do, cu_seqlens, initial_state, dstate, saved):
         make = torch.empty if cu_seqlens is None else torch.zeros
         d = {n: make(t.shape, dtype=t.dtype, device=dev)
@@ -154,7 +153,7 @@ def ss1d_delta_backward(q, k, v, g, beta, do, scale=None, cu_seqlens=None, initi
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(saved), do.data_ptr(), _ptr(dstate),
             d["q"].data_ptr(), d["k"].data_ptr(), d["v"].data_ptr(), d["g"].data_ptr(),
             d["beta"].data_ptr(), _ptr(d.get("initial_state")), B, L, S, HK, H, DK, DV, strides,
-            DK ** -0.5 if scale is None else scale, code, bnd._stream_handle(dev, stream)))
+            DK ** -0.5 if scale is None else scale, code, _handle(dev, stream)))
     return d
 
 
@@ -173,15 +172,15 @@ def ss1d_delta_step(q, k, v, g, beta, state, slots=None, scale=None, o=None, str
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be (S, H, DK, DV)")
     S = state.shape[0]
-    bnd._expect("state", state, (S, H, DK, DV), torch.float32, dev)
+    _expect("state", state, (S, H, DK, DV), torch.float32, dev)
     if slots is not None:
-        bnd._expect("slots", slots, (B,), torch.int32, dev)
+        _expect("slots", slots, (B,), torch.int32, dev)
     elif S != B:
         raise ValueError(f"state holds {S} sequences, expected {B} without slots")
-    with _scope(dev, stream, q, k, v, g, beta, state, slots):
+    with _scope(dev, stream, q, k, v, g, beta, state, slots, o):
         o = _output("o", o, (B, T, H, DV), q.dtype, dev)
         bnd._check(lib.ss1d_delta_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
             state.data_ptr(), _ptr(slots), o.data_ptr(), B, T, S, HK, H, DK, DV, strides,
-            DK ** -0.5 if scale is None else scale, code, bnd._stream_handle(dev, stream)))
+            DK ** -0.5 if scale is None else scale, code, _handle(dev, stream)))
     return o

@@ -7,7 +7,7 @@ from __future__ import annotations
 import torch
 
 from . import _binding as bnd
-from ._call import CODES, output, ptr, scope
+from ._call import CODES, expect, handle, output, ptr, scope
 
 
 def _shape(h, channels_first):
@@ -33,7 +33,7 @@ def _shape(h, channels_first):
 def _vectors(D, dev, rows, res_scale, **vectors):
     for name, w in vectors.items():
         if w is not None:
-            bnd._expect(name, w, (D,), torch.float32, dev)
+            expect(name, w, (D,), torch.float32, dev)
     for norm in ("post", "pre"):
         if vectors.get("b_" + norm) is not None and vectors["w_" + norm] is None:
             raise ValueError(f"b_{norm} needs w_{norm}")
@@ -42,7 +42,7 @@ def _vectors(D, dev, rows, res_scale, **vectors):
     G = res_scale.shape[0] if res_scale.dim() == 2 else 1
     if res_scale.dim() == 1:
         res_scale = res_scale[None]
-    bnd._expect("res_scale", res_scale, (G, D), torch.float32, dev)
+    expect("res_scale", res_scale, (G, D), torch.float32, dev)
     if G < 1 or rows % G:
         raise ValueError(f"res_scale has {G} rows, expected a divisor of {rows}")
     return G
@@ -69,17 +69,17 @@ def ss2d_norm_forward(h, residual=None, w_post=None, b_post=None, z=None, res_sc
     G = _vectors(D, dev, B if channels_first else B * L, res_scale, w_post=w_post, b_post=b_post,
                  w_pre=w_pre, b_pre=b_pre)
     if z is not None:
-        bnd._expect("z", z, h.shape, h.dtype, dev)
+        expect("z", z, h.shape, h.dtype, dev)
     ytype = h.dtype
     if residual is not None:
         if residual.dtype not in (h.dtype, torch.float32):
             raise TypeError(f"residual has dtype {residual.dtype}, expected {h.dtype} or float32")
         ytype = residual.dtype
-        bnd._expect("residual", residual, h.shape, ytype, dev)
+        expect("residual", residual, h.shape, ytype, dev)
     alone = w_post is None and z is None and residual is None and res_scale is None
     if alone and w_pre is None:
         raise ValueError("nothing to compute: give w_post, z, residual, res_scale or w_pre")
-    with scope(dev, stream, h, z, residual, res_scale, w_post, b_post, w_pre, b_pre):
+    with scope(dev, stream, h, z, residual, res_scale, w_post, b_post, w_pre, b_pre, y):
         if alone and y is None:
             kept = None
         else:
@@ -88,7 +88,7 @@ def ss2d_norm_forward(h, residual=None, w_post=None, b_post=None, z=None, res_sc
         bnd._check(lib.ss2d_norm_forward(
             h.data_ptr(), ptr(z), ptr(residual), ptr(res_scale), ptr(w_post), ptr(b_post),
             ptr(w_pre), ptr(b_pre), ptr(kept), ptr(n), B, L, D, G, 1 if channels_first else 0,
-            1 if layer else 0, eps, code, CODES[ytype], bnd._stream_handle(dev, stream)))
+            1 if layer else 0, eps, code, CODES[ytype], handle(dev, stream)))
     return (h if kept is None else y), n
 
 
@@ -119,7 +119,7 @@ def ss2d_norm_backward(h, y=None, dy=None, dn=None, residual=True, w_post=None, 
     for name, t, dtype in (("z", z, h.dtype), ("dn", dn, h.dtype), ("y", y, ytype),
                            ("dy", dy, ytype)):
         if t is not None:
-            bnd._expect(name, t, h.shape, dtype, dev)
+            expect(name, t, h.shape, dtype, dev)
     with scope(dev, stream, h, y, dy, dn, z, res_scale, w_post, b_post, w_pre):
         d = {"h": torch.empty_like(h)}
         if residual:
@@ -134,5 +134,5 @@ def ss2d_norm_backward(h, y=None, dy=None, dn=None, residual=True, w_post=None, 
                                                    ("z", "residual", "res_scale", "w_post",
                                                     "b_post", "w_pre", "b_pre")],
             B, L, D, G, 1 if channels_first else 0, 1 if layer else 0, eps, code, CODES[ytype],
-            bnd._stream_handle(dev, stream)))
+            handle(dev, stream)))
     return d
