@@ -1,7 +1,9 @@
 // The block norm with channels first, (B, D, L): a block takes a tile of adjacent positions
 // and all channels, 16 lanes across the positions and the other threads across the channels;
 // sums over the channels run in registers, across a wave and through LDS.  Every tensor is
-// read once and written once.  Bound by HBM.
+// read once and written once.  Bound by HBM.  64 maps of 192 x 56 x 56, bfloat16 with an fp32
+// residual stream: 131 us, of a floor of 92; blocks of 512 threads at 128 registers, two per CU
+// (one, at 134 registers: 184 us; 256 threads with 12 channels each: 163).
 #include <algorithm>
 
 #include "ss2d_norm.h"
