@@ -4,8 +4,9 @@
 // 8 values per thread are one 16-byte load of bfloat16, and the narrowest rows still fill a wave
 // with 8 of them.  602112 rows of 64 with gate, bfloat16: 38 us in the kernel (6.0 TB/s, part of
 // it from the last-level cache).  The backward holds the sums of its rows' four vectors in
-// registers and loads the next row while it computes: 25216 rows of 768: 124 us, of a floor of
-// 62; with the loads one behind the other and two barriers per sum it took 180.
+// registers and loads the next row while it computes: 25216 rows of 768: 103 us, of a floor of
+// 62; with LDS permutes for the sums 124, the loads one behind the other and two barriers per sum
+// as well 180.
 #include <algorithm>
 
 #include "ss2d_norm.h"
@@ -102,11 +103,8 @@ struct RowSum {
   float2 (*shared)[kThreads / 64];
   int turn = 0;
   __device__ __forceinline__ void operator()(float& a, float& b) {
-#pragma unroll
-    for (int d = 1; d < (kLanes < 64 ? kLanes : 64); d *= 2) {
-      a += __shfl_xor(a, d);
-      b += __shfl_xor(b, d);
-    }
+    a = lane_sum<(kLanes < 64 ? kLanes : 64)>(a);
+    b = lane_sum<(kLanes < 64 ? kLanes : 64)>(b);
     if constexpr (kLanes > 64) {
       const int wave = threadIdx.x >> 6;
       float2* buffer = shared[turn];
@@ -388,27 +386,29 @@ __global__ __launch_bounds__(1024) void k_norm_sums(Sums s) {
   }
 }
 
-// The same per group of res_scale: out[g][c] = sum over its parts, 64 columns and 4 groups of
-// parts per block.
-__global__ __launch_bounds__(256) void k_norm_group_sums(const float* parts, float* out, int64_t count,
-                                                         int D) {
-  __shared__ float buffer[4][64];
-  const int c = blockIdx.y * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+// The same per group of res_scale: out[g][c] = sum over its parts, 64 columns and a group of
+// parts per wave of a block.
+__global__ __launch_bounds__(1024) void k_norm_group_sums(const float* parts, float* out, int64_t count,
+                                                          int D) {
+  __shared__ float buffer[16][64];
+  const int c = blockIdx.y * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int64_t g = blockIdx.x;
   const float* p = parts + g * count * D + c;
   float x[8] = {};
   if (c < D) {
     int64_t b = w;
-    for (; b + 28 < count; b += 32)
+    for (; b + 7 * waves < count; b += 8 * waves)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] += p[(b + 4 * i) * D];
-    for (; b < count; b += 4) x[0] += p[b * D];
+      for (int i = 0; i < 8; ++i) x[i] += p[(b + i * waves) * D];
+    for (; b < count; b += waves) x[0] += p[b * D];
   }
   buffer[w][threadIdx.x & 63] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
   __syncthreads();
-  if (w == 0 && c < D)
-    out[g * D + c] = (buffer[0][threadIdx.x] + buffer[1][threadIdx.x]) +
-                     (buffer[2][threadIdx.x] + buffer[3][threadIdx.x]);
+  if (w == 0 && c < D) {
+    float t = 0.0f;
+    for (int i = 0; i < waves; ++i) t += buffer[i][threadIdx.x];
+    out[g * D + c] = t;
+  }
 }
 
 int lanes_of(int D) {
@@ -491,8 +491,9 @@ int launch_norm_sums(const Args& a, int64_t blocks, hipStream_t st) {
     hipLaunchKernelGGL(k_norm_sums, dim3((a.D + 63) / 64, kSums), dim3(1024), 0, st, s);
   }
   if (a.dscale && a.scale_parts != a.dscale)
-    hipLaunchKernelGGL(k_norm_group_sums, dim3(static_cast<unsigned>(a.G), (a.D + 63) / 64), dim3(256),
-                       0, st, a.scale_parts, a.dscale, a.blocks_per_group, a.D);
+    hipLaunchKernelGGL(k_norm_group_sums, dim3(static_cast<unsigned>(a.G), (a.D + 63) / 64),
+                       dim3(a.blocks_per_group >= 64 ? 1024 : 256), 0, st, a.scale_parts, a.dscale,
+                       a.blocks_per_group, a.D);
   return static_cast<int>(hipGetLastError());
 }
 
