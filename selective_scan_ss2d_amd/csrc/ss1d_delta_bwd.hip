@@ -17,6 +17,8 @@
 // registers (256 and up to 256 accumulation registers, one wave per SIMD; held to two waves per
 // SIMD it spills 120 of them and takes 486 us instead of 313 in segments of 20 chunks).  64 x
 // 3136 tokens of 3 heads of 64 in bfloat16: 530 us uncut, dq and dk 229 us.
+#include <type_traits>
+
 #include "ss1d_delta.h"
 
 namespace ss2d {
@@ -25,13 +27,30 @@ namespace {
 
 // Sums each register over the 32 lanes of a half: lane l of the half gets the sum of
 // register row_of(l) (each twice).  Halving the registers at every exchange costs 16
-// exchanges for 16 sums.
+// exchanges for 16 sums.  The first one, of rows of 16 lanes, is the swap instruction itself;
+// the others are DPP moves (rotation by 8; mirror of 8 and of 4, together lane ^ 4; lane ^ 2).
+template <int kXor> __device__ __forceinline__ float from_lane(float v) {
+  auto dpp = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  if constexpr (kXor == 8) return dpp(v, std::integral_constant<int, 0x128>{});
+  else if constexpr (kXor == 4)
+    return dpp(dpp(v, std::integral_constant<int, 0x141>{}), std::integral_constant<int, 0x1B>{});
+  else if constexpr (kXor == 2) return dpp(v, std::integral_constant<int, 0x4E>{});
+  else return dpp(v, std::integral_constant<int, 0xB1>{});
+}
 template <int kN> __device__ __forceinline__ void halve(float* x, int lane) {
-  const bool up = lane & (2 * kN);
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    const float keep = up ? x[kN + i] : x[i], send = up ? x[i] : x[kN + i];
-    x[i] = keep + __shfl_xor(send, 2 * kN);
+    if constexpr (kN == 8) {
+      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[i]), __float_as_uint(x[kN + i]),
+                                                      false, false);
+      x[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    } else {
+      const bool up = lane & (2 * kN);
+      const float keep = up ? x[kN + i] : x[i], send = up ? x[i] : x[kN + i];
+      x[i] = keep + from_lane<2 * kN>(send);
+    }
   }
   if constexpr (kN > 1) halve<kN / 2>(x, lane);
 }
@@ -40,7 +59,7 @@ __device__ __forceinline__ float sum_columns(const f32x16& v, int lane) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = v[i];
   halve<8>(x, lane);
-  return x[0] + __shfl_xor(x[0], 1);
+  return x[0] + from_lane<1>(x[0]);
 }
 __device__ __forceinline__ int row_of(int lane) { return (lane & 31) >> 1; }
 
