@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "ss2d_device.h"
+#include "ss2d_lanes.h"
 
 namespace ss2d {
 namespace delta {

@@ -17,8 +17,6 @@
 // registers (256 and up to 256 accumulation registers, one wave per SIMD; held to two waves per
 // SIMD it spills 120 of them and takes 486 us instead of 313 in segments of 20 chunks).  64 x
 // 3136 tokens of 3 heads of 64 in bfloat16: 530 us uncut, dq and dk 229 us.
-#include <type_traits>
-
 #include "ss1d_delta.h"
 
 namespace ss2d {
@@ -27,25 +25,13 @@ namespace {
 
 // Sums each register over the 32 lanes of a half: lane l of the half gets the sum of
 // register row_of(l) (each twice).  Halving the registers at every exchange costs 16
-// exchanges for 16 sums.  The first one, of rows of 16 lanes, is the swap instruction itself;
-// the others are DPP moves (rotation by 8; mirror of 8 and of 4, together lane ^ 4; lane ^ 2).
-template <int kXor> __device__ __forceinline__ float from_lane(float v) {
-  auto dpp = [](float x, auto ctrl) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
-  };
-  if constexpr (kXor == 8) return dpp(v, std::integral_constant<int, 0x128>{});
-  else if constexpr (kXor == 4)
-    return dpp(dpp(v, std::integral_constant<int, 0x141>{}), std::integral_constant<int, 0x1B>{});
-  else if constexpr (kXor == 2) return dpp(v, std::integral_constant<int, 0x4E>{});
-  else return dpp(v, std::integral_constant<int, 0xB1>{});
-}
+// exchanges for 16 sums; the first 8, between rows of 16 lanes, are the swap itself.
 template <int kN> __device__ __forceinline__ void halve(float* x, int lane) {
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
     if constexpr (kN == 8) {
-      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x[i]), __float_as_uint(x[kN + i]),
-                                                      false, false);
-      x[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+      swap_rows(x[i], x[kN + i]);
+      x[i] += x[kN + i];
     } else {
       const bool up = lane & (2 * kN);
       const float keep = up ? x[kN + i] : x[i], send = up ? x[i] : x[kN + i];
@@ -187,8 +173,7 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
           for (int r = 0; r < 16; ++r) dot = fmaf(dS[kt][r], S[r], dot);
         }
       dot = w.in ? dot * factor : 0.0f;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d);
+      dot = lane_sum<64>(dot);
       if (lane == 0 && w.store_cols > 0) a.pdots[(mark * a.H + w.hv) * tiles + w.tile] = dot;
     }
     factor = decay_state<KT>(dS, factor, gate[kC - 1]);

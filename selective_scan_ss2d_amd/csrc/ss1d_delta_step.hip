@@ -80,14 +80,11 @@ __global__ __launch_bounds__(64) void k_delta_step(StepArgs a) {
           sq[j] = fmaf(S[i][j], q[i], sq[j]);
         }
       }
+      qk = lane_sum<64, kLanes>(qk);
 #pragma unroll
-      for (int d = kLanes; d < 64; d *= 2) {
-        qk += __shfl_xor(qk, d);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          sk[j] += __shfl_xor(sk[j], d);
-          sq[j] += __shfl_xor(sq[j], d);
-        }
+      for (int j = 0; j < kVec; ++j) {
+        sk[j] = lane_sum<64, kLanes>(sk[j]);
+        sq[j] = lane_sum<64, kLanes>(sq[j]);
       }
       float o[kVec];
 #pragma unroll

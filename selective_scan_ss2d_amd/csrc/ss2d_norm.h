@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "ss2d_device.h"
+#include "ss2d_lanes.h"
 
 namespace ss2d {
 namespace norm {
@@ -46,34 +47,6 @@ __device__ __forceinline__ float sigmoid_f32(float v) {
 __device__ __forceinline__ float gate_value(float z, float sg) { return sg == 0.0f ? -0.0f : z * sg; }
 __device__ __forceinline__ float gate_slope(float z, float sg) {
   return sg == 0.0f ? 0.0f : (sg == 1.0f ? 1.0f : sg * fmaf(z, 1.0f - sg, 1.0f));
-}
-
-// v plus the v of lane ^ kXor.  Within 16 lanes by DPP: the mirrors do for 4 and 8 where the lanes
-// of each group of 4 (8) hold the same already, as they do in a sum that starts at 1; 16 and 32
-// by the half-row and half-wave swaps.  No LDS permutes: six sums of a 768-wide row's backward
-// were 72 of them, one after the other.
-template <int kXor>
-__device__ __forceinline__ float add_across(float v) {
-  if constexpr (kXor < 16) {
-    constexpr int kCtrl = kXor == 1 ? 0xB1 : kXor == 2 ? 0x4E : kXor == 4 ? 0x141 : 0x140;
-    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, true));
-  } else {
-    const uint32_t u = __float_as_uint(v);
-    const auto r = kXor == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
-                              : __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-}
-// Sum over kLanes adjacent lanes (a power of two), in all of them.
-template <int kLanes>
-__device__ __forceinline__ float lane_sum(float v) {
-  if constexpr (kLanes > 1) v = add_across<1>(v);
-  if constexpr (kLanes > 2) v = add_across<2>(v);
-  if constexpr (kLanes > 4) v = add_across<4>(v);
-  if constexpr (kLanes > 8) v = add_across<8>(v);
-  if constexpr (kLanes > 16) v = add_across<16>(v);
-  if constexpr (kLanes > 32) v = add_across<32>(v);
-  return v;
 }
 
 // kind: bit 0, fp32 y (with bfloat16 data); types (data, y).
