@@ -457,8 +457,8 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * strides: 9 element strides, (batch, token, head) of q, of k and of v, whose last axis is
  * contiguous (views into one fused projection, for instance; none negative); NULL for
  * contiguous tensors.  Every other tensor is contiguous.  H is a multiple of HK,
- * 1 <= DK <= 128 (SS2D_ERR_UNSUPPORTED above), any DV >= 1; v's token stride and H * DV are at
- * most 2^24 (SS2D_ERR_UNSUPPORTED above).
+ * 1 <= DK <= 128 (SS2D_ERR_UNSUPPORTED above), any DV >= 1; v's token stride, H * DV and HK * DK
+ * are at most 2^24 (SS2D_ERR_UNSUPPORTED above).
  *
  * cu_seqlens: NULL, and the B rows are S = B sequences of L tokens; or S + 1 ascending
  * offsets (device memory) into the L tokens of B = 1: sequence n holds tokens

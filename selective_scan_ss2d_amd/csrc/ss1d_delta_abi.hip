@@ -200,7 +200,7 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
                 vb = strided_bytes(B, L, H, DV, a->sv, e);
   if (qb < 0 || kb < 0 || vb < 0) return SS2D_ERR_SHAPE;
   // the kernels keep a chunk's row offsets in 32 bits
-  if (a->sv.l > kMaxLine || H * DV > kMaxLine) return SS2D_ERR_UNSUPPORTED;
+  if (a->sv.l > kMaxLine || H * DV > kMaxLine || HK * DK > kMaxLine) return SS2D_ERR_UNSUPPORTED;
   for (const void* p : {q, k, v})
     if (misaligned(p, static_cast<uintptr_t>(e))) return SS2D_ERR_ALIGN;
   for (const void* p : {static_cast<const void*>(g), static_cast<const void*>(beta),

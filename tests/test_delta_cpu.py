@@ -49,6 +49,12 @@ def test_sizes_refused(lib, change, code):
     assert step(lib, ptrs(8), **change) == want
 
 
+def test_rows_past_32_bit_offsets_refused(lib):
+    wide = dict(L=1, HK=1 << 18, H=1 << 18, DK=128, DV=1)
+    assert forward(lib, args(), **wide) == bnd.SS2D_ERR_UNSUPPORTED
+    assert forward(lib, args(), L=1, HK=1, H=1 << 18, DK=8, DV=128) == bnd.SS2D_ERR_UNSUPPORTED
+
+
 def test_sequences_refused(lib):
     assert forward(lib, args(), S=2) == bnd.SS2D_ERR_SHAPE                # dense: S is B
     assert forward(lib, args(cu=True), B=2, S=3) == bnd.SS2D_ERR_SHAPE    # packed: B is 1
