@@ -76,13 +76,13 @@ int64_t slot_count(int64_t L, int64_t S, int64_t T, bool packed, int64_t unit) {
 // Chunks per segment, 0 for whole sequences.  A segmented forward does the state's recurrence
 // about 2.5 times (M and Z, then the run), so it pays where most of the chip is idle otherwise:
 // below 384 waves of the chip's 1024 SIMDs (with 384, a training step over 64 x 3136 tokens of
-// 3 heads of 64 takes 1389 us whole and 1412 us in segments of 20 chunks; packed sequences, the
+// 3 heads of 64 takes 1343 us whole and 1388 us in segments of 20 chunks; packed sequences, the
 // longest of which the others wait for, below 1024: 25 prompts of 12007 tokens and 8 heads,
-// 600 waves, take 456 us whole and 205 us in segments).  The segments are
+// 600 waves, take 441 us whole and 190 us in segments).  The segments are
 // made long enough for about one wave per SIMD (1024), and no shorter than 8 chunks or
 // sqrt(C / 4) of the C chunks of a row, because the join runs through them one by one.  4096
-// tokens of 32 heads of 128: 310, 247, 246 and 213 us with 6, 8, 12 and 16 chunks (the rule
-// gives 16); 2 x 65536 fp32 tokens of 3 heads of 64: 758, 618, 610 and 681 us with 12, 16, 24
+// tokens of 32 heads of 128: 304, 249, 253 and 221 us with 6, 8, 12 and 16 chunks (the rule
+// gives 16); 2 x 65536 fp32 tokens of 3 heads of 64: 755, 617, 608 and 675 us with 12, 16, 24
 // and 32 (24).  Even, so that blocks of 64 tokens do not straddle them.
 int64_t segment_chunks(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DV, bool packed) {
   using ss2d::delta::kC;

@@ -16,7 +16,8 @@
 // The adjoint is bound by the latency of a chunk's chain, as the forward's scan is, and by its
 // registers (256 and up to 256 accumulation registers, one wave per SIMD; held to two waves per
 // SIMD it spills 120 of them and takes 486 us instead of 313 in segments of 20 chunks).  64 x
-// 3136 tokens of 3 heads of 64 in bfloat16: 530 us uncut, dq and dk 229 us.
+// 3136 tokens of 3 heads of 64 in bfloat16: 471 us uncut (520 with LDS permutes for the sums over
+// columns), dq and dk 230 us.
 #include "ss1d_delta.h"
 
 namespace ss2d {
@@ -239,7 +240,7 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
 // its registers and LDS are held to what lets two blocks share a CU (128 registers up to
 // DK = 64 where no value heads share a key head, which needs no second set of sums): six waves
 // at 242 registers, one block per CU, loads issued one behind the other: 480 us (64 x 3136
-// tokens of 3 heads of 64; 766 MB); eight at 128, all loads of 32 columns at once: 229 us.
+// tokens of 3 heads of 64; 766 MB); eight at 128, all loads of 32 columns at once: 230 us.
 template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows by 16 columns
   // parts of 32 rows by 16 columns: u = beta t and the state in 2 terms; do, dv and dS exact
   static constexpr int kWide = 4 + 2 * KT, kNarrow = 8 + 2 * KT;
