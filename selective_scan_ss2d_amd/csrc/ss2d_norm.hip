@@ -465,10 +465,11 @@ int launch_norm(const Args& a, int dtype, int ytype, bool first, bool vec, hipSt
              : launch_types<false>(a, dtype, ytype, false, blocks, st);
 }
 
-// About 4 blocks per CU, each with at least 4 rounds of its concurrent rows where there are
-// that many; small groups share a block.
+// About 2 blocks per CU, what their registers allow, each with at least 4 rounds of its
+// concurrent rows where there are that many (25216 rows of 768: 102 us and 9 for the sums; with
+// twice the blocks 104 and 11); small groups share a block.
 int64_t plan_norm_bwd(Args* a, bool first) {
-  constexpr int64_t kBlocks = 1024;
+  constexpr int64_t kBlocks = 512;
   const int64_t per = first ? 1 : rows_of_block(a->D);
   const int64_t rounds = first ? tiles_first(*a, true) : (a->group + per - 1) / per;  // of a group
   a->groups_per_block = 1;
