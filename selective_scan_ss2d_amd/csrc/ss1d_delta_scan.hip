@@ -14,7 +14,7 @@
 // zero) of all segments at once with the same recurrence, the join pass runs S through them,
 // and the forward then starts every segment from its state.  4096 tokens of 32 heads of 128 in
 // 8 segments: span 86 us, join 27, run 78; 2 x 65536 fp32 tokens of 3 heads of 64 in 86
-// segments: span 156, join 133 (1.5 us a segment, one after the other), run 222, and with the
+// segments: span 156, join 134 (1.5 us a segment, one after the other), run 224, and with the
 // chunk matrices 604 in all, where the uncut call took 10.5 ms.
 #include "ss1d_delta.h"
 
