@@ -664,6 +664,8 @@ __device__ __forceinline__ float decay_state(f32x16* X, float factor, float deca
 // exact to fp32, and one v_exp_f32 (1 ulp) makes it a factor.
 constexpr float kMinLog = -1000.0f;
 constexpr double kLog2eWide = 1.4426950408889634074;
+// (fmaxf would turn a NaN into the bound.)
+__device__ __forceinline__ float bounded_log(float g) { return g < kMinLog ? kMinLog : g; }
 __device__ __forceinline__ float decay_of(double diff) { return exp2_hw(static_cast<float>(diff)); }
 
 int launch_prep(const Args& a, int dtype, bool aligned, bool backward, hipStream_t st);

@@ -410,7 +410,7 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       }
     }
     if (g.wave == kGradWaves - 1) {  // read after the barriers below
-      double x = lane < valid ? fmaxf(gate, kMinLog) * kLog2eWide : 0.0;
+      double x = lane < valid ? bounded_log(gate) * kLog2eWide : 0.0;
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
         const double up = __shfl_up(x, d);

@@ -107,7 +107,7 @@ void k_delta_prep(Args a) {
   const int64_t row = seq.row + t0 + (col < valid ? col : 0);
   float gv = 0.0f, bv = 0.0f;
   if (col < valid) {
-    gv = fmaxf(a.g[row * a.H + hv], kMinLog);
+    gv = bounded_log(a.g[row * a.H + hv]);
     bv = a.beta[row * a.H + hv];
   }
   double G = gv * kLog2eWide;
