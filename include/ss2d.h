@@ -474,6 +474,12 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * gives its end state from a zero start, Z, and its matrix M, and the states between them follow
  * from S <- M S + Z, on operands of 3 terms for either type.
  *
+ * NaN and infinities: o, the end states and the gradients are NaN or infinite wherever the
+ * definition makes them so (NaN for either, also where it has an infinity).  In o and the end
+ * states nothing else is: a value of token t reaches no token before t, no other sequence or
+ * head and, if it is v's, no other column.  A gradient that the definition leaves finite may be
+ * NaN where it shares its sequence, head (q, k: key head) and block of 64 tokens with the value.
+ *
  * ss1d_delta_forward writes o and, if ht is not NULL, the end states; ht may be h0 itself
  * (in place).  saved (NULL, or ss1d_delta_saved_bytes bytes of device memory, aligned to 256)
  * keeps what ss1d_delta_backward starts from: the states before every 64 tokens and at the

@@ -145,8 +145,25 @@ void k_delta_prep(Args a) {
   // n (I + diag(beta) L) = l); backward, row i holds L_ij beta_j over j, with rows, columns and
   // the unknowns in reverse order, so that both are solved from the last to the first
   auto at = [](int i) { return kBackward ? kC - 1 - i : i; };
+  float finite = 0.0f;  // NaN if one of this lane's values is not finite
 #pragma unroll
-  for (int r = 0; r < 16; ++r) sh.m[at(acc_row(r, half)) * kC + at(own)] = low[r] * bown;
+  for (int r = 0; r < 16; ++r) {
+    const float value = low[r] * bown;
+    sh.m[at(acc_row(r, half)) * kC + at(own)] = value;
+    finite = fmaf(value, 0.0f, finite);
+  }
+  // The solve multiplies by the unknowns' leading zeros too, where a NaN or infinity would reach
+  // the tokens before it (backward: behind it).  From the first token that has one on, the matrix
+  // is then set to zero, and the unknowns of the tokens past that one to NaN.
+  int bad = kC;
+  if (__builtin_expect(__any(finite != finite), 0)) {
+    bad = finite != finite ? at(own) : kC;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) bad = min(bad, __shfl_xor(bad, d));
+    if (at(own) >= bad)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sh.m[at(acc_row(r, half)) * kC + at(own)] = 0.0f;
+  }
   float x[kC];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
@@ -161,6 +178,9 @@ void k_delta_prep(Args a) {
   for (int j = kC - 2; j >= 0; --j)
 #pragma unroll
     for (int k = kC - 1; k > j; --k) x[j] = fmaf(-sh.m[j * kC + k], x[k], x[j]);
+  if (__builtin_expect(bad < kC, 0) && at(own) > bad)
+#pragma unroll
+    for (int i = 0; i < kC; ++i) x[i] = __builtin_nanf("");
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     f32x8 v;

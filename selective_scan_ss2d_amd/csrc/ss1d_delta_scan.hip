@@ -22,6 +22,30 @@ namespace ss2d {
 namespace delta {
 namespace {
 
+// A product over the chunk's tokens multiplies by the structural zeros of N and P too, where a NaN
+// or an infinity would reach the tokens before it.  So its operand is clamped to the largest
+// bfloat16 (NaN becomes the lowest); the state's update takes the values as they are, all rows of
+// its column follow them, and where they have, o is set to NaN from the first such token on.
+constexpr float kLargest = 0x1.fep127f;
+__device__ __forceinline__ f32x16 clamped(const f32x16& x) {
+  f32x16 y;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) y[r] = __builtin_amdgcn_fmed3f(x[r], -kLargest, kLargest);
+  return y;
+}
+// That token, kC without one, and the column with NaN from token `from` on.
+__device__ __forceinline__ int first_bad(const f32x16& x, int half) {
+  int token = kC;
+#pragma unroll
+  for (int r = 15; r >= 0; --r)
+    if (!(fabsf(x[r]) <= kLargest)) token = acc_row(r, half);
+  return min(token, __shfl_xor(token, 32));
+}
+__device__ __forceinline__ void set_nan(f32x16& x, int from, int half) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) x[r] = acc_row(r, half) >= from ? __builtin_nanf("") : x[r];
+}
+
 // Operands hold 24 bits (3 bf16 terms), those of o 17 (2 terms, which leaves o to its own
 // rounding); with kSave, the training forward, o's hold 24 as well, because the backward
 // forms the decays' gradient from o.  kSpan: the span pass, no o; the tiles are those of Z,
@@ -128,11 +152,12 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
     const f32x16 gam = load_gate(gate, half) * factor, beta = load_gate(gate + 2 * kC, half);
     f32x16 t = v - gam * ks;
     f32x16 nr = {};
+    const f32x16 br = kSpan ? beta * t : clamped(beta * t);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       Wide<T, 3> nw, rw;
       get(nw, St::n(buf, s), lane);
-      set_wide(rw, part(beta * t, s));
+      set_wide(rw, part(br, s));
       nr = mma(nw, rw, nr);
     }
     t -= nr;
@@ -153,6 +178,11 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
         S[kt] = mma(kx, ew[s], S[kt]);
       }
     if constexpr (!kSpan) {
+      int bad = kC;
+      settled(S[0]);
+      const bool any_bad = __any(!(fabsf(S[0][0]) < __builtin_inff()));
+      if (__builtin_expect(any_bad, 0)) bad = first_bad(u, half);
+      u = clamped(u);
       f32x16 pu = {};
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -161,7 +191,12 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
         set_wide(uw, part(u, s));
         pu = mma(pw, uw, pu);
       }
-      const f32x16 o = a.scale * gam * qs + pu;
+      f32x16 o = a.scale * gam * qs + pu;
+      settled(o);
+      if (__builtin_expect(any_bad, 0)) {
+        set_nan(o, bad, half);
+        if (kSave) set_nan(t, bad + 1, half);
+      }
       store_tile<T>(o, oat, line * sizeof(T), oalign && whole, left, w.store_cols, lds, lane);
       oat += kC * int64_t(line);
       if (kSave) {

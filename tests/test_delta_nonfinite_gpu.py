@@ -71,6 +71,86 @@ def test_forward_hides_nothing(name, value, chunks, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("name, value", BAD)
+@pytest.mark.parametrize("token", [0, 31, 32, 45, 99])
+def test_forward_only_later_tokens(name, value, token, dtype):
+    """One bad value: the tokens before it, other rows, other heads and (for v) other columns
+    keep their bits."""
+    t = du.make_inputs(2, 100, 2, 4, 64, 48, dtype, seed=token, h0=2)
+    m = planted(t, name, value, 1, token, 2)
+    check_forward(m, dtype, forward(m), forward(t))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name, value", BAD)
+@pytest.mark.parametrize("shape", [(1, 70, 1, 1, 16, 31), (1, 70, 1, 2, 128, 100), (1, 40, 1, 1, 33, 160)])
+def test_forward_of_other_widths(shape, name, value, dtype):
+    t = du.make_inputs(*shape, dtype, seed=3)
+    m = planted(t, name, value, 0, 37, 0)
+    check_forward(m, dtype, forward(m), forward(t))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name, value", BAD)
+def test_forward_in_segments(name, value, dtype):
+    t = du.make_inputs(1, 300, 1, 2, 64, 64, dtype, seed=4, h0=1)
+    m = planted(t, name, value, 0, 150, 1)
+    with du.segments(2):
+        check_forward(m, dtype, forward(m), forward(t))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name, value", BAD)
+def test_other_packed_sequences_keep_their_bits(name, value, dtype):
+    cu = torch.tensor([0, 20, 75, 90], dtype=torch.int32)
+    t = du.make_inputs(1, 90, 1, 2, 64, 64, dtype, seed=5, h0=3)
+    m = planted(t, name, value, 0, 41, 1)
+    check_forward(m, dtype, forward(m, cu_seqlens=cu.cuda()), forward(t, cu_seqlens=cu.cuda()), cu)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_padding_behind_a_row(dtype):
+    """A padded batch: rows whose ends hold NaN in all inputs."""
+    lens = [70, 100, 1, 33]
+    t = du.make_inputs(4, 100, 1, 2, 64, 64, dtype, seed=6)
+    m = {n: t[n].clone() if t[n] is not None else None for n in t}
+    for b, n in enumerate(lens):
+        for name in du.NAMES:
+            m[name][b, n:] = math.nan
+    o, _ = forward(m)
+    clean, _ = forward(t)
+    for b, n in enumerate(lens):
+        assert torch.equal(o[b, :n], clean[b, :n]), b
+        assert torch.isnan(o[b, n:]).all(), b
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name, value", BAD)
+def test_training_forward(name, value, dtype):
+    t = du.make_inputs(1, 100, 1, 2, 64, 48, dtype, seed=9, h0=1)
+
+    def run(x):
+        d = du.to_gpu(x)
+        return ss.ss1d_delta_forward_save(*[d[n] for n in du.NAMES], scale=0.6, final_state=True,
+                                          initial_state=d["h0"])[:2]
+
+    m = planted(t, name, value, 0, 45, 1)
+    check_forward(m, dtype, run(m), run(t))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_sums_past_the_largest_value(dtype):
+    """Finite inputs whose products overflow from token 40 on reach no token before it."""
+    t = du.make_inputs(1, 100, 1, 1, 64, 64, dtype, seed=10)
+    m = {n: t[n].clone() if t[n] is not None else None for n in t}
+    m["k"][0, 40:44] *= 2.0 ** 100
+    m["v"][0, 50] *= 2.0 ** 126
+    got, clean = forward(m), forward(t)
+    assert torch.equal(got[0][0, :40], clean[0][0, :40])
+    assert not torch.isfinite(got[0][0, 60:]).any() and not torch.isfinite(got[1]).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("name, value", BAD)
 def test_step(name, value, dtype):
     """The form for single tokens: the same definition, its 3 tokens in order."""
     t = du.make_inputs(2, 3, 2, 4, 64, 48, dtype, seed=7, h0=2)
