@@ -79,7 +79,7 @@ def ss2d_norm_forward(h, residual=None, w_post=None, b_post=None, z=None, res_sc
     alone = w_post is None and z is None and residual is None and res_scale is None
     if alone and w_pre is None:
         raise ValueError("nothing to compute: give w_post, z, residual, res_scale or w_pre")
-    with scope(dev, stream, h, z, residual, res_scale, w_post, b_post, w_pre, b_pre, y):
+    with scope(dev, stream, h, z, residual, res_scale, w_post, b_post, w_pre, b_pre, y, n):
         if alone and y is None:
             kept = None
         else:
