@@ -23,22 +23,9 @@ from ._binding import (LIBRARY_PATH, SS2D_BF16, SS2D_ERR_ALIAS, SS2D_ERR_ALIGN, 
                        ss1d_bidir_forward_routes_save, ss2d_backward_routes_saved,
                        ss1d_bidir_backward_routes_saved, scratch_trim)
 
-
-def __getattr__(name):  # the sequence operators import torch; the rest of the package does not
-    import importlib
-    for module, names in _LAZY.items():
-        if name in names:
-            value = getattr(importlib.import_module("." + module, __name__), name)
-            globals()[name] = value
-            return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-
-
-_LAZY = {
-    "_delta": ("ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_backward",
-               "ss1d_delta_step"),
-    "_norm": ("ss2d_norm_forward", "ss2d_norm_backward"),
-}
+from ._delta import (ss1d_delta_backward, ss1d_delta_forward, ss1d_delta_forward_save,
+                     ss1d_delta_step)
+from ._norm import ss2d_norm_backward, ss2d_norm_forward
 
 __all__ = [
     "ss2d_forward", "ss1d_bidir_forward", "ss2d_forward_ex", "ss1d_bidir_forward_ex",

@@ -155,9 +155,15 @@ def _check(status: int) -> None:
         raise SS2DError(status, msg)
 
 
+_loaded = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _loaded
+    if _loaded is None:  # an import statement costs 0.1 us each time, some calls make ten
+        import torch
+        _loaded = torch
+    return _loaded
 
 
 def _dtype_code(t) -> int:

@@ -4,15 +4,21 @@ from __future__ import annotations
 
 import contextlib
 
-import torch
-
 from . import _binding as bnd
+from ._binding import _torch
 
-CODES = {torch.float32: bnd.SS2D_F32, torch.bfloat16: bnd.SS2D_BF16}
+
+def code_of(dtype):
+    """The data type's code, None for a type that the operators do not take."""
+    torch = _torch()
+    if dtype is torch.bfloat16:
+        return bnd.SS2D_BF16
+    return bnd.SS2D_F32 if dtype is torch.float32 else None
 
 
 @contextlib.contextmanager
 def _switched(device, stream):
+    torch = _torch()
     with torch.cuda.device(device), torch.cuda.stream(stream or torch.cuda.current_stream(device)):
         yield
 
@@ -20,6 +26,7 @@ def _switched(device, stream):
 def scope(device, stream, *tensors):
     """The device and stream that a call's outputs and scratch belong to: a context only
     where they are not the current ones already.  tensors: the caller's, None among them."""
+    torch = _torch()
     if stream is None and device.index == torch.cuda.current_device():
         return contextlib.nullcontext()
     if stream is not None:  # their memory is not to be reused before the call has run
@@ -32,13 +39,13 @@ def scope(device, stream, *tensors):
 def handle(device, stream):
     """The HIP stream that a call runs on (without making a torch.cuda.Stream, 2 us)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream
 
 
 def expect(name, t, shape, dtype, device):
     """Checks a contiguous tensor."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+    if not (isinstance(t, _torch().Tensor) and t.shape == shape and t.dtype is dtype
             and t.device == device and t.is_contiguous()):
         bnd._expect(name, t, shape, dtype, device)  # says what is wrong
 
@@ -49,6 +56,6 @@ def ptr(t):
 
 def output(name, t, shape, dtype, device):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch().empty(shape, dtype=dtype, device=device)
     expect(name, t, shape, dtype, device)
     return t

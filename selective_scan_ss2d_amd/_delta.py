@@ -6,16 +6,15 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 from . import _binding as bnd
-from ._call import (CODES, expect as _expect, handle as _handle, output as _output, ptr as _ptr,
+from ._binding import _torch
+from ._call import (code_of, expect as _expect, handle as _handle, output as _output, ptr as _ptr,
                     scope as _scope)
 
 
 def _strided(name, t, shape, dtype, device):
     """Checks a tensor whose last axis alone has to be contiguous."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -30,6 +29,7 @@ def _strided(name, t, shape, dtype, device):
 def _inputs(q, k, v, g, beta):
     """Checks the rule's inputs; (B, L, HK, DK, H, DV), the data type's code and the strides
     (None for contiguous tensors)."""
+    torch = _torch()
     if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor):
         raise TypeError("q and v must be torch.Tensors")
     if q.dim() != 4 or v.dim() != 4:
@@ -37,7 +37,7 @@ def _inputs(q, k, v, g, beta):
     dev, dtype = q.device, q.dtype
     if dev.type != "cuda":
         raise ValueError("q must be a GPU tensor")
-    code = CODES.get(dtype)
+    code = code_of(dtype)
     if code is None:
         raise TypeError(f"q must be float32 or bfloat16, not {dtype}")
     B, L, HK, DK = q.shape
@@ -60,14 +60,14 @@ def _sequences(cu_seqlens, B, device):
         return B
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must hold S + 1 offsets")
-    _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, _torch().int32, device)
     if B != 1:
         raise ValueError("packed sequences (cu_seqlens) need a batch of 1")
     return cu_seqlens.shape[0] - 1
 
 
 def _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o, stream, save):
-    lib = bnd.load_library()
+    torch, lib = _torch(), bnd.load_library()
     (B, L, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
     dev = q.device
     S = _sequences(cu_seqlens, B, dev)
@@ -131,7 +131,7 @@ def ss1d_delta_backward(q, k, v, g, beta, do, scale=None, cu_seqlens=None, initi
     saved: the buffer of ss1d_delta_forward_save for the same inputs; None computes it again.
     Rows outside of every packed sequence are zero.
     """
-    lib = bnd.load_library()
+    torch, lib = _torch(), bnd.load_library()
     (B, L, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
     dev = q.device
     S = _sequences(cu_seqlens, B, dev)
@@ -166,7 +166,7 @@ def ss1d_delta_step(q, k, v, g, beta, state, slots=None, scale=None, o=None, str
     stay as they are; rows that name one slot are successive tokens of one sequence, in row
     order.  Returns o (B, T, H, DV).
     """
-    lib = bnd.load_library()
+    torch, lib = _torch(), bnd.load_library()
     (B, T, HK, DK, H, DV), code, strides = _inputs(q, k, v, g, beta)
     dev = q.device
     if not isinstance(state, torch.Tensor) or state.dim() != 4:

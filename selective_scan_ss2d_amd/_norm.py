@@ -4,19 +4,18 @@ Argument checks and marshalling only; every step runs in the library's HIP kerne
 """
 from __future__ import annotations
 
-import torch
-
 from . import _binding as bnd
-from ._call import CODES, expect, handle, output, ptr, scope
+from ._binding import _torch
+from ._call import code_of, expect, handle, output, ptr, scope
 
 
 def _shape(h, channels_first):
     """(B, L, D) of h and the data type's code."""
-    if not isinstance(h, torch.Tensor):
+    if not isinstance(h, _torch().Tensor):
         raise TypeError("h must be a torch.Tensor")
     if h.device.type != "cuda":
         raise ValueError("h must be a GPU tensor")
-    code = CODES.get(h.dtype)
+    code = code_of(h.dtype)
     if code is None:
         raise TypeError(f"h must be float32 or bfloat16, not {h.dtype}")
     if h.dim() < (3 if channels_first else 1):
@@ -33,7 +32,7 @@ def _shape(h, channels_first):
 def _vectors(D, dev, rows, res_scale, **vectors):
     for name, w in vectors.items():
         if w is not None:
-            expect(name, w, (D,), torch.float32, dev)
+            expect(name, w, (D,), _torch().float32, dev)
     for norm in ("post", "pre"):
         if vectors.get("b_" + norm) is not None and vectors["w_" + norm] is None:
             raise ValueError(f"b_{norm} needs w_{norm}")
@@ -42,7 +41,7 @@ def _vectors(D, dev, rows, res_scale, **vectors):
     G = res_scale.shape[0] if res_scale.dim() == 2 else 1
     if res_scale.dim() == 1:
         res_scale = res_scale[None]
-    expect("res_scale", res_scale, (G, D), torch.float32, dev)
+    expect("res_scale", res_scale, (G, D), _torch().float32, dev)
     if G < 1 or rows % G:
         raise ValueError(f"res_scale has {G} rows, expected a divisor of {rows}")
     return G
@@ -63,7 +62,7 @@ def ss2d_norm_forward(h, residual=None, w_post=None, b_post=None, z=None, res_sc
     (channels first: of images).  Returns (y, n), n None without w_pre; y is h itself if
     nothing but the second norm is asked for.  y may be given as the residual (in place).
     """
-    lib = bnd.load_library()
+    torch, lib = _torch(), bnd.load_library()
     (B, L, D), code = _shape(h, channels_first)
     dev = h.device
     G = _vectors(D, dev, B if channels_first else B * L, res_scale, w_post=w_post, b_post=b_post,
@@ -88,7 +87,7 @@ def ss2d_norm_forward(h, residual=None, w_post=None, b_post=None, z=None, res_sc
         bnd._check(lib.ss2d_norm_forward(
             h.data_ptr(), ptr(z), ptr(residual), ptr(res_scale), ptr(w_post), ptr(b_post),
             ptr(w_pre), ptr(b_pre), ptr(kept), ptr(n), B, L, D, G, 1 if channels_first else 0,
-            1 if layer else 0, eps, code, CODES[ytype], handle(dev, stream)))
+            1 if layer else 0, eps, code, code_of(ytype), handle(dev, stream)))
     return (h if kept is None else y), n
 
 
@@ -102,7 +101,7 @@ def ss2d_norm_backward(h, y=None, dy=None, dn=None, residual=True, w_post=None, 
     gradients of h and of what was given of residual, z, res_scale, w_post, b_post, w_pre and
     b_pre, each with its input's shape.
     """
-    lib = bnd.load_library()
+    torch, lib = _torch(), bnd.load_library()
     (B, L, D), code = _shape(h, channels_first)
     dev = h.device
     G = _vectors(D, dev, B if channels_first else B * L, res_scale, w_post=w_post, b_post=b_post,
@@ -133,6 +132,6 @@ def ss2d_norm_backward(h, y=None, dy=None, dn=None, residual=True, w_post=None, 
             ptr(dy), ptr(dn), d["h"].data_ptr(), *[ptr(d.get(k)) for k in
                                                    ("z", "residual", "res_scale", "w_post",
                                                     "b_post", "w_pre", "b_pre")],
-            B, L, D, G, 1 if channels_first else 0, 1 if layer else 0, eps, code, CODES[ytype],
+            B, L, D, G, 1 if channels_first else 0, 1 if layer else 0, eps, code, code_of(ytype),
             handle(dev, stream)))
     return d
