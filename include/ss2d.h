@@ -469,14 +469,14 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  *
  * Arithmetic: S, the chunk's triangular solve and every sum are fp32 for both data types.
  * For bfloat16 data a product's fp32 operand runs on the bf16 matrix cores as the sum of 3
- * bfloat16 terms (24 bits), o's as 2 (17 bits) before its single rounding; fp32 data use the
- * fp32 matrix instructions.  Few or long sequences are cut into segments that run at once: each
+ * bfloat16 terms (24 bits), those of o, dq and dk as 2 (17 bits) before their single rounding;
+ * fp32 data use the fp32 matrix instructions.  Few or long sequences are cut into segments that run at once: each
  * gives its end state from a zero start, Z, and its matrix M, and the states between them follow
  * from S <- M S + Z, on operands of 3 terms for either type.
  *
  * NaN and infinities: o, the end states and the gradients are NaN or infinite wherever the
- * definition makes them so (NaN for either, also where it has an infinity).  In o and the end
- * states nothing else is: a value of token t reaches no token before t, no other sequence or
+ * definition makes them so (an infinity may come out as NaN).  In o and the end states nothing
+ * else is: a value of token t reaches no token before t, no other sequence or
  * head and, if it is v's, no other column.  A gradient that the definition leaves finite may be
  * NaN where it shares its sequence, head (q, k: key head) and block of 64 tokens with the value.
  *
@@ -501,8 +501,8 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * The shared conventions hold, except that kernel timing does not cover these entry points.
  * Scratch (the step has none): per token, the chunks' matrices, about 0.4 KB per value head and
  * 6 DK (fp32: 12 DK) bytes per key head, DK rounded up to 32, 64 or 128; per segment and head,
- * M, Z and a state; the backward's gradients of the states, one per 64 tokens and head, and
- * partial sums. */
+ * M, Z and a state; the backward's gradients of the states in fp32, one per 64 tokens and head,
+ * for bfloat16 data dv in fp32, and partial sums. */
 int ss1d_delta_forward(const void *q, const void *k, const void *v, const float *g,
                        const float *beta, const float *h0, const int32_t *cu_seqlens, void *o,
                        float *ht, void *saved, int64_t B, int64_t L, int64_t S, int64_t HK,

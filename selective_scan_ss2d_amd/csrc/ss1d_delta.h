@@ -71,7 +71,8 @@ struct Args {
   const float* dht;            // gradient of the end states, or NULL
   void *dq, *dk, *dv;
   float *dg, *dbeta, *dh0;     // dh0 may be NULL
-  void* dmarks;                // gradients of the states after every 64 tokens, data type
+  float* dmarks;               // gradients of the states after every 64 tokens
+  float* dvs;                  // dv in fp32, (T, H, DV); for fp32 data dv itself
   float *pbeta, *pgate;        // per tile of 32 columns: w.t and do.o - dv.v of every token
   float* pdots;                // per 64 tokens, head and tile: <dS, S> after them
   int64_t marks_n;             // slots of 64 tokens

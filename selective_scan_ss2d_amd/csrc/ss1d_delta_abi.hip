@@ -354,12 +354,13 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   a.p_planes = 3;
 
   // scratch: the chunk matrices (first the forward's where nothing was kept, then the
-  // backward's in their place), the states' gradients, the gates' partial sums
+  // backward's in their place), the states' gradients and dv in fp32, the gates' partial sums
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t tiles = (DV + 31) / 32;
   const Scratch w = scratch_layout(a, dtype);
   const size_t dmarks = w.bytes,
-               pbeta = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * e),
+               dvs = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * 4),
+               pbeta = dvs + (dtype == SS2D_F32 ? 0 : ss2d::host_align256(size_t(T) * H * DV * 4)),
                pgate = pbeta + ss2d::host_align256(size_t(tiles) * T * H * 4),
                pdots = pgate + ss2d::host_align256(size_t(tiles) * T * H * 4),
                keep = pdots + ss2d::host_align256(size_t(a.marks_n) * H * tiles * 4),
@@ -369,7 +370,8 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   rc = ss2d::host_scratch_alloc(&ws, bytes, st);
   if (rc != SS2D_OK) return rc;
   set_scratch(&a, ws, w);
-  a.dmarks = ws + dmarks;
+  a.dmarks = reinterpret_cast<float*>(ws + dmarks);
+  a.dvs = dtype == SS2D_F32 ? static_cast<float*>(dv) : reinterpret_cast<float*>(ws + dvs);
   a.pbeta = reinterpret_cast<float*>(ws + pbeta);
   a.pgate = reinterpret_cast<float*>(ws + pgate);
   a.pdots = reinterpret_cast<float*>(ws + pdots);

@@ -16,8 +16,8 @@
 // The adjoint is bound by the latency of a chunk's chain, as the forward's scan is, and by its
 // registers (256 and up to 256 accumulation registers, one wave per SIMD; held to two waves per
 // SIMD it spills 120 of them and takes 486 us instead of 313 in segments of 20 chunks).  64 x
-// 3136 tokens of 3 heads of 64 in bfloat16: 471 us uncut (520 with LDS permutes for the sums over
-// columns), dq and dk 230 us.
+// 3136 tokens of 3 heads of 64 in bfloat16: 490 us uncut (457 before it kept dv and the states' gradients
+// in fp32, 520 with LDS permutes for the sums over columns), dq and dk 274 us.
 #include "ss1d_delta.h"
 
 namespace ss2d {
@@ -83,7 +83,7 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
   T* out0 = static_cast<T*>(a.dv) + first;
   const bool valign = aligned16(v0, vline, w.cols), dalign = aligned16(d0, line * sizeof(T), w.cols);
   const bool oalign = aligned16(out0, line * sizeof(T), w.store_cols);
-  const bool salign = aligned16(nullptr, line * 4, w.cols);
+  const bool salign = aligned16(nullptr, line * 4, w.cols), walign = aligned16(nullptr, line * 4, w.store_cols);
   const bool malign = aligned16(nullptr, a.DV * 4, w.cols) && a.DK % 32 == 0;
   St stage;
   Tile<T> vx, dx;
@@ -162,8 +162,8 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
     settled(y);
     settled(dv);
     if (ends) {
-      store_state<T, KT>(dS, static_cast<T*>(a.dmarks) + (mark * a.H + w.hv) * a.DK * a.DV + 32 * w.tile,
-                         factor, a, w, lds);
+      store_state<float, KT>(dS, a.dmarks + (mark * a.H + w.hv) * a.DK * a.DV + 32 * w.tile, factor, a, w,
+                             lds);
       float dot = 0.0f;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
@@ -200,6 +200,8 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
     if constexpr (!kSpan) {
       // dv, and what the gates' gradients take from these 32 columns
       store_tile<T>(dv, out0 + at, line * sizeof(T), oalign && whole, valid, w.store_cols, lds, lane);
+      if constexpr (sizeof(T) == 2)
+        store_tile<float>(dv, a.dvs + first + at, line * 4, walign && whole, valid, w.store_cols, lds, lane);
       f32x16 sb = y * tx.columns(salign && whole, a.ts + first + at, line * 4, valid, w.cols, lds, lane);
       f32x16 sg = dout * ox.columns(salign && whole, a.os + first + at, line * 4, valid, w.cols, lds, lane) -
                   dv * vx.columns(valign && whole, v0 + t0 * a.sv.l, vline, valid, w.cols, lds, lane);
@@ -233,23 +235,27 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
 // part from the states and two for dk's part from the block itself (added to the former at
 // the end).  The matrices whose columns (DV) are contracted pass through LDS 32 columns at a
 // time, split into bfloat16 terms once for all waves, the next 32 already on their way.  For
-// bfloat16 data one operand of every product has 2 terms (or is exact), so each product
-// carries at most one operand rounding besides the output's own.
+// bfloat16 data the fp32 operands (u, dv, the states and their gradients, dP and dL) take 2 terms,
+// 17 bits: dk is a difference of their products, which with dv and the states' gradients in
+// bfloat16 was 1.4 times as far from 64 bits as its own rounding (2.3e-3 against 1.7e-3 without
+// decay), and a third term would add half as many products again to change nothing but the last
+// of those 17 bits.
 //
 // Bound by the loads' latency: a block is three round trips to memory and little else.  So
 // its registers and LDS are held to what lets two blocks share a CU (128 registers up to
 // DK = 64 where no value heads share a key head, which needs no second set of sums): six waves
 // at 242 registers, one block per CU, loads issued one behind the other: 480 us (64 x 3136
-// tokens of 3 heads of 64; 766 MB); eight at 128, all loads of 32 columns at once: 230 us.
+// tokens of 3 heads of 64, dv and the states' gradients then in bfloat16); eight at 128, all loads
+// of 32 columns at once: 223 us, and 274 with those two in fp32 (920 MB).
 template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows by 16 columns
-  // parts of 32 rows by 16 columns: u = beta t and the state in 2 terms; do, dv and dS exact
-  static constexpr int kWide = 4 + 2 * KT, kNarrow = 8 + 2 * KT;
+  // parts of 32 rows by 16 columns: u = beta t, dv, the state and its gradient in 2 terms; do exact
+  static constexpr int kWide = 8 + 4 * KT, kNarrow = 4;
   static constexpr int kU = 0;                                   // 64 rows
-  static constexpr int kS = kU + 4 * wide_planes<T, 2>();        // DK rows
-  static constexpr int kDo = kS + 2 * KT * wide_planes<T, 2>();  // 64 rows
-  static constexpr int kDv = kDo + 4 * exact_planes<T>();        // 64 rows
-  static constexpr int kDs = kDv + 4 * exact_planes<T>();        // DK rows
-  static constexpr int kKeys = kDs + 2 * KT * exact_planes<T>(); // K^T and Q^T of both halves
+  static constexpr int kDv = kU + 4 * wide_planes<T, 2>();       // 64 rows
+  static constexpr int kS = kDv + 4 * wide_planes<T, 2>();       // DK rows
+  static constexpr int kDs = kS + 2 * KT * wide_planes<T, 2>();  // DK rows
+  static constexpr int kDo = kDs + 2 * KT * wide_planes<T, 2>(); // 64 rows
+  static constexpr int kKeys = kDo + 4 * exact_planes<T>();      // K^T and Q^T of both halves
   static constexpr int kKeyPlanes = 8 * KT * exact_planes<T>();
   static constexpr int kPlanes = kKeys + kKeyPlanes;
 };
@@ -343,26 +349,27 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
     Piece<float> wide[kWs];
     float beta[kWs];
     const int prow = lane >> 1, pcol = 8 * (lane & 1), to = 32 * (lane & 1) + swap23(prow);
+    auto row_of_part = [&](int part) {  // of a wide one: u, dv, the state, its gradient
+      return 32 * ((part < 8 ? part & 3 : part < 8 + 2 * KT ? part - 8 : part - 8 - 2 * KT) >> 1) + prow;
+    };
     auto fetch = [&](int c0) {
 #pragma unroll
       for (int i = 0; i < kWs; ++i) {
         const int part = min(g.wave + kGradWaves * i, Pn::kWide - 1);
-        const bool tokens = part < 4;
-        const int row = 32 * ((tokens ? part : part - 4) >> 1) + prow;
+        const bool tokens = part < 8;
+        const int row = row_of_part(part);
         const int at = row < (tokens ? valid : a.DK) ? row : 0;
-        const float* base = tokens ? a.ts + head_at : a.marks + state_at;
+        const float* base = tokens ? (part < 4 ? a.ts : a.dvs) + head_at
+                                   : (part < 8 + 2 * KT ? a.marks : a.dmarks) + state_at;
         wide[i].template load<kAligned>(base + at * (tokens ? line : a.DV), c0 + 16 * (part & 1) + pcol, a.DV);
         beta[i] = a.beta[(g.row0 + (tokens ? at : 0)) * a.H + hv];
       }
 #pragma unroll
       for (int i = 0; i < kNs; ++i) {
         const int part = min(g.wave + kGradWaves * i, Pn::kNarrow - 1);
-        const bool tokens = part < 8;
-        const int row = 32 * ((tokens ? part & 3 : part - 8) >> 1) + prow;
-        const int at = row < (tokens ? valid : a.DK) ? row : 0;
-        const T* base = static_cast<const T*>(part < 4 ? a.dout : tokens ? a.dv : a.dmarks) +
-                        (tokens ? head_at : state_at);
-        narrow[i].template load<kAligned>(base + at * (tokens ? line : a.DV), c0 + 16 * (part & 1) + pcol, a.DV);
+        const int row = 32 * (part >> 1) + prow, at = row < valid ? row : 0;
+        narrow[i].template load<kAligned>(static_cast<const T*>(a.dout) + head_at + at * line,
+                                          c0 + 16 * (part & 1) + pcol, a.DV);
       }
     };
     auto commit = [&](int c0) {
@@ -370,24 +377,19 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
       for (int i = 0; i < kWs; ++i) {
         const int part = g.wave + kGradWaves * i;
         if (part >= Pn::kWide) break;
-        const bool tokens = part < 4;
-        const int row = 32 * ((tokens ? part : part - 4) >> 1) + prow;
         const Piece<float> x = wide[i].template taken<kAligned>(c0 + 16 * (part & 1) + pcol, a.DV,
-                                                                row < (tokens ? valid : a.DK));
+                                                                row_of_part(part) < (part < 8 ? valid : a.DK));
         f32x8 v;
         __builtin_memcpy(&v, x.u, 32);
         Wide<T, 2> w;
-        set_wide(w, tokens ? v * beta[i] : v);
+        set_wide(w, part < 4 ? v * beta[i] : v);
         put(panels + (Pn::kU + part * wide_planes<T, 2>()) * kPlane, to, w);
       }
 #pragma unroll
       for (int i = 0; i < kNs; ++i) {
         const int part = g.wave + kGradWaves * i;
         if (part >= Pn::kNarrow) break;
-        const bool tokens = part < 8;
-        const int row = 32 * ((tokens ? part & 3 : part - 8) >> 1) + prow;
-        narrow[i].template taken<kAligned>(c0 + 16 * (part & 1) + pcol, a.DV,
-                                           row < (tokens ? valid : a.DK))
+        narrow[i].template taken<kAligned>(c0 + 16 * (part & 1) + pcol, a.DV, 32 * (part >> 1) + prow < valid)
             .put(panels + (Pn::kDo + part * exact_planes<T>()) * kPlane, to);
       }
     };
@@ -450,23 +452,21 @@ __device__ __forceinline__ void grad_wave(const GradBlock& g) {
           p[0] = mma(wide_of(Pn::kU, 0), d, p[0]);
           if (mine == 1) p[1] = mma(wide_of(Pn::kU, 1), d, p[1]);
         } else if constexpr (kKind == 1) {
-          const Exact<T> d = exact_of(Pn::kDv, mine);
-          const Wide<T, 2> u = wide_of(Pn::kU, mine);
+          const Wide<T, 2> d = wide_of(Pn::kDv, mine), u = wide_of(Pn::kU, mine);
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
             y[KT + kt] = mma(d, wide_of(Pn::kS, kt), y[KT + kt]);
-            y[kt] = mma(u, exact_of(Pn::kDs, kt), y[kt]);
+            y[kt] = mma(u, wide_of(Pn::kDs, kt), y[kt]);
           }
         } else if constexpr (kKind == 2) {
           const Wide<T, 2> u = wide_of(Pn::kU, mine);
           p[0] = mma(exact_of(Pn::kDo, 0), u, p[0]);  // not used by the later 32 tokens
           p[1] = mma(exact_of(Pn::kDo, 1), u, p[1]);
         } else {
-          const Wide<T, 2> u = wide_of(Pn::kU, mine);
-          const Exact<T> d = exact_of(Pn::kDv, mine);
+          const Wide<T, 2> u = wide_of(Pn::kU, mine), d = wide_of(Pn::kDv, mine);
           if (mine == 0) {
             p[0] = mma(u, d, p[0]);
-            p[1] = mma(exact_of(Pn::kDv, 1), u, p[1]);
+            p[1] = mma(wide_of(Pn::kDv, 1), u, p[1]);
           } else {
             p[0] = mma(wide_of(Pn::kU, 0), d, p[0]);
             p[1] = mma(u, d, p[1]);
