@@ -86,6 +86,7 @@ int64_t slot_count(int64_t L, int64_t S, int64_t T, bool packed, int64_t unit) {
 // and 32 (24).  Even, so that blocks of 64 tokens do not straddle them.
 int64_t segment_chunks(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DV, bool packed) {
   using ss2d::delta::kC;
+  if (T == 0) return 0;
   if (g_segment_override >= 0) return g_segment_override;
   const int64_t chunks = (L + kC - 1) / kC, tiles = (DV + 31) / 32;
   const int64_t waves = S * H * tiles, total = (T / kC + (packed ? S : 0)) * H * tiles;

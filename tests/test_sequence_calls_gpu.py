@@ -65,3 +65,23 @@ def test_every_given_tensor_is_recorded_on_the_calls_stream(monkeypatch):
     slots = torch.zeros(1, dtype=torch.int32, device="cuda")
     ss.ss1d_delta_step(*[x[:, :1].contiguous() for x in seq], end, slots=slots, o=o[:, :1].contiguous(), stream=s)
     assert {(x.data_ptr(), s.cuda_stream) for x in (end, slots)} <= seen
+
+
+@pytest.mark.parametrize("chunks", [-1, 0, 2])
+@pytest.mark.parametrize("packed", [False, True])
+def test_rows_without_tokens(packed, chunks):
+    """No token at all, in whole sequences and in segments: the states pass through."""
+    t = du.to_gpu(du.make_inputs(1 if packed else 3, 0, 1, 2, 64, 48, torch.float32, h0=3))
+    seq = [t[n] for n in du.NAMES]
+    kw = dict(initial_state=t["h0"])
+    if packed:
+        kw["cu_seqlens"] = torch.zeros(4, dtype=torch.int32, device="cuda")
+    with du.segments(chunks):
+        o, end = ss.ss1d_delta_forward(*seq, final_state=True, **kw)
+        assert o.shape == t["v"].shape and torch.equal(end, t["h0"])
+        o, end, saved = ss.ss1d_delta_forward_save(*seq, final_state=True, **kw)
+        assert torch.equal(end, t["h0"])
+        g = torch.randn_like(end)
+        for kept in (saved, None):
+            d = ss.ss1d_delta_backward(*seq, t["do"], dstate=g, saved=kept, **kw)
+            assert torch.equal(d["initial_state"], g) and d["v"].shape == t["v"].shape
