@@ -216,7 +216,7 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
   const int64_t tiles = (DV + 31) / 32;
   const int64_t units = a->seglen ? a->seg_slots : S;
   if ((a->slots * H / 4 + 1) * 256 > kMaxThreads ||
-      std::max(units, S) * H * (tiles + 8) * 64 > kMaxThreads ||
+      std::max(units, S) * H > kMaxThreads / ((tiles + 8) * 64) ||
       a->marks_n * HK * 64 * ss2d::delta::kGradWaves > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
     return SS2D_ERR_SHAPE;
   return SS2D_OK;

@@ -186,3 +186,11 @@ def test_binding_refuses():
         ss.ss1d_delta_forward(None, t, t, t, t)
     with pytest.raises(ValueError):
         ss.ss1d_delta_step(t[0], t, t, t, t, t)
+
+
+def test_launches_past_64_bits_refused(lib):
+    """The threads of a launch are counted without passing 64 bits themselves: 64 * 9 of each
+    sequence and head here, 2^64 and a few million in all."""
+    H = 30000
+    S = -(-(1 << 64) // (576 * H))
+    assert forward(lib, args(ht=True), B=S, S=S, L=0, HK=1, H=H, DK=1, DV=1) == bnd.SS2D_ERR_SHAPE
