@@ -29,6 +29,8 @@ def scope(device, stream, *tensors):
     torch = _torch()
     if stream is None and device.index == torch.cuda.current_device():
         return contextlib.nullcontext()
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
     if stream is not None:  # their memory is not to be reused before the call has run
         for t in tensors:
             if isinstance(t, torch.Tensor):

@@ -58,6 +58,8 @@ def _inputs(q, k, v, g, beta):
 def _sequences(cu_seqlens, B, device):
     if cu_seqlens is None:
         return B
+    if not isinstance(cu_seqlens, _torch().Tensor):
+        raise TypeError("cu_seqlens must be a torch.Tensor")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must hold S + 1 offsets")
     _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, _torch().int32, device)

@@ -75,6 +75,8 @@ def ss2d_norm_forward(h, residual=None, w_post=None, b_post=None, z=None, res_sc
             raise TypeError(f"residual has dtype {residual.dtype}, expected {h.dtype} or float32")
         ytype = residual.dtype
         expect("residual", residual, h.shape, ytype, dev)
+    if n is not None and w_pre is None:
+        raise ValueError("n needs w_pre")
     alone = w_post is None and z is None and residual is None and res_scale is None
     if alone and w_pre is None:
         raise ValueError("nothing to compute: give w_post, z, residual, res_scale or w_pre")

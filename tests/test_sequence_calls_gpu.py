@@ -85,3 +85,9 @@ def test_rows_without_tokens(packed, chunks):
         for kept in (saved, None):
             d = ss.ss1d_delta_backward(*seq, t["do"], dstate=g, saved=kept, **kw)
             assert torch.equal(d["initial_state"], g) and d["v"].shape == t["v"].shape
+
+
+def test_a_second_output_without_its_norm_is_refused():
+    t = norm_inputs()
+    with pytest.raises(ValueError, match="n needs w_pre"):
+        ss.ss2d_norm_forward(t["h"], residual=t["residual"], n=torch.empty_like(t["h"]))
