@@ -142,6 +142,7 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
         du = mma(pw, Exact<T>{dw.p[0]}, du);
       }
     }
+    settled(du);
     // what this one wants at its end
     if (!kSpan && valign && whole) vx.fetch(v0 + t0 * a.sv.l, vline, lane);
     if (!kSpan && salign && whole) {
