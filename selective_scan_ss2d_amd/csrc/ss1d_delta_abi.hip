@@ -74,11 +74,15 @@ int64_t slot_count(int64_t L, int64_t S, int64_t T, bool packed, int64_t unit) {
 }
 
 // Chunks per segment, 0 for whole sequences.  A segmented forward does the state's recurrence
-// about 2.5 times (M and Z, then the run), so it pays where most of the chip is idle otherwise:
-// below 384 waves of the chip's 1024 SIMDs (with 384, a training step over 64 x 3136 tokens of
-// 3 heads of 64 takes 1343 us whole and 1388 us in segments of 20 chunks; packed sequences, the
-// longest of which the others wait for, below 1024: 25 prompts of 12007 tokens and 8 heads,
-// 600 waves, take 441 us whole and 190 us in segments).  The segments are
+// about 2.5 times (M and Z, then the run), so it pays where most of the chip is idle otherwise.
+// Dense sequences are cut below 320 waves, of the chip's 1024 SIMDs.  Forward and training step,
+// time in segments over time whole, 29 shapes of 32 to 512 chunks, widths 32 to 128, both types:
+//   144 to 256 waves   0.59 to 0.89   (8 x 1024 tokens of 16 heads of 64: 107 against 120 us)
+//   288                0.92, 0.97
+//   320 to 384         0.83 to 1.28, on average 1.04 (shorter ones lose, the longest win)
+//   512                0.92 to 1.24, on average 1.06
+// Packed sequences, the longest of which the others wait for, below 1024: 25 prompts of 12007
+// tokens and 8 heads, 600 waves, take 441 us whole and 190 us in segments.  The segments are
 // made long enough for about one wave per SIMD (1024), and no shorter than 8 chunks or
 // sqrt(C / 4) of the C chunks of a row, because the join runs through them one by one.  4096
 // tokens of 32 heads of 128: 304, 249, 253 and 221 us with 6, 8, 12 and 16 chunks (the rule
@@ -90,7 +94,7 @@ int64_t segment_chunks(int64_t L, int64_t S, int64_t T, int64_t H, int64_t DV, b
   if (g_segment_override >= 0) return g_segment_override;
   const int64_t chunks = (L + kC - 1) / kC, tiles = (DV + 31) / 32;
   const int64_t waves = S * H * tiles, total = (T / kC + (packed ? S : 0)) * H * tiles;
-  if (waves >= (packed ? 1024 : 384)) return 0;
+  if (waves >= (packed ? 1024 : 320)) return 0;
   int64_t len = std::max<int64_t>(8, (total + 1023) / 1024);
   len = std::max<int64_t>(len, static_cast<int64_t>(std::ceil(std::sqrt(static_cast<double>(chunks) / 4))));
   len += len & 1;
