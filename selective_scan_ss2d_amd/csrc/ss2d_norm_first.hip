@@ -1,9 +1,14 @@
 // The block norm with channels first, (B, D, L): a block takes a tile of adjacent positions
 // and all channels, 16 lanes across the positions and the other threads across the channels;
 // sums over the channels run in registers, across a wave and through LDS.  Every tensor is
-// read once and written once.  Bound by HBM.  64 maps of 192 x 56 x 56, bfloat16 with an fp32
-// residual stream: 122 us, of a floor of 92; blocks of 512 threads at 128 registers, two per CU
-// (one, at 134 registers: 184 us; 256 threads with 12 channels each: 163).
+// read once and written once.  Bound by HBM up to D = 192.  64 maps of 192 x 56 x 56, bfloat16 with an
+// fp32 residual stream: 122 us, of a floor of 92; blocks of 512 threads at 128 registers, two per CU
+// (one, at 134 registers: 184 us; 256 threads with 12 channels each: 163).  Wider maps (as many
+// values, L = 784) take 183 us at D = 256, 197 at 384 and 261 at 768: one block per CU, narrower tiles.
+// The backward takes 312 us of a floor of 138 at D = 192, 377 at 384, and is far from it above:
+// a thread's channels with their five sums do not fit the 128 registers that 1024 threads leave
+// each, 40 of them go to scratch for D 385 to 512 (538 us), 150 to 180 up to 768 (824 us) and 320 to
+// 340 up to 1024 (1012 us).
 #include <algorithm>
 
 #include "ss2d_norm.h"
@@ -379,21 +384,32 @@ void backward(const Args& a, int64_t blocks, hipStream_t st) {
                      dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, a);
 }
 
+// Widths by powers of two and one and a half times those, so that at most a third of a block's
+// channels lie past the last one.  3.9e7 values (64 maps of 192 x 56 x 56), bfloat16 with an fp32
+// residual stream, with powers of two alone and with the steps in between: forward 155 and 139 us
+// at D = 96, 202 and 138 at 192, 216 and 197 at 384, 285 and 261 at 768; backward 312 and 285, 338
+// and 312, 570 and 377, 1151 and 824.
 template <typename T, typename Y, bool kWide>
 int launch_channels(const Args& a, bool bwd, int64_t blocks, hipStream_t st) {
   if (bwd) {
     if (a.D <= 64) backward<T, Y, 256, 4, 4, kWide>(a, blocks, st);
+    else if (a.D <= 96) backward<T, Y, 512, 3, 4, kWide>(a, blocks, st);
     else if (a.D <= 128) backward<T, Y, 512, 4, 4, kWide>(a, blocks, st);
     else if (a.D <= 192) backward<T, Y, 512, 6, 2, kWide>(a, blocks, st);
     else if (a.D <= 256) backward<T, Y, 512, 8, 2, kWide>(a, blocks, st);
+    else if (a.D <= 384) backward<T, Y, 1024, 6, 1, kWide>(a, blocks, st);
     else if (a.D <= 512) backward<T, Y, 1024, 8, 1, kWide>(a, blocks, st);
+    else if (a.D <= 768) backward<T, Y, 1024, 12, 1, kWide>(a, blocks, st);
     else backward<T, Y, 1024, 16, 1, kWide>(a, blocks, st);
   } else {
     if (a.D <= 64) forward<T, Y, 256, 4, 4, kWide>(a, blocks, st);
+    else if (a.D <= 96) forward<T, Y, 512, 3, 4, kWide>(a, blocks, st);
     else if (a.D <= 128) forward<T, Y, 512, 4, 4, kWide>(a, blocks, st);
     else if (a.D <= 192) forward<T, Y, 512, 6, 4, kWide>(a, blocks, st);
     else if (a.D <= 256) forward<T, Y, 512, 8, 4, kWide>(a, blocks, st);
+    else if (a.D <= 384) forward<T, Y, 1024, 6, 2, kWide>(a, blocks, st);
     else if (a.D <= 512) forward<T, Y, 1024, 8, 2, kWide>(a, blocks, st);
+    else if (a.D <= 768) forward<T, Y, 1024, 12, 1, kWide>(a, blocks, st);
     else forward<T, Y, 1024, 16, 1, kWide>(a, blocks, st);
   }
   return static_cast<int>(hipGetLastError());
