@@ -470,9 +470,9 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * Arithmetic: S, the chunk's triangular solve and every sum are fp32 for both data types.
  * For bfloat16 data a product's fp32 operand runs on the bf16 matrix cores as the sum of 3
  * bfloat16 terms (24 bits), those of o, dq and dk as 2 (17 bits) before their single rounding;
- * fp32 data use the fp32 matrix instructions.  Few or long sequences are cut into segments that run at once: each
- * gives its end state from a zero start, Z, and its matrix M, and the states between them follow
- * from S <- M S + Z, on operands of 3 terms for either type.
+ * fp32 data use the fp32 matrix instructions.  Few or long sequences are cut into segments that
+ * run at once: each gives its end state from a zero start, Z, and its matrix M, and the states
+ * between them follow from S <- M S + Z, on operands of 3 terms for either type.
  *
  * NaN and infinities: o, the end states and the gradients are NaN or infinite wherever the
  * definition makes them so (an infinity may come out as NaN).  In o and the end states nothing
@@ -490,7 +490,8 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * if dh0 is not NULL, h0 in fp32; all contiguous.  saved: what ss1d_delta_forward kept for the
  * same inputs (other contents give undefined gradients), or NULL to compute it again.  dout
  * is contiguous.  Rows outside of every sequence are left as they are.  The gradient of a g
- * below -1000, whose decay is 0, is 0.
+ * below -1000, whose decay is 0, is 0; others are differences of sums, fp32, of dout.o and dv.v
+ * over up to 64 tokens: their accuracy is absolute, also where strong decays leave little of them.
  *
  * ss1d_delta_step is the form for serving: T tokens (few) of each of B sequences, whose
  * states are updated in place: row b's state is state[slots[b]], or state[b] with slots

@@ -86,3 +86,43 @@ def test_dq_and_dk(case, chunks, dtype):
         err = (got[n].double().cpu() - ref[n]).abs()
         over = err - tol - (du.BF16_HALF * ref[n].abs() if dtype == torch.bfloat16 else 0.0)
         assert float(over.max()) <= 0, f"d{n}: over by {float(over.max()):.2e} (error {float(err.max()):.2e})"
+
+
+def gate_magnitudes(t, scale):
+    """The summed magnitudes of what dg of every token is the difference of: do.o and dv.v of the
+    tokens from it to its block's end, and <dS, S> behind the block (float64)."""
+    q, k, v, g, beta = (t[n].double() for n in du.NAMES)
+    B, L, H, DV = v.shape
+    rep = H // q.shape[2]
+    out = torch.zeros(B, L, H).double()
+    for b in range(B):
+        S = t["h0"][b].double() if t["h0"] is not None else torch.zeros(H, q.shape[3], DV).double()
+        o, end, states = du.rule(q[b], k[b], v[b], g[b], beta[b], scale, S)
+        kb, qb = k[b].repeat_interleave(rep, 1), q[b].repeat_interleave(rep, 1)
+        do = t["do"][b].double()
+        dS, total = torch.zeros_like(S), torch.zeros(H).double()
+        for j in range(L - 1, -1, -1):
+            if j == L - 1 or (j + 1) % BLOCK == 0:
+                total = (dS.abs() * (states[j + 1] if j + 1 < L else end).abs()).sum((1, 2))
+            dS = dS + scale * qb[j][:, :, None] * do[j][:, None, :]
+            dv = beta[b, j][:, None] * (dS * kb[j][:, :, None]).sum(1)
+            dS = (dS - kb[j][:, :, None] * dv[:, None, :]) * g[b, j].exp()[:, None, None]
+            total = total + (do[j].abs() * o[j].abs()).sum(1) + (dv.abs() * v[b, j].abs()).sum(1)
+            out[b, j] = total
+    return out
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("least, most", [(0.0, 0.2), (0.0, 10.0), (0.0, 80.0), (5.0, 20.0), (40.0, 80.0)])
+def test_dg_of_decays_from_weak_to_strong(least, most, dtype):
+    """dg keeps an absolute accuracy, also where strong decays leave almost nothing of it: fp32
+    roundings of what it is the difference of, each the end of sums over DK, DV and a chunk."""
+    t = du.make_inputs(1, 200, 1, 2, 64, 48, dtype, seed=int(most), h0=1)
+    t["g"] = -(least + (most - least) * torch.rand(t["g"].shape, generator=torch.Generator().manual_seed(1)))
+    d = du.to_gpu(t)
+    args = [d[n] for n in du.NAMES]
+    got = ss.ss1d_delta_backward(*args, d["do"], scale=0.3, initial_state=d["h0"])
+    ref, _ = du.adjoint(t, 0.3)
+    tol = du.F32_HALF * (64 + 48 + 5 * BLOCK) * gate_magnitudes(t, 0.3)
+    over = (got["g"].double().cpu() - ref["g"]).abs() - tol
+    assert float(over.max()) <= 0, f"over by {float(over.max()):.2e}"
