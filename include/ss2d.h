@@ -499,7 +499,11 @@ int ss1d_bidir_forward_routes_lr(const void *u, const void *dt_lr, const float *
  * its rows of o included.  Rows that name the same slot are successive tokens of one
  * sequence, in row order.
  *
- * The shared conventions hold, except that kernel timing does not cover these entry points.
+ * The shared conventions hold, except that kernel timing does not cover these entry points, and
+ * that under stream capture scratch has to be the caller's: the _ws forms take it (scratch: device
+ * memory aligned to 256, of scratch_bytes >= ss1d_delta_scratch_bytes, SS2D_ERR_SCRATCH below; NULL:
+ * the library's, and SS2D_ERR_SCRATCH under capture), the others use the library's.  A captured
+ * graph then holds kernels only, and its scratch is its own for as long as the caller keeps it.
  * Scratch (the step has none): per token, the chunks' matrices, about 0.4 KB per value head and
  * 6 DK (fp32: 12 DK) bytes per key head, DK rounded up to 32, 64 or 128; per segment and head,
  * M, Z and a state; the backward's gradients of the states in fp32, one per 64 tokens and head,
@@ -509,6 +513,17 @@ int ss1d_delta_forward(const void *q, const void *k, const void *v, const float 
                        float *ht, void *saved, int64_t B, int64_t L, int64_t S, int64_t HK,
                        int64_t H, int64_t DK, int64_t DV, const int64_t *strides, float scale,
                        int dtype, void *stream);
+
+int ss1d_delta_forward_ws(const void *q, const void *k, const void *v, const float *g,
+                          const float *beta, const float *h0, const int32_t *cu_seqlens, void *o,
+                          float *ht, void *saved, void *scratch, int64_t scratch_bytes, int64_t B,
+                          int64_t L, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                          const int64_t *strides, float scale, int dtype, void *stream);
+
+/* Bytes of scratch (-1 for sizes that the operator rejects) of a forward (backward 0) or a backward
+ * (1); kept: whether `saved` is given to it; packed: whether cu_seqlens is. */
+int64_t ss1d_delta_scratch_bytes(int backward, int kept, int64_t B, int64_t L, int64_t S, int64_t HK,
+                                 int64_t H, int64_t DK, int64_t DV, int dtype, int packed);
 
 /* Bytes of `saved` (-1 for sizes that the operator rejects); packed: whether cu_seqlens is
  * given. */
@@ -521,6 +536,14 @@ int ss1d_delta_backward(const void *q, const void *k, const void *v, const float
                         void *dv, float *dg, float *dbeta, float *dh0, int64_t B, int64_t L,
                         int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
                         const int64_t *strides, float scale, int dtype, void *stream);
+
+int ss1d_delta_backward_ws(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, const float *h0, const int32_t *cu_seqlens,
+                           const void *saved, const void *dout, const float *dht, void *dq, void *dk,
+                           void *dv, float *dg, float *dbeta, float *dh0, void *scratch,
+                           int64_t scratch_bytes, int64_t B, int64_t L, int64_t S, int64_t HK,
+                           int64_t H, int64_t DK, int64_t DV, const int64_t *strides, float scale,
+                           int dtype, void *stream);
 
 /* Testing and tuning, as ss2d_set_launch_plan: for later calls from this host thread, the
  * chunks of 32 tokens per segment (even; 0: whole sequences, -1: automatic) that the forward
@@ -561,7 +584,8 @@ int ss1d_delta_step(const void *q, const void *k, const void *v, const float *g,
  * dn are needed with w_pre.  The vectors' sums over rows run in a fixed order (no atomics);
  * without rows they are 0.
  *
- * The shared conventions hold; kernel timing does not cover these entry points. */
+ * The shared conventions hold; kernel timing does not cover these entry points, and the backward's
+ * scratch is as the gated delta rule's (ss2d_norm_backward_ws, ss2d_norm_scratch_bytes). */
 int ss2d_norm_forward(const void *h, const void *z, const void *residual, const float *res_scale,
                       const float *w_post, const float *b_post, const float *w_pre,
                       const float *b_pre, void *y, void *n, int64_t B, int64_t L, int64_t D,
@@ -574,6 +598,17 @@ int ss2d_norm_backward(const void *h, const void *z, const float *res_scale, con
                        float *dw_post, float *db_post, float *dw_pre, float *db_pre, int64_t B,
                        int64_t L, int64_t D, int64_t G, int channels_first, int layer, float eps,
                        int dtype, int ytype, void *stream);
+
+int ss2d_norm_backward_ws(const void *h, const void *z, const float *res_scale, const float *w_post,
+                          const float *b_post, const float *w_pre, const void *y, const void *dy,
+                          const void *dn, void *dh, void *dz, void *dresidual, float *dres_scale,
+                          float *dw_post, float *db_post, float *dw_pre, float *db_pre, void *scratch,
+                          int64_t scratch_bytes, int64_t B, int64_t L, int64_t D, int64_t G,
+                          int channels_first, int layer, float eps, int dtype, int ytype,
+                          void *stream);
+
+/* Bytes of ss2d_norm_backward_ws's scratch (-1 for sizes that it rejects). */
+int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int channels_first);
 
 /* ---- launch-plan override (testing and tuning, not part of the operator) ---------------
  * Sets, for calls made later from the calling host thread only, the lanes that share one

@@ -72,6 +72,11 @@ SIGNATURES = {
                                                                    ctypes.c_int, _P]),
     "ss1d_delta_backward": (ctypes.c_int, [_P] * 16 + [_I64] * 7 + [_P, ctypes.c_float,
                                                                     ctypes.c_int, _P]),
+    "ss1d_delta_forward_ws": (ctypes.c_int, [_P] * 11 + [_I64] * 8 + [_P, ctypes.c_float,
+                                                                      ctypes.c_int, _P]),
+    "ss1d_delta_backward_ws": (ctypes.c_int, [_P] * 17 + [_I64] * 8 + [_P, ctypes.c_float,
+                                                                       ctypes.c_int, _P]),
+    "ss1d_delta_scratch_bytes": (_I64, [ctypes.c_int] * 2 + [_I64] * 7 + [ctypes.c_int] * 2),
     "ss1d_delta_set_segment": (ctypes.c_int, [_I64]),
     "ss1d_delta_saved_bytes": (_I64, [_I64] * 6 + [ctypes.c_int]),
     "ss1d_delta_step": (ctypes.c_int, [_P] * 8 + [_I64] * 7 + [_P, ctypes.c_float, ctypes.c_int,
@@ -80,6 +85,9 @@ SIGNATURES = {
                           + [ctypes.c_float] + [ctypes.c_int] * 2 + [_P]),
     "ss2d_norm_backward": (ctypes.c_int, [_P] * 17 + [_I64] * 4 + [ctypes.c_int] * 2
                            + [ctypes.c_float] + [ctypes.c_int] * 2 + [_P]),
+    "ss2d_norm_backward_ws": (ctypes.c_int, [_P] * 18 + [_I64] * 5 + [ctypes.c_int] * 2
+                              + [ctypes.c_float] + [ctypes.c_int] * 2 + [_P]),
+    "ss2d_norm_scratch_bytes": (_I64, [_I64] * 4 + [ctypes.c_int]),
     "ss2d_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ss2d_abi_version": (ctypes.c_int, []),
     "ss2d_last_hip_error": (ctypes.c_int, []),

@@ -61,3 +61,10 @@ def output(name, t, shape, dtype, device):
         return _torch().empty(shape, dtype=dtype, device=device)
     expect(name, t, shape, dtype, device)
     return t
+
+
+def scratch(size, device):
+    """Scratch of a call on the current stream (size -1: of a call that will be refused).  It goes
+    back to torch's allocator when the call returns, which hands it to later work of the same stream
+    only; in a captured graph it belongs to the graph."""
+    return _torch().empty(max(256, size), dtype=_torch().uint8, device=device)

@@ -9,7 +9,7 @@ import ctypes
 from . import _binding as bnd
 from ._binding import _torch
 from ._call import (code_of, expect as _expect, handle as _handle, output as _output, ptr as _ptr,
-                    scope as _scope)
+                    scope as _scope, scratch as _scratch)
 
 
 def _strided(name, t, shape, dtype, device):
@@ -85,11 +85,13 @@ def _forward(q, k, v, g, beta, scale, cu_seqlens, initial_state, final_state, o,
         if save:
             size = lib.ss1d_delta_saved_bytes(B, L, S, H, DK, DV, cu_seqlens is not None)
             saved = torch.empty(max(0, size), dtype=torch.uint8, device=dev)
-        bnd._check(lib.ss1d_delta_forward(
+        ws = _scratch(lib.ss1d_delta_scratch_bytes(0, save, B, L, S, HK, H, DK, DV, code,
+                                                   cu_seqlens is not None), dev)
+        bnd._check(lib.ss1d_delta_forward_ws(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-            _ptr(initial_state), _ptr(cu_seqlens), o.data_ptr(), _ptr(ht), _ptr(saved), B, L, S,
-            HK, H, DK, DV, strides, DK ** -0.5 if scale is None else scale, code,
-            _handle(dev, stream)))
+            _ptr(initial_state), _ptr(cu_seqlens), o.data_ptr(), _ptr(ht), _ptr(saved),
+            ws.data_ptr(), ws.numel(), B, L, S, HK, H, DK, DV, strides,
+            DK ** -0.5 if scale is None else scale, code, _handle(dev, stream)))
     return o, ht, saved
 
 
@@ -150,12 +152,15 @@ def ss1d_delta_backward(q, k, v, g, beta, do, scale=None, cu_seqlens=None, initi
              for n, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta))}
         if initial_state is not None:
             d["initial_state"] = torch.empty_like(initial_state)
-        bnd._check(lib.ss1d_delta_backward(
+        ws = _scratch(lib.ss1d_delta_scratch_bytes(1, saved is not None, B, L, S, HK, H, DK, DV,
+                                                   code, cu_seqlens is not None), dev)
+        bnd._check(lib.ss1d_delta_backward_ws(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
             _ptr(initial_state), _ptr(cu_seqlens), _ptr(saved), do.data_ptr(), _ptr(dstate),
             d["q"].data_ptr(), d["k"].data_ptr(), d["v"].data_ptr(), d["g"].data_ptr(),
-            d["beta"].data_ptr(), _ptr(d.get("initial_state")), B, L, S, HK, H, DK, DV, strides,
-            DK ** -0.5 if scale is None else scale, code, _handle(dev, stream)))
+            d["beta"].data_ptr(), _ptr(d.get("initial_state")), ws.data_ptr(), ws.numel(), B, L, S,
+            HK, H, DK, DV, strides, DK ** -0.5 if scale is None else scale, code,
+            _handle(dev, stream)))
     return d
 
 

@@ -6,7 +6,7 @@ from __future__ import annotations
 
 from . import _binding as bnd
 from ._binding import _torch
-from ._call import code_of, expect, handle, output, ptr, scope
+from ._call import code_of, expect, handle, output, ptr, scope, scratch
 
 
 def _shape(h, channels_first):
@@ -129,11 +129,12 @@ def ss2d_norm_backward(h, y=None, dy=None, dn=None, residual=True, w_post=None, 
                         ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)):
             if t is not None:
                 d[name] = torch.empty_like(t)
-        bnd._check(lib.ss2d_norm_backward(
+        ws = scratch(lib.ss2d_norm_scratch_bytes(B, L, D, G, 1 if channels_first else 0), dev)
+        bnd._check(lib.ss2d_norm_backward_ws(
             h.data_ptr(), ptr(z), ptr(res_scale), ptr(w_post), ptr(b_post), ptr(w_pre), ptr(y),
             ptr(dy), ptr(dn), d["h"].data_ptr(), *[ptr(d.get(k)) for k in
                                                    ("z", "residual", "res_scale", "w_post",
                                                     "b_post", "w_pre", "b_pre")],
-            B, L, D, G, 1 if channels_first else 0, 1 if layer else 0, eps, code, code_of(ytype),
-            handle(dev, stream)))
+            ws.data_ptr(), ws.numel(), B, L, D, G, 1 if channels_first else 0, 1 if layer else 0,
+            eps, code, code_of(ytype), handle(dev, stream)))
     return d

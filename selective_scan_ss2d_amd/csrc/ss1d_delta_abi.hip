@@ -165,6 +165,24 @@ Scratch scratch_layout(const Args& a, int dtype) {
   return s;
 }
 
+// What follows from the sizes alone.
+void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+               bool packed) {
+  const int64_t T = B * L;
+  a->S = S;
+  a->L = L;
+  a->T = T;
+  a->H = static_cast<int>(H);
+  a->HK = static_cast<int>(HK);
+  a->rep = static_cast<int>(H / HK);
+  a->DK = static_cast<int>(DK);
+  a->DV = static_cast<int>(DV);
+  a->slots = slot_count(L, S, T, packed, ss2d::delta::kC);
+  a->marks_n = slot_count(L, S, T, packed, ss2d::delta::kMark);
+  a->seglen = segment_chunks(L, S, T, H, DV, packed);
+  a->seg_slots = a->seglen ? slot_count(L, S, T, packed, a->seglen * ss2d::delta::kC) : 0;
+}
+
 // The inputs of the forward and the backward: checks them and fills `a`; the spans of the
 // inputs go to ins[0..5].
 int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, const float* g,
@@ -172,6 +190,7 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
                int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV, const int64_t* strides,
                float scale, int dtype) {
   const int64_t T = B * L, e = dtype == SS2D_F32 ? 4 : 2;
+  set_sizes(a, B, L, S, HK, H, DK, DV, cu != nullptr);
   a->q = q;
   a->k = k;
   a->v = v;
@@ -187,19 +206,7 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
     a->sk = {strides[3], strides[4], strides[5]};
     a->sv = {strides[6], strides[7], strides[8]};
   }
-  a->S = S;
-  a->L = L;
-  a->T = T;
-  a->H = static_cast<int>(H);
-  a->HK = static_cast<int>(HK);
-  a->rep = static_cast<int>(H / HK);
-  a->DK = static_cast<int>(DK);
-  a->DV = static_cast<int>(DV);
   a->scale = scale;
-  a->slots = slot_count(L, S, T, cu != nullptr, ss2d::delta::kC);
-  a->marks_n = slot_count(L, S, T, cu != nullptr, ss2d::delta::kMark);
-  a->seglen = segment_chunks(L, S, T, H, DV, cu != nullptr);
-  a->seg_slots = a->seglen ? slot_count(L, S, T, cu != nullptr, a->seglen * ss2d::delta::kC) : 0;
   const int64_t qb = strided_bytes(B, L, HK, DK, a->sq, e),
                 kb = strided_bytes(B, L, HK, DK, a->sk, e),
                 vb = strided_bytes(B, L, H, DV, a->sv, e);
@@ -224,6 +231,50 @@ int set_inputs(Args* a, Span* ins, const void* q, const void* k, const void* v, 
       a->marks_n * HK * 64 * ss2d::delta::kGradWaves > kMaxThreads || (a->marks_n * H / 4 + 1) * 256 > kMaxThreads)
     return SS2D_ERR_SHAPE;
   return SS2D_OK;
+}
+
+// The backward's: the chunk matrices (first the forward's where nothing was kept, then the
+// backward's in their place), the states' gradients and dv in fp32, the gates' partial sums, and
+// what a forward keeps where nothing was.
+struct BackwardScratch {
+  Scratch chunks;
+  size_t dmarks, dvs, pbeta, pgate, pdots, keep, unused_o, bytes;
+};
+BackwardScratch backward_layout(const Args& a, int dtype, bool kept, bool packed) {
+  using ss2d::host_align256;
+  const int64_t tiles = (a.DV + 31) / 32, e = dtype == SS2D_F32 ? 4 : 2;
+  const size_t rows = size_t(a.T) * a.H, marks = size_t(a.marks_n) * a.H;
+  BackwardScratch w;
+  w.chunks = scratch_layout(a, dtype);
+  w.dmarks = host_align256(w.chunks.bytes);
+  w.dvs = w.dmarks + host_align256(marks * a.DK * a.DV * 4);
+  w.pbeta = w.dvs + (dtype == SS2D_F32 ? 0 : host_align256(rows * a.DV * 4));
+  w.pgate = w.pbeta + host_align256(tiles * rows * 4);
+  w.pdots = w.pgate + host_align256(tiles * rows * 4);
+  w.keep = w.pdots + host_align256(marks * tiles * 4);
+  w.unused_o = w.keep + (kept ? 0 : size_t(saved_layout(a.L, a.S, a.T, a.H, a.DK, a.DV, packed).bytes));
+  w.bytes = w.unused_o + (kept ? 0 : host_align256(rows * a.DV * e));
+  return w;
+}
+
+// The caller's scratch, or the library's (`own`), which hip records as nodes of their own in a
+// captured graph: refused there.
+struct Workspace {
+  char* at = nullptr;
+  bool own = false;
+};
+int take_scratch(Workspace* w, void* given, int64_t given_bytes, size_t bytes, hipStream_t st) {
+  if (given) {
+    w->at = static_cast<char*>(given);
+    return given_bytes >= 0 && size_t(given_bytes) >= bytes ? SS2D_OK : SS2D_ERR_SCRATCH;
+  }
+  w->own = true;
+  return ss2d::host_scratch_outside_graphs(&w->at, bytes, st);
+}
+int finish(const Workspace& w, int err, hipStream_t st) {
+  const hipError_t fe = w.own ? hipFreeAsync(w.at, st) : hipSuccess;
+  if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
+  return fe == hipSuccess ? SS2D_OK : ss2d::host_hip_fail(fe);
 }
 
 bool aligned_keys(const Args& a, int64_t e) {
@@ -262,11 +313,31 @@ int64_t ss1d_delta_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t H, int64
   return saved_layout(L, S, B * L, H, DK, DV, packed != 0).bytes;
 }
 
+int64_t ss1d_delta_scratch_bytes(int backward, int kept, int64_t B, int64_t L, int64_t S, int64_t HK,
+                                 int64_t H, int64_t DK, int64_t DV, int dtype, int packed) {
+  if (check_sizes(B, L, S, HK, H, DK, DV, dtype, packed != 0) != SS2D_OK) return -1;
+  Args a{};
+  set_sizes(&a, B, L, S, HK, H, DK, DV, packed != 0);
+  a.p_planes = backward || kept ? 3 : 2;
+  const size_t bytes = backward ? backward_layout(a, dtype, kept != 0, packed != 0).bytes
+                                : scratch_layout(a, dtype).bytes;
+  return static_cast<int64_t>(bytes);
+}
+
 int ss1d_delta_forward(const void* q, const void* k, const void* v, const float* g,
                        const float* beta, const float* h0, const int32_t* cu_seqlens, void* o,
                        float* ht, void* saved, int64_t B, int64_t L, int64_t S, int64_t HK,
                        int64_t H, int64_t DK, int64_t DV, const int64_t* strides, float scale,
                        int dtype, void* stream) {
+  return ss1d_delta_forward_ws(q, k, v, g, beta, h0, cu_seqlens, o, ht, saved, nullptr, 0, B, L, S, HK, H, DK,
+                               DV, strides, scale, dtype, stream);
+}
+
+int ss1d_delta_forward_ws(const void* q, const void* k, const void* v, const float* g,
+                          const float* beta, const float* h0, const int32_t* cu_seqlens, void* o,
+                          float* ht, void* saved, void* scratch, int64_t scratch_bytes, int64_t B,
+                          int64_t L, int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
+                          const int64_t* strides, float scale, int dtype, void* stream) {
   const bool packed = cu_seqlens != nullptr;
   int rc = check_sizes(B, L, S, HK, H, DK, DV, dtype, packed);
   if (rc != SS2D_OK) return rc;
@@ -282,12 +353,16 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
   if (rc != SS2D_OK) return rc;
   a.o = o;
   a.ht = ht;
-  if (misaligned(o, static_cast<uintptr_t>(e)) || misaligned(ht, 4) || misaligned(saved, 256))
+  if (misaligned(o, static_cast<uintptr_t>(e)) || misaligned(ht, 4) || misaligned(saved, 256) ||
+      misaligned(scratch, 256))
     return SS2D_ERR_ALIGN;
   const int64_t state = S * H * DK * DV * 4;
   const Saved sv = saved_layout(L, S, T, H, DK, DV, packed);
-  const Span outs[] = {{o, T * H * DV * e}, {ht, state}, {saved, sv.bytes}};
-  rc = check_pointers(ins, 6, outs, 3);
+  a.p_planes = saved ? 3 : 2;
+  const Scratch w = scratch_layout(a, dtype);
+  const Span outs[] = {{o, T * H * DV * e}, {ht, state}, {saved, sv.bytes},
+                       {scratch, static_cast<int64_t>(w.bytes)}};
+  rc = check_pointers(ins, 6, outs, 4);
   if (rc != SS2D_OK) return rc;
   // the end states may replace the initial ones: each wave reads its columns first, several
   // segments of a sequence read the join's copy
@@ -296,19 +371,13 @@ int ss1d_delta_forward(const void* q, const void* k, const void* v, const float*
     if (!(x.p == ht && ht == h0) && check_pointers(first, 1, &x, 1) != SS2D_OK)
       return SS2D_ERR_ALIAS;
 
-  a.p_planes = saved ? 3 : 2;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const Scratch w = scratch_layout(a, dtype);
-  char* ws = nullptr;
-  rc = ss2d::host_scratch_alloc(&ws, w.bytes, st);
+  Workspace ws;
+  rc = take_scratch(&ws, scratch, scratch_bytes, w.bytes, st);
   if (rc != SS2D_OK) return rc;
-  set_scratch(&a, ws, w);
+  set_scratch(&a, ws.at, w);
   if (saved) set_saved(&a, saved, sv);
-  const int err = run_forward(a, dtype, saved != nullptr, st);
-  const hipError_t fe = hipFreeAsync(ws, st);
-  if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
-  if (fe != hipSuccess) return ss2d::host_hip_fail(fe);
-  return SS2D_OK;
+  return finish(ws, run_forward(a, dtype, saved != nullptr, st), st);
 }
 
 int ss1d_delta_backward(const void* q, const void* k, const void* v, const float* g,
@@ -317,6 +386,17 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
                         void* dv, float* dg, float* dbeta, float* dh0, int64_t B, int64_t L,
                         int64_t S, int64_t HK, int64_t H, int64_t DK, int64_t DV,
                         const int64_t* strides, float scale, int dtype, void* stream) {
+  return ss1d_delta_backward_ws(q, k, v, g, beta, h0, cu_seqlens, saved, dout, dht, dq, dk, dv, dg, dbeta, dh0,
+                                nullptr, 0, B, L, S, HK, H, DK, DV, strides, scale, dtype, stream);
+}
+
+int ss1d_delta_backward_ws(const void* q, const void* k, const void* v, const float* g,
+                           const float* beta, const float* h0, const int32_t* cu_seqlens,
+                           const void* saved, const void* dout, const float* dht, void* dq, void* dk,
+                           void* dv, float* dg, float* dbeta, float* dh0, void* scratch,
+                           int64_t scratch_bytes, int64_t B, int64_t L, int64_t S, int64_t HK,
+                           int64_t H, int64_t DK, int64_t DV, const int64_t* strides, float scale,
+                           int dtype, void* stream) {
   const bool packed = cu_seqlens != nullptr;
   int rc = check_sizes(B, L, S, HK, H, DK, DV, dtype, packed);
   if (rc != SS2D_OK) return rc;
@@ -337,16 +417,19 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   for (const void* p : {static_cast<const void*>(dht), static_cast<const void*>(dg),
                         static_cast<const void*>(dbeta), static_cast<const void*>(dh0)})
     if (misaligned(p, 4)) return SS2D_ERR_ALIGN;
-  if (misaligned(saved, 256)) return SS2D_ERR_ALIGN;
+  if (misaligned(saved, 256) || misaligned(scratch, 256)) return SS2D_ERR_ALIGN;
   const int64_t state = S * H * DK * DV * 4;
   const Saved sv = saved_layout(L, S, T, H, DK, DV, packed);
+  a.p_planes = 3;
+  const BackwardScratch w = backward_layout(a, dtype, saved != nullptr, packed);
   ins[6] = {h0, state};
   ins[7] = {saved, sv.bytes};
   ins[8] = {dout, T * H * DV * e};
   ins[9] = {dht, state};
   const Span outs[] = {{dq, T * HK * DK * e}, {dk, T * HK * DK * e}, {dv, T * H * DV * e},
-                       {dg, T * H * 4}, {dbeta, T * H * 4}, {dh0, state}};
-  rc = check_pointers(ins, 10, outs, 6);
+                       {dg, T * H * 4}, {dbeta, T * H * 4}, {dh0, state},
+                       {scratch, static_cast<int64_t>(w.bytes)}};
+  rc = check_pointers(ins, 10, outs, 7);
   if (rc != SS2D_OK) return rc;
   a.dout = dout;
   a.dht = dht;
@@ -356,36 +439,23 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   a.dg = dg;
   a.dbeta = dbeta;
   a.dh0 = dh0;
-  a.p_planes = 3;
 
-  // scratch: the chunk matrices (first the forward's where nothing was kept, then the
-  // backward's in their place), the states' gradients and dv in fp32, the gates' partial sums
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int64_t tiles = (DV + 31) / 32;
-  const Scratch w = scratch_layout(a, dtype);
-  const size_t dmarks = w.bytes,
-               dvs = dmarks + ss2d::host_align256(size_t(a.marks_n) * H * DK * DV * 4),
-               pbeta = dvs + (dtype == SS2D_F32 ? 0 : ss2d::host_align256(size_t(T) * H * DV * 4)),
-               pgate = pbeta + ss2d::host_align256(size_t(tiles) * T * H * 4),
-               pdots = pgate + ss2d::host_align256(size_t(tiles) * T * H * 4),
-               keep = pdots + ss2d::host_align256(size_t(a.marks_n) * H * tiles * 4),
-               unused_o = keep + (saved ? 0 : size_t(sv.bytes)),
-               bytes = unused_o + (saved ? 0 : ss2d::host_align256(size_t(T) * H * DV * e));
-  char* ws = nullptr;
-  rc = ss2d::host_scratch_alloc(&ws, bytes, st);
+  Workspace ws;
+  rc = take_scratch(&ws, scratch, scratch_bytes, w.bytes, st);
   if (rc != SS2D_OK) return rc;
-  set_scratch(&a, ws, w);
-  a.dmarks = reinterpret_cast<float*>(ws + dmarks);
-  a.dvs = dtype == SS2D_F32 ? static_cast<float*>(dv) : reinterpret_cast<float*>(ws + dvs);
-  a.pbeta = reinterpret_cast<float*>(ws + pbeta);
-  a.pgate = reinterpret_cast<float*>(ws + pgate);
-  a.pdots = reinterpret_cast<float*>(ws + pdots);
+  set_scratch(&a, ws.at, w.chunks);
+  a.dmarks = reinterpret_cast<float*>(ws.at + w.dmarks);
+  a.dvs = dtype == SS2D_F32 ? static_cast<float*>(dv) : reinterpret_cast<float*>(ws.at + w.dvs);
+  a.pbeta = reinterpret_cast<float*>(ws.at + w.pbeta);
+  a.pgate = reinterpret_cast<float*>(ws.at + w.pgate);
+  a.pdots = reinterpret_cast<float*>(ws.at + w.pdots);
   int err = 0;
   if (saved) {
     set_saved(&a, const_cast<void*>(saved), sv);
   } else {
-    set_saved(&a, ws + keep, sv);
-    a.o = ws + unused_o;
+    set_saved(&a, ws.at + w.keep, sv);
+    a.o = ws.at + w.unused_o;
     err = run_forward(a, dtype, true, st);
   }
   const bool alk = aligned_keys(a, e);
@@ -397,10 +467,7 @@ int ss1d_delta_backward(const void* q, const void* k, const void* v, const float
   if (!err) err = ss2d::delta::launch_adjoint(a, dtype, false, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_grads(a, dtype, alv, st);
   if (!err && a.marks_n > 0) err = ss2d::delta::launch_gate_grads(a, st);
-  const hipError_t fe = hipFreeAsync(ws, st);
-  if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
-  if (fe != hipSuccess) return ss2d::host_hip_fail(fe);
-  return SS2D_OK;
+  return finish(ws, err, st);
 }
 
 int ss1d_delta_step(const void* q, const void* k, const void* v, const float* g,

@@ -819,6 +819,12 @@ int ss2d::host_hip_fail(hipError_t e) { return hip_fail(e); }
 int ss2d::host_scratch_alloc(char** ws, size_t bytes, hipStream_t st) {
   return scratch_alloc(ws, bytes, st);
 }
+int ss2d::host_scratch_outside_graphs(char** ws, size_t bytes, hipStream_t st) {
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  const hipError_t e = hipStreamIsCapturing(st, &status);
+  if (e != hipSuccess) return hip_fail(e);
+  return status == hipStreamCaptureStatusNone ? scratch_alloc(ws, bytes, st) : SS2D_ERR_SCRATCH;
+}
 
 extern "C" {
 

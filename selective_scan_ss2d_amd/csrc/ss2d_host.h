@@ -14,6 +14,10 @@ int host_hip_fail(hipError_t e);
 // Stream-ordered scratch on the current device; release it with hipFreeAsync on `st`.
 int host_scratch_alloc(char** ws, size_t bytes, hipStream_t st);
 
+// The same for callers that can bring scratch of their own: SS2D_ERR_SCRATCH while `st` is being
+// captured, where the allocation would become a node of the graph.
+int host_scratch_outside_graphs(char** ws, size_t bytes, hipStream_t st);
+
 constexpr int64_t kHostMaxElems = int64_t(1) << 62;
 
 inline bool host_mul_ok(int64_t a, int64_t b, int64_t* out) {

@@ -46,6 +46,23 @@ void set_shape(Args* a, int64_t B, int64_t L, int64_t D, int64_t G, int first, i
   a->eps = eps;
 }
 
+// The backward's plan, and its scratch: the blocks' sums of the four vectors, and of res_scale's
+// gradient where several blocks share a group.  Without rows there are no blocks, and the sums
+// over them write zeros.
+struct Scratch {
+  int64_t blocks;
+  size_t parts, bytes;
+};
+Scratch scratch_layout(Args* a, int first) {
+  const bool none = a->B == 0 || a->L == 0;
+  Scratch w;
+  w.blocks = none ? 0 : ss2d::norm::plan_norm_bwd(a, first != 0);
+  if (none) a->blocks_per_group = 0;
+  w.parts = ss2d::host_align256(size_t(w.blocks) * ss2d::norm::kSums * a->D * 4);
+  w.bytes = w.parts + (a->blocks_per_group > 1 ? size_t(a->G) * a->blocks_per_group * a->D * 4 : 0);
+  return w;
+}
+
 int overlap(const Span* outs, int n_out, const Span* ins, int n_in) {
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < n_in; ++j)
@@ -112,12 +129,31 @@ int ss2d_norm_forward(const void* h, const void* z, const void* residual, const 
   return err ? ss2d::host_hip_fail(static_cast<hipError_t>(err)) : SS2D_OK;
 }
 
+int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int channels_first) {
+  if (check(B, L, D, G, channels_first, 0.0f, SS2D_F32, SS2D_F32) != SS2D_OK) return -1;
+  Args a{};
+  set_shape(&a, B, L, D, G, channels_first, 0, 0.0f);
+  return static_cast<int64_t>(scratch_layout(&a, channels_first).bytes);
+}
+
 int ss2d_norm_backward(const void* h, const void* z, const float* res_scale, const float* w_post,
                        const float* b_post, const float* w_pre, const void* y, const void* dy,
                        const void* dn, void* dh, void* dz, void* dresidual, float* dres_scale,
                        float* dw_post, float* db_post, float* dw_pre, float* db_pre, int64_t B,
                        int64_t L, int64_t D, int64_t G, int channels_first, int layer, float eps,
                        int dtype, int ytype, void* stream) {
+  return ss2d_norm_backward_ws(h, z, res_scale, w_post, b_post, w_pre, y, dy, dn, dh, dz, dresidual, dres_scale,
+                               dw_post, db_post, dw_pre, db_pre, nullptr, 0, B, L, D, G, channels_first, layer,
+                               eps, dtype, ytype, stream);
+}
+
+int ss2d_norm_backward_ws(const void* h, const void* z, const float* res_scale, const float* w_post,
+                          const float* b_post, const float* w_pre, const void* y, const void* dy,
+                          const void* dn, void* dh, void* dz, void* dresidual, float* dres_scale,
+                          float* dw_post, float* db_post, float* dw_pre, float* db_pre, void* scratch,
+                          int64_t scratch_bytes, int64_t B, int64_t L, int64_t D, int64_t G,
+                          int channels_first, int layer, float eps, int dtype, int ytype,
+                          void* stream) {
   int rc = check(B, L, D, G, channels_first, eps, dtype, ytype);
   if (rc != SS2D_OK) return rc;
   const bool none = B == 0 || L == 0;  // the vectors' gradients are then 0
@@ -137,15 +173,18 @@ int ss2d_norm_backward(const void* h, const void* z, const float* res_scale, con
                          static_cast<const float*>(dw_post), static_cast<const float*>(db_post),
                          static_cast<const float*>(dw_pre), static_cast<const float*>(db_pre)})
     if (off(p, 4)) return SS2D_ERR_ALIGN;
+  if (off(scratch, 256)) return SS2D_ERR_ALIGN;
+  Args a{};
+  set_shape(&a, B, L, D, G, channels_first, layer, eps);
+  const Scratch w = scratch_layout(&a, channels_first);
   const int64_t m = B * L * D;
   const Span ins[] = {{h, m * e}, {z, m * e}, {res_scale, G * D * 4}, {w_post, D * 4},
                       {b_post, D * 4}, {w_pre, D * 4}, {y, m * ye}, {dy, m * ye}, {dn, m * e}};
   const Span outs[] = {{dh, m * e}, {dz, m * e}, {dresidual, m * ye}, {dres_scale, G * D * 4},
-                       {dw_post, D * 4}, {db_post, D * 4}, {dw_pre, D * 4}, {db_pre, D * 4}};
-  rc = overlap(outs, 8, ins, 9);
+                       {dw_post, D * 4}, {db_post, D * 4}, {dw_pre, D * 4}, {db_pre, D * 4},
+                       {scratch, static_cast<int64_t>(w.bytes)}};
+  rc = overlap(outs, 9, ins, 9);
   if (rc != SS2D_OK) return rc;
-  Args a{};
-  set_shape(&a, B, L, D, G, channels_first, layer, eps);
   a.h = h;
   a.z = z;
   a.scale = res_scale;
@@ -170,19 +209,15 @@ int ss2d_norm_backward(const void* h, const void* z, const float* res_scale, con
                         static_cast<const void*>(w_pre)})
     vec = vec && !off(p, 16);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int64_t blocks = none ? 0 : ss2d::norm::plan_norm_bwd(&a, channels_first != 0);
-  if (none) a.blocks_per_group = 0;  // the sums below then write zeros
-  const size_t parts = ss2d::host_align256(size_t(blocks) * ss2d::norm::kSums * D * 4);
-  const bool direct = a.blocks_per_group == 1;
-  const size_t groups = dres_scale && !direct ? size_t(a.G) * a.blocks_per_group * D * 4 : 0;
-  char* ws = nullptr;
-  rc = ss2d::host_scratch_alloc(&ws, parts + groups, st);
+  char* ws = static_cast<char*>(scratch);
+  if (!scratch) rc = ss2d::host_scratch_outside_graphs(&ws, w.bytes, st);
+  else if (scratch_bytes < 0 || size_t(scratch_bytes) < w.bytes) rc = SS2D_ERR_SCRATCH;
   if (rc != SS2D_OK) return rc;
   a.parts = reinterpret_cast<float*>(ws);
-  a.scale_parts = direct ? dres_scale : reinterpret_cast<float*>(ws + parts);
+  a.scale_parts = a.blocks_per_group == 1 ? dres_scale : reinterpret_cast<float*>(ws + w.parts);
   int err = none ? 0 : ss2d::norm::launch_norm_bwd(a, dtype, ytype, channels_first != 0, vec, st);
-  if (!err && (dw_post || dw_pre || dres_scale)) err = ss2d::norm::launch_norm_sums(a, blocks, st);
-  const hipError_t fe = hipFreeAsync(ws, st);
+  if (!err && (dw_post || dw_pre || dres_scale)) err = ss2d::norm::launch_norm_sums(a, w.blocks, st);
+  const hipError_t fe = scratch ? hipSuccess : hipFreeAsync(ws, st);
   if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
   if (fe != hipSuccess) return ss2d::host_hip_fail(fe);
   return SS2D_OK;
