@@ -58,7 +58,8 @@
  *     ss2d_scratch_trim hands it back; the device's default pool and its attributes are not
  *     touched.  Under stream capture the
  *     scratch becomes an allocation node of the graph (no synchronisation, copy or memset
- *     is enqueued, so every entry point can be captured).
+ *     is enqueued, so every entry point can be captured; verified for one live graph at a
+ *     time).  The sequence operators take the caller's scratch there instead, see below.
  *   - Results are deterministic: identical inputs, shapes and device give bitwise identical
  *     y (no atomics; the routes are summed in the fixed order 0, 1, 2, 3).
  *   - B == 0 or D == 0 is a valid empty call: it returns SS2D_OK, launches nothing and reads
