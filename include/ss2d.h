@@ -77,6 +77,8 @@
 extern "C" {
 #endif
 
+/* The ss1d_delta_* and ss2d_norm_* entry points came within version 12: a client that may meet an
+ * older library of that version looks for them by name. */
 #define SS2D_ABI_VERSION 12
 
 /* Status codes returned by every entry point. */

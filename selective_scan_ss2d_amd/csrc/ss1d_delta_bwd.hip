@@ -16,8 +16,8 @@
 // The adjoint is bound by the latency of a chunk's chain, as the forward's scan is, and by its
 // registers (256 and up to 256 accumulation registers, one wave per SIMD; held to two waves per
 // SIMD it spills 120 of them and takes 486 us instead of 313 in segments of 20 chunks).  64 x
-// 3136 tokens of 3 heads of 64 in bfloat16: 490 us uncut (457 before it kept dv and the states' gradients
-// in fp32, 520 with LDS permutes for the sums over columns), dq and dk 274 us.
+// 3136 tokens of 3 heads of 64 in bfloat16: 478 to 490 us uncut (457 before it kept dv and the
+// states' gradients in fp32), dq and dk 266 to 274 us.
 #include "ss1d_delta.h"
 
 namespace ss2d {
@@ -239,15 +239,15 @@ __attribute__((amdgpu_waves_per_eu(kSpan ? 2 : 1))) void k_delta_adjoint(Args a)
 // bfloat16 data the fp32 operands (u, dv, the states and their gradients, dP and dL) take 2 terms,
 // 17 bits: dk is a difference of their products, which with dv and the states' gradients in
 // bfloat16 was 1.4 times as far from 64 bits as its own rounding (2.3e-3 against 1.7e-3 without
-// decay), and a third term would add half as many products again to change nothing but the last
-// of those 17 bits.
+// decay); a third term would add half as many products again for bits that the results' rounding
+// drops.
 //
 // Bound by the loads' latency: a block is three round trips to memory and little else.  So
 // its registers and LDS are held to what lets two blocks share a CU (128 registers up to
 // DK = 64 where no value heads share a key head, which needs no second set of sums): six waves
 // at 242 registers, one block per CU, loads issued one behind the other: 480 us (64 x 3136
 // tokens of 3 heads of 64, dv and the states' gradients then in bfloat16); eight at 128, all loads
-// of 32 columns at once: 223 us, and 274 with those two in fp32 (920 MB).
+// of 32 columns at once: 223 us, and 266 to 274 with those two in fp32 (920 MB).
 template <typename T, int KT> struct Panels {  // 32 columns: planes of 32 rows by 16 columns
   // parts of 32 rows by 16 columns: u = beta t, dv, the state and its gradient in 2 terms; do exact
   static constexpr int kWide = 8 + 4 * KT, kNarrow = 4;
