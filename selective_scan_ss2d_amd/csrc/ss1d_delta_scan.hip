@@ -23,22 +23,22 @@ namespace delta {
 namespace {
 
 // A product over the chunk's tokens multiplies by the structural zeros of N and P too, where a NaN
-// or an infinity would reach the tokens before it.  So its operand is clamped to the largest
-// bfloat16 (NaN becomes the lowest); the state's update takes the values as they are, all rows of
-// its column follow them, and where they have, o is set to NaN from the first such token on.
-constexpr float kLargest = 0x1.fep127f;
-__device__ __forceinline__ f32x16 clamped(const f32x16& x) {
+// or an infinity would reach the tokens before it.  So its operand is clamped to the largest value
+// that its terms hold (NaN becomes the lowest); the state's update takes the values as they are, all
+// rows of its column follow them, and where they have, o is set to NaN from the first such token on.
+template <typename T> constexpr float kLargest = sizeof(T) == 4 ? 0x1.fffffep127f : 0x1.fep127f;
+template <typename T> __device__ __forceinline__ f32x16 clamped(const f32x16& x) {
   f32x16 y;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) y[r] = __builtin_amdgcn_fmed3f(x[r], -kLargest, kLargest);
+  for (int r = 0; r < 16; ++r) y[r] = __builtin_amdgcn_fmed3f(x[r], -kLargest<T>, kLargest<T>);
   return y;
 }
 // That token, kC without one, and the column with NaN from token `from` on.
-__device__ __forceinline__ int first_bad(const f32x16& x, int half) {
+template <typename T> __device__ __forceinline__ int first_bad(const f32x16& x, int half) {
   int token = kC;
 #pragma unroll
   for (int r = 15; r >= 0; --r)
-    if (!(fabsf(x[r]) <= kLargest)) token = acc_row(r, half);
+    if (!(fabsf(x[r]) <= kLargest<T>)) token = acc_row(r, half);
   return min(token, __shfl_xor(token, 32));
 }
 __device__ __forceinline__ void set_nan(f32x16& x, int from, int half) {
@@ -152,7 +152,7 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
     const f32x16 gam = load_gate(gate, half) * factor, beta = load_gate(gate + 2 * kC, half);
     f32x16 t = v - gam * ks;
     f32x16 nr = {};
-    const f32x16 br = kSpan ? beta * t : clamped(beta * t);
+    const f32x16 br = kSpan ? beta * t : clamped<T>(beta * t);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       Wide<T, 3> nw, rw;
@@ -181,8 +181,8 @@ __attribute__((amdgpu_waves_per_eu(kMode == kSaving && KT == 4 ? 1 : 2))) void k
       int bad = kC;
       settled(S[0]);
       const bool any_bad = __any(!(fabsf(S[0][0]) < __builtin_inff()));
-      if (__builtin_expect(any_bad, 0)) bad = first_bad(u, half);
-      u = clamped(u);
+      if (__builtin_expect(any_bad, 0)) bad = first_bad<T>(u, half);
+      u = clamped<T>(u);
       f32x16 pu = {};
 #pragma unroll
       for (int s = 0; s < 2; ++s) {

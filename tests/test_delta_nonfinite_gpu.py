@@ -149,6 +149,20 @@ def test_sums_past_the_largest_value(dtype):
     assert not torch.isfinite(got[0][0, 60:]).any() and not torch.isfinite(got[1]).any()
 
 
+def test_the_largest_values_are_values():
+    """fp32 values up to the largest one are neither cut nor taken for infinite: exact here, one token
+    at a time with orthogonal keys."""
+    big = torch.finfo(torch.float32).max
+    t = du.make_inputs(1, 3, 1, 1, 8, 32, torch.float32, seed=11, decay=0.0)
+    for n in ("q", "k"):
+        t[n] = torch.eye(8)[None, :3, None].clone()
+    t["beta"][:] = 1.0
+    t["v"][0, 1, 0, 3], t["v"][0, 2, 0, 4] = big, -big
+    o, end = forward(t, scale=1.0)
+    assert torch.equal(o.cpu(), t["v"])
+    assert torch.equal(end.cpu()[0, 0, :3], t["v"][0, :, 0])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("name, value", BAD)
 def test_step(name, value, dtype):
