@@ -93,7 +93,8 @@ extern "C" {
 #define SS2D_ERR_HIP 5         /* a HIP runtime call failed (see ss2d_last_hip_error)       */
 #define SS2D_ERR_ALIAS 6       /* an output overlaps an input (or another output)            */
 #define SS2D_ERR_SCRATCH 7     /* ss2d_forward_noalloc: the call needs more scratch than
-                                  SS2D_NOALLOC_SCRATCH_BYTES                               */
+                                  SS2D_NOALLOC_SCRATCH_BYTES; _ws entry points: it needs more
+                                  than is given, or none is given under stream capture     */
 
 /* Data types of x, dt_raw, Bs, Cs and y. */
 #define SS2D_F32 0

@@ -1078,12 +1078,13 @@ const char* ss2d_status_string(int status) {
     case SS2D_OK: return "success";
     case SS2D_ERR_NULL: return "a required pointer is NULL";
     case SS2D_ERR_SHAPE: return "invalid or out-of-range dimensions";
-    case SS2D_ERR_UNSUPPORTED: return "unsupported state size N or data type";
+    case SS2D_ERR_UNSUPPORTED: return "unsupported state size N, width, option or data type";
     case SS2D_ERR_ALIGN: return "a pointer is not aligned to its element size";
     case SS2D_ERR_HIP: return "a HIP runtime call failed";
     case SS2D_ERR_ALIAS: return "the output overlaps an input";
     case SS2D_ERR_SCRATCH:
-      return "the call needs more scratch than the fixed array of ss2d_forward_noalloc holds";
+      return "scratch: more than ss2d_forward_noalloc's array holds, less given than the call "
+             "needs, or none given under stream capture";
     default: return "unknown status";
   }
 }
