@@ -47,8 +47,12 @@ def handle(device, stream):
 
 def expect(name, t, shape, dtype, device):
     """Checks a contiguous tensor."""
-    if not (isinstance(t, _torch().Tensor) and t.shape == shape and t.dtype is dtype
-            and t.device == device and t.is_contiguous()):
+    try:
+        fits = (t.shape == shape and t.dtype is dtype and t.device == device
+                and t.is_contiguous())
+    except AttributeError:
+        fits = False
+    if not fits:
         bnd._expect(name, t, shape, dtype, device)  # says what is wrong
 
 

@@ -14,8 +14,6 @@ from ._call import (code_of, expect as _expect, handle as _handle, output as _ou
 
 def _strided(name, t, shape, dtype, device):
     """Checks a tensor whose last axis alone has to be contiguous."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
@@ -30,8 +28,9 @@ def _inputs(q, k, v, g, beta):
     """Checks the rule's inputs; (B, L, HK, DK, H, DV), the data type's code and the strides
     (None for contiguous tensors)."""
     torch = _torch()
-    if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor):
-        raise TypeError("q and v must be torch.Tensors")
+    tensor = torch.Tensor
+    if not (isinstance(q, tensor) and isinstance(k, tensor) and isinstance(v, tensor)):
+        raise TypeError("q, k and v must be torch.Tensors")
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be (B, L, HK, DK) and v (B, L, H, DV)")
     dev, dtype = q.device, q.dtype
