@@ -77,8 +77,8 @@
 extern "C" {
 #endif
 
-/* The ss1d_delta_* and ss2d_norm_* entry points came within version 12: a client that may meet an
- * older library of that version looks for them by name. */
+/* The ss1d_delta_*, ss2d_norm_*, ss1d_scan_*, ss1d_conv_* and ss2d_group_norm_* entry points came
+ * within version 12: a client that may meet an older library of that version looks for them by name. */
 #define SS2D_ABI_VERSION 12
 
 /* Status codes returned by every entry point. */
@@ -613,6 +613,144 @@ int ss2d_norm_backward_ws(const void *h, const void *z, const float *res_scale, 
 
 /* Bytes of ss2d_norm_backward_ws's scratch (-1 for sizes that it rejects). */
 int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int channels_first);
+
+/* ---- selective scan in token order -----------------------------------------------------------
+ * The scan of one causal route over tokens, with states in and out: per sequence and channel d, a
+ * state h of N values that starts at h0 (zero without one) and per token
+ *   delta = softplus(dt_raw + dt_bias),   h_n <- exp(-exp(A_log_n) delta) h_n + delta B_n u,
+ *   y = (sum_n C_n h_n + Ds u) SiLU(z)                        (z NULL: no gate)
+ * (the explainer's SelectiveSSM, whose scan and gate these are).  Channels last:
+ *   u, dt_raw, z, y (B, L, D)  dtype       A_log (D, N), Ds, dt_bias (D)   fp32
+ *   Bs, Cs          (B, L, G, N) dtype     h0, ht                (S, D, N)  fp32
+ * B and C are shared by the D / G channels of a group (channel d: group d / (D / G)).
+ * strides: 12 element strides, (batch, token) of u, of dt_raw and of z, then (batch, token, group)
+ * of Bs and of Cs, whose last axes are contiguous (views into one projection, for instance; none
+ * negative, token and group strides at most 2^24, SS2D_ERR_SHAPE above; z's unused without z); NULL
+ * for contiguous tensors.  Every other tensor is contiguous.  1 <= N <= 32 (SS2D_ERR_UNSUPPORTED
+ * above), D a multiple of G, at most 2^24.
+ *
+ * cu_seqlens: NULL, and the B rows are S = B sequences of L tokens; or S + 1 ascending offsets
+ * (device memory) into the L tokens of B = 1, as for the gated delta rule: tokens outside of every
+ * sequence are neither read nor written, and the kernels cut offsets to [0, L].
+ *
+ * Arithmetic: delta, the state, every sum and the gate are fp32; outputs are rounded once.  Few
+ * sequences are cut into segments that run at once from a zero start and are joined by
+ * h <- exp(A sum delta) h + end.  NaN and infinities reach what the definition says, and nothing
+ * before their token, of another sequence or, if they are u's, dt_raw's or z's, another channel
+ * (an infinity may come out as NaN); dB and dC of their token and group are sums over channels.
+ *
+ * ss1d_scan_forward writes y and, if ht is not NULL, the end states; ht may be h0 itself (in place).
+ * saved (NULL, or ss1d_scan_saved_bytes bytes of device memory, aligned to 256) keeps what
+ * ss1d_scan_backward starts from: the states before every 16 tokens (8 for N > 16).
+ *
+ * ss1d_scan_backward: the gradients of sum(dy * y) + sum(dht * ht) (dht NULL: none) with respect to
+ * u, dt_raw, z (given with z), Bs and Cs in dtype, and in fp32 A_log, Ds, dt_bias and, if dh0 is not
+ * NULL, h0; all contiguous, as dy.  saved: what ss1d_scan_forward kept for the same inputs (other
+ * contents give undefined gradients), or NULL to compute it again.  Rows outside of every sequence are
+ * left as they are.  Sums run in a fixed order (no atomics); without tokens those over tokens are 0.
+ *
+ * ss1d_scan_step is the form for serving: T tokens (few) of each of B sequences, whose states are
+ * updated in place: row b's state is state[slots[b]], or state[b] with slots NULL (then S = B).  A row
+ * whose slot is negative or >= S is padding: nothing of it is read or written, its rows of y included.
+ * Rows that name the same slot are successive tokens of one sequence, in row order.
+ *
+ * The shared conventions hold, except that kernel timing does not cover these entry points and that
+ * under stream capture scratch has to be the caller's: scratch is device memory aligned to 256 of
+ * scratch_bytes >= ss1d_scan_scratch_bytes (SS2D_ERR_SCRATCH below), or NULL for the library's
+ * (SS2D_ERR_SCRATCH under capture where any is needed).  The step needs none; a forward 8 N + 4 bytes
+ * per segment and channel; a backward fp32 sums of dB and dC for every 64 channels of a group, those of
+ * the parameters for every segment, and without `saved` the same and an unused y. */
+int ss1d_scan_forward(const void *u, const void *dt_raw, const float *A_log, const void *Bs,
+                      const void *Cs, const float *Ds, const float *dt_bias, const void *z,
+                      const float *h0, const int32_t *cu_seqlens, void *y, float *ht, void *saved,
+                      void *scratch, int64_t scratch_bytes, int64_t B, int64_t L, int64_t S, int64_t D,
+                      int64_t G, int64_t N, const int64_t *strides, int dtype, void *stream);
+
+int ss1d_scan_backward(const void *u, const void *dt_raw, const float *A_log, const void *Bs,
+                       const void *Cs, const float *Ds, const float *dt_bias, const void *z,
+                       const float *h0, const int32_t *cu_seqlens, const void *saved, const void *dy,
+                       const float *dht, void *du, void *ddt_raw, float *dA_log, void *dBs, void *dCs,
+                       float *dDs, float *ddt_bias, void *dz, float *dh0, void *scratch,
+                       int64_t scratch_bytes, int64_t B, int64_t L, int64_t S, int64_t D, int64_t G,
+                       int64_t N, const int64_t *strides, int dtype, void *stream);
+
+/* Bytes of scratch (-1 for sizes that the operator rejects) of a forward (backward 0) or a backward
+ * (1); kept: whether `saved` is given to it; packed: whether cu_seqlens is. */
+int64_t ss1d_scan_scratch_bytes(int backward, int kept, int64_t B, int64_t L, int64_t S, int64_t D,
+                                int64_t G, int64_t N, int dtype, int packed);
+
+/* Bytes of `saved` (-1 for sizes that the operator rejects). */
+int64_t ss1d_scan_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t D, int64_t N, int packed);
+
+/* Testing and tuning, as ss2d_set_launch_plan: for later calls from this host thread, the tokens of a
+ * segment, rounded up to the kernels' tile (0: whole sequences, -1: automatic).  Returns SS2D_OK or
+ * SS2D_ERR_SHAPE. */
+int ss1d_scan_set_segment(int64_t tokens);
+
+int ss1d_scan_step(const void *u, const void *dt_raw, const float *A_log, const void *Bs,
+                   const void *Cs, const float *Ds, const float *dt_bias, const void *z, float *state,
+                   const int32_t *slots, void *y, int64_t B, int64_t T, int64_t S, int64_t D, int64_t G,
+                   int64_t N, const int64_t *strides, int dtype, void *stream);
+
+/* ---- short causal convolution -------------------------------------------------------------------
+ * The depthwise convolution before the scan (the explainer's Conv1d with padding d_conv - 1, cut to
+ * the tokens, and its SiLU), with the inputs before a sequence carried from call to call:
+ *   y_t = act(conv_b + sum_{j < KW} conv_w_j x_{t - KW + 1 + j}),   act = SiLU (silu 1) or none (0)
+ * per channel; x before a sequence's first token is its initial state, zero without one.
+ *   x, y (B, L, D) dtype      conv_w (D, KW), conv_b (D, or NULL) fp32
+ *   h0, ht (S, KW - 1, D) dtype: the KW - 1 inputs before the next token, the oldest first.
+ * strides: 2 element strides, (batch, token) of x, whose last axis is contiguous; NULL for a
+ * contiguous tensor.  1 <= KW <= 8 (SS2D_ERR_UNSUPPORTED above).  cu_seqlens, S, packed rows, ht in
+ * place, padding rows and repeated slots of the step, scratch: as for the scan above.  Sums are fp32,
+ * y is rounded once.
+ *
+ * ss1d_conv_backward: the gradients of sum(dy * y) + sum(dht * ht) with respect to x and, if dh0 is
+ * not NULL, h0 in dtype, conv_w and (given with conv_b) conv_b in fp32; contiguous, as dy and dht.
+ * Scratch (ss1d_conv_scratch_bytes): partial sums of the taps' gradients, in a fixed order. */
+int ss1d_conv_forward(const void *x, const float *conv_w, const float *conv_b, const void *h0,
+                      const int32_t *cu_seqlens, void *y, void *ht, int64_t B, int64_t L, int64_t S,
+                      int64_t D, int64_t KW, const int64_t *strides, int silu, int dtype, void *stream);
+
+int ss1d_conv_backward(const void *x, const float *conv_w, const float *conv_b, const void *h0,
+                       const int32_t *cu_seqlens, const void *dy, const void *dht, void *dx,
+                       float *dconv_w, float *dconv_b, void *dh0, void *scratch, int64_t scratch_bytes,
+                       int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, const int64_t *strides,
+                       int silu, int dtype, void *stream);
+
+/* Bytes of ss1d_conv_backward's scratch (-1 for sizes that it rejects). */
+int64_t ss1d_conv_scratch_bytes(int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, int dtype,
+                                int packed);
+
+int ss1d_conv_step(const void *x, const float *conv_w, const float *conv_b, void *state,
+                   const int32_t *slots, void *y, int64_t B, int64_t T, int64_t S, int64_t D, int64_t KW,
+                   const int64_t *strides, int silu, int dtype, void *stream);
+
+/* ---- group norm ---------------------------------------------------------------------------------
+ * The norm of the backbone's convolution stages, over positions and groups of channels, with its
+ * activation:
+ *   y = act((x - mean) / sqrt(var + eps) * weight + bias),   act = SiLU (silu 1) or none (0)
+ * with mean and var (of the values themselves, about their mean) over the L positions and C / G
+ * channels of an image's group.
+ *   x, y (B, L, C) dtype, channels last (L = H * W for maps);  weight, bias (C) fp32, NULL for 1 and 0
+ *   stats (B, G, 2) fp32, or NULL: mean and 1 / sqrt(var + eps), written by the forward for the
+ *     backward, which computes them again without.
+ * All contiguous.  C a multiple of G, at most 2^20; L below 2^31.  Statistics are fp32, by the mean
+ * first and then the squares about it.
+ *
+ * ss2d_group_norm_backward: the gradients of sum(dy * y): dx in dtype, dweight and dbias (given with
+ * weight, with bias) in fp32, summed in a fixed order; without positions they are 0.
+ * Scratch (ss2d_group_norm_scratch_bytes; kept: whether stats is given): as for the scan above. */
+int ss2d_group_norm_forward(const void *x, const float *weight, const float *bias, void *y, float *stats,
+                            void *scratch, int64_t scratch_bytes, int64_t B, int64_t L, int64_t C,
+                            int64_t G, int silu, float eps, int dtype, void *stream);
+
+int ss2d_group_norm_backward(const void *x, const float *weight, const float *bias, const float *stats,
+                             const void *dy, void *dx, float *dweight, float *dbias, void *scratch,
+                             int64_t scratch_bytes, int64_t B, int64_t L, int64_t C, int64_t G, int silu,
+                             float eps, int dtype, void *stream);
+
+int64_t ss2d_group_norm_scratch_bytes(int backward, int kept, int64_t B, int64_t L, int64_t C, int64_t G,
+                                      int dtype);
 
 /* ---- launch-plan override (testing and tuning, not part of the operator) ---------------
  * Sets, for calls made later from the calling host thread only, the lanes that share one

@@ -25,7 +25,11 @@ from ._binding import (LIBRARY_PATH, SS2D_BF16, SS2D_ERR_ALIAS, SS2D_ERR_ALIGN, 
 
 from ._delta import (ss1d_delta_backward, ss1d_delta_forward, ss1d_delta_forward_save,
                      ss1d_delta_step)
+from ._conv import ss1d_conv_backward, ss1d_conv_forward, ss1d_conv_step
+from ._group import ss2d_group_norm_backward, ss2d_group_norm_forward
 from ._norm import ss2d_norm_backward, ss2d_norm_forward
+from ._scan import (ss1d_scan_backward, ss1d_scan_forward, ss1d_scan_forward_save,
+                    ss1d_scan_step)
 
 __all__ = [
     "ss2d_forward", "ss1d_bidir_forward", "ss2d_forward_ex", "ss1d_bidir_forward_ex",
@@ -44,4 +48,7 @@ __all__ = [
     "ss1d_bidir_backward_routes_saved", "scratch_trim",
     "ss1d_delta_forward", "ss1d_delta_forward_save", "ss1d_delta_backward",
     "ss1d_delta_step", "ss2d_norm_forward", "ss2d_norm_backward",
+    "ss1d_scan_forward", "ss1d_scan_forward_save", "ss1d_scan_backward", "ss1d_scan_step",
+    "ss1d_conv_forward", "ss1d_conv_backward", "ss1d_conv_step",
+    "ss2d_group_norm_forward", "ss2d_group_norm_backward",
 ]

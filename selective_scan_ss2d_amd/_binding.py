@@ -88,6 +88,21 @@ SIGNATURES = {
     "ss2d_norm_backward_ws": (ctypes.c_int, [_P] * 18 + [_I64] * 5 + [ctypes.c_int] * 2
                               + [ctypes.c_float] + [ctypes.c_int] * 2 + [_P]),
     "ss2d_norm_scratch_bytes": (_I64, [_I64] * 4 + [ctypes.c_int]),
+    "ss1d_scan_forward": (ctypes.c_int, [_P] * 14 + [_I64] * 7 + [_P, ctypes.c_int, _P]),
+    "ss1d_scan_backward": (ctypes.c_int, [_P] * 23 + [_I64] * 7 + [_P, ctypes.c_int, _P]),
+    "ss1d_scan_scratch_bytes": (_I64, [ctypes.c_int] * 2 + [_I64] * 6 + [ctypes.c_int] * 2),
+    "ss1d_scan_saved_bytes": (_I64, [_I64] * 5 + [ctypes.c_int]),
+    "ss1d_scan_set_segment": (ctypes.c_int, [_I64]),
+    "ss1d_scan_step": (ctypes.c_int, [_P] * 11 + [_I64] * 6 + [_P, ctypes.c_int, _P]),
+    "ss1d_conv_forward": (ctypes.c_int, [_P] * 7 + [_I64] * 5 + [_P] + [ctypes.c_int] * 2 + [_P]),
+    "ss1d_conv_backward": (ctypes.c_int, [_P] * 12 + [_I64] * 6 + [_P] + [ctypes.c_int] * 2 + [_P]),
+    "ss1d_conv_scratch_bytes": (_I64, [_I64] * 5 + [ctypes.c_int] * 2),
+    "ss1d_conv_step": (ctypes.c_int, [_P] * 6 + [_I64] * 5 + [_P] + [ctypes.c_int] * 2 + [_P]),
+    "ss2d_group_norm_forward": (ctypes.c_int, [_P] * 6 + [_I64] * 5 + [ctypes.c_int, ctypes.c_float,
+                                                                       ctypes.c_int, _P]),
+    "ss2d_group_norm_backward": (ctypes.c_int, [_P] * 9 + [_I64] * 5 + [ctypes.c_int, ctypes.c_float,
+                                                                        ctypes.c_int, _P]),
+    "ss2d_group_norm_scratch_bytes": (_I64, [ctypes.c_int] * 2 + [_I64] * 4 + [ctypes.c_int]),
     "ss2d_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ss2d_abi_version": (ctypes.c_int, []),
     "ss2d_last_hip_error": (ctypes.c_int, []),

@@ -72,3 +72,34 @@ def scratch(size, device):
     back to torch's allocator when the call returns, which hands it to later work of the same stream
     only; in a captured graph it belongs to the graph."""
     return _torch().empty(max(256, size), dtype=_torch().uint8, device=device)
+
+
+def rows(name, t, shape, dtype, device):
+    """Checks a (batch, token, ...) tensor whose last axis alone has to be contiguous; whether all
+    of it is."""
+    try:
+        fits = t.shape == shape and t.dtype is dtype and t.device == device
+        if fits and t.is_contiguous():
+            return True
+        fits = fits and (t.stride(-1) == 1 or shape[-1] <= 1)
+    except AttributeError:
+        fits = False
+    if not fits:
+        bnd._expect(name, t, shape, dtype, device)  # says what is wrong
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return False
+
+
+def packed_sequences(cu_seqlens, B, device):
+    """The number of sequences: the rows, or those that the offsets name."""
+    if cu_seqlens is None:
+        return B
+    torch = _torch()
+    if not isinstance(cu_seqlens, torch.Tensor):
+        raise TypeError("cu_seqlens must be a torch.Tensor")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must hold S + 1 offsets")
+    expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device)
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need a batch of 1")
+    return cu_seqlens.shape[0] - 1
