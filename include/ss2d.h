@@ -682,10 +682,11 @@ int64_t ss1d_scan_scratch_bytes(int backward, int kept, int64_t B, int64_t L, in
 /* Bytes of `saved` (-1 for sizes that the operator rejects). */
 int64_t ss1d_scan_saved_bytes(int64_t B, int64_t L, int64_t S, int64_t D, int64_t N, int packed);
 
-/* Testing and tuning, as ss2d_set_launch_plan: for later calls from this host thread, the tokens of a
- * segment, rounded up to the kernels' tile (0: whole sequences, -1: automatic).  Returns SS2D_OK or
- * SS2D_ERR_SHAPE. */
-int ss1d_scan_set_segment(int64_t tokens);
+/* Testing and tuning, as ss2d_set_launch_plan: for later calls from this host thread, the lanes that
+ * share a channel in a forward without `saved` (4 or 16; 0: automatic) and the tokens of a segment,
+ * rounded up to the kernels' tile (0: whole sequences, -1: automatic).  Returns SS2D_OK,
+ * SS2D_ERR_UNSUPPORTED for other lanes or SS2D_ERR_SHAPE. */
+int ss1d_scan_set_plan(int lanes, int64_t tokens);
 
 int ss1d_scan_step(const void *u, const void *dt_raw, const float *A_log, const void *Bs,
                    const void *Cs, const float *Ds, const float *dt_bias, const void *z, float *state,

@@ -92,7 +92,7 @@ SIGNATURES = {
     "ss1d_scan_backward": (ctypes.c_int, [_P] * 23 + [_I64] * 7 + [_P, ctypes.c_int, _P]),
     "ss1d_scan_scratch_bytes": (_I64, [ctypes.c_int] * 2 + [_I64] * 6 + [ctypes.c_int] * 2),
     "ss1d_scan_saved_bytes": (_I64, [_I64] * 5 + [ctypes.c_int]),
-    "ss1d_scan_set_segment": (ctypes.c_int, [_I64]),
+    "ss1d_scan_set_plan": (ctypes.c_int, [ctypes.c_int, _I64]),
     "ss1d_scan_step": (ctypes.c_int, [_P] * 11 + [_I64] * 6 + [_P, ctypes.c_int, _P]),
     "ss1d_conv_forward": (ctypes.c_int, [_P] * 7 + [_I64] * 5 + [_P] + [ctypes.c_int] * 2 + [_P]),
     "ss1d_conv_backward": (ctypes.c_int, [_P] * 12 + [_I64] * 6 + [_P] + [ctypes.c_int] * 2 + [_P]),

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ss1d_sequences.h"
 #include "ss2d_device.h"
@@ -46,7 +47,8 @@ struct Args {
   int64_t seglen;       // tokens of a segment (a multiple of the tile), 0: whole sequences
   int64_t units;        // segments, or sequences
   int D, G, N;
-  int cbg;              // channel blocks of a group
+  int cbg;              // channel blocks (of kBlockCh) of a group
+  int lanes;            // of a channel in the forward: 4 or 16
   // backward
   const void* dy;
   const float* dht;
@@ -72,23 +74,94 @@ __device__ __forceinline__ float quad_scatter_sum(float v0, float v1, float v2, 
   return (high ? b : a) + quad_perm<2, 3, 0, 1>(high ? a : b);
 }
 
+// kNS states of a lane from LDS or memory rows on 16 bytes.
+template <int kNS> __device__ __forceinline__ void load_states(const float* p, float* x) {
+  if constexpr (kNS % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < kNS; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + i);
+      x[i] = v.x;
+      x[i + 1] = v.y;
+      x[i + 2] = v.z;
+      x[i + 3] = v.w;
+    }
+  } else if constexpr (kNS == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+  } else {
+    x[0] = *p;
+  }
+}
+
+template <int I, int N, typename F> __device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<I + 1, N>(f);
+  }
+}
+
+// A value that the compiler takes for a new one, so that nothing derived from it leaves the loop.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Element `at` past a uniform pointer.  A load with the byte offset in 32 bits, extended beside it
+// (`at` opaque, where the extension would be moved out of a loop), keeps the pointer in scalar
+// registers and one vector register for the lane.
+template <typename T> __device__ __forceinline__ const T& element(const T* p, uint32_t at) {
+  return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + at * uint32_t(sizeof(T)));
+}
+template <typename T> __device__ __forceinline__ T& element(T* p, uint32_t at) {
+  return *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + at * uint32_t(sizeof(T)));
+}
+
 // The place of a block: its unit, group and first channel.  The channel blocks of a unit follow
 // each other on one XCD, whose L2 then holds the lines of u, dt_raw, z, B and C that they share.
 struct Place {
   int64_t unit;
   int g, cb, c0;   // group, channel block of it, first channel within the group
 };
-__device__ __forceinline__ Place place_of(const Args& a, unsigned lin, unsigned total) {
+__device__ __forceinline__ Place place_of(const Args& a, int channels, unsigned lin, unsigned total) {
   const unsigned id = xcd_local_order(lin, total);
-  const unsigned per = a.G * a.cbg;
+  const unsigned cbg = (a.D / a.G + channels - 1) / channels, per = a.G * cbg;
   Place p;
-  p.unit = id / per;
+  p.unit = uniform(id / per);
   const unsigned r = id % per;
-  p.g = r / a.cbg;
-  p.cb = r % a.cbg;
-  p.c0 = p.cb * kBlockCh;
+  p.g = r / cbg;
+  p.cb = r % cbg;
+  p.c0 = p.cb * channels;
   return p;
 }
+
+// B and C of a tile of kTile steps as a block's 256 threads load them: a thread takes one n of one of
+// the two, and every kRows-th step.  Element e = thread + 256 m is step e / (2 kNP), B before C.
+template <typename T, int kTile, int kNP> struct Operands {
+  static constexpr int kRows = kThreads / (2 * kNP), kPer = kTile > kRows ? kTile / kRows : 1;
+  const T* p;
+  int stride, step;
+  bool on;
+  T raw[kPer];
+  __device__ __forceinline__ void start(const Args& a, int64_t b, int64_t row, int g, bool both, bool b_only) {
+    const int tid = threadIdx.x, n = tid % kNP;
+    const bool is_c = tid / kNP % 2;
+    step = tid / (2 * kNP);
+    on = n < a.N && step < kTile && (both || is_c != b_only);
+    const RowStrides s = is_c ? a.sc : a.sb;
+    p = static_cast<const T*>(is_c ? a.Cs : a.Bs) + b * s.b + (row + step) * s.l + g * (is_c ? a.scg : a.sbg) + n;
+    stride = static_cast<int>(s.l);
+  }
+  // the first `rows` steps of the tile; then on by `moved` steps
+  __device__ __forceinline__ void load(int rows, int moved) {
+#pragma unroll
+    for (int m = 0; m < kPer; ++m) {
+      raw[m] = T(0);
+      if (on && step + m * kRows < rows) raw[m] = element(p, opaque(stride) * uint32_t(m * kRows));
+    }
+    p += int64_t(moved) * stride;
+  }
+};
 
 }  // namespace sscan
 }  // namespace ss2d

@@ -15,7 +15,9 @@ using ss2d::RowStrides;
 using ss2d::sscan::Args;
 using ss2d::sscan::StepArgs;
 
-// Segment length in tokens that a test forces on its own thread (ss1d_scan_set_segment); -1: the rule's.
+// The plan that a test forces on its own thread (ss1d_scan_set_plan): lanes of a channel (0: the
+// rule's) and tokens of a segment (-1: the rule's).
+thread_local int g_lanes_override = 0;
 thread_local int64_t g_segment_override = -1;
 
 constexpr int64_t kMaxTokens = int64_t(1) << 40;
@@ -98,34 +100,60 @@ int check_overlap(const Span* ins, int n_in, const Span* outs, int n_out) {
   return SS2D_OK;
 }
 
-// Tokens of a segment, 0 for whole sequences.
-int64_t segment_tokens(int64_t L, int64_t S, int64_t T, int64_t D, int64_t G, int64_t N, bool packed) {
-  const int64_t tile = ss2d::sscan::tile_steps(N);
-  if (T == 0 || D == 0 || S == 0) return 0;
-  if (g_segment_override >= 0) return (g_segment_override + tile - 1) / tile * tile;
-  const int64_t Dg = D / G, waves = S * G * ((Dg + 15) / 16);
-  if (waves >= 1024) return 0;
-  const int64_t total = T / tile * G * ((Dg + 15) / 16);   // tiles of all waves
-  int64_t len = std::max<int64_t>(4, (total + 1023) / 1024);
-  len *= tile;
-  return 2 * len <= L ? len : 0;
+// How a call is cut: the lanes of a channel, and the tokens of a segment (0: whole sequences).  The
+// forward takes what these estimates of its time find shortest, in us, fitted to 60 shapes of 64 to
+// 65536 tokens, 192 to 12288 channels, N 8 to 32 (`quads`: waves with four lanes per channel):
+//   four lanes, whole       0.117 longest       (1024 tokens: 120; up to 1024 waves, 0.65 a wave more)
+//   16 lanes, whole         (0.025 + 0.0275 waves / 1024) longest     (1024 x 4096 channels: 56)
+//   four lanes, segments    14 + 1.2e-4 a token and wave   (1024 x 4096: 51; 4096 x 4096: 140, whole 475)
+// each token's time by its states (kNS of a lane).  Segments are made for 4096 waves, four per SIMD,
+// of 32 tokens at least: 4096 tokens x 4096 channels take 213, 158, 140 and 144 us in 4, 8, 16 and 32
+// segments.  Of packed sequences the longest is not known here: four times their mean is assumed.
+// A forward that keeps states runs by four lanes.  The backward, whose waves fill a SIMD by twos, is
+// cut below 2048 waves: 8 x 2048 tokens of 2048 channels take 758 us whole, 627 in segments.
+void set_plan(Args* a, int64_t B, int64_t L, bool packed, bool saves, bool backward) {
+  const int64_t S = a->q.S, T = a->q.T, Dg = a->D / a->G, tile = ss2d::sscan::tile_steps(a->N);
+  a->lanes = 4;
+  a->seglen = 0;
+  a->units = S;
+  if (T == 0 || a->D == 0 || S == 0) return;
+  const int64_t per = a->G * ((Dg + 15) / 16), quads = S * per;  // waves of a sequence, of all
+  // equal segments of the dense rows, as many as keep to 4096 waves
+  const int64_t parts = std::max<int64_t>(2, 4096 / std::max<int64_t>(1, quads));
+  const int64_t fair = packed ? T * per / 4096 : (L + parts - 1) / parts;
+  const int64_t len = std::max<int64_t>(32, (fair + tile - 1) / tile * tile);
+  const double longest = packed ? std::min<double>(T, 4.0 * T / S) : L;
+  const double states = (ss2d::sscan::lane_states(a->N) + 3) / 7.0;
+  const double rows = a->N > 16 ? 1.35 : 1.0, fill = std::max(1.0, quads * 4 / 1024.0);
+  const double whole = 0.117 * longest * states * std::max(1.0, 0.35 + 0.65 * quads / 1024.0);
+  const double by16 = (0.025 + 0.0275 * fill) * longest * rows;
+  const double cut = 2 * len <= longest ? 14 + 1.2e-4 * T * per * states : 1e30;
+  if (backward) {
+    if (quads < 2048 && 2 * len <= longest) a->seglen = len;
+  } else if (cut < whole && (saves || cut < by16)) {
+    a->seglen = len;
+  } else if (!saves && by16 < whole) {
+    a->lanes = 16;
+  }
+  if (g_segment_override >= 0) a->seglen = (g_segment_override + tile - 1) / tile * tile;
+  if (g_lanes_override) a->lanes = saves ? 4 : g_lanes_override;
+  if (a->seglen) a->units = ss2d::unit_count(L, S, T, packed, a->seglen);
 }
 
 void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t D, int64_t G, int64_t N, const int32_t* cu,
-               bool packed) {
+               bool packed, bool saves, bool backward) {
   a->q = {cu, S, L, B * L};
   a->D = static_cast<int>(D);
   a->G = static_cast<int>(G);
   a->N = static_cast<int>(N);
   a->cbg = static_cast<int>((D / G + ss2d::sscan::kBlockCh - 1) / ss2d::sscan::kBlockCh);
-  a->seglen = segment_tokens(L, S, B * L, D, G, N, packed);
-  a->units = a->seglen ? ss2d::unit_count(L, S, B * L, packed, a->seglen) : S;
+  set_plan(a, B, L, packed, saves, backward);
 }
 
 bool launchable(const Args& a, bool packed) {
-  return a.units <= kMaxThreads / ss2d::sscan::kThreads / std::max(1, a.G * a.cbg) &&
+  return a.units <= kMaxThreads / ss2d::sscan::kThreads / (4 * std::max(1, a.G * a.cbg)) &&
          a.q.S <= (kMaxThreads - 256) / std::max<int64_t>(1, int64_t(a.D) * a.N) &&
-         ss2d::unit_count(a.q.L, a.q.S, a.q.T, packed, 64) <= kMaxThreads / 256;
+         ss2d::unit_count(a.q.L, a.q.S, a.q.T, packed, 16) <= kMaxThreads / 256;
 }
 
 int64_t mark_bytes(int64_t L, int64_t S, int64_t T, int64_t D, int64_t N, bool packed) {
@@ -133,12 +161,15 @@ int64_t mark_bytes(int64_t L, int64_t S, int64_t T, int64_t D, int64_t N, bool p
       size_t(ss2d::unit_count(L, S, T, packed, ss2d::sscan::tile_steps(N))) * D * N * 4));
 }
 
+// Scratch: the segments' states (again: of the forward that a backward without `saved` runs, cut as a
+// saving forward is, so that its gradients are the same bit for bit), then the backward's.
 struct Layout {
   size_t end, start, delta, bc, params, marks, y, bytes;
 };
-Layout layout(const Args& a, bool backward, bool kept, bool packed, int64_t e) {
+Layout layout(const Args& a, const Args& again, bool backward, bool kept, bool packed, int64_t e) {
   using ss2d::host_align256;
-  const size_t seg = a.seglen ? size_t(a.units) * a.D : 0;
+  size_t seg = a.seglen ? size_t(a.units) * a.D : 0;
+  if (backward && !kept && again.seglen) seg = std::max(seg, size_t(again.units) * a.D);
   Layout w;
   w.end = 0;
   w.start = host_align256(seg * a.N * 4);
@@ -211,8 +242,10 @@ void set_inputs(Args* a, const Data& x, const void* u, const void* dt, const voi
 
 extern "C" {
 
-int ss1d_scan_set_segment(int64_t tokens) {
+int ss1d_scan_set_plan(int lanes, int64_t tokens) {
+  if (lanes != 0 && lanes != 4 && lanes != 16) return SS2D_ERR_UNSUPPORTED;
   if (tokens < -1 || tokens > (int64_t(1) << 30)) return SS2D_ERR_SHAPE;
+  g_lanes_override = lanes;
   g_segment_override = tokens;
   return SS2D_OK;
 }
@@ -226,8 +259,10 @@ int64_t ss1d_scan_scratch_bytes(int backward, int kept, int64_t B, int64_t L, in
                                 int64_t N, int dtype, int packed) {
   if (check_sizes(B, L, S, D, G, N, dtype, packed != 0) != SS2D_OK) return -1;
   Args a{};
-  set_sizes(&a, B, L, S, D, G, N, nullptr, packed != 0);
-  return static_cast<int64_t>(layout(a, backward != 0, kept != 0, packed != 0, dtype == SS2D_F32 ? 4 : 2).bytes);
+  set_sizes(&a, B, L, S, D, G, N, nullptr, packed != 0, backward || kept, backward != 0);
+  Args again{};
+  set_sizes(&again, B, L, S, D, G, N, nullptr, packed != 0, true, false);
+  return static_cast<int64_t>(layout(a, again, backward != 0, kept != 0, packed != 0, dtype == SS2D_F32 ? 4 : 2).bytes);
 }
 
 int ss1d_scan_forward(const void* u, const void* dt_raw, const float* A_log, const void* Bs, const void* Cs,
@@ -253,9 +288,9 @@ int ss1d_scan_forward(const void* u, const void* dt_raw, const float* A_log, con
     if (off(p, 4)) return SS2D_ERR_ALIGN;
   if (off(y, e) || off(saved, 256) || off(scratch, 256)) return SS2D_ERR_ALIGN;
   Args a{};
-  set_sizes(&a, B, L, S, D, G, N, cu_seqlens, packed);
+  set_sizes(&a, B, L, S, D, G, N, cu_seqlens, packed, saved != nullptr, false);
   if (!launchable(a, packed)) return SS2D_ERR_SHAPE;
-  const Layout w = layout(a, false, true, packed, e);
+  const Layout w = layout(a, a, false, true, packed, e);
   const int64_t states = S * D * N * 4;
   ins[5] = {A_log, D * N * 4};
   ins[6] = {Ds, D * 4};
@@ -313,9 +348,11 @@ int ss1d_scan_backward(const void* u, const void* dt_raw, const float* A_log, co
     if (off(p, e)) return SS2D_ERR_ALIGN;
   if (off(saved, 256) || off(scratch, 256)) return SS2D_ERR_ALIGN;
   Args a{};
-  set_sizes(&a, B, L, S, D, G, N, cu_seqlens, packed);
-  if (!launchable(a, packed)) return SS2D_ERR_SHAPE;
-  const Layout w = layout(a, true, saved != nullptr, packed, e);
+  set_sizes(&a, B, L, S, D, G, N, cu_seqlens, packed, true, true);
+  Args again{};
+  set_sizes(&again, B, L, S, D, G, N, cu_seqlens, packed, true, false);
+  if (!launchable(a, packed) || !launchable(again, packed)) return SS2D_ERR_SHAPE;
+  const Layout w = layout(a, again, true, saved != nullptr, packed, e);
   const int64_t states = S * D * N * 4, wide = B * L * D * e, bc = B * L * G * N * e;
   ins[5] = {A_log, D * N * 4};
   ins[6] = {Ds, D * 4};
@@ -352,8 +389,11 @@ int ss1d_scan_backward(const void* u, const void* dt_raw, const float* A_log, co
   int err = 0;
   if (!saved) {  // the states before every tile, by the forward
     a.marks = reinterpret_cast<float*>(ws.at + w.marks);
-    a.y = ws.at + w.y;
-    err = none ? 0 : run_forward(a, dtype, st);
+    set_inputs(&again, x, u, dt_raw, z, Bs, Cs, A_log, Ds, dt_bias, h0);
+    set_segments(&again, ws.at, w);
+    again.marks = a.marks;
+    again.y = ws.at + w.y;
+    err = none ? 0 : run_forward(again, dtype, st);
   }
   if (!err && a.units > 0) {
     if (a.seglen) err = ss2d::sscan::launch_scan_adjoint_segments(a, dtype, st);

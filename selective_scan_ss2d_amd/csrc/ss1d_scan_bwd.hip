@@ -41,21 +41,23 @@ __device__ __forceinline__ void channel_sums(float* dB, float* dC, float* out) {
 
 // kAll: the gradients; else what a segment's start sends on from nothing behind it, and the
 // segment's sum of delta.
-template <typename T, int kNS, bool kAll>
-__global__ __launch_bounds__(kThreads) void k_scan_adjoint(Args a) {
+template <typename T, int kNS, bool kAll, bool kGate>
+__global__ __launch_bounds__(kThreads, 2) void k_scan_adjoint(Args a) {
   constexpr int kTile = tile_of(kNS), kOwn = kTile / 4, kNP = 4 * kNS, kNY = (kNS + 1) / 2;
-  constexpr int kBC = kTile * 2 * kNP, kPer = (kBC + kThreads - 1) / kThreads;
+  constexpr int kBC = kTile * 2 * kNP, kPer = Operands<T, kTile, kNP>::kPer;
   __shared__ __align__(16) float sBC[2][kBC];
   __shared__ float sums[kAll ? 2 : 1][kAll ? 4 * kBC : 1];  // (wave, step, B then C)
 
-  const Place p = place_of(a, blockIdx.x, gridDim.x);
+  const Place p = place_of(a, kBlockCh, blockIdx.x, gridDim.x);
   int64_t idx = 0;
-  const Sequence q = a.seglen ? sequence_of(a.q, p.unit, a.seglen, &idx) : sequence(a.q, p.unit);
+  const Sequence q = uniform(a.seglen ? sequence_of(a.q, p.unit, a.seglen, &idx) : sequence(a.q, p.unit));
+  idx = uniform(idx);
   const int64_t t_begin = idx * a.seglen;
   const bool empty = idx > 0 && t_begin >= q.len;
+  if (!kAll && idx == 0) return;  // nothing before a sequence's first segment needs its carry
   const int64_t t_end = empty ? t_begin : (a.seglen ? min(q.len, t_begin + a.seglen) : q.len);
 
-  const int tid = threadIdx.x, lane = tid & 63, s = lane & 3, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, s = lane & 3, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int Dg = a.D / a.G, c = p.c0 + (tid >> 2);
   const bool on = c < Dg, wave_on = p.c0 + wave * 16 < Dg;
   const int waves = min(4, (Dg - p.c0 + 15) / 16);
@@ -79,158 +81,208 @@ __global__ __launch_bounds__(kThreads) void k_scan_adjoint(Args a) {
   const int64_t row = q.begin + t_begin + (tiles - 1) * kTile;  // of the tile to load next
   const T* pu = static_cast<const T*>(a.u) + q.b * a.su.b + row * a.su.l;
   const T* pd = static_cast<const T*>(a.dt) + q.b * a.sd.b + row * a.sd.l;
-  const T* pz = a.z ? static_cast<const T*>(a.z) + q.b * a.sz.b + row * a.sz.l : nullptr;
+  const T* pz = kGate ? static_cast<const T*>(a.z) + q.b * a.sz.b + row * a.sz.l : nullptr;
   const T* pg = static_cast<const T*>(a.dy) + (q.b * a.q.L + row) * a.D;
-  const T* pB = static_cast<const T*>(a.Bs) + q.b * a.sb.b + row * a.sb.l + p.g * a.sbg;
-  const T* pC = static_cast<const T*>(a.Cs) + q.b * a.sc.b + row * a.sc.l + p.g * a.scg;
-  const uint32_t ul = a.su.l, dl_ = a.sd.l, zl = a.sz.l, gl = a.D;
-  int64_t out_row = q.b * a.q.L + row;  // of the tile that is computed
-  const float* mark = kAll ? a.marks + ((first_unit(a.q, q, kTile) + t_begin / kTile + tiles - 1) * a.D + d) * a.N
-                                 + s * kNS : nullptr;
+    const int64_t out_row = q.b * a.q.L + row;  // of the last tile
+  T* qu = kAll ? static_cast<T*>(a.du) + out_row * a.D : nullptr;
+  T* qd = kAll ? static_cast<T*>(a.ddt) + out_row * a.D : nullptr;
+  T* qz = kAll && kGate ? static_cast<T*>(a.dz) + out_row * a.D : nullptr;
+  const float* mark = kAll ? a.marks + (first_unit(a.q, q, kTile) + t_begin / kTile + tiles - 1) * a.D * a.N : nullptr;
+  const bool whole_mark = kNS >= 4 && a.N == 4 * kNS;
+  const uint32_t om = uint32_t(d) * a.N + s * kNS;
 
-  T ru[kOwn], rd[kOwn], rz[kOwn], rg[kOwn], rbc[kPer];
-  float rh[kNS];
-  auto fetch = [&](int64_t left) {
-    const int last = left >= kTile ? kTile - 1 : static_cast<int>(left) - 1;
+  T ru[kOwn] = {}, rd[kOwn] = {}, rz[kOwn] = {}, rg[kOwn] = {};
+  float rh[kNS] = {};
+  Operands<T, kTile, kNP> bc_in;
+  bc_in.start(a, q.b, row, p.g, kAll, false);
+  // the lane's element of a tile's first four rows
+  const uint32_t ou = s * uint32_t(a.su.l) + d, od = s * uint32_t(a.sd.l) + d, oz = s * uint32_t(a.sz.l) + d,
+                 og = s * uint32_t(a.D) + d;
+  // loads a tile of `rows` steps (none: 0) and goes on to the one before it
+  auto fetch = [&](int rows) {
+    const uint32_t cu = opaque(ou), cd = opaque(od), cz = opaque(oz), cg = opaque(og), cm = opaque(om);
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
-      const uint32_t r = min(s + 4 * j, last);
-      if (kAll) ru[j] = pu[r * ul + d];
-      rd[j] = pd[r * dl_ + d];
-      if (pz) rz[j] = pz[r * zl + d];
-      rg[j] = pg[r * gl + d];
+      if (s + 4 * j < rows) {
+        if (kAll) ru[j] = element(pu + j * 4 * a.su.l, cu);
+        rd[j] = element(pd + j * 4 * a.sd.l, cd);
+        if (kGate) rz[j] = element(pz + j * 4 * a.sz.l, cz);
+        rg[j] = element(pg + j * 4 * int64_t(a.D), cg);
+      }
     }
+    bc_in.load(rows, -kTile);
+    if (kAll && rows > 0) {
+      if (whole_mark) {
+        load_states<kNS>(&element(mark, cm), rh);
+      } else {
 #pragma unroll
-    for (int m = 0; m < kPer; ++m) {
-      const int e = tid + m * kThreads;
-      const int n = e % kNP, which = e / kNP % 2, t = e / (2 * kNP);
-      rbc[m] = T(0);
-      if (e < kBC && n < a.N && t <= last) {
-        if (which == 1) rbc[m] = pC[uint32_t(t) * uint32_t(a.sc.l) + n];
-        else if (kAll) rbc[m] = pB[uint32_t(t) * uint32_t(a.sb.l) + n];
+        for (int i = 0; i < kNS; ++i) rh[i] = s * kNS + i < a.N ? element(mark, cm + i) : 0.0f;
       }
     }
     if (kAll) {
-#pragma unroll
-      for (int i = 0; i < kNS; ++i) rh[i] = s * kNS + i < a.N ? mark[i] : 0.0f;
       mark -= int64_t(a.D) * a.N;
+      pu -= kTile * a.su.l;
     }
-    pu -= kTile * a.su.l;
     pd -= kTile * a.sd.l;
-    if (pz) pz -= kTile * a.sz.l;
-    pg -= int64_t(kTile) * a.D;
-    pB -= kTile * a.sb.l;
-    pC -= kTile * a.sc.l;
+    if (kGate) pz -= kTile * a.sz.l;
+    pg -= kTile * int64_t(a.D);
   };
-  // the block's sums of a tile whose first row is `first`, of `left` tokens
-  auto flush = [&](int buf, int64_t first, int64_t left) {
-    const int64_t T_all = a.q.T;
+  // the block's sums of a tile of `left` tokens, from the last tile on
+  float* parts = kAll ? a.bc_parts + ((int64_t(p.cb) * a.q.T + out_row) * a.G + p.g) * 2 * a.N : nullptr;
+  auto flush = [&](int buf, int left) {
 #pragma unroll
     for (int m = 0; m < kPer; ++m) {
-      const int e = tid + m * kThreads;
-      const int n = e % kNP, which = e / kNP % 2, t = e / (2 * kNP);
-      if (e < kBC && n < a.N && t < left) {
-        float v = 0.0f;
-        for (int w = 0; w < waves; ++w) v += sums[buf][w * kBC + e];
-        a.bc_parts[((int64_t(p.cb) * T_all + first + t) * a.G + p.g) * 2 * a.N + which * a.N + n] = v;
+      const int e = tid + m * kThreads, n = tid % kNP, t = e / (2 * kNP);
+      if (n < a.N && t < left) {
+        const float* from = sums[buf] + e;
+        float v = from[0];
+        for (int w = 1; w < waves; ++w) v += from[w * kBC];
+        element(parts, opaque(uint32_t(t) * uint32_t(a.G * 2 * a.N) + tid / kNP % 2 * a.N + n)) = v;
       }
     }
+    parts -= int64_t(kTile) * a.G * 2 * a.N;
   };
 
-  if (tiles > 0) fetch(steps - (tiles - 1) * kTile);
+  if (tiles > 0) fetch(static_cast<int>(steps - (tiles - 1) * kTile));
   int buf = 0;
   for (int64_t k = tiles - 1; k >= 0; --k, buf ^= 1) {
-    const int64_t left = steps - k * kTile;
+    const int left = static_cast<int>(min(steps - k * kTile, int64_t(kTile)));
 #pragma unroll
     for (int m = 0; m < kPer; ++m)
-      if (tid + m * kThreads < kBC) sBC[buf][tid + m * kThreads] = Elem<T>::to_f32(rbc[m]);
+      if (tid + m * kThreads < kBC) sBC[buf][tid + m * kThreads] = Elem<T>::to_f32(bc_in.raw[m]);
     float u[kOwn], raw[kOwn], z[kOwn], g[kOwn], h0[kNS];
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
       u[j] = kAll ? Elem<T>::to_f32(ru[j]) : 0.0f;
       raw[j] = Elem<T>::to_f32(rd[j]);
-      z[j] = pz ? Elem<T>::to_f32(rz[j]) : 0.0f;
+      z[j] = kGate ? Elem<T>::to_f32(rz[j]) : 0.0f;
       g[j] = Elem<T>::to_f32(rg[j]);
     }
 #pragma unroll
     for (int i = 0; i < kNS; ++i) h0[i] = kAll ? rh[i] : 0.0f;
-    if (k > 0) fetch(kTile);
+    if (!kAll) fetch(k > 0 ? kTile : 0);
     __syncthreads();
-    if (kAll && k < tiles - 1) flush(buf ^ 1, out_row + kTile, left - kTile);
+    if (kAll && k < tiles - 1) flush(buf ^ 1, static_cast<int>(min(steps - (k + 1) * kTile, int64_t(kTile))));
+    if (kAll && !wave_on) fetch(k > 0 ? kTile : 0);  // its share of B and C
     if (wave_on) {
       float delta[kOwn], w[kOwn], gy[kOwn], sg[kOwn];
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) {
-        const bool in = on && s + 4 * j < left;
         raw[j] += bias;
-        delta[j] = in ? softplus_f32(raw[j]) : 0.0f;
-        w[j] = in ? delta[j] * u[j] : 0.0f;
-        gy[j] = in ? g[j] : 0.0f;
+        delta[j] = softplus_f32(raw[j]);
+        w[j] = delta[j] * u[j];
+        gy[j] = g[j];
         sg[j] = 0.0f;
-        if (pz) {
+        if (kGate) {
           sg[j] = __builtin_amdgcn_rcpf(1.0f + exp2_hw(-z[j] * kLog2e));
-          gy[j] = in ? g[j] * (sg[j] == 0.0f ? -0.0f : z[j] * sg[j]) : 0.0f;
+          gy[j] *= sg[j] == 0.0f ? -0.0f : z[j] * sg[j];
         }
-        sum_delta += delta[j];
+      }
+      if (!on || left < kTile) {  // lanes and steps that are not there change nothing
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+          const bool in = on && s + 4 * j < left;
+          delta[j] = in ? delta[j] : 0.0f;
+          w[j] = in ? w[j] : 0.0f;
+          gy[j] = in ? gy[j] : 0.0f;
+        }
       }
       const float* bc = sBC[buf] + s * kNS;
       if constexpr (!kAll) {
 #pragma unroll
-        for (int t = kTile - 1; t >= 0; --t) {
-          const float dt = from_owner<4>(delta[t / 4], t % 4), gt = from_owner<4>(gy[t / 4], t % 4);
+        for (int j = kOwn - 1; j >= 0; --j) {
+          float C[4][kNS], as[4][kNS];
 #pragma unroll
-          for (int i = 0; i < kNS; ++i)
-            carry[i] = exp2_hw(dt * Ap[i]) * fmaf(gt, bc[t * 2 * kNP + kNP + i], carry[i]);
+          for (int r = 0; r < 4; ++r) load_states<kNS>(bc + (4 * j + r) * 2 * kNP + kNP, C[r]);
+          unrolled<0, 4>([&](auto r) {
+            const float dt = from_owner<4>(delta[j], r);
+#pragma unroll
+            for (int i = 0; i < kNS; ++i) as[r][i] = exp2_hw(dt * Ap[i]);
+          });
+          unrolled<0, 4>([&](auto k) {
+            constexpr int r = 3 - k;
+            const float gt = from_owner<4>(gy[j], r);
+#pragma unroll
+            for (int i = 0; i < kNS; ++i) carry[i] = as[r][i] * fmaf(gt, C[r][i], carry[i]);
+          });
+          sum_delta += delta[j];
         }
       } else {
-        float as[kTile][kNS], hs[kTile][kNS];
+        float as[kTile][kNS], hs[kTile + 1][kNS];
+#pragma unroll
+        for (int i = 0; i < kNS; ++i) hs[0][i] = h0[i];
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
-          float y[4];
+          __builtin_amdgcn_sched_barrier(0);
+          float B[4][kNS], C[4][kNS], y[4];
+          unrolled<0, 4>([&](auto r) {
+            const float dt = from_owner<4>(delta[j], r);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
+            for (int i = 0; i < kNS; ++i) as[4 * j + r][i] = exp2_hw(dt * Ap[i]);
+          });
+          unrolled<0, 4>([&](auto r) {
+            if (r % 2 == 0) {  // two steps' operands
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int i = r; i <= r + 1; ++i) {
+                load_states<kNS>(bc + (4 * j + i) * 2 * kNP, B[i]);
+                if (kGate) load_states<kNS>(bc + (4 * j + i) * 2 * kNP + kNP, C[i]);
+              }
+            }
+            const float wt = from_owner<4>(w[j], r);
             const int t = 4 * j + r;
-            const float dt = from_owner<4>(delta[j], r), wt = from_owner<4>(w[j], r);
             y[r] = 0.0f;
 #pragma unroll
             for (int i = 0; i < kNS; ++i) {
-              as[t][i] = exp2_hw(dt * Ap[i]);
-              hs[t][i] = fmaf(as[t][i], t ? hs[t ? t - 1 : 0][i] : h0[i], wt * bc[t * 2 * kNP + i]);
-              if (pz) y[r] = fmaf(bc[t * 2 * kNP + kNP + i], hs[t][i], y[r]);
+              hs[t + 1][i] = fmaf(as[t][i], hs[t][i], wt * B[r][i]);
+              if (kGate) y[r] = i ? fmaf(C[r][i], hs[t + 1][i], y[r]) : C[r][i] * hs[t + 1][i];
             }
-          }
-          if (pz) {
+          });
+          if (kGate) {
             const float v = fmaf(skip, u[j], quad_scatter_sum(y[0], y[1], y[2], y[3], odd, high));
             // SiLU'(z) = sigmoid(z) (1 + z (1 - sigmoid(z)))
             const float slope = sg[j] == 0.0f ? 0.0f : (sg[j] == 1.0f ? 1.0f : sg[j] * fmaf(z[j], 1.0f - sg[j], 1.0f));
-            if (on && s + 4 * j < left)
-              static_cast<T*>(a.dz)[out_row * a.D + uint32_t(s + 4 * j) * gl + d] = Elem<T>::from_f32(g[j] * v * slope);
+            if (on && s + 4 * j < left) element(qz + j * 4 * int64_t(a.D), opaque(og)) = Elem<T>::from_f32(g[j] * v * slope);
           }
         }
+        // B and C are read again: kept from above, they would take 128 registers
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int j = kOwn - 1; j >= 0; --j) {
-          float P[4], Q[4], acc[kNY];
-#pragma unroll
-          for (int r = 3; r >= 0; --r) {
+          // groups of steps are kept apart, or their operands would not fit the registers; the next
+          // tile is loaded once half of the states held here are used up
+          __builtin_amdgcn_sched_barrier(0);
+          if (j == kOwn / 2 - 1) fetch(k > 0 ? kTile : 0);
+          __builtin_amdgcn_sched_barrier(0);
+          float P[4], Q[4], acc[kNY], B[4][kNS], C[4][kNS];
+          unrolled<0, 4>([&](auto k) {
+            constexpr int r = 3 - k;
             const int t = 4 * j + r;
+            if (r % 2 == 1) {  // two steps' operands
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int i = r - 1; i <= r; ++i) {
+                load_states<kNS>(bc + (4 * j + i) * 2 * kNP, B[i]);
+                load_states<kNS>(bc + (4 * j + i) * 2 * kNP + kNP, C[i]);
+              }
+            }
             const float dt = from_owner<4>(delta[j], r), wt = from_owner<4>(w[j], r), gt = from_owner<4>(gy[j], r);
             float dB[kNS], dC[kNS], out[kNY];
-            P[r] = Q[r] = 0.0f;
 #pragma unroll
             for (int i = 0; i < kNS; ++i) {
-              const float lam = fmaf(gt, bc[t * 2 * kNP + kNP + i], carry[i]);
+              const float lam = fmaf(gt, C[r][i], carry[i]);
               dB[i] = lam * wt;
-              dC[i] = gt * hs[t][i];
-              Q[r] = fmaf(lam, bc[t * 2 * kNP + i], Q[r]);
+              dC[i] = gt * hs[t + 1][i];
+              Q[r] = i ? fmaf(lam, B[r][i], Q[r]) : lam * B[r][i];
               carry[i] = as[t][i] * lam;
-              const float v = carry[i] * (t ? hs[t ? t - 1 : 0][i] : h0[i]);
+              const float v = carry[i] * hs[t][i];
               dA[i] = fmaf(dt, v, dA[i]);
-              P[r] = fmaf(v, Ap[i], P[r]);
+              P[r] = i ? fmaf(v, Ap[i], P[r]) : v * Ap[i];
             }
             channel_sums<kNS>(dB, dC, out);
 #pragma unroll
-            for (int m = 0; m < kNY; ++m) acc[m] = bank == r ? out[m] : (r == 3 ? 0.0f : acc[m]);
-          }
+            for (int m = 0; m < kNY; ++m) acc[m] = r == 3 || bank == r ? out[m] : acc[m];
+          });
           // a lane's sums are those of step 4 j + bank
           float* to = sums[buf] + wave * kBC + (4 * j + bank) * 2 * kNP + (lane >> 5) * kNP + s * kNS;
           if constexpr (kNS == 1) {
@@ -241,25 +293,28 @@ __global__ __launch_bounds__(kThreads) void k_scan_adjoint(Args a) {
           }
           const float ps = quad_scatter_sum(P[0], P[1], P[2], P[3], odd, high) * kLn2;
           const float qs = quad_scatter_sum(Q[0], Q[1], Q[2], Q[3], odd, high);
-          const bool in = on && s + 4 * j < left;
           const float draw = fmaf(u[j], qs, ps) * __builtin_amdgcn_rcpf(1.0f + exp2_hw(-raw[j] * kLog2e));
           const float du = fmaf(delta[j], qs, skip * gy[j]);
-          if (in) {
-            const int64_t at = out_row * a.D + uint32_t(s + 4 * j) * gl + d;
-            static_cast<T*>(a.du)[at] = Elem<T>::from_f32(du);
-            static_cast<T*>(a.ddt)[at] = Elem<T>::from_f32(draw);
+          if (on && s + 4 * j < left) {
+            const uint32_t at = opaque(og);
+            element(qu + j * 4 * int64_t(a.D), at) = Elem<T>::from_f32(du);
+            element(qd + j * 4 * int64_t(a.D), at) = Elem<T>::from_f32(draw);
             dD = fmaf(gy[j], u[j], dD);
             dbias += draw;
           }
         }
       }
     }
-    out_row -= kTile;
+    if (kAll) {
+      qu -= int64_t(kTile) * a.D;
+      qd -= int64_t(kTile) * a.D;
+      if (kGate) qz -= int64_t(kTile) * a.D;
+    }
   }
   if constexpr (kAll) {
     if (tiles > 0) {
       __syncthreads();
-      flush(buf ^ 1, out_row + kTile, min(steps, int64_t(kTile)));
+      flush(buf ^ 1, static_cast<int>(min(steps, int64_t(kTile))));
     }
     dD = group_sum<4>(dD);
     dbias = group_sum<4>(dbias);
@@ -287,22 +342,29 @@ __global__ __launch_bounds__(kThreads) void k_scan_adjoint(Args a) {
   }
 }
 
-// dB and dC: the sums over the channel blocks, for units of 64 tokens of one sequence.
-constexpr int kSumTokens = 64;
+// dB and dC: the sums over the channel blocks, for units of kSumTokens tokens of one sequence.
+constexpr int kSumTokens = 16;
 template <typename T>
 __global__ __launch_bounds__(256) void k_scan_sum_bc(Args a) {
   int64_t idx;
   const Sequence q = sequence_of(a.q, blockIdx.x, kSumTokens, &idx);
   const int64_t t0 = idx * kSumTokens;
   if (t0 >= q.len) return;
-  const int64_t row = q.b * a.q.L + q.begin + t0, width = int64_t(a.G) * 2 * a.N;
-  const int64_t count = min(q.len - t0, int64_t(kSumTokens)) * width, stride = a.q.T * width;
+  const int64_t row = q.b * a.q.L + q.begin + t0;
+  const int width = a.G * 2 * a.N, count = static_cast<int>(min(q.len - t0, int64_t(kSumTokens))) * width;
+  const int64_t stride = a.q.T * width;
   const float* parts = a.bc_parts + row * width;
-  for (int64_t e = threadIdx.x; e < count; e += 256) {
-    float v = 0.0f;
-    for (int b = 0; b < a.cbg; ++b) v += parts[b * stride + e];
-    const int64_t tg = e / (2 * a.N);
-    const int n = static_cast<int>(e % (2 * a.N));
+  for (int e = threadIdx.x; e < count; e += 256) {
+    constexpr int kAhead = 8;
+    float x[kAhead] = {};
+    const float* p = parts + e;
+    int b = 0;
+    for (; b + kAhead <= a.cbg; b += kAhead, p += kAhead * stride)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) x[i] += p[i * stride];
+    for (; b < a.cbg; ++b, p += stride) x[0] += *p;
+    const float v = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    const int tg = e / (2 * a.N), n = e % (2 * a.N);
     T* to = static_cast<T*>(n < a.N ? a.dB : a.dC);
     to[(row * a.G + tg) * a.N + (n < a.N ? n : n - a.N)] = Elem<T>::from_f32(v);
   }
@@ -335,16 +397,22 @@ __global__ __launch_bounds__(1024) void k_scan_sum_params(Args a) {
   else a.dbias[d] = v;
 }
 
+template <typename T, int kNS, bool kAll>
+int launch_gate(const Args& a, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.units * a.G * a.cbg)), block(kThreads);
+  if (a.z) hipLaunchKernelGGL((k_scan_adjoint<T, kNS, kAll, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_scan_adjoint<T, kNS, kAll, false>), grid, block, 0, st, a);
+  return static_cast<int>(hipGetLastError());
+}
+
 template <typename T, bool kAll>
 int launch_states(const Args& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.units * a.G * a.cbg)), block(kThreads);
   switch (lane_states(a.N)) {
-    case 1: hipLaunchKernelGGL((k_scan_adjoint<T, 1, kAll>), grid, block, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_scan_adjoint<T, 2, kAll>), grid, block, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((k_scan_adjoint<T, 4, kAll>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_scan_adjoint<T, 8, kAll>), grid, block, 0, st, a); break;
+    case 1: return launch_gate<T, 1, kAll>(a, st);
+    case 2: return launch_gate<T, 2, kAll>(a, st);
+    case 4: return launch_gate<T, 4, kAll>(a, st);
+    default: return launch_gate<T, 8, kAll>(a, st);
   }
-  return static_cast<int>(hipGetLastError());
 }
 
 }  // namespace

@@ -1,5 +1,6 @@
 // The token-order selective scan, forward: whole sequences or segments of them.
 #include <algorithm>
+#include <type_traits>
 
 #include "ss1d_scan.h"
 
@@ -7,46 +8,55 @@ namespace ss2d {
 namespace sscan {
 namespace {
 
-// kNS states of a lane from LDS or memory rows on 16 bytes.
-template <int kNS> __device__ __forceinline__ void load_states(const float* p, float* x) {
-  if constexpr (kNS % 4 == 0) {
+// kS lanes share a channel (4: a quad, 16: a row of 16 lanes), each with kNS of its states and every
+// kS-th step of a tile.
+template <int kS, int kOwner> __device__ __forceinline__ float from_step(float v) {
+  if constexpr (kS == 4) return from_owner<4>(v, kOwner);
+  else return dpp_move<0x150 + kOwner>(v);  // row_newbcast
+}
+
+// Sums each of kS values over the lanes of a channel: lane s gets the sum of v[s].
+template <int kS> __device__ __forceinline__ float scatter_sum(const float* v, int s) {
+  const bool b0 = s & 1, b1 = s & 2;
+  float a[kS / 4];
+  if constexpr (kS == 4) return quad_scatter_sum(v[0], v[1], v[2], v[3], b0, b1);
 #pragma unroll
-    for (int i = 0; i < kNS; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + i);
-      x[i] = v.x;
-      x[i + 1] = v.y;
-      x[i + 2] = v.z;
-      x[i + 3] = v.w;
-    }
-  } else if constexpr (kNS == 2) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    x[0] = v.x;
-    x[1] = v.y;
-  } else {
-    x[0] = *p;
+  for (int i = 0; i < kS / 4; ++i) a[i] = quad_scatter_sum(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], b0, b1);
+  if constexpr (kS == 16) {  // a[i] belongs to quad i: lanes 8 apart first, then 4
+    const bool b2 = s & 4, b3 = s & 8;
+    float x = (b3 ? a[2] : a[0]) + from_lane<8>(b3 ? a[0] : a[2]);
+    float y = (b3 ? a[3] : a[1]) + from_lane<8>(b3 ? a[1] : a[3]);
+    a[0] = (b2 ? y : x) + from_lane<4>(b2 ? x : y);
   }
+  return a[0];
 }
 
 // kOut: outputs, end states and marks; else a segment's end state from a zero start and its sum
 // of delta.
-template <typename T, int kNS, bool kOut>
-__global__ __launch_bounds__(kThreads) void k_scan_tokens(Args a) {
-  constexpr int kTile = tile_of(kNS), kOwn = kTile / 4, kNP = 4 * kNS;
-  constexpr int kBC = kTile * 2 * kNP, kPer = (kBC + kThreads - 1) / kThreads;
-  __shared__ __align__(16) float sBC[2][kBC];  // rows of a step: B, then C
+template <typename T, int kS, int kNS, bool kOut, bool kGate>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4)))
+void k_scan_tokens(Args a) {
+  constexpr int kMark = tile_of(kNS), kTile = kS == 4 ? kMark : 64, kOwn = kTile / kS, kNP = kS * kNS;
+  constexpr int kWaveCh = 64 / kS, kCh = kThreads / kS;
+  constexpr int kBC = kTile * 2 * kNP, kPer = Operands<T, kTile, kNP>::kPer;
+  // B and C of a tile: rows of a step (B, then C) for a quad; for 16 lanes rows of a state, padded
+  constexpr int kRow = kS == 4 ? 2 * kNP : kTile + 4, kSize = kS == 4 ? kBC : 2 * kNP * kRow;
+  __shared__ __align__(16) float sBC[2][kSize];
 
-  const Place p = place_of(a, blockIdx.x, gridDim.x);
+  const Place p = place_of(a, kCh, blockIdx.x, gridDim.x);
   int64_t idx = 0;
-  const Sequence q = a.seglen ? sequence_of(a.q, p.unit, a.seglen, &idx) : sequence(a.q, p.unit);
+  const Sequence q = uniform(a.seglen ? sequence_of(a.q, p.unit, a.seglen, &idx) : sequence(a.q, p.unit));
+  idx = uniform(idx);
   const int64_t t_begin = idx * a.seglen;
   if (idx > 0 && t_begin >= q.len) return;  // an empty unit
+  // nothing follows a sequence's last segment, so that nobody needs its end state
+  if (!kOut && t_begin + a.seglen >= q.len) return;
   const int64_t t_end = a.seglen ? min(q.len, t_begin + a.seglen) : q.len;
 
-  const int tid = threadIdx.x, lane = tid & 63, s = lane & 3;
-  const int Dg = a.D / a.G, c = p.c0 + (tid >> 2);
-  const bool on = c < Dg, wave_on = p.c0 + (tid >> 6) * 16 < Dg;
+  const int tid = threadIdx.x, lane = tid & 63, s = lane % kS;
+  const int Dg = a.D / a.G, c = p.c0 + tid / kS;
+  const bool on = c < Dg, wave_on = p.c0 + __builtin_amdgcn_readfirstlane(tid >> 6) * kWaveCh < Dg;
   const int d = p.g * Dg + (on ? c : Dg - 1);
-  const bool odd = s & 1, high = s & 2;
 
   float Ap[kNS], h[kNS];
 #pragma unroll
@@ -71,97 +81,127 @@ __global__ __launch_bounds__(kThreads) void k_scan_tokens(Args a) {
   const int64_t row = q.begin + t_begin;
   const T* pu = static_cast<const T*>(a.u) + q.b * a.su.b + row * a.su.l;
   const T* pd = static_cast<const T*>(a.dt) + q.b * a.sd.b + row * a.sd.l;
-  const T* pz = kOut && a.z ? static_cast<const T*>(a.z) + q.b * a.sz.b + row * a.sz.l : nullptr;
-  const T* pB = static_cast<const T*>(a.Bs) + q.b * a.sb.b + row * a.sb.l + p.g * a.sbg;
-  const T* pC = static_cast<const T*>(a.Cs) + q.b * a.sc.b + row * a.sc.l + p.g * a.scg;
+  const T* pz = kGate ? static_cast<const T*>(a.z) + q.b * a.sz.b + row * a.sz.l : nullptr;
   T* py = kOut ? static_cast<T*>(a.y) + (q.b * a.q.L + row) * a.D : nullptr;
-  const uint32_t ul = a.su.l, dl_ = a.sd.l, zl = a.sz.l;
 
-  T ru[kOwn], rd[kOwn], rz[kOwn], rbc[kPer];
-  auto fetch = [&](int64_t left) {
-    const bool full = left >= kTile;
-    const int last = full ? kTile - 1 : static_cast<int>(left) - 1;
+  T ru[kOwn] = {}, rd[kOwn] = {}, rz[kOwn] = {};
+  Operands<T, kTile, kNP> bc_in;
+  bc_in.start(a, q.b, row, p.g, kOut, true);
+  // the lane's element of a tile's first kS rows
+  const uint32_t ou = s * uint32_t(a.su.l) + d, od = s * uint32_t(a.sd.l) + d, oz = s * uint32_t(a.sz.l) + d,
+                 oy = s * uint32_t(a.D) + d;
+  auto fetch = [&](int rows) {
+    const uint32_t cu = opaque(ou), cd = opaque(od), cz = opaque(oz);
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
-      const uint32_t r = min(s + 4 * j, last);
-      ru[j] = pu[r * ul + d];
-      rd[j] = pd[r * dl_ + d];
-      if (kOut && pz) rz[j] = pz[r * zl + d];
-    }
-#pragma unroll
-    for (int m = 0; m < kPer; ++m) {
-      const int e = tid + m * kThreads;
-      const int n = e % kNP, which = e / kNP % 2, t = e / (2 * kNP);
-      rbc[m] = T(0);
-      if (e < kBC && n < a.N && t <= last) {
-        if (which == 0) rbc[m] = pB[uint32_t(t) * uint32_t(a.sb.l) + n];
-        else if (kOut) rbc[m] = pC[uint32_t(t) * uint32_t(a.sc.l) + n];
+      if (s + kS * j < rows) {
+        ru[j] = element(pu + j * kS * a.su.l, cu);
+        rd[j] = element(pd + j * kS * a.sd.l, cd);
+        if (kGate) rz[j] = element(pz + j * kS * a.sz.l, cz);
       }
     }
+    bc_in.load(rows, kTile);
     pu += kTile * a.su.l;
     pd += kTile * a.sd.l;
-    if (kOut && pz) pz += kTile * a.sz.l;
-    pB += kTile * a.sb.l;
-    pC += kTile * a.sc.l;
+    if (kGate) pz += kTile * a.sz.l;
   };
 
   float* mark = nullptr;
-  if (kOut && a.marks)
-    mark = a.marks + ((first_unit(a.q, q, kTile) + t_begin / kTile) * a.D + d) * a.N + s * kNS;
+  if (kOut && kS == 4 && a.marks)
+    mark = a.marks + (first_unit(a.q, q, kMark) + t_begin / kMark) * a.D * a.N;
+  const uint32_t om = uint32_t(d) * a.N + s * kNS;
+  const bool whole_mark = kNS == 4 && a.N == 16;
   float sum_delta = 0.0f;
   int64_t left = t_end - t_begin;
-  if (left > 0) fetch(left);
+  if (left > 0) fetch(static_cast<int>(min(left, int64_t(kTile))));
   for (int buf = 0; left > 0; left -= kTile, buf ^= 1) {
+    const int rows = static_cast<int>(min(left, int64_t(kTile)));
 #pragma unroll
-    for (int m = 0; m < kPer; ++m)
-      if (tid + m * kThreads < kBC) sBC[buf][tid + m * kThreads] = Elem<T>::to_f32(rbc[m]);
+    for (int m = 0; m < kPer; ++m) {
+      const int e = tid + m * kThreads;
+      if (kBC % kThreads == 0 || e < kBC) {
+        if constexpr (kS == 4) sBC[buf][e] = Elem<T>::to_f32(bc_in.raw[m]);
+        else sBC[buf][e % (2 * kNP) * kRow + e / (2 * kNP)] = Elem<T>::to_f32(bc_in.raw[m]);
+      }
+    }
     float u[kOwn], delta[kOwn], z[kOwn], w[kOwn];
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
       u[j] = Elem<T>::to_f32(ru[j]);
       delta[j] = Elem<T>::to_f32(rd[j]);
-      z[j] = kOut && pz ? Elem<T>::to_f32(rz[j]) : 0.0f;
+      z[j] = kGate ? Elem<T>::to_f32(rz[j]) : 0.0f;
     }
-    if (left > kTile) fetch(left - kTile);
+    fetch(static_cast<int>(max(int64_t(0), min(left - kTile, int64_t(kTile)))));
     __syncthreads();
     if (wave_on) {
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) {
-        const bool in = s + 4 * j < left;
-        delta[j] = in ? softplus_f32(delta[j] + bias) : 0.0f;
-        w[j] = in ? delta[j] * u[j] : 0.0f;
-        sum_delta += delta[j];
+        delta[j] = softplus_f32(delta[j] + bias);
+        w[j] = delta[j] * u[j];
       }
-      if (kOut && mark) {
-        if (on) {
+      if (rows < kTile) {
 #pragma unroll
-          for (int i = 0; i < kNS; ++i)
-            if (s * kNS + i < a.N) mark[i] = h[i];
+        for (int j = 0; j < kOwn; ++j) {
+          const bool in = s + kS * j < rows;
+          delta[j] = in ? delta[j] : 0.0f;
+          w[j] = in ? w[j] : 0.0f;
         }
-        mark += int64_t(a.D) * a.N;
       }
-      const float* bc = sBC[buf] + s * kNS;
+      if (!kOut) {
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) sum_delta += delta[j];
+      }
+      const float* bc = sBC[buf] + (kS == 4 ? s * kNS : s * kNS * kRow);
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) {
-        float y[4];
+        if (kOut && kS == 4 && kS * j % kMark == 0 && mark && kS * j < rows) {
+          if (on && whole_mark) {
+            *reinterpret_cast<float4*>(&element(mark, opaque(om))) = make_float4(h[0], h[1 % kNS], h[2 % kNS], h[3 % kNS]);
+          } else if (on) {
+  #pragma unroll
+            for (int i = 0; i < kNS; ++i)
+              if (s * kNS + i < a.N) element(mark, opaque(om) + i) = h[i];
+          }
+          mark += int64_t(a.D) * a.N;
+        }
+        float B[kS][kNS], C[kS][kNS], as[kS][kNS], y[kS];
+        if constexpr (kS == 4) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float dt = from_owner<4>(delta[j], r), wt = from_owner<4>(w[j], r);
-          float B[kNS], C[kNS];
-          load_states<kNS>(bc + (4 * j + r) * 2 * kNP, B);
-          if (kOut) load_states<kNS>(bc + (4 * j + r) * 2 * kNP + kNP, C);
+          for (int r = 0; r < kS; ++r) {
+            load_states<kNS>(bc + (kS * j + r) * kRow, B[r]);
+            if (kOut) load_states<kNS>(bc + (kS * j + r) * kRow + kNP, C[r]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kNS; ++i)
+#pragma unroll
+            for (int r = 0; r < kS; r += 4) {
+              const float4 vb = *reinterpret_cast<const float4*>(bc + i * kRow + kS * j + r);
+              B[r][i] = vb.x, B[r + 1][i] = vb.y, B[r + 2][i] = vb.z, B[r + 3][i] = vb.w;
+              if (kOut) {
+                const float4 vc = *reinterpret_cast<const float4*>(bc + (kNP + i) * kRow + kS * j + r);
+                C[r][i] = vc.x, C[r + 1][i] = vc.y, C[r + 2][i] = vc.z, C[r + 3][i] = vc.w;
+              }
+            }
+        }
+        unrolled<0, kS>([&](auto r) {
+          const float dt = from_step<kS, r>(delta[j]);
+#pragma unroll
+          for (int i = 0; i < kNS; ++i) as[r][i] = exp2_hw(dt * Ap[i]);
+        });
+        unrolled<0, kS>([&](auto r) {
+          const float wt = from_step<kS, r>(w[j]);
           y[r] = 0.0f;
 #pragma unroll
           for (int i = 0; i < kNS; ++i) {
-            h[i] = fmaf(exp2_hw(dt * Ap[i]), h[i], wt * B[i]);
-            if (kOut) y[r] = fmaf(C[i], h[i], y[r]);
+            h[i] = fmaf(as[r][i], h[i], wt * B[r][i]);
+            if (kOut) y[r] = i ? fmaf(C[r][i], h[i], y[r]) : C[r][i] * h[i];
           }
-        }
+        });
         if constexpr (kOut) {
-          float v = quad_scatter_sum(y[0], y[1], y[2], y[3], odd, high);
-          v = fmaf(skip, u[j], v);
-          if (pz) v *= silu_f32(z[j]);
-          if (on && s + 4 * j < left) py[uint32_t(s + 4 * j) * uint32_t(a.D) + d] = Elem<T>::from_f32(v);
+          float v = fmaf(skip, u[j], scatter_sum<kS>(y, s));
+          if (kGate) v *= silu_f32(z[j]);
+          if (on && s + kS * j < rows) element(py + j * kS * int64_t(a.D), opaque(oy)) = Elem<T>::from_f32(v);
         }
       }
     }
@@ -204,9 +244,9 @@ __global__ __launch_bounds__(256) void k_scan_join(Args a) {
     float end[kAhead], delta[kAhead];
 #pragma unroll
     for (int m = 0; m < kAhead; ++m) {
-      const int64_t k = min(j + m, count - 1), unit = first + (kBack ? count - 1 - k : k);
-      end[m] = a.seg_end[unit * per + i];
-      delta[m] = a.seg_delta[unit * a.D + d];
+      const int64_t k = j + m, unit = first + (kBack ? count - 1 - k : k);
+      end[m] = k < count - 1 ? a.seg_end[unit * per + i] : 0.0f;  // of the last nothing is kept
+      delta[m] = k < count - 1 ? a.seg_delta[unit * a.D + d] : 0.0f;
     }
 #pragma unroll
     for (int m = 0; m < kAhead; ++m) {
@@ -218,16 +258,25 @@ __global__ __launch_bounds__(256) void k_scan_join(Args a) {
   }
 }
 
+template <typename T, int kS, int kNS, bool kOut>
+int launch_gate(const Args& a, hipStream_t st) {
+  const int per = (a.D / a.G + kThreads / kS - 1) / (kThreads / kS);
+  const dim3 grid(static_cast<unsigned>(a.units * a.G * per)), block(kThreads);
+  if (kOut && a.z) hipLaunchKernelGGL((k_scan_tokens<T, kS, kNS, kOut, kOut>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_scan_tokens<T, kS, kNS, kOut, false>), grid, block, 0, st, a);
+  return static_cast<int>(hipGetLastError());
+}
+
 template <typename T, bool kOut>
 int launch_states(const Args& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.units * a.G * a.cbg)), block(kThreads);
+  if (kOut && a.lanes == 16)
+    return a.N <= 16 ? launch_gate<T, 16, 1, true>(a, st) : launch_gate<T, 16, 2, true>(a, st);
   switch (lane_states(a.N)) {
-    case 1: hipLaunchKernelGGL((k_scan_tokens<T, 1, kOut>), grid, block, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((k_scan_tokens<T, 2, kOut>), grid, block, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((k_scan_tokens<T, 4, kOut>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((k_scan_tokens<T, 8, kOut>), grid, block, 0, st, a); break;
+    case 1: return launch_gate<T, 4, 1, kOut>(a, st);
+    case 2: return launch_gate<T, 4, 2, kOut>(a, st);
+    case 4: return launch_gate<T, 4, 4, kOut>(a, st);
+    default: return launch_gate<T, 4, 8, kOut>(a, st);
   }
-  return static_cast<int>(hipGetLastError());
 }
 
 }  // namespace

@@ -68,4 +68,14 @@ __device__ __forceinline__ Sequence sequence_of(const Sequences& q, int64_t unit
   return s;
 }
 
+// A value that is the same in every lane of a wave, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
+  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+__device__ __forceinline__ Sequence uniform(const Sequence& s) {
+  return {uniform(s.n), uniform(s.b), uniform(s.begin), uniform(s.len)};
+}
+
 }  // namespace ss2d

@@ -186,20 +186,20 @@ def adjoint(t, cu=None):
     return d, bounds
 
 
-class segments:
-    """Forces the scan's segment length (tokens; 0: whole sequences) for this thread's calls inside
-    the block."""
+class plan:
+    """Forces the scan's segment length (tokens; 0: whole sequences) and the lanes of a channel in the
+    forward (0: the rule's) for this thread's calls inside the block."""
 
-    def __init__(self, tokens):
-        self.tokens = tokens
+    def __init__(self, tokens=-1, lanes=0):
+        self.tokens, self.lanes = tokens, lanes
 
     def __enter__(self):
         from selective_scan_ss2d_amd import _binding as bnd
-        assert bnd.load_library().ss1d_scan_set_segment(self.tokens) == 0
+        assert bnd.load_library().ss1d_scan_set_plan(self.lanes, self.tokens) == 0
 
     def __exit__(self, *exc):
         from selective_scan_ss2d_amd import _binding as bnd
-        bnd.load_library().ss1d_scan_set_segment(-1)
+        bnd.load_library().ss1d_scan_set_plan(0, -1)
 
 
 # ---- the convolution -------------------------------------------------------------------------

@@ -52,13 +52,16 @@ def test_forward(case):
     t = su.make_inputs(B, L, D, G, N, dtype, seed=L + N, gate=gate, h0=B if h0 else 0, views=views)
     ref, ends, hm = su.reference(t)
     d = gpu(t)
-    with su.segments(seg):
-        y, end = ss.ss1d_scan_forward(*args(d), z=d["z"], initial_state=d["h0"], final_state=True)
-        alone = ss.ss1d_scan_forward(*args(d), z=d["z"], initial_state=d["h0"])
+    for lanes in (16, 4):
+        with su.plan(seg, lanes):
+            y, end = ss.ss1d_scan_forward(*args(d), z=d["z"], initial_state=d["h0"], final_state=True)
+            alone = ss.ss1d_scan_forward(*args(d), z=d["z"], initial_state=d["h0"])
+        su.check(y, ref, "y", *su.y_bounds(t, hm))
+        su.check(end, ends, "end states", su.state_bound(t, hm))
+        assert torch.equal(y, alone)
+    with su.plan(seg):
         y2, end2, saved = ss.ss1d_scan_forward_save(*args(d), z=d["z"], initial_state=d["h0"], final_state=True)
-    su.check(y, ref, "y", *su.y_bounds(t, hm))
-    su.check(end, ends, "end states", su.state_bound(t, hm))
-    assert torch.equal(y, alone) and torch.equal(y, y2) and torch.equal(end, end2)
+    assert torch.equal(y, y2) and torch.equal(end, end2)  # both by four lanes
 
 
 PACKED = [
@@ -78,15 +81,16 @@ def test_packed_forward(case):
     t = su.make_inputs(1, T, D, G, N, dtype, seed=T + N, gate=gate, h0=len(cu) - 1)
     ref, ends, hm = su.reference(t, cu)
     d, at = gpu(t), torch.tensor(cu, dtype=torch.int32).cuda()
-    y = torch.full_like(d["u"], 7.0)  # tokens outside of every sequence stay
-    state = d["h0"].clone()
-    with su.segments(seg):
-        y, end = ss.ss1d_scan_forward(*args(d), z=d["z"], cu_seqlens=at, initial_state=state, final_state=state, y=y)
-    assert end is state
-    ref[0, :cu[0]] = 7.0
+    ref[0, :cu[0]] = 7.0  # tokens outside of every sequence stay
     ref[0, cu[-1]:] = 7.0
-    su.check(y, ref, "y", *su.y_bounds(t, hm, cu))
-    su.check(end, ends, "end states", su.state_bound(t, hm, cu))
+    for lanes in (4, 16):
+        y, state = torch.full_like(d["u"], 7.0), d["h0"].clone()
+        with su.plan(seg, lanes):
+            y, end = ss.ss1d_scan_forward(*args(d), z=d["z"], cu_seqlens=at, initial_state=state, final_state=state,
+                                          y=y)
+        assert end is state
+        su.check(y, ref, "y", *su.y_bounds(t, hm, cu))
+        su.check(end, ends, "end states", su.state_bound(t, hm, cu))
 
 
 def check_gradients(t, got, cu=None):
@@ -104,7 +108,7 @@ def test_backward(case):
     t = su.make_inputs(B, L, D, G, N, dtype, seed=L + N, gate=gate, h0=B if h0 else 0, views=views)
     d = gpu(t)
     kw = dict(z=d["z"], initial_state=d["h0"])
-    with su.segments(seg):
+    with su.plan(seg):
         _, saved = ss.ss1d_scan_forward_save(*args(d), **kw)
         got = ss.ss1d_scan_backward(*args(d), d["dy"], dstate=d["dht"], saved=saved, **kw)
         again = ss.ss1d_scan_backward(*args(d), d["dy"], dstate=d["dht"], **kw)
@@ -119,7 +123,7 @@ def test_packed_backward(case):
     t = su.make_inputs(1, T, D, G, N, dtype, seed=T + N, gate=gate, h0=len(cu) - 1)
     d, at = gpu(t), torch.tensor(cu, dtype=torch.int32).cuda()
     kw = dict(z=d["z"], initial_state=d["h0"], cu_seqlens=at)
-    with su.segments(seg):
+    with su.plan(seg):
         _, saved = ss.ss1d_scan_forward_save(*args(d), **kw)
         got = ss.ss1d_scan_backward(*args(d), d["dy"], dstate=d["dht"], saved=saved, **kw)
         again = ss.ss1d_scan_backward(*args(d), d["dy"], dstate=d["dht"], **kw)
@@ -229,19 +233,19 @@ def test_extreme_steps():
     t["A_log"][3] = -float("inf")        # no decay at all
     ref, ends, hm = su.reference(t)
     d = gpu(t)
-    for seg in (0, 16):
-        with su.segments(seg):
+    for seg, lanes in ((0, 4), (16, 4), (0, 16), (16, 16)):
+        with su.plan(seg, lanes):
             y, end = ss.ss1d_scan_forward(*args(d), z=d["z"], initial_state=d["h0"], final_state=True)
         su.check(y, ref, "y", *su.y_bounds(t, hm))
         su.check(end, ends, "end", su.state_bound(t, hm))
 
 
 @pytest.mark.parametrize("name", ["u", "dt_raw", "z", "Bs", "Cs"])
-@pytest.mark.parametrize("seg", [0, 16])
-def test_nan_reaches_no_earlier_token_nor_other_sequence(name, seg):
+@pytest.mark.parametrize("seg, lanes", [(0, 4), (16, 4), (0, 16), (16, 16)])
+def test_nan_reaches_no_earlier_token_nor_other_sequence(name, seg, lanes):
     t = su.make_inputs(2, 60, 40, 2, 16, F32, seed=4)
     d = gpu(t)
-    with su.segments(seg):
+    with su.plan(seg, lanes):
         clean, end0 = ss.ss1d_scan_forward(*args(d), z=d["z"], final_state=True)
         d[name][1, 30].view(-1)[3] = float("nan")
         y, end = ss.ss1d_scan_forward(*args(d), z=d["z"], final_state=True)
@@ -262,7 +266,7 @@ def test_padded_offsets_touch_nothing_else():
     big = torch.full((3, 64, 40), 3.0, device="cuda")
     cu = torch.tensor([-5, 40, 20, 900, 64], dtype=torch.int32, device="cuda")
     for seg in (0, 16):
-        with su.segments(seg):
+        with su.plan(seg):
             ss.ss1d_scan_forward(*args(t), z=t["z"], cu_seqlens=cu, final_state=True, y=big[1:2])
             ss.ss1d_scan_backward(*args(t), t["dy"], z=t["z"], cu_seqlens=cu)
     assert (big[0] == 3.0).all() and (big[2] == 3.0).all()

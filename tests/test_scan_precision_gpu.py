@@ -33,7 +33,7 @@ def test_scan(B, L, D, G, N, seg, dtype):
     g64, _ = su.adjoint(t)
     d = gpu(t)
     kw = dict(z=d["z"], initial_state=d["h0"])
-    with su.segments(seg):
+    with su.plan(seg):
         y, h, saved = ss.ss1d_scan_forward_save(*args(d), final_state=True, **kw)
         g = ss.ss1d_scan_backward(*args(d), d["dy"], dstate=d["dht"], saved=saved, **kw)
     check(y, y64, "y", dtype)
