@@ -14,8 +14,6 @@ namespace ss2d {
 namespace conv {
 
 constexpr int kMaxKW = 8;
-constexpr int kRun = 32;      // tokens of a unit (at least kMaxKW - 1, so that only a sequence's
-                              // first unit reads its initial state)
 constexpr int kThreads = 256;
 
 struct Args {
@@ -26,6 +24,8 @@ struct Args {
   RowStrides sx;
   Sequences q;
   int64_t units;
+  int run;             // tokens of a unit: at least kMaxKW - 1, so that only a sequence's first unit
+                       // reads its initial state
   int D, KW, silu;
   // backward
   const void *dy, *dht;
@@ -34,15 +34,20 @@ struct Args {
   float* parts;        // (unit blocks, KW + 1, D)
   // step
   void* state;         // (S, KW - 1, D)
-  const int32_t* slots;
+  Slots slots;
 };
 
 // Threads that share a row of D channels of a block, in pieces of `width` channels.
 int lanes_of(int64_t D, int width);
+// Tokens of a unit: as many as leave 2048 waves, from 8 to 24, or 32 in the backward, which reads KW - 1
+// more on either side of its unit.
+int run_of(int64_t tokens, int64_t D, bool backward);
 // Blocks along the units of the backward.
 int64_t unit_blocks(const Args& a, int width);
-// Channels of a thread: one 16-byte piece (vec) or one.
-inline int width_of(int dtype, bool vec) { return vec ? (dtype == 0 ? 4 : 8) : 1; }
+// Channels of a thread: four (vec), or one.  Eight bfloat16 values, 16 bytes, take too many registers:
+// forward 150 against 96, 48.6 against 44.6 us (12007 tokens x 4096); backward 246 against 144, 55.7
+// against 44.0 us (128 x 197 tokens x 768).
+inline int width_of(bool vec) { return vec ? 4 : 1; }
 
 int launch_conv(const Args& a, int dtype, bool vec, hipStream_t st);
 int launch_conv_bwd(const Args& a, int dtype, bool vec, hipStream_t st);

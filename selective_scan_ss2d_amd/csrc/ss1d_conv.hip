@@ -1,5 +1,5 @@
 // The short causal convolution: forward, backward, and the form for single tokens.  A thread takes
-// 16 bytes of channels through a unit of kRun tokens of one sequence, its last KW - 1 inputs in
+// four adjacent channels through a unit of tokens of one sequence, its last KW - 1 inputs in
 // registers; blocks lay their threads over channels first, then over units.
 #include <algorithm>
 
@@ -9,15 +9,20 @@ namespace ss2d {
 namespace conv {
 namespace {
 
+// kV adjacent channels as they come from memory, in one access.
+template <typename T, int kV> struct alignas(kV * sizeof(T)) Values { T v[kV]; };
 template <typename T, int kV> struct Piece {
   T v[kV];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kV * sizeof(T) == 16) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-    else v[0] = *p;
+    const auto x = *reinterpret_cast<const Values<T, kV>*>(p);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = x.v[i];
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kV * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
-    else *p = v[0];
+    Values<T, kV> x;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) x.v[i] = v[i];
+    *reinterpret_cast<Values<T, kV>*>(p) = x;
   }
   __device__ __forceinline__ void to(float* x) const {
 #pragma unroll
@@ -74,8 +79,8 @@ __global__ __launch_bounds__(kThreads) void k_conv(Args a, int lanes, int cblock
   const int64_t unit = int64_t(blockIdx.x / cblocks) * (kThreads / lanes) + threadIdx.x / lanes;
   if (c >= a.D || unit >= a.units) return;
   int64_t idx = 0;
-  const Sequence q = sequence_of(a.q, unit, kRun, &idx);
-  const int64_t t0 = idx * kRun, end = min(q.len, t0 + kRun);
+  const Sequence q = sequence_of(a.q, unit, a.run, &idx);
+  const int64_t t0 = idx * a.run, end = min(q.len, t0 + a.run);
   if (idx > 0 && t0 >= q.len) return;
   float w[kV * kKW], b[kV];
   load_taps<kKW, kV>(a, c, w, b);
@@ -138,8 +143,8 @@ __global__ __launch_bounds__(kThreads) void k_conv_bwd(Args a, int lanes, int cb
   if (on) load_taps<kKW, kV>(a, c, w, b);
   for (int64_t unit = block * rows + threadIdx.x / lanes; unit < a.units && on; unit += blocks * rows) {
     int64_t idx = 0;
-    const Sequence q = sequence_of(a.q, unit, kRun, &idx);
-    const int64_t t0 = idx * kRun, end = min(q.len, t0 + kRun);
+    const Sequence q = sequence_of(a.q, unit, a.run, &idx);
+    const int64_t t0 = idx * a.run, end = min(q.len, t0 + a.run);
     if (idx > 0 && t0 >= q.len) continue;
     const T* x = static_cast<const T*>(a.x) + q.b * a.sx.b + q.begin * a.sx.l + c;
     const int64_t at = (q.b * a.q.L + q.begin) * a.D + c;
@@ -273,20 +278,16 @@ __global__ __launch_bounds__(1024) void k_conv_sums(Args a, int64_t count) {
   else if (a.db) a.db[d] = v;
 }
 
-// q.L tokens of each of q.T / q.L rows, states in place; q.S states.
+// q.L tokens of each row, states in place.
 template <typename T, int kKW, int kV>
 __global__ __launch_bounds__(64) void k_conv_step(Args a, int cblocks) {
   const int c = (static_cast<int>(blockIdx.x % cblocks) * 64 + static_cast<int>(threadIdx.x)) * kV;
-  const int64_t rows = a.q.T / a.q.L;
-  int64_t r = blockIdx.x / cblocks, slot = r;
-  if (a.slots) {
-    slot = a.slots[r];
-    if (slot < 0 || slot >= a.q.S) return;  // a padded row: nothing is read or written
-    // rows that name one slot are further tokens of one sequence: the first of them does them all
-    bool earlier = false;
-    for (int64_t i = threadIdx.x; i < r; i += 64) earlier |= a.slots[i] == slot;
-    if (__any(earlier)) return;
-  }
+  __shared__ uint32_t seen[2];
+  int r = blockIdx.x / cblocks;
+  find_repeats(a.slots, r, 1, seen);
+  const int slot = slot_of(a.slots, r, 0, seen);
+  if (slot < 0) return;
+  const bool more = a.slots.at && seen[1];
   const bool on = c < a.D;
   const int cc = on ? c : 0;
   float w[kV * kKW], b[kV], xs[kKW][kV];
@@ -311,15 +312,9 @@ __global__ __launch_bounds__(64) void k_conv_step(Args a, int cblocks) {
 #pragma unroll
       for (int i = 0; i < kKW - 1; ++i) held[i] = held[i + 1];
     }
-    if (!a.slots) break;
-    int64_t next = rows;  // the next row of the same slot
-    for (int64_t base = r + 1; base < rows && next == rows; base += 64) {
-      const int64_t i = base + threadIdx.x;
-      const uint64_t hit = __ballot(i < rows && a.slots[i < rows ? i : r] == slot);
-      if (hit) next = base + __ffsll(static_cast<unsigned long long>(hit)) - 1;
-    }
-    if (next == rows) break;
-    r = next;
+    if (!more) break;
+    r = next_of(a.slots, r, slot);
+    if (r >= a.slots.rows) break;
   }
   if (!on) return;
 #pragma unroll
@@ -331,7 +326,7 @@ enum Kind { kForward, kBackward, kStep };
 template <typename T, int kKW, int kV> int launch_one(const Args& a, Kind kind, hipStream_t st) {
   if (kind == kStep) {
     const int cblocks = (a.D + 64 * kV - 1) / (64 * kV);
-    const int64_t blocks = a.q.T / a.q.L * cblocks;
+    const int64_t blocks = int64_t(a.slots.rows) * cblocks;
     hipLaunchKernelGGL((k_conv_step<T, kKW, kV>), dim3(static_cast<unsigned>(blocks)), dim3(64), 0, st, a, cblocks);
     return static_cast<int>(hipGetLastError());
   }
@@ -359,7 +354,7 @@ template <typename T, int kV> int launch_taps(const Args& a, Kind kind, hipStrea
 
 int launch_types(const Args& a, int dtype, bool vec, Kind kind, hipStream_t st) {
   if (dtype == 0) return vec ? launch_taps<float, 4>(a, kind, st) : launch_taps<float, 1>(a, kind, st);
-  return vec ? launch_taps<uint16_t, 8>(a, kind, st) : launch_taps<uint16_t, 1>(a, kind, st);
+  return vec ? launch_taps<uint16_t, 4>(a, kind, st) : launch_taps<uint16_t, 1>(a, kind, st);
 }
 
 }  // namespace
@@ -377,6 +372,11 @@ int lanes_of(int64_t D, int width) {
     }
   }
   return best;
+}
+
+int run_of(int64_t tokens, int64_t D, bool backward) {
+  const double waves = static_cast<double>(tokens) * D / (64 * 4 * 2048.0);  // of a run of one token
+  return static_cast<int>(std::clamp(waves, 1.0, backward ? 4.0 * 8 : 3.0 * 8)) / 8 * 8 + (waves < 8 ? 8 : 0);
 }
 
 int64_t unit_blocks(const Args& a, int width) {

@@ -1,7 +1,9 @@
 // C entry points of the short causal convolution: argument checks, the backward's partial sums.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ss1d_conv.h"
 #include "ss2d.h"
@@ -49,23 +51,24 @@ int set_rows(Args* a, int64_t* bytes, int64_t B, int64_t L, int64_t D, const int
   return SS2D_OK;
 }
 
-void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, const int32_t* cu, bool packed) {
+void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, const int32_t* cu, bool packed,
+               bool backward) {
   a->q = {cu, S, L, B * L};
   a->D = static_cast<int>(D);
   a->KW = static_cast<int>(KW);
+  a->run = ss2d::conv::run_of(B * L, D, backward);
   // a sequence without tokens still hands its state on: one unit of each
-  a->units = S == 0 ? 0 : ss2d::unit_count(L, S, B * L, packed, ss2d::conv::kRun);
+  a->units = S == 0 ? 0 : ss2d::unit_count(L, S, B * L, packed, a->run);
 }
 
 bool launchable(int64_t units, int64_t D) {
   return units + 8 <= (kMaxThreads - 256 * 4096) / (D + 256);
 }
 
-// Whether rows go in 16-byte pieces.
+// Whether rows go in pieces of four channels.
 bool pieces(const Args& a, int64_t e, std::initializer_list<const void*> data) {
-  const int64_t unit = 16 / e;
-  bool ok = a.D % unit == 0 && a.sx.b % unit == 0 && a.sx.l % unit == 0;
-  for (const void* p : data) ok = ok && !off(p, 16);
+  bool ok = a.D % 4 == 0 && a.sx.b % 4 == 0 && a.sx.l % 4 == 0;
+  for (const void* p : data) ok = ok && !off(p, 4 * e);
   return ok;
 }
 
@@ -92,12 +95,10 @@ int copy_states(const void* from, void* to, int64_t bytes, hipStream_t st) {
   return static_cast<int>(hipGetLastError());
 }
 
-// Blocks along the units for either width of a thread: the more, for which scratch is made.
-int64_t part_blocks(const Args& a, int dtype) {
-  return std::max(ss2d::conv::unit_blocks(a, 1), ss2d::conv::unit_blocks(a, ss2d::conv::width_of(dtype, true)));
-}
-int64_t part_bytes(const Args& a, int dtype) {
-  return static_cast<int64_t>(ss2d::host_align256(size_t(part_blocks(a, dtype)) * (a.KW + 1) * a.D * 4));
+// Bytes of partial sums, with the blocks along the units for either width of a thread.
+int64_t part_bytes(const Args& a) {
+  const int64_t blocks = std::max(ss2d::conv::unit_blocks(a, 1), ss2d::conv::unit_blocks(a, ss2d::conv::width_of(true)));
+  return static_cast<int64_t>(ss2d::host_align256(size_t(blocks) * (a.KW + 1) * a.D * 4));
 }
 
 }  // namespace
@@ -124,7 +125,7 @@ int ss1d_conv_forward(const void* x, const float* conv_w, const float* conv_b, c
   for (const void* p : {static_cast<const void*>(conv_w), static_cast<const void*>(conv_b),
                         static_cast<const void*>(cu_seqlens)})
     if (off(p, 4)) return SS2D_ERR_ALIGN;
-  set_sizes(&a, B, L, S, D, KW, cu_seqlens, packed);
+  set_sizes(&a, B, L, S, D, KW, cu_seqlens, packed, false);
   if (!launchable(a.units, D)) return SS2D_ERR_SHAPE;
   ins[1] = {conv_w, D * KW * 4};
   ins[2] = {conv_b, D * 4};
@@ -151,8 +152,8 @@ int ss1d_conv_forward(const void* x, const float* conv_w, const float* conv_b, c
 int64_t ss1d_conv_scratch_bytes(int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, int dtype, int packed) {
   if (check_sizes(B, L, S, D, KW, dtype, packed != 0) != SS2D_OK) return -1;
   Args a{};
-  set_sizes(&a, B, L, S, D, KW, nullptr, packed != 0);
-  return part_bytes(a, dtype);
+  set_sizes(&a, B, L, S, D, KW, nullptr, packed != 0, true);
+  return part_bytes(a);
 }
 
 int ss1d_conv_backward(const void* x, const float* conv_w, const float* conv_b, const void* h0,
@@ -180,9 +181,9 @@ int ss1d_conv_backward(const void* x, const float* conv_w, const float* conv_b, 
                         static_cast<const void*>(dconv_b)})
     if (off(p, 4)) return SS2D_ERR_ALIGN;
   if (off(scratch, 256)) return SS2D_ERR_ALIGN;
-  set_sizes(&a, B, L, S, D, KW, cu_seqlens, packed);
+  set_sizes(&a, B, L, S, D, KW, cu_seqlens, packed, true);
   if (!launchable(a.units, D)) return SS2D_ERR_SHAPE;
-  const int64_t bytes = part_bytes(a, dtype);
+  const int64_t bytes = part_bytes(a);
   ins[1] = {conv_w, D * KW * 4};
   ins[2] = {conv_b, D * 4};
   ins[3] = {cu_seqlens, packed ? (S + 1) * 4 : 0};
@@ -212,7 +213,7 @@ int ss1d_conv_backward(const void* x, const float* conv_w, const float* conv_b, 
   const bool vec = pieces(a, e, {x, h0, dy, dht, dx, dh0});
   int err = none && !packed ? copy_states(dht, dh0, states, st) : 0;
   if (!err && a.units > 0) err = ss2d::conv::launch_conv_bwd(a, dtype, vec, st);
-  const int64_t blocks = a.units > 0 ? ss2d::conv::unit_blocks(a, ss2d::conv::width_of(dtype, vec)) : 0;
+  const int64_t blocks = a.units > 0 ? ss2d::conv::unit_blocks(a, ss2d::conv::width_of(vec)) : 0;
   if (!err) err = ss2d::conv::launch_conv_sums(a, blocks, st);
   const hipError_t fe = scratch ? hipSuccess : hipFreeAsync(ws, st);
   if (err) return ss2d::host_hip_fail(static_cast<hipError_t>(err));
@@ -253,7 +254,7 @@ int ss1d_conv_step(const void* x, const float* conv_w, const float* conv_b, void
   a.b = conv_b;
   a.y = y;
   a.state = state;
-  a.slots = slots;
+  a.slots = {slots, static_cast<int>(B), S};
   a.D = static_cast<int>(D);
   a.KW = static_cast<int>(KW);
   a.silu = silu;

@@ -101,22 +101,6 @@ template <int I, int N, typename F> __device__ __forceinline__ void unrolled(F&&
   }
 }
 
-// A value that the compiler takes for a new one, so that nothing derived from it leaves the loop.
-__device__ __forceinline__ uint32_t opaque(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
-// Element `at` past a uniform pointer.  A load with the byte offset in 32 bits, extended beside it
-// (`at` opaque, where the extension would be moved out of a loop), keeps the pointer in scalar
-// registers and one vector register for the lane.
-template <typename T> __device__ __forceinline__ const T& element(const T* p, uint32_t at) {
-  return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + at * uint32_t(sizeof(T)));
-}
-template <typename T> __device__ __forceinline__ T& element(T* p, uint32_t at) {
-  return *reinterpret_cast<T*>(reinterpret_cast<char*>(p) + at * uint32_t(sizeof(T)));
-}
-
 // The place of a block: its unit, group and first channel.  The channel blocks of a unit follow
 // each other on one XCD, whose L2 then holds the lines of u, dt_raw, z, B and C that they share.
 struct Place {

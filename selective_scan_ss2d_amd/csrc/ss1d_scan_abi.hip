@@ -77,6 +77,7 @@ int set_data(Data* x, Span* ins, const void* u, const void* dt, const void* z, c
     x->scg = st[11];
   }
   if (x->sbg < 0 || x->scg < 0 || x->sbg > kMaxLine || x->scg > kMaxLine) return SS2D_ERR_SHAPE;
+  if ((G - 1) * std::max(x->sbg, x->scg) > kMaxLine) return SS2D_ERR_SHAPE;
   const int64_t bytes[5] = {strided_bytes(B, L, D, x->su, e), strided_bytes(B, L, D, x->sd, e),
                             z ? strided_bytes(B, L, D, x->sz, e) : 0,
                             strided_bytes(B, L, (G - 1) * x->sbg + N, x->sb, e),
@@ -432,10 +433,15 @@ int ss1d_scan_step(const void* u, const void* dt_raw, const float* A_log, const 
   const Span outs[] = {{y, B * T * D * e}, {state, n * 4}};
   rc = check_overlap(ins, 9, outs, 2);
   if (rc != SS2D_OK) return rc;
-  if (B > kMaxThreads / 64 / ((D + 15) / 16)) return SS2D_ERR_SHAPE;
-  StepArgs a{u, dt_raw, z, Bs, Cs, A_log, Ds, dt_bias, slots, state, y, x.su, x.sd, x.sz, x.sb, x.sc, x.sbg, x.scg,
-             B, T, S, static_cast<int>(D), static_cast<int>(G), static_cast<int>(N), false};
-  a.vec = (N == 16 || N == 32) && !off(state, 16) && !off(A_log, 16);
+  if (B > kMaxThreads / 64 / ((D + 15) / 16) || T >= (int64_t(1) << 31)) return SS2D_ERR_SHAPE;
+  StepArgs a{u, dt_raw, z, Bs, Cs, A_log, Ds, dt_bias, {slots, static_cast<int>(B), S}, state, y,
+             x.su, x.sd, x.sz, x.sb, x.sc, x.sbg, x.scg, static_cast<int>(T), static_cast<int>(D),
+             static_cast<int>(G), static_cast<int>(N), false, 1};
+  a.whole = (N == 16 || N == 32) && !off(state, 16) && !off(A_log, 16) && !off(Bs, 4 * e) && !off(Cs, 4 * e);
+  for (int64_t v : {x.sb.b, x.sb.l, x.sbg, x.sc.b, x.sc.l, x.scg}) a.whole = a.whole && v % 4 == 0;
+  // rows of a block: 8192 waves are enough to hide the loads (256 rows of 4096 channels: 45, 37, 32, 32
+  // and 33 us with 65536, 32768, 16384, 8192 and 4096), and share what the channels' parameters cost
+  a.rows = static_cast<int>(std::clamp<int64_t>(B * ((D + 15) / 16) / 8192, 1, 16));
   const int err = ss2d::sscan::launch_scan_step(a, dtype, static_cast<hipStream_t>(stream));
   return err ? ss2d::host_hip_fail(static_cast<hipError_t>(err)) : SS2D_OK;
 }

@@ -10,14 +10,14 @@ namespace sscan {
 struct StepArgs {
   const void *u, *dt, *z, *Bs, *Cs;   // (B, T, D), z NULL for none; (B, T, G, N)
   const float *A_log, *Ds, *bias;
-  const int32_t* slots;               // (B) or NULL (row b's state is state[b])
+  Slots slots;                        // of the B rows, into state
   float* state;                       // (S, D, N)
   void* y;                            // (B, T, D)
   RowStrides su, sd, sz, sb, sc;
   int64_t sbg, scg;
-  int64_t B, T, S;
-  int D, G, N;
-  bool vec;                           // state and A_log in pieces of 16 bytes
+  int T, D, G, N;
+  bool whole;                         // N is 16 or 32, and its rows lie on four values
+  int rows;                           // rows of a block
 };
 
 int launch_scan_step(const StepArgs& a, int dtype, hipStream_t st);

@@ -6,110 +6,131 @@ namespace ss2d {
 namespace sscan {
 namespace {
 
-// kNS adjacent states of a lane, vec: on kNS * 4 bytes and none past N.
-template <int kNS>
-__device__ __forceinline__ void take_states(const float* p, int left, bool vec, float other, float* x) {
-  if constexpr (kNS >= 4) {
-    if (vec) {
+// kNS adjacent values of a lane from memory.  kWhole: N is four lanes' values, and the rows lie on
+// the size of four of them; else one by one, none past N.
+template <int kNS, bool kWhole, typename T>
+__device__ __forceinline__ void take(const T* p, int left, T* x) {
+  if constexpr (kWhole) {
+    struct alignas(4 * sizeof(T)) Four { T v[4]; };
 #pragma unroll
-      for (int i = 0; i < kNS; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p + i);
-        x[i] = v.x;
-        x[i + 1] = v.y;
-        x[i + 2] = v.z;
-        x[i + 3] = v.w;
-      }
-      return;
+    for (int i = 0; i < kNS; i += 4) {
+      const Four f = *reinterpret_cast<const Four*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i + j] = f.v[j];
     }
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < kNS; ++i) x[i] = i < left ? p[i] : other;
+    for (int i = 0; i < kNS; ++i) x[i] = i < left ? p[i] : T(0);
+  }
 }
 
-template <typename T, int kNS>
-__global__ __launch_bounds__(64) void k_scan_step(StepArgs a) {
-  const int lane = threadIdx.x, s = lane & 3;
-  const int64_t unit = blockIdx.x;
-  const int blocks = (a.D + 15) / 16;
-  const int ch = static_cast<int>(unit % blocks) * 16 + (lane >> 2);
-  int64_t b = unit / blocks;
-  const bool on = ch < a.D;
-  const int d = on ? ch : a.D - 1, g = d / (a.D / a.G);
-  const int n0 = s * kNS, left = a.N - n0;
-
-  int64_t slot = b;
-  if (a.slots) {
-    slot = a.slots[b];
-    if (slot < 0 || slot >= a.S) return;  // a padded row: nothing is read or written
-    // Rows that name one slot are further tokens of one sequence, in row order: the first of
-    // them does them all, so that no two waves hold the same state.
-    bool earlier = false;
-    for (int64_t i = lane; i < b; i += 64) earlier |= a.slots[i] == slot;
-    if (__any(earlier)) return;
+// A token as it comes from memory; the rows of b and t by uniform pointers, the lane's place in them
+// by 32-bit offsets.
+template <typename T, int kNS, bool kWhole, bool kGate> struct Token {
+  T u, dt, z, B[kNS], C[kNS];
+  __device__ __forceinline__ void load(const StepArgs& a, int b, int t, uint32_t d, uint32_t nb, uint32_t nc, int left) {
+    u = element(static_cast<const T*>(a.u) + b * a.su.b + t * a.su.l, opaque(d));
+    dt = element(static_cast<const T*>(a.dt) + b * a.sd.b + t * a.sd.l, opaque(d));
+    z = kGate ? element(static_cast<const T*>(a.z) + b * a.sz.b + t * a.sz.l, opaque(d)) : T(0);
+    take<kNS, kWhole>(&element(static_cast<const T*>(a.Bs) + b * a.sb.b + t * a.sb.l, opaque(nb)), left, B);
+    take<kNS, kWhole>(&element(static_cast<const T*>(a.Cs) + b * a.sc.b + t * a.sc.l, opaque(nc)), left, C);
   }
-  float* at = a.state + (slot * a.D + d) * a.N + n0;
-  float h[kNS], Ap[kNS];
-  take_states<kNS>(at, left, a.vec, 0.0f, h);
-  take_states<kNS>(a.A_log + int64_t(d) * a.N + n0, left, a.vec, 0.0f, Ap);
+};
+
+// A block takes a quarter as many channels as threads, of a.rows rows one after the other, each one's
+// state and first token loaded while the one before is computed.
+template <typename T, int kNS, bool kWhole, bool kGate>
+__global__ __launch_bounds__(256) void k_scan_step(StepArgs a) {
+  __shared__ uint32_t seen[2];
+  const int lane = threadIdx.x & 63, s = lane & 3;
+  const int channels = blockDim.x / 4, blocks = (a.D + channels - 1) / channels;
+  const int ch = static_cast<int>(blockIdx.x % blocks) * channels + static_cast<int>(threadIdx.x >> 2);
+  const int b0 = static_cast<int>(blockIdx.x / blocks) * a.rows, n = min(a.slots.rows - b0, a.rows);
+  const bool on = ch < a.D;
+  const uint32_t d = on ? ch : a.D - 1, g = d / (a.D / a.G), n0 = s * kNS;
+  const uint32_t nb = g * uint32_t(a.sbg) + n0, nc = g * uint32_t(a.scg) + n0, at = d * a.N + n0;
+  const int left = a.N - static_cast<int>(n0);
+  const int64_t state_row = int64_t(a.D) * a.N;
+  float Ap[kNS];
+  take<kNS, kWhole>(a.A_log + at, left, Ap);
+  const float bias = a.bias[d], skip = a.Ds[d];
+  find_repeats(a.slots, b0, n, seen);
+  float h_in[kNS] = {};
+  Token<T, kNS, kWhole, kGate> in{};
+  int slot_in = slot_of(a.slots, b0, 0, seen);
+  auto fetch = [&](int b) {
+    if (slot_in < 0) return;
+    take<kNS, kWhole>(&element(static_cast<const float*>(a.state) + slot_in * state_row, opaque(at)), left, h_in);
+    in.load(a, b, 0, d, nb, nc, left);
+  };
+  fetch(b0);
 #pragma unroll
   for (int i = 0; i < kNS; ++i) Ap[i] = -expf(Ap[i]) * kLog2e;
-  const float bias = a.bias[d], skip = a.Ds[d];
-  for (;;) {
-    for (int64_t t = 0; t < a.T; ++t) {
-      const float u = Elem<T>::load(static_cast<const T*>(a.u) + b * a.su.b + t * a.su.l + d);
-      const float raw = Elem<T>::load(static_cast<const T*>(a.dt) + b * a.sd.b + t * a.sd.l + d);
-      const float z = a.z ? Elem<T>::load(static_cast<const T*>(a.z) + b * a.sz.b + t * a.sz.l + d) : 0.0f;
-      const T* pB = static_cast<const T*>(a.Bs) + b * a.sb.b + t * a.sb.l + g * a.sbg + n0;
-      const T* pC = static_cast<const T*>(a.Cs) + b * a.sc.b + t * a.sc.l + g * a.scg + n0;
-      T B[kNS], C[kNS];
+  for (int i = 0; i < n; ++i) {
+    int b = b0 + i;
+    const int slot = slot_in;
+    float h[kNS];
+    Token<T, kNS, kWhole, kGate> x = in;
 #pragma unroll
-      for (int i = 0; i < kNS; ++i) {
-        B[i] = i < left ? pB[i] : T(0);
-        C[i] = i < left ? pC[i] : T(0);
+    for (int k = 0; k < kNS; ++k) h[k] = h_in[k];
+    if (i + 1 < n) {
+      slot_in = slot_of(a.slots, b0, i + 1, seen);
+      fetch(b + 1);
+    }
+    if (slot < 0) continue;
+    const bool more = a.slots.at && (__builtin_amdgcn_readfirstlane(seen[1]) >> i & 1);
+    for (;;) {
+      for (int t = 0;;) {
+        const float u = Elem<T>::to_f32(x.u);
+        const float delta = softplus_f32(Elem<T>::to_f32(x.dt) + bias), w = delta * u;
+        float y = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNS; ++k) {
+          h[k] = fmaf(exp2_hw(delta * Ap[k]), h[k], w * Elem<T>::to_f32(x.B[k]));
+          y = fmaf(Elem<T>::to_f32(x.C[k]), h[k], y);
+        }
+        y = fmaf(skip, u, group_sum<4>(y));
+        if (kGate) y *= silu_f32(Elem<T>::to_f32(x.z));
+        if (on && s == 0) element(static_cast<T*>(a.y) + (int64_t(b) * a.T + t) * a.D, opaque(d)) = Elem<T>::from_f32(y);
+        if (++t >= a.T) break;
+        x.load(a, b, t, d, nb, nc, left);
       }
-      const float delta = softplus_f32(raw + bias), w = delta * u;
-      float y = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kNS; ++i) {
-        h[i] = fmaf(exp2_hw(delta * Ap[i]), h[i], w * Elem<T>::to_f32(B[i]));
-        y = fmaf(Elem<T>::to_f32(C[i]), h[i], y);
-      }
-      y = fmaf(skip, u, group_sum<4>(y));
-      if (a.z) y *= silu_f32(z);
-      if (on && s == 0) static_cast<T*>(a.y)[(b * a.T + t) * a.D + d] = Elem<T>::from_f32(y);
+      if (!more) break;
+      b = next_of(a.slots, b, slot);
+      if (b >= a.slots.rows) break;
+      x.load(a, b, 0, d, nb, nc, left);
     }
-    if (!a.slots) break;
-    int64_t next = a.B;  // the next row of the same slot
-    for (int64_t base = b + 1; base < a.B && next == a.B; base += 64) {
-      const int64_t i = base + lane;
-      const uint64_t hit = __ballot(i < a.B && a.slots[i < a.B ? i : b] == slot);
-      if (hit) next = base + __ffsll(static_cast<unsigned long long>(hit)) - 1;
-    }
-    if (next == a.B) break;
-    b = next;
-  }
-  if (!on) return;
-  if constexpr (kNS >= 4) {
-    if (a.vec) {
+    if (!on) continue;
+    float* to = &element(a.state + slot * state_row, opaque(at));
+    if constexpr (kWhole) {
 #pragma unroll
-      for (int i = 0; i < kNS; i += 4)
-        *reinterpret_cast<float4*>(at + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
-      return;
+      for (int k = 0; k < kNS; k += 4)
+        *reinterpret_cast<float4*>(to + k) = make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kNS; ++k)
+        if (k < left) to[k] = h[k];
     }
   }
-#pragma unroll
-  for (int i = 0; i < kNS; ++i)
-    if (i < left) at[i] = h[i];
+}
+
+template <typename T, int kNS, bool kWhole>
+int launch_gate(const StepArgs& a, hipStream_t st) {
+  // 64 channels a block, whose rows of u, dt_raw, z and y then fill lines, where that leaves 1024 waves
+  const int64_t rows = (a.slots.rows + a.rows - 1) / a.rows;
+  const int threads = rows * ((a.D + 63) / 64) >= 256 ? 256 : 64, channels = threads / 4;
+  const dim3 grid(static_cast<unsigned>(rows * ((a.D + channels - 1) / channels))), block(threads);
+  if (a.z) hipLaunchKernelGGL((k_scan_step<T, kNS, kWhole, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_scan_step<T, kNS, kWhole, false>), grid, block, 0, st, a);
+  return static_cast<int>(hipGetLastError());
 }
 
 template <typename T>
 int launch_t(const StepArgs& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.B * ((a.D + 15) / 16))), block(64);
-  if (a.N <= 4) hipLaunchKernelGGL((k_scan_step<T, 1>), grid, block, 0, st, a);
-  else if (a.N <= 8) hipLaunchKernelGGL((k_scan_step<T, 2>), grid, block, 0, st, a);
-  else if (a.N <= 16) hipLaunchKernelGGL((k_scan_step<T, 4>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_scan_step<T, 8>), grid, block, 0, st, a);
-  return static_cast<int>(hipGetLastError());
+  if (a.whole) return a.N == 16 ? launch_gate<T, 4, true>(a, st) : launch_gate<T, 8, true>(a, st);
+  if (a.N <= 4) return launch_gate<T, 1, false>(a, st);
+  if (a.N <= 8) return launch_gate<T, 2, false>(a, st);
+  return a.N <= 16 ? launch_gate<T, 4, false>(a, st) : launch_gate<T, 8, false>(a, st);
 }
 
 }  // namespace

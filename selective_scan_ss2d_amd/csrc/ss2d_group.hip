@@ -13,20 +13,44 @@ namespace ss2d {
 namespace group {
 namespace {
 
+// kV adjacent values as they come from memory: one 16-byte access, or one value.
 template <typename T, int kV> struct Piece {
-  T v[kV];
+  static constexpr bool kWide = kV > 1;
+  static constexpr int kWords = kWide ? 4 : 1;
+  uint32_t w[kWords];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kV * sizeof(T) == 16) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-    else v[0] = *p;
+    if constexpr (kWide) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (sizeof(T) == 4) {
+      w[0] = __float_as_uint(*p);
+    } else {
+      w[0] = uint32_t(*p) << 16;
+    }
   }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kV * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
-    else *p = v[0];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (!kWide) return __uint_as_float(w[0]);
+    else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
-  __device__ __forceinline__ float at(int i) const { return Elem<T>::to_f32(v[i]); }
+  static __device__ __forceinline__ void store(T* p, const float* x) {
+    if constexpr (kWide) {
+      T v[kV];
+#pragma unroll
+      for (int i = 0; i < kV; ++i) v[i] = Elem<T>::from_f32(x[i]);
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+    } else {
+      *p = Elem<T>::from_f32(x[0]);
+    }
+  }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) v[i] = T(0);
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // Conversions on either side of this are made twice rather than kept in registers between.
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
   }
 };
 
@@ -55,28 +79,31 @@ template <int kThreads> __device__ __forceinline__ Tile tile_of(const Args& a, i
   return t;
 }
 
-// Sums of every channel of a set over the block's threads, from part[row][set]: rows p, p + P, ...
-// into row p, in place (row p is read by the thread that writes it alone).  Returns P.
-template <int kThreads> __device__ __forceinline__ int column_sums(float* part, int set, int rows) {
-  const int P = min(max(1, kThreads / set), rows);
-  __syncthreads();
-  for (int i = threadIdx.x; i < P * set; i += kThreads) {
-    const int c = i % set, p = i / set;
-    float v = part[p * set + c];
-    for (int r = p + P; r < rows; r += P) v += part[r * set + c];
-    part[p * set + c] = v;
+// Sums of every channel of a set over the rows of part[row][set], in part[0]: rows are folded by 8 at
+// most, rows p, p + P, ... into row p, in place (row p is read by the thread that writes it alone).
+template <int kThreads, int kParts>
+__device__ __forceinline__ void fold(float (*part)[kThreads * kParts], int arrays, int set, int rows) {
+  while (rows > 1) {
+    const int P = (rows + 7) / 8;
+    __syncthreads();
+    for (int i = threadIdx.x; i < P * set; i += kThreads)
+      for (int k = 0; k < arrays; ++k) {
+        float v = part[k][i];
+        for (int r = i + P * set; r < rows * set; r += P * set) v += part[k][r];
+        part[k][i] = v;
+      }
+    rows = P;
   }
   __syncthreads();
-  return P;
 }
 
-// Every group's sum of part[0 .. P - 1][set], over `count`, into out[group].
+// Every group's sum of row[set], over `count`, into out[group].
 template <int kThreads>
-__device__ __forceinline__ void group_sums(const float* part, int set, int P, int cg, float count, float* out) {
+__device__ __forceinline__ void group_sums(const float* row, int set, int cg, float count, float* out) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int g = wave; g < set / cg; g += kThreads / 64) {
     float v = 0.0f;
-    for (int i = lane; i < P * cg; i += 64) v += part[i / cg * set + g * cg + i % cg];
+    for (int i = lane; i < cg; i += 64) v += row[g * cg + i];
     v = lane_sum<64>(v);
     if (lane == 0) out[g] = v / count;
   }
@@ -85,61 +112,68 @@ __device__ __forceinline__ void group_sums(const float* part, int set, int P, in
 
 // The mean and r of every group of the set, of values held in registers.
 template <typename T, int kV, int kRows, int kThreads>
-__device__ __forceinline__ void statistics(const Args& a, const Tile& t, const Piece<T, kV>* x, float* part,
-                                           float* mean, float* r) {
+__device__ __forceinline__ void statistics(const Args& a, const Tile& t, Piece<T, kV>* x,
+                                           float (*part)[kThreads * kV], float* mean, float* r) {
   const float count = static_cast<float>(a.L) * a.cg;
-  float s[kV];
+  const int at = t.row * a.set + t.cv * kV;
+  float s[kV] = {};
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)  // rows past the end hold zeros
+#pragma unroll
+    for (int k = 0; k < kV; ++k) s[k] += x[i].at(k);
+#pragma unroll
+  for (int k = 0; k < kV; ++k)
+    if (t.on) part[0][at + k] = s[k];
+  fold<kThreads, kV>(part, 1, a.set, t.pass);
+  group_sums<kThreads>(part[0], a.set, a.cg, count, mean);
+  float m[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
+    m[k] = mean[(t.cv * kV + k) / a.cg];
     s[k] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) s[k] += x[i].at(k);  // rows past the end hold zeros
-    if (t.on) part[t.row * a.set + t.cv * kV + k] = s[k];
   }
-  group_sums<kThreads>(part, a.set, column_sums<kThreads>(part, a.set, t.pass), a.cg, count, mean);
 #pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    const float m = mean[(t.cv * kV + k) / a.cg];
-    s[k] = 0.0f;
+  for (int i = 0; i < kRows; ++i) {
+    x[i].renew();
+    if (t.row + i * t.pass < a.L)
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float d = x[i].at(k) - m;
-      s[k] = t.row + i * t.pass < a.L ? fmaf(d, d, s[k]) : s[k];
-    }
+      for (int k = 0; k < kV; ++k) {
+        const float d = x[i].at(k) - m[k];
+        s[k] = fmaf(d, d, s[k]);
+      }
   }
 #pragma unroll
   for (int k = 0; k < kV; ++k)
-    if (t.on) part[t.row * a.set + t.cv * kV + k] = s[k];
-  group_sums<kThreads>(part, a.set, column_sums<kThreads>(part, a.set, t.pass), a.cg, count, r);
+    if (t.on) part[0][at + k] = s[k];
+  fold<kThreads, kV>(part, 1, a.set, t.pass);
+  group_sums<kThreads>(part[0], a.set, a.cg, count, r);
   for (int g = threadIdx.x; g < a.set / a.cg; g += kThreads) r[g] = 1.0f / sqrtf(r[g] + a.eps);
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) x[i].renew();
 }
 
 constexpr int kMaxGroups = 256;  // of a set
+// Rows of a thread at most: registers for two blocks of 512 threads per CU.
+constexpr int kDeepest = 20, kDeepestBack = 10;
 
 template <typename T, int kV, int kRows, int kThreads>
 __global__ __launch_bounds__(kThreads) void k_group(Args a) {
-  __shared__ float part[kThreads * kV], mean[kMaxGroups], r[kMaxGroups];
+  __shared__ float part[1][kThreads * kV], mean[kMaxGroups], r[kMaxGroups];
   const unsigned id = xcd_local_order(blockIdx.x, gridDim.x);
   const int64_t b = id / a.sets;
   const int c0 = static_cast<int>(id % a.sets) * a.set;
   const Tile t = tile_of<kThreads>(a, kV);
   const int c = c0 + t.cv * kV;
-  const int64_t base = b * a.L * a.C + c;
-  const T* x = static_cast<const T*>(a.x) + base;
-  Piece<T, kV> rows[kRows];
+  const int64_t base = b * a.L * a.C + c, step = int64_t(t.pass) * a.C;
+  Piece<T, kV> x[kRows];
+  const T* from = static_cast<const T*>(a.x) + base + int64_t(t.row) * a.C;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    rows[i].zero();
-    if (t.on && t.row + i * t.pass < a.L) rows[i].load(x + int64_t(t.row + i * t.pass) * a.C);
+  for (int i = 0; i < kRows; ++i, from += step) {
+    x[i].zero();
+    if (t.on && t.row + i * t.pass < a.L) x[i].load(from);
   }
-  float w[kV], bias[kV];
-#pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    w[k] = a.w ? a.w[c + k] : 1.0f;
-    bias[k] = a.b ? a.b[c + k] : 0.0f;
-  }
-  statistics<T, kV, kRows, kThreads>(a, t, rows, part, mean, r);
+  statistics<T, kV, kRows, kThreads>(a, t, x, part, mean, r);
   if (a.stats)
     for (int g = threadIdx.x; g < a.set / a.cg; g += kThreads) {
       float* to = a.stats + (b * a.G + c0 / a.cg + g) * 2;
@@ -147,25 +181,25 @@ __global__ __launch_bounds__(kThreads) void k_group(Args a) {
       to[1] = r[g];
     }
   if (!t.on) return;
-  float m[kV];
+  float m[kV], w[kV], bias[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
     const int g = (t.cv * kV + k) / a.cg;
     m[k] = mean[g];
-    w[k] *= r[g];
+    w[k] = (a.w ? a.w[c + k] : 1.0f) * r[g];
+    bias[k] = a.b ? a.b[c + k] : 0.0f;
   }
-  T* y = static_cast<T*>(a.y) + base;
+  T* to = static_cast<T*>(a.y) + base + int64_t(t.row) * a.C;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kRows; ++i, to += step) {
     if (t.row + i * t.pass >= a.L) break;
-    Piece<T, kV> out;
+    float v[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      float v = affine(rows[i].at(k) - m[k], w[k], bias[k]);
-      if (a.silu) v = silu_f32(v);
-      out.v[k] = Elem<T>::from_f32(v);
+      v[k] = affine(x[i].at(k) - m[k], w[k], bias[k]);
+      if (a.silu) v[k] = silu_f32(v[k]);
     }
-    out.store(y + int64_t(t.row + i * t.pass) * a.C);
+    Piece<T, kV>::store(to, v);
   }
 }
 
@@ -179,16 +213,16 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(Args a) {
   const int c0 = static_cast<int>(id % a.sets) * a.set;
   const Tile t = tile_of<kThreads>(a, kV);
   const int c = c0 + t.cv * kV;
-  const int64_t base = b * a.L * a.C + c;
-  const T *x = static_cast<const T*>(a.x) + base, *dy = static_cast<const T*>(a.dy) + base;
+  const int64_t base = b * a.L * a.C + c + int64_t(t.row) * a.C, step = int64_t(t.pass) * a.C;
+  const T *from = static_cast<const T*>(a.x) + base, *dfrom = static_cast<const T*>(a.dy) + base;
   Piece<T, kV> xs[kRows], ds[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kRows; ++i, from += step, dfrom += step) {
     xs[i].zero();
     ds[i].zero();
     if (t.on && t.row + i * t.pass < a.L) {
-      xs[i].load(x + int64_t(t.row + i * t.pass) * a.C);
-      ds[i].load(dy + int64_t(t.row + i * t.pass) * a.C);
+      xs[i].load(from);
+      ds[i].load(dfrom);
     }
   }
   float w[kV], bias[kV];
@@ -199,76 +233,77 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(Args a) {
   }
   if (a.given) {
     for (int g = threadIdx.x; g < a.set / a.cg; g += kThreads) {
-      const float* from = a.stats + (b * a.G + c0 / a.cg + g) * 2;
-      mean[g] = from[0];
-      r[g] = from[1];
+      const float* s = a.stats + (b * a.G + c0 / a.cg + g) * 2;
+      mean[g] = s[0];
+      r[g] = s[1];
     }
     __syncthreads();
   } else {
-    statistics<T, kV, kRows, kThreads>(a, t, xs, part[0], mean, r);
+    statistics<T, kV, kRows, kThreads>(a, t, xs, part, mean, r);
   }
-  float m[kV], rs[kV];
+  float m[kV], rs[kV], sd[kV] = {}, sn[kV] = {};
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
     const int g = (t.cv * kV + k) / a.cg;
     m[k] = mean[g];
     rs[k] = r[g];
-    float sd = 0.0f, sn = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float n = (xs[i].at(k) - m[k]) * rs[k];
-      float d = ds[i].at(k);
-      if (a.silu) d *= slope(affine(n, w[k], bias[k]));
-      const bool in = t.row + i * t.pass < a.L;
-      sd += in ? d : 0.0f;
-      sn = in ? fmaf(d, n, sn) : sn;
-    }
-    if (t.on) {
-      part[0][t.row * a.set + t.cv * kV + k] = sd;
-      part[1][t.row * a.set + t.cv * kV + k] = sn;
-    }
   }
-  const int P = column_sums<kThreads>(part[0], a.set, t.pass);
-  column_sums<kThreads>(part[1], a.set, t.pass);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (t.row + i * t.pass < a.L)
+#pragma unroll
+      for (int k = 0; k < kV; ++k) {
+        const float n = (xs[i].at(k) - m[k]) * rs[k];
+        float d = ds[i].at(k);
+        if (a.silu) d *= slope(affine(n, w[k], bias[k]));
+        sd[k] += d;
+        sn[k] = fmaf(d, n, sn[k]);
+        if constexpr (sizeof(T) == 4) ds[i].w[k] = __float_as_uint(d);  // else d is made again below
+      }
+    xs[i].renew();
+    ds[i].renew();
+  }
+#pragma unroll
+  for (int k = 0; k < kV; ++k)
+    if (t.on) {
+      part[0][t.row * a.set + t.cv * kV + k] = sd[k];
+      part[1][t.row * a.set + t.cv * kV + k] = sn[k];
+    }
+  fold<kThreads, kV>(part, 2, a.set, t.pass);
   for (int i = threadIdx.x; i < a.set; i += kThreads) {
-    float sd = 0.0f, sn = 0.0f;
-    for (int p = 0; p < P; ++p) {
-      sd += part[0][p * a.set + i];
-      sn += part[1][p * a.set + i];
+    const float wi = a.w ? a.w[c0 + i] : 1.0f, d = part[0][i], n = part[1][i];
+    if (a.dw || a.db) {
+      a.parts[(b * 2) * a.C + c0 + i] = d;
+      a.parts[(b * 2 + 1) * a.C + c0 + i] = n;
     }
-    if (a.parts) {
-      a.parts[(b * 2) * a.C + c0 + i] = sd;
-      a.parts[(b * 2 + 1) * a.C + c0 + i] = sn;
-    }
-    const float wi = a.w ? a.w[c0 + i] : 1.0f;
-    part[0][i] = sd * wi;
-    part[1][i] = sn * wi;
+    part[0][i] = d * wi;
+    part[1][i] = n * wi;
   }
   __syncthreads();
   const float count = static_cast<float>(a.L) * a.cg;
-  group_sums<kThreads>(part[0], a.set, 1, a.cg, count, mean);
-  group_sums<kThreads>(part[1], a.set, 1, a.cg, count, r);
+  group_sums<kThreads>(part[0], a.set, a.cg, count, mean);
+  group_sums<kThreads>(part[1], a.set, a.cg, count, r);
   if (!t.on) return;
-  T* dx = static_cast<T*>(a.dx) + base;
-  float se[kV], sn[kV];
+  T* to = static_cast<T*>(a.dx) + base;
+  float se[kV], sx[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
     const int g = (t.cv * kV + k) / a.cg;
     se[k] = mean[g];
-    sn[k] = r[g];
+    sx[k] = r[g];
   }
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kRows; ++i, to += step) {
     if (t.row + i * t.pass >= a.L) break;
-    Piece<T, kV> out;
+    float v[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       const float n = (xs[i].at(k) - m[k]) * rs[k];
       float d = ds[i].at(k);
-      if (a.silu) d *= slope(affine(n, w[k], bias[k]));
-      out.v[k] = Elem<T>::from_f32(rs[k] * (fmaf(d, w[k], -se[k]) - n * sn[k]));
+      if (sizeof(T) != 4 && a.silu) d *= slope(affine(n, w[k], bias[k]));
+      v[k] = rs[k] * (fmaf(d, w[k], -se[k]) - n * sx[k]);
     }
-    out.store(dx + int64_t(t.row + i * t.pass) * a.C);
+    Piece<T, kV>::store(to, v);
   }
 }
 
@@ -410,14 +445,13 @@ __global__ __launch_bounds__(256) void k_group_apply(Args a, int lanes, int cblo
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (t + i * p.rows >= p.count) break;
-      Piece<T, kV> out;
+      float f[kV];
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        float f = affine(v[i].at(k) - m[k], w[k], b[k]);
-        if (a.silu) f = silu_f32(f);
-        out.v[k] = Elem<T>::from_f32(f);
+        f[k] = affine(v[i].at(k) - m[k], w[k], b[k]);
+        if (a.silu) f[k] = silu_f32(f[k]);
       }
-      out.store(y + (t + i * p.rows) * a.C);
+      Piece<T, kV>::store(y + (t + i * p.rows) * a.C, f);
     }
   }
 }
@@ -526,15 +560,15 @@ __global__ __launch_bounds__(256) void k_group_bwd_apply(Args a, int lanes, int 
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (t + i * p.rows >= p.count) break;
-      Piece<T, kV> out;
+      float f[kV];
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
         const float n = (v[i].at(k) - m[k]) * r[k];
         float d = g[i].at(k);
         if (a.silu) d *= slope(affine(n, w[k], b[k]));
-        out.v[k] = Elem<T>::from_f32(r[k] * (fmaf(d, w[k], -se[k]) - n * sn[k]));
+        f[k] = r[k] * (fmaf(d, w[k], -se[k]) - n * sn[k]);
       }
-      out.store(dx + (t + i * p.rows) * a.C);
+      Piece<T, kV>::store(dx + (t + i * p.rows) * a.C, f);
     }
   }
 }
@@ -578,32 +612,26 @@ int lanes_of(int64_t C, int width) {
   return best;
 }
 
-template <typename T, int kV, int kThreads, bool kBack>
-int launch_rows(const Args& a, int rows, hipStream_t st) {
+template <typename T, int kV, int kThreads, int kRows, int... kMore>
+int launch_rows(const Args& a, int rows, bool back, hipStream_t st) {
+  if constexpr (sizeof...(kMore) > 0)
+    if (rows > kRows) return launch_rows<T, kV, kThreads, kMore...>(a, rows, back, st);
   const dim3 grid(static_cast<unsigned>(a.B * a.sets)), block(kThreads);
-#define SS2D_GROUP_ROWS(n)                                                                      \
-  if (rows <= n) {                                                                              \
-    if constexpr (kBack) hipLaunchKernelGGL((k_group_bwd<T, kV, n, kThreads>), grid, block, 0, st, a); \
-    else hipLaunchKernelGGL((k_group<T, kV, n, kThreads>), grid, block, 0, st, a);              \
-    return static_cast<int>(hipGetLastError());                                                 \
+  if (!back) {
+    hipLaunchKernelGGL((k_group<T, kV, kRows, kThreads>), grid, block, 0, st, a);
+  } else if constexpr (kThreads < 1024 && kRows <= kDeepestBack) {
+    hipLaunchKernelGGL((k_group_bwd<T, kV, kRows, kThreads>), grid, block, 0, st, a);
+  } else {
+    return static_cast<int>(hipErrorInvalidValue);
   }
-  SS2D_GROUP_ROWS(1)
-  SS2D_GROUP_ROWS(2)
-  SS2D_GROUP_ROWS(4)
-  SS2D_GROUP_ROWS(8)
-  if constexpr (!kBack) {
-    SS2D_GROUP_ROWS(16)
-  }
-#undef SS2D_GROUP_ROWS
-  return static_cast<int>(hipErrorInvalidValue);
+  return static_cast<int>(hipGetLastError());
 }
 
 template <typename T, int kV> int launch_t(const Args& a, const Plan& p, bool back, hipStream_t st) {
   if (p.rows > 0) {
-    if (back) return p.threads == 256 ? launch_rows<T, kV, 256, true>(a, p.rows, st)
-                                      : launch_rows<T, kV, 512, true>(a, p.rows, st);
-    return p.threads == 256 ? launch_rows<T, kV, 256, false>(a, p.rows, st)
-                            : launch_rows<T, kV, 1024, false>(a, p.rows, st);
+    if (p.threads == 256) return launch_rows<T, kV, 256, 1, 2, 4>(a, p.rows, back, st);
+    if (p.threads == 512) return launch_rows<T, kV, 512, 2, 4, 6, 8, 10, 14, 20>(a, p.rows, back, st);
+    return launch_rows<T, kV, 1024, 10, 14, 20>(a, p.rows, back, st);
   }
   const int lanes = lanes_of(a.C, kV), cblocks = (a.C + lanes * kV - 1) / (lanes * kV);
   const dim3 grid(static_cast<unsigned>(a.B * a.chunks * cblocks)), block(256);
@@ -632,17 +660,19 @@ int launch_any(const Args& a, const Plan& p, int dtype, bool back, hipStream_t s
 Plan plan(int64_t B, int64_t L, int64_t C, int64_t G, int dtype, bool vec, bool backward) {
   Plan p{vec ? (dtype == 0 ? 4 : 8) : 1, 0, 0, 0};
   const int64_t cg = C / G, e = dtype == 0 ? 4 : 2;
-  const int most = backward ? 512 : 1024, deepest = backward ? 8 : 16;
+  const int deepest = backward ? kDeepestBack : kDeepest;
   auto rows = [&](int64_t set, int threads) {  // 0: does not fit
     const int64_t nv = set / p.width, pass = nv <= threads ? threads / nv : 0;
     const int64_t r = pass ? (L + pass - 1) / pass : deepest + 1;
     return r <= deepest ? static_cast<int>(std::max<int64_t>(r, 1)) : 0;
   };
   int64_t set = std::lcm(cg, int64_t(p.width));
-  if (set / cg > kMaxGroups || !rows(set, most)) return p;
-  // rows of a set grow to 64 bytes, where that still fits
+  if (set / cg > kMaxGroups) return p;
+  const int most = rows(set, 512) || backward ? 512 : 1024;
+  if (!rows(set, most)) return p;
+  // rows of a set grow to 64 bytes, where that still fits and leaves two blocks per CU
   for (int64_t f = 2; set * e < 64 && f <= C / set; ++f)
-    if (C % (set * f) == 0 && set * f / cg <= kMaxGroups && rows(set * f, most)) {
+    if (C % (set * f) == 0 && set * f / cg <= kMaxGroups && B * (C / (set * f)) >= 512 && rows(set * f, most)) {
       set *= f;
       f = 1;
     }
