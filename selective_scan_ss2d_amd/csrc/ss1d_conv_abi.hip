@@ -228,6 +228,7 @@ int ss1d_conv_step(const void* x, const float* conv_w, const float* conv_b, void
   int64_t n;
   if (S < 0 || S >= kMaxTokens || (!slots && S != B)) return SS2D_ERR_SHAPE;
   if (!ss2d::host_mul_ok(S, (KW - 1) * D, &n) || n > ss2d::kHostMaxElems / 4096) return SS2D_ERR_SHAPE;
+  if (D > 0 && B > kMaxThreads / 64 / ((D + 63) / 64)) return SS2D_ERR_SHAPE;
   if (B == 0 || T == 0 || D == 0) return SS2D_OK;
   if (!x || !conv_w || !y || (KW > 1 && !state)) return SS2D_ERR_NULL;
   const int64_t e = dtype == SS2D_F32 ? 4 : 2;
@@ -247,7 +248,6 @@ int ss1d_conv_step(const void* x, const float* conv_w, const float* conv_b, void
   const Span outs[] = {{y, B * T * D * e}, {state, n * e}};
   rc = overlap(outs, 2, ins, 4);
   if (rc != SS2D_OK) return rc;
-  if (B > kMaxThreads / 64 / ((D + 63) / 64)) return SS2D_ERR_SHAPE;
   a.q = {nullptr, S, T, B * T};
   a.x = x;
   a.w = conv_w;

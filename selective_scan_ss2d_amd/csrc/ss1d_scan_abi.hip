@@ -414,6 +414,7 @@ int ss1d_scan_step(const void* u, const void* dt_raw, const float* A_log, const 
   int64_t n;
   if (S < 0 || S >= kMaxTokens || (!slots && S != B)) return SS2D_ERR_SHAPE;
   if (!ss2d::host_mul_ok(S, D * N, &n) || n > ss2d::kHostMaxElems / 4096) return SS2D_ERR_SHAPE;
+  if (D > 0 && (B > kMaxThreads / 64 / ((D + 15) / 16) || T >= (int64_t(1) << 31))) return SS2D_ERR_SHAPE;
   if (B == 0 || T == 0 || D == 0) return SS2D_OK;
   if (!u || !dt_raw || !A_log || !Bs || !Cs || !Ds || !dt_bias || !state || !y) return SS2D_ERR_NULL;
   const int64_t e = dtype == SS2D_F32 ? 4 : 2;
@@ -433,7 +434,6 @@ int ss1d_scan_step(const void* u, const void* dt_raw, const float* A_log, const 
   const Span outs[] = {{y, B * T * D * e}, {state, n * 4}};
   rc = check_overlap(ins, 9, outs, 2);
   if (rc != SS2D_OK) return rc;
-  if (B > kMaxThreads / 64 / ((D + 15) / 16) || T >= (int64_t(1) << 31)) return SS2D_ERR_SHAPE;
   StepArgs a{u, dt_raw, z, Bs, Cs, A_log, Ds, dt_bias, {slots, static_cast<int>(B), S}, state, y,
              x.su, x.sd, x.sz, x.sb, x.sc, x.sbg, x.scg, static_cast<int>(T), static_cast<int>(D),
              static_cast<int>(G), static_cast<int>(N), false, 1};

@@ -225,37 +225,58 @@ void k_scan_tokens(Args a) {
 
 // The segments of a sequence one after the other: each one's start state from the one before it,
 // or with kBack, from the last to the first, what the adjoint sends to its end from behind it.
-template <bool kBack>
-__global__ __launch_bounds__(256) void k_scan_join(Args a) {
-  const int64_t per = int64_t(a.D) * a.N, at = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (at >= a.q.S * per) return;
-  const Sequence q = sequence(a.q, at / per);
-  const int64_t i = at % per, d = i / a.N;
+// A thread carries one state.  With kWaves > 1 the block's waves take the same 64 states over parts of
+// the segments: each folds its own from zero, then starts from the fold of those before it, for the
+// latency of the loads bounds this kernel.  Measured, one wave and 16: 171 segments (2 x 65,536 tokens of
+// 192 channels, 16 states) 21.7 and 11 us; 87 segments of 25 packed sequences of 1000 channels 7.5 and
+// 57; 16 segments of one prompt of 4096 channels 5.2 and 24.
+template <bool kBack, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void k_scan_join(Args a) {
+  constexpr int kAhead = kWaves > 1 ? 16 : 8;
+  __shared__ float ends[kWaves][64], deltas[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t per = int64_t(a.D) * a.N, at = int64_t(blockIdx.x) * 64 + lane;
+  const bool valid = at < a.q.S * per;
+  const Sequence q = sequence(a.q, valid ? at / per : 0);
+  const int64_t i = valid ? at % per : 0, d = i / a.N;
   const int64_t count = (q.len + a.seglen - 1) / a.seglen, first = first_unit(a.q, q, a.seglen);
+  const int64_t part = (count + kWaves - 1) / kWaves;
+  const int64_t k0 = part * wave, k1 = valid ? min(count, k0 + part) : 0;
   const float Ap = -expf(a.A_log[i]) * kLog2e;
   const float* from = kBack ? a.dht : a.h0;
-  float h = from ? from[at] : 0.0f;
-  if (count == 0) {  // its one unit, without tokens, hands the state on
-    a.seg_start[first * per + i] = h;
-    return;
-  }
-  constexpr int kAhead = 8;
-  for (int64_t j = 0; j < count; j += kAhead) {
-    float end[kAhead], delta[kAhead];
+  float h = from && valid ? from[at] : 0.0f;
+  // segments k0 to k1 from the state h
+  auto walk = [&](float h, bool write, float& sum) {
+    for (int64_t j = k0; j < k1; j += kAhead) {
+      float end[kAhead], delta[kAhead];
 #pragma unroll
-    for (int m = 0; m < kAhead; ++m) {
-      const int64_t k = j + m, unit = first + (kBack ? count - 1 - k : k);
-      end[m] = k < count - 1 ? a.seg_end[unit * per + i] : 0.0f;  // of the last nothing is kept
-      delta[m] = k < count - 1 ? a.seg_delta[unit * a.D + d] : 0.0f;
-    }
+      for (int m = 0; m < kAhead; ++m) {
+        // (a load behind a condition of its own would wait for the one before it)
+        const int64_t k = min(j + m, k1 - 1), unit = first + (kBack ? count - 1 - k : k);
+        end[m] = a.seg_end[unit * per + i];
+        delta[m] = a.seg_delta[unit * a.D + d];
+      }
 #pragma unroll
-    for (int m = 0; m < kAhead; ++m) {
-      if (j + m >= count) break;
-      const int64_t unit = first + (kBack ? count - 1 - (j + m) : j + m);
-      a.seg_start[unit * per + i] = h;
-      h = fmaf(exp2_hw(Ap * delta[m]), h, end[m]);
+      for (int m = 0; m < kAhead; ++m) {
+        if (j + m >= k1) break;
+        const int64_t unit = first + (kBack ? count - 1 - (j + m) : j + m);
+        if (write) a.seg_start[unit * per + i] = h;
+        if (j + m == count - 1) break;  // of the last segment neither is kept
+        h = fmaf(exp2_hw(Ap * delta[m]), h, end[m]);
+        sum += delta[m];
+      }
     }
+    return h;
+  };
+  float sum = 0.0f;
+  if (kWaves > 1) {
+    ends[wave][lane] = walk(0.0f, false, sum);
+    deltas[wave][lane] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) h = fmaf(exp2_hw(Ap * deltas[w][lane]), h, ends[w][lane]);
   }
+  walk(h, true, sum);
+  if (valid && count == 0 && wave == 0) a.seg_start[first * per + i] = h;  // a unit without tokens hands it on
 }
 
 template <typename T, int kS, int kNS, bool kOut>
@@ -290,10 +311,13 @@ int launch_scan_segments(const Args& a, int dtype, hipStream_t st) {
 }
 
 int launch_scan_join(const Args& a, bool back, hipStream_t st) {
-  const int64_t n = a.q.S * a.D * a.N;
-  const dim3 grid(static_cast<unsigned>((n + 255) / 256)), block(256);
-  if (back) hipLaunchKernelGGL(k_scan_join<true>, grid, block, 0, st, a);
-  else hipLaunchKernelGGL(k_scan_join<false>, grid, block, 0, st, a);
+  constexpr int kWaves = 16;
+  const bool many = a.units > a.q.S * 16;  // more segments a sequence than one wave has in flight
+  const dim3 grid(static_cast<unsigned>((a.q.S * a.D * a.N + 63) / 64)), block(many ? 64 * kWaves : 64);
+  if (back && many) hipLaunchKernelGGL((k_scan_join<true, kWaves>), grid, block, 0, st, a);
+  else if (back) hipLaunchKernelGGL((k_scan_join<true, 1>), grid, block, 0, st, a);
+  else if (many) hipLaunchKernelGGL((k_scan_join<false, kWaves>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_scan_join<false, 1>), grid, block, 0, st, a);
   return static_cast<int>(hipGetLastError());
 }
 

@@ -43,6 +43,8 @@ CASES = [
     (1, 41, 40, 1, 17, F32, True, True, False, 8),
     (2, 50, 70, 1, 32, BF16, True, True, True, 16),
     (1, 50, 130, 2, 32, F32, False, True, False, 0),
+    (2, 331, 20, 1, 16, F32, True, True, False, 8),  # 42 segments, joined by 16 waves
+    (1, 270, 33, 1, 5, BF16, True, True, False, 8),
 ]
 
 
@@ -71,6 +73,7 @@ PACKED = [
     (90, [0, 1, 2, 3, 90], 65, 1, 8, F32, False, 32),
     (64, [0, 16, 32, 64], 64, 1, 4, BF16, True, 16),
     (33, [0, 0, 0, 33], 40, 1, 32, F32, True, 8),
+    (560, [0, 200, 200, 203, 560], 24, 1, 7, F32, True, 8),  # the same join for sequences of 0 to 45 segments
     (0, [0, 0, 0], 20, 1, 16, F32, True, -1),
 ]
 
