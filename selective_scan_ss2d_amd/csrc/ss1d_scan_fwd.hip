@@ -1,4 +1,15 @@
 // The token-order selective scan, forward: whole sequences or segments of them.
+//
+// A state takes an exponential (two slots of the vector pipe or more), a product for delta A, and three
+// multiply-adds per token; a channel softplus, its gate, and the sum over its states.  That, not HBM, is
+// what bounds it.  Four lanes share a channel: each computes softplus, delta u and the gate of every
+// fourth step, so that these cost a quarter, and hands them to the others.  One lane per channel with B and C as scalar
+// operands took 971 us for 598 (16 x 2048 tokens of 4096 channels): nothing hid the scalar loads.
+// The chain of a sequence leaves few waves; a segmented call first computes every segment's end
+// from zero (no C, no outputs), joins them, and runs again from the joined states.
+// Measured, bf16 with gate, 16 states: a prompt of 4096 tokens, 4096 channels, in 16 segments 62 + 5 +
+// 89 us (the vector pipes 77% busy; HBM would take 27); 8 x 2048 tokens of 2048 channels, whole, saving
+// states, 240 (55% busy, one wave per SIMD); fp32, 2 x 65,536 tokens of 192 channels, 88 + 11 + 115.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,7 +43,8 @@ template <int kS> __device__ __forceinline__ float scatter_sum(const float* v, i
 }
 
 // kOut: outputs, end states and marks; else a segment's end state from a zero start and its sum
-// of delta.
+// of delta.  B and C of a tile lie in LDS (read by all channels of the block), a lane's steps of u, dt_raw
+// and z are loaded a tile ahead.
 template <typename T, int kS, int kNS, bool kOut, bool kGate>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 4)))
 void k_scan_tokens(Args a) {

@@ -7,6 +7,8 @@
 namespace ss2d {
 namespace sscan {
 
+constexpr int kStepCh = 64;  // channels of a block, four lanes each
+
 struct StepArgs {
   const void *u, *dt, *z, *Bs, *Cs;   // (B, T, D), z NULL for none; (B, T, G, N)
   const float *A_log, *Ds, *bias;

@@ -4,6 +4,10 @@
 // about it are summed over the block, and y is written.  Where a group is too large for that, chunks
 // of positions give every channel's mean and sum of squares about it, one wave per group joins
 // them, and another pass normalises.
+// What bounds it is HBM where a block's loads of a few hundred KB are in flight at once: bf16, 64 maps of
+// 56 x 56 x 192, 154 MB, 40 us (3.8 TB/s: two blocks of a CU load and write in turn); fp32, 64 of 28 x 28 x
+// 384, 154 MB forward 31 us, 231 MB backward 60 to 76 (its registers hold x and dy of 10 rows, which
+// leaves two blocks of 512 threads per CU).
 #include <algorithm>
 #include <numeric>
 
@@ -675,7 +679,8 @@ int launch_any(const Args& a, const Plan& p, int dtype, bool back, hipStream_t s
 //   threads and rows that hold nothing: bf16 128 x 196 x 768 in 32 groups, sets of 24, 48 and 96 channels,
 //     58, 78 and 92% of the registers in use: 27.4, 27.3 and 23.1;
 //   two blocks of 512 threads for every CU, or calls are as long as a thread has rows: 8 x 1024 x 512 by
-//     1024, 512 and 256 threads, 2, 4 and 8 rows: 12.4, 13.2, 13.3;
+//     1024, 512 and 256 threads, 2, 4 and 8 rows: 12.4, 13.2, 13.3; then wide pieces gain nothing, and
+//     many threads cost: 1 x 256 x 256 by 32 blocks of 256 and by 8 of 1024: 6.8 and 10.0;
 //   pieces of a row that lines hold in part: 64 x 1024 x 512, pieces of 32, 64 and 128 bytes: 36.5, 36.7,
 //     29.9; fp32, 64, 128 and 256 bytes: 64.0, 54.9, 58.3 (the last by 1024 threads);
 //   barriers of many threads: 100 x 100 x 1000, 10 rows of 256 threads and 5 of 512: 16.9 and 18.7;
@@ -692,9 +697,11 @@ Plan plan(int64_t B, int64_t L, int64_t C, int64_t G, int dtype, bool vec, bool 
       if (pass == 0 || B > ((int64_t(1) << 32) - 1) / threads / (C / set)) continue;  // threads of one launch
       const int rows = rows_of((L + pass - 1) / pass, backward);
       if (!rows) continue;
-      double cost = std::max(static_cast<double>(rows) * threads / (static_cast<double>(L) * nv), rows / call);
-      if (backward) cost *= (1 + 0.035 * rows) * (1 + 8.0 / (set * e)) * (threads > 256 ? 1.05 : 1.0);
-      else cost *= (1 + 24.0 / (set * e)) * (threads > 512 ? 1.25 : threads > 256 ? 1.1 : rows > 10 ? 1.2 : 1.0);
+      const double width = 1 + (backward ? 8.0 : 24.0) / (set * e);
+      const double held = static_cast<double>(rows) * threads / (static_cast<double>(L) * nv);
+      double cost = std::max(held * width, rows / call);
+      if (backward) cost *= (1 + 0.035 * rows) * (threads > 256 ? 1.05 : 1.0);
+      else cost *= threads > 512 ? 1.25 : threads > 256 ? 1.1 : rows > 10 ? 1.2 : 1.0;
       if (cost < least) {
         least = cost;
         p.set = static_cast<int>(set);
