@@ -230,7 +230,7 @@ int ss1d_conv_step(const void* x, const float* conv_w, const float* conv_b, void
   if (!ss2d::host_mul_ok(S, (KW - 1) * D, &n) || n > ss2d::kHostMaxElems / 4096) return SS2D_ERR_SHAPE;
   if (D > 0 && B > kMaxThreads / 64 / ((D + 63) / 64)) return SS2D_ERR_SHAPE;
   if (B == 0 || T == 0 || D == 0) return SS2D_OK;
-  if (!x || !conv_w || !y || (KW > 1 && !state)) return SS2D_ERR_NULL;
+  if (!x || !conv_w || !y || (KW > 1 && S > 0 && !state)) return SS2D_ERR_NULL;
   const int64_t e = dtype == SS2D_F32 ? 4 : 2;
   Args a{};
   Span ins[4];

@@ -416,7 +416,7 @@ int ss1d_scan_step(const void* u, const void* dt_raw, const float* A_log, const 
   if (!ss2d::host_mul_ok(S, D * N, &n) || n > ss2d::kHostMaxElems / 4096) return SS2D_ERR_SHAPE;
   if (D > 0 && (B > kMaxThreads / 256 / ((D + 63) / 64) || T >= (int64_t(1) << 31))) return SS2D_ERR_SHAPE;
   if (B == 0 || T == 0 || D == 0) return SS2D_OK;
-  if (!u || !dt_raw || !A_log || !Bs || !Cs || !Ds || !dt_bias || !state || !y) return SS2D_ERR_NULL;
+  if (!u || !dt_raw || !A_log || !Bs || !Cs || !Ds || !dt_bias || (!state && S > 0) || !y) return SS2D_ERR_NULL;
   const int64_t e = dtype == SS2D_F32 ? 4 : 2;
   Data x;
   Span ins[9];

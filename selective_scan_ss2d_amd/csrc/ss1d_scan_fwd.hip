@@ -324,8 +324,10 @@ int launch_scan_segments(const Args& a, int dtype, hipStream_t st) {
 
 int launch_scan_join(const Args& a, bool back, hipStream_t st) {
   constexpr int kWaves = 16;
-  const bool many = a.units > a.q.S * 16;  // more segments a sequence than one wave has in flight
-  const dim3 grid(static_cast<unsigned>((a.q.S * a.D * a.N + 63) / 64)), block(many ? 64 * kWaves : 64);
+  const int64_t blocks = (a.q.S * a.D * a.N + 63) / 64;
+  // more segments a sequence than one wave has in flight, and few enough blocks for one launch
+  const bool many = a.units > a.q.S * 16 && blocks < (1 << 21);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(many ? 64 * kWaves : 64);
   if (back && many) hipLaunchKernelGGL((k_scan_join<true, kWaves>), grid, block, 0, st, a);
   else if (back) hipLaunchKernelGGL((k_scan_join<true, 1>), grid, block, 0, st, a);
   else if (many) hipLaunchKernelGGL((k_scan_join<false, kWaves>), grid, block, 0, st, a);

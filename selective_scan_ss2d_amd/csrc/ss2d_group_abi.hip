@@ -30,8 +30,8 @@ int check(int64_t B, int64_t L, int64_t C, int64_t G, float eps, int dtype) {
   if (!ss2d::host_mul_ok(B, L, &rows) || !ss2d::host_mul_ok(std::max(rows, B), C, &n) ||
       n > ss2d::kHostMaxElems / 64)
     return SS2D_ERR_SHAPE;
-  // threads of one launch, at least one block per image and 64 bytes of its channels
-  if (B > (int64_t(1) << 32) / 2048 / ((C + 15) / 16)) return SS2D_ERR_SHAPE;
+  // threads of one launch: a wave per group of an image, a block per image and 32 channels
+  if (B > (int64_t(1) << 25) / G || B > (int64_t(1) << 23) / ((C + 31) / 32)) return SS2D_ERR_SHAPE;
   return SS2D_OK;
 }
 

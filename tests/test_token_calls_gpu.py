@@ -289,6 +289,42 @@ def test_group_norm_past_32_bit_elements(shape, G):
         assert float(err.max()) <= 1e-4
 
 
+def test_steps_of_padding_alone():
+    """A pool without a state: every row is padding."""
+    t = gpu(su.make_inputs(3, 1, 40, 1, 16, BF16, seed=4))
+    c = {n: x.cuda() for n, x in su.conv_inputs(3, 1, 40, 4, BF16, seed=4, h0=3).items()}
+    slots = torch.tensor([0, -1, 5], dtype=torch.int32, device="cuda")
+    y = torch.full_like(t["u"], 3.0)
+    ss.ss1d_scan_step(*args(t), torch.empty(0, 40, 16, device="cuda"), slots=slots, y=y)
+    ss.ss1d_conv_step(c["x"], c["conv_w"], torch.empty(0, 3, 40, device="cuda", dtype=BF16), c["conv_b"], slots=slots, y=y)
+    torch.cuda.synchronize()
+    assert (y == 3.0).all()
+
+
+@pytest.mark.parametrize("B, L, C, G", [(400000, 1, 64, 4), (300000, 2, 24, 3), (5000, 33, 40, 40)])
+def test_group_norm_of_many_images(B, L, C, G):
+    """Each image's outputs and gradient are those of a call of few, up to the cut of its sums."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x, dy = (torch.randn(B, L, C, generator=gen, device="cuda") for _ in range(2))
+    w, b = torch.rand(C, generator=gen, device="cuda"), torch.rand(C, generator=gen, device="cuda")
+    y = ss.ss2d_group_norm_forward(x, G, weight=w, bias=b)
+    d = ss.ss2d_group_norm_backward(x, dy, G, weight=w, bias=b)
+    few = [x[-7:].clone(), dy[-7:].clone()]
+    want = ss.ss2d_group_norm_forward(few[0], G, weight=w, bias=b)
+    dwant = ss.ss2d_group_norm_backward(*few, G, weight=w, bias=b)["x"]
+    # sums of up to 64 values in another order; 1 / sqrt(var) of a group stays below 30
+    for got, ref in ((y[-7:], want), (d["x"][-7:], dwant)):
+        assert float((got - ref).abs().max()) <= 2e-4
+    unit = ((x.double().view(B, L, G, -1) - x.double().view(B, L, G, -1).mean((1, 3), keepdim=True)))
+    unit = (unit / (unit.square().mean((1, 3), keepdim=True) + 1e-5).sqrt()).view(B, L, C)
+    pre = unit * w + b
+    sg = torch.sigmoid(pre)
+    e = dy * sg * (1 + pre * (1 - sg))
+    for name, ref in (("weight", (e * unit).sum((0, 1))), ("bias", e.sum((0, 1)))):
+        # pairs of sums over B images in fp32: sqrt of the count of roundings of terms of size about 1
+        assert float((d[name] - ref).abs().max()) <= 4 * su.F32_HALF * B * L, name
+
+
 def block(t, conv, scan):
     """The inner part of a block over tokens: the convolution, B, C and delta from its output, the scan."""
     x = conv(t["x"])
