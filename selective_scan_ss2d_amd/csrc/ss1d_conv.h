@@ -39,9 +39,8 @@ struct Args {
 
 // Threads that share a row of D channels of a block, in pieces of `width` channels.
 int lanes_of(int64_t D, int width);
-// Tokens of a unit: as many as leave 2048 waves, from 8 to 24, or 32 in the backward, which reads KW - 1
-// more on either side of its unit.
-int run_of(int64_t tokens, int64_t D, bool backward);
+// Tokens of a unit, of B rows (`rows`, 0: of packed sequences, S of them).
+int run_of(int64_t rows, int64_t tokens, int64_t S, int64_t D, int KW, int dtype, bool backward);
 // Blocks along the units of the backward.
 int64_t unit_blocks(const Args& a, int width);
 // Channels of a thread: four (vec), or one.  Eight bfloat16 values, 16 bytes, take too many registers:

@@ -2,9 +2,10 @@
 // four adjacent channels through a unit of tokens of one sequence, its last KW - 1 inputs in
 // registers; blocks lay their threads over channels first, then over units.
 // Every tensor passes once, which is what bounds it: forward 12,007 tokens of 4096 channels, 198 MB, bf16,
-// 38 us (5.2 TB/s); 25,216 tokens of 768 channels 19 us; backward there, with x, dy and dx, 116 MB, 38 to
-// 44, of which half is vector work (two activations' slopes and KW products three times).  Eight channels a
-// thread leave too few threads in flight, eight rows ahead too few registers (62 us for 46).
+// 37 us (5.3 TB/s); 25,216 tokens of 768 channels 17 us; backward there, with x, dy and dx, 116 MB, 35, of
+// which a third is vector work (the activation's slope, KW products three times) that three waves per
+// SIMD do not hide.  Eight channels a thread leave too few threads in flight, eight rows ahead too few
+// registers (62 us for 46).
 #include <algorithm>
 
 #include "ss1d_conv.h"
@@ -380,13 +381,23 @@ int lanes_of(int64_t D, int width) {
   return best;
 }
 
-// Tokens of a thread: 8 to 24 (backward 32), as many as leave 2048 waves; each run reads KW - 1 tokens
-// of its neighbour again.  Runs of 8, 16, 24, 32, 48 in us: forward 64 x 197 x 768 11.9, 12.9, 13.1, 15.3,
-// 15.4; 8 x 2048 x 4096 58.8, 51.4, 50.9, 51.1, 53.2; with backward 64 x 197 x 768 42.1, 39.5, 41.2, 48.3,
-// 53.9; 1 x 4000 x 4096 71.9, 59.1, 54.7, 57.5, 66.8.
-int run_of(int64_t tokens, int64_t D, bool backward) {
-  const double waves = static_cast<double>(tokens) * D / (64 * 4 * 2048.0);  // of a run of one token
-  return static_cast<int>(std::clamp(waves, 1.0, backward ? 4.0 * 8 : 3.0 * 8)) / 8 * 8 + (waves < 8 ? 8 : 0);
+// Tokens of a thread: as few (8 at least, backward 12) as let all waves be on the chip at once, in equal
+// runs; each run reads KW - 1 tokens of its neighbour again, and waves that come in a second round
+// wait for the first.  Where that takes runs above 64 tokens there are many rounds, and runs of 24 do.  With
+// runs of 13, 16, 20, 25, 32 and 41 tokens, us, the rule's marked: forward 128 x 197 x 768 19.5, *17.4,
+// 17.2, 17.2, 19.4, 18.8; 12,007 packed tokens of 4096 channels 46.2, 43.6, 41.3, 43.2, 44.1, *39.5 (37:
+// 45.5); with the forward before it, backward 128 x 197 x 768 63.9, 64.2, 64.4, *56.4, 61.7, 61.3; 64 of
+// them *37.2, 39.1, 38.4, 40.4, 45.8, 46.5; fp32 128 of them 99.9, 99.9, 94.9, 97.0, 102.6, *88.1.
+int run_of(int64_t rows, int64_t tokens, int64_t S, int64_t D, int KW, int dtype, bool backward) {
+  // waves on a SIMD, by the kernels' registers
+  const int wide = dtype == 0 ? 1 : 0, deep = KW > 4 ? 1 : 0;
+  const int64_t waves = 1024 * (backward ? (wide || deep ? 2 : 3) : 5 - wide - deep);
+  // runs of a dense row; or of all packed tokens, of which each sequence may end in one of its own
+  const int64_t all = waves * 256 / std::max<int64_t>(1, D);
+  const int64_t runs = rows > 0 ? all / rows : all - S;
+  const int64_t length = rows > 0 ? tokens / rows : tokens;
+  const int64_t run = runs > 0 ? (length + runs - 1) / runs : length;
+  return static_cast<int>(run > 64 ? 24 : std::max<int64_t>(run, backward ? 12 : 8));
 }
 
 int64_t unit_blocks(const Args& a, int width) {

@@ -51,12 +51,12 @@ int set_rows(Args* a, int64_t* bytes, int64_t B, int64_t L, int64_t D, const int
   return SS2D_OK;
 }
 
-void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, const int32_t* cu, bool packed,
-               bool backward) {
+void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, int dtype, const int32_t* cu,
+               bool packed, bool backward) {
   a->q = {cu, S, L, B * L};
   a->D = static_cast<int>(D);
   a->KW = static_cast<int>(KW);
-  a->run = ss2d::conv::run_of(B * L, D, backward);
+  a->run = ss2d::conv::run_of(packed ? 0 : B, B * L, S, D, static_cast<int>(KW), dtype, backward);
   // a sequence without tokens still hands its state on: one unit of each
   a->units = S == 0 ? 0 : ss2d::unit_count(L, S, B * L, packed, a->run);
 }
@@ -125,7 +125,7 @@ int ss1d_conv_forward(const void* x, const float* conv_w, const float* conv_b, c
   for (const void* p : {static_cast<const void*>(conv_w), static_cast<const void*>(conv_b),
                         static_cast<const void*>(cu_seqlens)})
     if (off(p, 4)) return SS2D_ERR_ALIGN;
-  set_sizes(&a, B, L, S, D, KW, cu_seqlens, packed, false);
+  set_sizes(&a, B, L, S, D, KW, dtype, cu_seqlens, packed, false);
   if (!launchable(a.units, D)) return SS2D_ERR_SHAPE;
   ins[1] = {conv_w, D * KW * 4};
   ins[2] = {conv_b, D * 4};
@@ -152,7 +152,7 @@ int ss1d_conv_forward(const void* x, const float* conv_w, const float* conv_b, c
 int64_t ss1d_conv_scratch_bytes(int64_t B, int64_t L, int64_t S, int64_t D, int64_t KW, int dtype, int packed) {
   if (check_sizes(B, L, S, D, KW, dtype, packed != 0) != SS2D_OK) return -1;
   Args a{};
-  set_sizes(&a, B, L, S, D, KW, nullptr, packed != 0, true);
+  set_sizes(&a, B, L, S, D, KW, dtype, nullptr, packed != 0, true);
   return part_bytes(a);
 }
 
@@ -181,7 +181,7 @@ int ss1d_conv_backward(const void* x, const float* conv_w, const float* conv_b, 
                         static_cast<const void*>(dconv_b)})
     if (off(p, 4)) return SS2D_ERR_ALIGN;
   if (off(scratch, 256)) return SS2D_ERR_ALIGN;
-  set_sizes(&a, B, L, S, D, KW, cu_seqlens, packed, true);
+  set_sizes(&a, B, L, S, D, KW, dtype, cu_seqlens, packed, true);
   if (!launchable(a.units, D)) return SS2D_ERR_SHAPE;
   const int64_t bytes = part_bytes(a);
   ins[1] = {conv_w, D * KW * 4};
