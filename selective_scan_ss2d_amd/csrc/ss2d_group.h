@@ -42,7 +42,7 @@ struct Plan {
   int width, rows, threads, set;
 };
 Plan plan(int64_t B, int64_t L, int64_t C, int64_t G, int dtype, bool vec, bool backward);
-int64_t chunk_positions(int64_t B, int64_t L, int64_t C);
+int64_t chunk_positions(int64_t B, int64_t L, int64_t C, int dtype);
 
 int launch_group(const Args& a, const Plan& p, int dtype, hipStream_t st);
 int launch_group_bwd(const Args& a, const Plan& p, int dtype, hipStream_t st);

@@ -35,7 +35,7 @@ int check(int64_t B, int64_t L, int64_t C, int64_t G, float eps, int dtype) {
   return SS2D_OK;
 }
 
-void set_shape(Args* a, int64_t B, int64_t L, int64_t C, int64_t G, int silu, float eps) {
+void set_shape(Args* a, int64_t B, int64_t L, int64_t C, int64_t G, int silu, float eps, int dtype) {
   a->B = B;
   a->L = L;
   a->C = static_cast<int>(C);
@@ -43,7 +43,7 @@ void set_shape(Args* a, int64_t B, int64_t L, int64_t C, int64_t G, int silu, fl
   a->cg = static_cast<int>(C / G);
   a->silu = silu;
   a->eps = eps;
-  a->chunk = ss2d::group::chunk_positions(B, L, C);
+  a->chunk = ss2d::group::chunk_positions(B, L, C, dtype);
   a->chunks = (L + a->chunk - 1) / a->chunk;
 }
 
@@ -97,7 +97,7 @@ extern "C" {
 int64_t ss2d_group_norm_scratch_bytes(int backward, int kept, int64_t B, int64_t L, int64_t C, int64_t G, int dtype) {
   if (check(B, L, C, G, 0.0f, dtype) != SS2D_OK) return -1;
   Args a{};
-  set_shape(&a, B, L, C, G, 0, 0.0f);
+  set_shape(&a, B, L, C, G, 0, 0.0f, dtype);
   size_t bytes = 0;  // of either width of a thread
   for (bool vec : {false, true}) {
     if (vec && C % (dtype == SS2D_F32 ? 4 : 8) != 0) continue;
@@ -118,7 +118,7 @@ int ss2d_group_norm_forward(const void* x, const float* weight, const float* bia
   if (off(x, e) || off(y, e) || off(weight, 4) || off(bias, 4) || off(stats, 4) || off(scratch, 256))
     return SS2D_ERR_ALIGN;
   Args a{};
-  set_shape(&a, B, L, C, G, silu, eps);
+  set_shape(&a, B, L, C, G, silu, eps, dtype);
   const Plan p = ss2d::group::plan(B, L, C, G, dtype, pieces(C, e, x, y, nullptr), false);
   const Layout w = layout(a, p, false, stats != nullptr);
   const Span ins[] = {{x, m * e}, {weight, C * 4}, {bias, C * 4}};
@@ -160,7 +160,7 @@ int ss2d_group_norm_backward(const void* x, const float* weight, const float* bi
     if (off(p, 4)) return SS2D_ERR_ALIGN;
   if (off(scratch, 256)) return SS2D_ERR_ALIGN;
   Args a{};
-  set_shape(&a, B, L, C, G, silu, eps);
+  set_shape(&a, B, L, C, G, silu, eps, dtype);
   const Plan p = ss2d::group::plan(B, L, C, G, dtype, pieces(C, e, x, dy, dx), true);
   const Layout w = layout(a, p, true, stats != nullptr);
   const Span ins[] = {{x, m * e}, {weight, C * 4}, {bias, C * 4}, {stats, B * G * 8}, {dy, m * e}};
