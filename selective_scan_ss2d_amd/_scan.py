@@ -129,8 +129,8 @@ def ss1d_scan_backward(u, dt_raw, A_log, Bs, Cs, Ds, dt_bias, dy, z=None, cu_seq
         expect("saved", saved, (max(0, size),), torch.uint8, dev)
     with scope(dev, stream, u, dt_raw, A_log, Bs, Cs, Ds, dt_bias, z, dy, cu_seqlens, initial_state,
                dstate, saved):
-        make = torch.zeros if packed else torch.empty
-        d = {n: make(t.shape, dtype=t.dtype, device=dev)
+        make = torch.zeros if packed else torch.empty  # rows outside of every sequence are not written
+        d = {n: (torch.empty if n in ("A_log", "Ds", "dt_bias") else make)(t.shape, dtype=t.dtype, device=dev)
              for n, t in (("u", u), ("dt_raw", dt_raw), ("A_log", A_log), ("Bs", Bs), ("Cs", Cs),
                           ("Ds", Ds), ("dt_bias", dt_bias))}
         if z is not None:

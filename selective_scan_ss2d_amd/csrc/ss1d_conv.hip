@@ -371,7 +371,7 @@ int launch_types(const Args& a, int dtype, bool vec, Kind kind, hipStream_t st) 
 // step of 8 x 20,000 tokens of 40 channels, 10 of 32 threads at work and 10 of 16, 66.4 and 44.6 us.
 int lanes_of(int64_t D, int width) {
   const int64_t pieces = (D + width - 1) / width;
-  int best = width == 1 ? 32 : 8;
+  int best = width == 1 && pieces > 16 ? 32 : 8;
   int64_t least = (pieces + best - 1) / best * best;
   for (int lanes = 2 * best; lanes <= kThreads; lanes *= 2) {
     const int64_t covered = (pieces + lanes - 1) / lanes * lanes;

@@ -627,12 +627,13 @@ __global__ __launch_bounds__(1024) void k_group_sums(Args a, int64_t count) {
   if (out) out[c % a.C] = v;
 }
 
-// The widest row of threads, of 256 down to 8 (32 of single values, or rows are read in pieces of 32
-// bytes), whose blocks leave the fewest threads idle: bf16 64 x 3136 x 64 in one group, 8 of 32 threads
-// at work and 8 of 8, 44.9 and 32.1 us.
+// The widest row of threads, of 256 down to 8 (32 of single values of rows of more than 16, which would
+// be read in pieces of 32 bytes), whose blocks leave the fewest threads idle: bf16 64 x 3136 x 64 in one
+// group, 8 of 32 threads at work and 8 of 8, 44.9 and 32.1 us; 256 x 7778 x 5, 5 of 32 and of 8, 99.9 and
+// 41.1.
 int lanes_of(int64_t C, int width) {
   const int64_t pieces = (C + width - 1) / width;
-  int best = width == 1 ? 32 : 8;
+  int best = width == 1 && pieces > 16 ? 32 : 8;
   int64_t least = (pieces + best - 1) / best * best;
   for (int lanes = 2 * best; lanes <= 256; lanes *= 2) {
     const int64_t covered = (pieces + lanes - 1) / lanes * lanes;
