@@ -36,6 +36,7 @@ CASES = [
     (1, 100, 264, 4, BF16, True, True, True, True), (2, 65, 130, 8, F32, True, True, True, False),
     (2, 2, 24, 8, BF16, True, True, True, False), (1, 97, 1100, 5, BF16, True, True, False, True),
     (2, 40, 40, 6, F32, False, False, True, True), (1, 64, 136, 7, BF16, True, True, True, False),
+    (8, 197, 8192, 4, BF16, True, True, True, False), (3, 900, 2050, 8, F32, True, True, False, True),  # longer runs
 ]
 
 

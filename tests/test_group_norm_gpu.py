@@ -18,6 +18,9 @@ CASES = [
     ((1, 5000, 16), 2, F32, True, True), ((1, 20000, 8), 1, BF16, True, True), ((1, 2100, 63), 1, F32, True, True),
     ((2, 33, 1032), 3, BF16, True, True), ((70, 4, 64), 2, F32, True, True), ((1, 4, 4, 9000), 1, F32, True, True),
     ((1, 8500, 264), 33, BF16, True, True),
+    # by chunks: rows of 8 and 16 threads, of single values, and joins of 64 to 1024 threads
+    ((2, 90000, 24), 3, BF16, True, True), ((1, 60000, 72), 1, F32, True, True), ((3, 9000, 5), 1, BF16, True, True),
+    ((1, 66000, 64), 8, BF16, True, True), ((5, 5000, 33), 1, F32, False, True),
 ]
 
 
