@@ -633,7 +633,9 @@ int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int 
  * (device memory) into the L tokens of B = 1, as for the gated delta rule: tokens outside of every
  * sequence are neither read nor written, and the kernels cut offsets to [0, L].
  *
- * Arithmetic: delta, the state, every sum and the gate are fp32; outputs are rounded once.  Few
+ * Arithmetic: delta, the state, every sum and the gate are fp32; outputs are rounded once.  A rate
+ * exp(A_log) log2(e) above the largest fp32 (A_log of 88.4 or more) is taken as that: the state is
+ * forgotten at every token whose delta is not 0.  Few
  * sequences are cut into segments that run at once from a zero start and are joined by
  * h <- exp(A sum delta) h + end.  NaN and infinities reach what the definition says, and nothing
  * before their token, of another sequence or, if they are u's, dt_raw's or z's, another channel

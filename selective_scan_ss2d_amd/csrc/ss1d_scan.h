@@ -12,6 +12,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 #include <type_traits>
 
@@ -66,6 +67,14 @@ int launch_scan_adjoint_segments(const Args& a, int dtype, hipStream_t st);
 int launch_scan_sums(const Args& a, int dtype, hipStream_t st);
 
 // ---- device pieces -----------------------------------------------------------------------------
+// A log2(e) of a state.  Held at the largest fp32 where exp(A_log) passes it: a step of delta 0 (past the
+// end of a tile, or of a lane past the channels) then leaves the state alone, and a decay of 0 times the
+// rate stays 0 in the gradients, where infinity would make both NaN.  (The comparison keeps a NaN.)
+__device__ __forceinline__ float decay_rate(float A_log) {
+  const float v = -expf(A_log) * kLog2e;
+  return v < -FLT_MAX ? -FLT_MAX : v;
+}
+
 // Sums four values over a quad: lane s gets the sum of v_s.
 __device__ __forceinline__ float quad_scatter_sum(float v0, float v1, float v2, float v3, bool odd,
                                                   bool high) {

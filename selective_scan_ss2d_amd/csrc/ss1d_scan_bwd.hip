@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_adjoint(Args a) {
 #pragma unroll
   for (int i = 0; i < kNS; ++i) {
     const int n = s * kNS + i;
-    Ap[i] = n < a.N ? -expf(a.A_log[int64_t(d) * a.N + n]) * kLog2e : -1.0f;
+    Ap[i] = n < a.N ? decay_rate(a.A_log[int64_t(d) * a.N + n]) : -1.0f;
     carry[i] = !empty && behind && n < a.N && on ? behind[(p.unit * a.D + d) * a.N + n] : 0.0f;
     dA[i] = 0.0f;
   }

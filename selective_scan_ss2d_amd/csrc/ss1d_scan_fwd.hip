@@ -75,7 +75,7 @@ void k_scan_tokens(Args a) {
   for (int i = 0; i < kNS; ++i) {
     const int n = s * kNS + i;
     // states past N decay to nothing; their B and C are zero
-    Ap[i] = n < a.N ? -expf(a.A_log[int64_t(d) * a.N + n]) * kLog2e : -1.0f;
+    Ap[i] = n < a.N ? decay_rate(a.A_log[int64_t(d) * a.N + n]) : -1.0f;
     h[i] = 0.0f;
   }
   if constexpr (kOut) {
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_scan_join(Args a) {
   const int64_t count = (q.len + a.seglen - 1) / a.seglen, first = first_unit(a.q, q, a.seglen);
   const int64_t part = (count + kWaves - 1) / kWaves;
   const int64_t k0 = part * wave, k1 = valid ? min(count, k0 + part) : 0;
-  const float Ap = -expf(a.A_log[i]) * kLog2e;
+  const float Ap = decay_rate(a.A_log[i]);
   const float* from = kBack ? a.dht : a.h0;
   float h = from && valid ? from[at] : 0.0f;
   // segments k0 to k1 from the state h

@@ -2,6 +2,7 @@
 // registers, advance them over the call's few tokens and write them back in place.
 // What bounds it is HBM, the states in and out: 256 rows of 4096 channels of 16 states, 143 MB, in 32 us
 // (4.5 TB/s); of one row the latency of its loads, 3.5 us.
+#include "ss1d_scan.h"
 #include "ss1d_scan_step.h"
 
 namespace ss2d {
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(4 * kStepCh) void k_scan_step(StepArgs a) {
   };
   fetch(b0);
 #pragma unroll
-  for (int i = 0; i < kNS; ++i) Ap[i] = -expf(Ap[i]) * kLog2e;
+  for (int i = 0; i < kNS; ++i) Ap[i] = decay_rate(Ap[i]);
   for (int i = 0; i < n; ++i) {
     int b = b0 + i;
     const int slot = slot_in;

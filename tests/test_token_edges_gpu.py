@@ -1,0 +1,57 @@
+"""Calls of the token-order scan, its convolution and the group norm at the ends of what their definitions
+cover: decays past fp32, no positions, no channels, views whose unused strides are wide."""
+import pytest
+import torch
+
+import selective_scan_ss2d_amd as ss
+from selective_scan_ss2d_amd import _binding as bnd
+from tests import scan_util as su
+from tests import token_util as tu
+from tests.test_scan_gpu import args, gpu
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("L, N", [(41, 16), (48, 16), (21, 32), (70, 5)])
+@pytest.mark.parametrize("seg, lanes", [(0, 4), (16, 4), (0, 16), (16, 16)])
+def test_decays_past_fp32(L, N, seg, lanes):
+    """exp(A_log) above the largest fp32: the state forgets everything at each token, whether or not the
+    length is whole tiles; channels up to the block's last, whose values idle lanes copy."""
+    t = su.make_inputs(2, L, 70, 1, N, F32, seed=L, h0=2)
+    t["A_log"][3, :2], t["A_log"][40], t["A_log"][69] = 89.0, 200.0, 500.0
+    d = gpu(t)
+    kw = dict(z=d["z"], initial_state=d["h0"])
+    with su.plan(seg, lanes):
+        y, end = ss.ss1d_scan_forward(*args(d), final_state=True, **kw)
+        _, saved = ss.ss1d_scan_forward_save(*args(d), **kw)
+        got = ss.ss1d_scan_backward(*args(d), d["dy"], dstate=d["dht"], saved=saved, **kw)
+    tu.check_scan(t, y, end, got)
+
+
+def test_infinite_decay():
+    """A_log of +infinity: the same as any that forgets everything; of NaN: its channel is NaN, no other."""
+    t = gpu(su.make_inputs(1, 41, 40, 1, 16, F32, seed=3, h0=1))
+    t["A_log"][7] = 300.0
+    want = ss.ss1d_scan_forward(*args(t), z=t["z"], initial_state=t["h0"], final_state=True)
+    t["A_log"][7] = float("inf")
+    for seg, lanes in ((0, 4), (16, 4), (0, 16)):
+        with su.plan(seg, lanes):
+            got = ss.ss1d_scan_forward(*args(t), z=t["z"], initial_state=t["h0"], final_state=True)
+        assert torch.allclose(got[0], want[0], rtol=1e-4, atol=1e-4) and torch.allclose(got[1], want[1], rtol=1e-4, atol=1e-4)
+    t["A_log"][7, 3] = float("nan")
+    state = t["h0"].clone()
+    one = [t[n][:, :1].contiguous() if n in ("u", "dt_raw", "Bs", "Cs") else t[n] for n in su.NAMES]
+    for y, end in (ss.ss1d_scan_forward(*args(t), z=t["z"], initial_state=t["h0"], final_state=True),
+                   (ss.ss1d_scan_step(*one, state, z=t["z"][:, :1].contiguous()), state)):
+        assert y[:, :, 7].isnan().all() and end[:, 7, 3].isnan().all()
+        assert int(y.isnan().sum()) == y.shape[1] and int(end.isnan().sum()) == 1
+
+
+def test_step_decays_past_fp32():
+    t = su.make_inputs(3, 2, 40, 1, 16, F32, seed=5, h0=3)
+    t["A_log"][3], t["A_log"][39] = 89.0, 200.0
+    d = gpu(t)
+    state = d["h0"].clone()
+    y = ss.ss1d_scan_step(*args(d), state, z=d["z"])
+    tu.check_scan(t, y, state, None)
