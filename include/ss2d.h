@@ -625,8 +625,8 @@ int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int 
  * B and C are shared by the D / G channels of a group (channel d: group d / (D / G)).
  * strides: 12 element strides, (batch, token) of u, of dt_raw and of z, then (batch, token, group)
  * of Bs and of Cs, whose last axes are contiguous (views into one projection, for instance; none
- * negative, token and group strides at most 2^24, SS2D_ERR_SHAPE above; z's unused without z); NULL
- * for contiguous tensors.  Every other tensor is contiguous.  1 <= N <= 32 (SS2D_ERR_UNSUPPORTED
+ * negative, token and group strides of more than one token or group at most 2^24, SS2D_ERR_SHAPE above;
+ * z's unused without z); NULL for contiguous tensors.  Every other tensor is contiguous.  1 <= N <= 32 (SS2D_ERR_UNSUPPORTED
  * above), D a multiple of G, at most 2^24.
  *
  * cu_seqlens: NULL, and the B rows are S = B sequences of L tokens; or S + 1 ascending offsets

@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include "ss1d_scan.h"
 #include "ss1d_scan_step.h"
@@ -76,6 +77,11 @@ int set_data(Data* x, Span* ins, const void* u, const void* dt, const void* z, c
     x->sc = {st[9], st[10]};
     x->scg = st[11];
   }
+  // the strides of one token and of one group are not used, however wide
+  if (L <= 1)
+    for (RowStrides* s : {&x->su, &x->sd, &x->sz, &x->sb, &x->sc}) s->l = std::min(s->l, kMaxLine);
+  if (G == 1)
+    for (int64_t* s : {&x->sbg, &x->scg}) *s = std::min(*s, kMaxLine);
   if (x->sbg < 0 || x->scg < 0 || x->sbg > kMaxLine || x->scg > kMaxLine) return SS2D_ERR_SHAPE;
   if ((G - 1) * std::max(x->sbg, x->scg) > kMaxLine) return SS2D_ERR_SHAPE;
   const int64_t bytes[5] = {strided_bytes(B, L, D, x->su, e), strided_bytes(B, L, D, x->sd, e),

@@ -55,3 +55,37 @@ def test_step_decays_past_fp32():
     state = d["h0"].clone()
     y = ss.ss1d_scan_step(*args(d), state, z=d["z"])
     tu.check_scan(t, y, state, None)
+
+
+def test_wide_strides_of_one_token_and_of_one_group():
+    """Time-first projections viewed batch-first, of one token; groups behind tokens, of one group."""
+    B, D, N = 1100, 8192, 16
+    assert B * 2 * D > 1 << 24
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(BF16)
+
+    u, dt = (normal(1, B, 2 * D).transpose(0, 1)[..., :D] for _ in range(2))
+    Bs, Cs = (normal(B, 1, 1, N) for _ in range(2))
+    par = (torch.zeros(D, N, device="cuda"), torch.ones(D, device="cuda"), torch.full((D,), -2.0, device="cuda"))
+
+    def step(u, dt):
+        state = torch.zeros(B, D, N, device="cuda")
+        return ss.ss1d_scan_step(u, dt, par[0], Bs, Cs, par[1], par[2], state), state
+
+    for got, want in zip(step(u, dt), step(u.contiguous(), dt.contiguous())):
+        assert torch.equal(got, want)
+    L, W, D = 20, 1 << 20, 40
+    wide = normal(1, 1, L, W).transpose(1, 2)  # group stride L W, token stride W
+    u, dt = (normal(1, L, D) for _ in range(2))
+    par = (torch.zeros(D, N, device="cuda"), torch.ones(D, device="cuda"), torch.full((D,), -2.0, device="cuda"))
+    assert wide.stride(2) > 1 << 24
+
+    def both(Bs, Cs):
+        a = (u, dt, par[0], Bs, Cs, par[1], par[2])
+        return [ss.ss1d_scan_forward(*a)] + list(ss.ss1d_scan_backward(*a, u).values())
+
+    views = wide[..., :N], wide[..., N:2 * N]
+    for got, want in zip(both(*views), both(*[v.contiguous() for v in views])):
+        assert torch.equal(got, want)
