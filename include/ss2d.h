@@ -736,7 +736,7 @@ int ss1d_conv_step(const void *x, const float *conv_w, const float *conv_b, void
  * channels of an image's group.
  *   x, y (B, L, C) dtype, channels last (L = H * W for maps);  weight, bias (C) fp32, NULL for 1 and 0
  *   stats (B, G, 2) fp32, or NULL: mean and 1 / sqrt(var + eps), written by the forward for the
- *     backward, which computes them again without.
+ *     backward, which computes them again without (no positions: 0 and 1 / sqrt(eps)).
  * All contiguous.  C a multiple of G, at most 2^20; L below 2^31; B G at most 2^25, B C about 2^28
  * (SS2D_ERR_SHAPE above).  Statistics are fp32, by the mean
  * first and then the squares about it.

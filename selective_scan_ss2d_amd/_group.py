@@ -40,7 +40,7 @@ def ss2d_group_norm_forward(x, groups, weight=None, bias=None, silu=True, eps=1e
     the C / groups channels of a group of each of the B images; act is SiLU, or nothing with
     silu=False.  x (B, ..., C) float32 or bfloat16, contiguous; weight and bias (C) float32.
     Returns y, or with stats=True the pair (y, stats (B, groups, 2) float32), the groups' mean and
-    1 / sqrt(var + eps), which the backward takes.
+    1 / sqrt(var + eps) (0 and 1 / sqrt(eps) without positions), which the backward takes.
     """
     torch, lib = _torch(), bnd.load_library()
     (B, L, C), code = _shape(x, groups, weight, bias)

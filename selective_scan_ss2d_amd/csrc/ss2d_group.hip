@@ -436,7 +436,7 @@ __global__ __launch_bounds__(1024) void k_group_join(Args a) {
   __shared__ float waves[16];
   const int64_t id = blockIdx.x, b = id / a.G;
   const float* parts = a.parts + b * a.chunks * 2 * a.C + id % a.G * a.cg;
-  const float total = static_cast<float>(a.L) * a.cg;
+  const float total = static_cast<float>(max(a.L, int64_t(1))) * a.cg;  // (without positions 0 / cg)
   auto positions = [&](uint32_t k) { return static_cast<float>(min(a.L - k * a.chunk, a.chunk)); };
   const float mean =
       join_sum(parts, a, waves, [&](float m, float, uint32_t k, uint32_t) { return positions(k) * m; }) / total;
@@ -674,9 +674,10 @@ template <typename T, int kV> int launch_t(const Args& a, const Plan& p, bool ba
   int joined = 64;  // threads of a join, of eight items each
   while (joined < 1024 && joined * 8 < a.chunks * a.cg) joined *= 2;
   if (!a.given) {
-    hipLaunchKernelGGL((k_group_chunks<T, kV>), grid, block, 0, st, a, lanes, cblocks);
+    if (a.chunks > 0) hipLaunchKernelGGL((k_group_chunks<T, kV>), grid, block, 0, st, a, lanes, cblocks);
     hipLaunchKernelGGL(k_group_join, groups, dim3(joined), 0, st, a);
   }
+  if (a.chunks == 0) return static_cast<int>(hipGetLastError());  // no positions: the statistics alone
   if (!back) {
     hipLaunchKernelGGL((k_group_apply<T, kV>), grid, block, 0, st, a, lanes, cblocks);
   } else {

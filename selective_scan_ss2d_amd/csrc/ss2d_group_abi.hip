@@ -112,8 +112,8 @@ int ss2d_group_norm_forward(const void* x, const float* weight, const float* bia
                             int silu, float eps, int dtype, void* stream) {
   int rc = check(B, L, C, G, eps, dtype);
   if (rc != SS2D_OK) return rc;
-  if (B == 0 || L == 0) return SS2D_OK;
-  if (!x || !y) return SS2D_ERR_NULL;
+  if (B == 0 || (L == 0 && !stats)) return SS2D_OK;
+  if (L > 0 && (!x || !y)) return SS2D_ERR_NULL;
   const int64_t e = dtype == SS2D_F32 ? 4 : 2, m = B * L * C;
   if (off(x, e) || off(y, e) || off(weight, 4) || off(bias, 4) || off(stats, 4) || off(scratch, 256))
     return SS2D_ERR_ALIGN;

@@ -89,3 +89,13 @@ def test_wide_strides_of_one_token_and_of_one_group():
     views = wide[..., :N], wide[..., N:2 * N]
     for got, want in zip(both(*views), both(*[v.contiguous() for v in views])):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_group_statistics_without_positions(dtype):
+    for shape, G, eps in (((2, 0, 8), 2, 1e-5), ((3, 5, 0, 33), 33, 0.25), ((1, 0, 4096), 1, 1e-3), ((0, 4, 8), 2, 1e-5)):
+        torch.full((1 << 18,), 7.0, device="cuda")  # what the allocator hands out next
+        y, stats = ss.ss2d_group_norm_forward(torch.zeros(shape, device="cuda", dtype=dtype), G, eps=eps, stats=True)
+        assert y.shape == shape and stats.shape == (shape[0], G, 2)
+        assert not stats[..., 0].any()
+        assert torch.allclose(stats[..., 1], torch.full_like(stats[..., 1], eps ** -0.5), rtol=4 * su.F32_HALF)
