@@ -649,7 +649,7 @@ int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int 
  * u, dt_raw, z (given with z), Bs and Cs in dtype, and in fp32 A_log, Ds, dt_bias and, if dh0 is not
  * NULL, h0; all contiguous, as dy.  saved: what ss1d_scan_forward kept for the same inputs (other
  * contents give undefined gradients), or NULL to compute it again.  Rows outside of every sequence are
- * left as they are.  Sums run in a fixed order (no atomics); without tokens those over tokens are 0.
+ * left as they are.  Sums run in a fixed order (no atomics); those over no tokens or no channels are 0.
  *
  * ss1d_scan_step is the form for serving: T tokens (few) of each of B sequences, whose states are
  * updated in place: row b's state is state[slots[b]], or state[b] with slots NULL (then S = B).  A row

@@ -334,11 +334,12 @@ int ss1d_scan_backward(const void* u, const void* dt_raw, const float* A_log, co
   const bool packed = cu_seqlens != nullptr;
   int rc = check_sizes(B, L, S, D, G, N, dtype, packed);
   if (rc != SS2D_OK) return rc;
-  if (D == 0) return SS2D_OK;
   const bool none = B * L == 0;
-  if (!none && (!u || !dt_raw || !Bs || !Cs || !dy || !du || !ddt_raw || !dBs || !dCs || (z != nullptr) != (dz != nullptr)))
+  if (D == 0 && none) return SS2D_OK;
+  if (!none && (!dBs || !dCs)) return SS2D_ERR_NULL;
+  if (!none && D > 0 && (!u || !dt_raw || !Bs || !Cs || !dy || !du || !ddt_raw || (z != nullptr) != (dz != nullptr)))
     return SS2D_ERR_NULL;
-  if (!A_log || !Ds || !dt_bias || !dA_log || !dDs || !ddt_bias) return SS2D_ERR_NULL;
+  if (D > 0 && (!A_log || !Ds || !dt_bias || !dA_log || !dDs || !ddt_bias)) return SS2D_ERR_NULL;
   const int64_t e = dtype == SS2D_F32 ? 4 : 2;
   Data x;
   Span ins[13];
@@ -394,7 +395,7 @@ int ss1d_scan_backward(const void* u, const void* dt_raw, const float* A_log, co
   a.par_parts = reinterpret_cast<float*>(ws.at + w.params);
   a.marks = const_cast<float*>(static_cast<const float*>(saved));
   int err = 0;
-  if (!saved) {  // the states before every tile, by the forward
+  if (!saved && D > 0) {  // the states before every tile, by the forward
     a.marks = reinterpret_cast<float*>(ws.at + w.marks);
     set_inputs(&again, x, u, dt_raw, z, Bs, Cs, A_log, Ds, dt_bias, h0);
     set_segments(&again, ws.at, w);
@@ -402,7 +403,7 @@ int ss1d_scan_backward(const void* u, const void* dt_raw, const float* A_log, co
     again.y = ws.at + w.y;
     err = none ? 0 : run_forward(again, dtype, st);
   }
-  if (!err && a.units > 0) {
+  if (!err && a.units > 0 && D > 0) {
     if (a.seglen) err = ss2d::sscan::launch_scan_adjoint_segments(a, dtype, st);
     if (!err && a.seglen) err = ss2d::sscan::launch_scan_join(a, true, st);
     if (!err) err = ss2d::sscan::launch_scan_adjoint(a, dtype, st);

@@ -439,6 +439,7 @@ int launch_scan_sums(const Args& a, int dtype, hipStream_t st) {
     else hipLaunchKernelGGL(k_scan_sum_bc<uint16_t>, grid, block, 0, st, a);
   }
   const int64_t width = int64_t(a.D) * (a.N + 2);
+  if (width == 0) return static_cast<int>(hipGetLastError());  // no channels: dB and dC, of 0, alone
   hipLaunchKernelGGL(k_scan_sum_params, dim3(static_cast<unsigned>((width + 63) / 64)), dim3(1024), 0, st, a);
   return static_cast<int>(hipGetLastError());
 }

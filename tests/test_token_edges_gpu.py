@@ -99,3 +99,22 @@ def test_group_statistics_without_positions(dtype):
         assert y.shape == shape and stats.shape == (shape[0], G, 2)
         assert not stats[..., 0].any()
         assert torch.allclose(stats[..., 1], torch.full_like(stats[..., 1], eps ** -0.5), rtol=4 * su.F32_HALF)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cu", [None, [0, 2, 2, 5]])
+def test_gradients_without_channels(cu, dtype):
+    """dBs and dCs are sums over the channels, of which there may be none."""
+    B, S = (2, 2) if cu is None else (1, 3)
+    u, bc = torch.zeros(B, 5, 0, device="cuda", dtype=dtype), torch.ones(B, 5, 2, 16, device="cuda", dtype=dtype)
+    none, A = torch.zeros(0, device="cuda"), torch.zeros(0, 16, device="cuda")
+    at = torch.tensor(cu, dtype=torch.int32, device="cuda") if cu else None
+    for z, h0 in ((None, None), (u, torch.zeros(S, 0, 16, device="cuda"))):
+        kw = dict(z=z, initial_state=h0, cu_seqlens=at)
+        y, saved = ss.ss1d_scan_forward_save(u, u, A, bc, bc, none, none, **kw)
+        assert y.shape == u.shape
+        for kept in (saved, None):
+            torch.full((1 << 18,), 7.0, device="cuda")  # what the allocator hands out next
+            d = ss.ss1d_scan_backward(u, u, A, bc, bc, none, none, u, saved=kept, **kw)
+            assert d["Bs"].shape == bc.shape and not d["Bs"].any() and not d["Cs"].any()
+            assert d["u"].shape == u.shape and d["A_log"].shape == A.shape
