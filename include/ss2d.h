@@ -629,6 +629,11 @@ int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int 
  * z's unused without z); NULL for contiguous tensors.  Every other tensor is contiguous.  1 <= N <= 32 (SS2D_ERR_UNSUPPORTED
  * above), D a multiple of G, at most 2^24.
  *
+ * Calls with a launch past 2^32 threads are refused (SS2D_ERR_SHAPE): of more than 2^24 blocks, each 64
+ * channels (16 in short calls of few channels) of a group and of a sequence or segment; cut into
+ * segments with S D N at 2^32; backward with 2^28 tokens, every sequence's in whole sixteens, or with
+ * D (N + 2) at 2^28.
+ *
  * cu_seqlens: NULL, and the B rows are S = B sequences of L tokens; or S + 1 ascending offsets
  * (device memory) into the L tokens of B = 1, as for the gated delta rule: tokens outside of every
  * sequence are neither read nor written, and the kernels cut offsets to [0, L].

@@ -157,10 +157,16 @@ void set_sizes(Args* a, int64_t B, int64_t L, int64_t S, int64_t D, int64_t G, i
   set_plan(a, B, L, packed, saves, backward);
 }
 
-bool launchable(const Args& a, bool packed) {
-  return a.units <= kMaxThreads / ss2d::sscan::kThreads / (4 * std::max(1, a.G * a.cbg)) &&
-         a.q.S <= (kMaxThreads - 256) / std::max<int64_t>(1, int64_t(a.D) * a.N) &&
-         ss2d::unit_count(a.q.L, a.q.S, a.q.T, packed, 16) <= kMaxThreads / 256;
+// Whether the threads of each launch that the call makes can be counted in 32 bits: the scan's blocks, of
+// kThreads / lanes channels; a join's states; the backward's sums over channel blocks, of 16 tokens a
+// block, and over units, of 64 columns.
+bool launchable(const Args& a, bool packed, bool backward) {
+  const int channels = ss2d::sscan::kThreads / (backward ? 4 : a.lanes);
+  const int64_t blocks = a.G * ((a.D / a.G + channels - 1) / channels), per = int64_t(a.D) * a.N;
+  if (a.units > kMaxThreads / ss2d::sscan::kThreads / std::max<int64_t>(1, blocks)) return false;
+  if (a.seglen && a.q.S > (kMaxThreads - 256) / std::max<int64_t>(1, per)) return false;
+  return !backward || (ss2d::unit_count(a.q.L, a.q.S, a.q.T, packed, 16) <= kMaxThreads / 256 &&
+                       (int64_t(a.D) * (a.N + 2) + 63) / 64 <= kMaxThreads / 1024);
 }
 
 int64_t mark_bytes(int64_t L, int64_t S, int64_t T, int64_t D, int64_t N, bool packed) {
@@ -296,7 +302,7 @@ int ss1d_scan_forward(const void* u, const void* dt_raw, const float* A_log, con
   if (off(y, e) || off(saved, 256) || off(scratch, 256)) return SS2D_ERR_ALIGN;
   Args a{};
   set_sizes(&a, B, L, S, D, G, N, cu_seqlens, packed, saved != nullptr, false);
-  if (!launchable(a, packed)) return SS2D_ERR_SHAPE;
+  if (!launchable(a, packed, false)) return SS2D_ERR_SHAPE;
   const Layout w = layout(a, a, false, true, packed, e);
   const int64_t states = S * D * N * 4;
   ins[5] = {A_log, D * N * 4};
@@ -359,7 +365,7 @@ int ss1d_scan_backward(const void* u, const void* dt_raw, const float* A_log, co
   set_sizes(&a, B, L, S, D, G, N, cu_seqlens, packed, true, true);
   Args again{};
   set_sizes(&again, B, L, S, D, G, N, cu_seqlens, packed, true, false);
-  if (!launchable(a, packed) || !launchable(again, packed)) return SS2D_ERR_SHAPE;
+  if (!launchable(a, packed, true) || (!saved && !launchable(again, packed, false))) return SS2D_ERR_SHAPE;
   const Layout w = layout(a, again, true, saved != nullptr, packed, e);
   const int64_t states = S * D * N * 4, wide = B * L * D * e, bc = B * L * G * N * e;
   ins[5] = {A_log, D * N * 4};

@@ -118,3 +118,22 @@ def test_gradients_without_channels(cu, dtype):
             d = ss.ss1d_scan_backward(u, u, A, bc, bc, none, none, u, saved=kept, **kw)
             assert d["Bs"].shape == bc.shape and not d["Bs"].any() and not d["Cs"].any()
             assert d["u"].shape == u.shape and d["A_log"].shape == A.shape
+
+
+def test_scan_of_more_states_than_threads_of_a_launch():
+    """70,000 sequences of 4096 channels of 16 states, which nothing joins: each is that of a call of few."""
+    B, L, D, N = 70000, 2, 4096, 16
+    assert B * D * N > 1 << 32
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    u, dt = (torch.randn(B, L, D, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    Bs, Cs = (torch.randn(B, L, 1, N, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    par = (torch.zeros(D, N, device="cuda"), torch.ones(D, device="cuda"), torch.full((D,), -2.0, device="cuda"))
+
+    def run(rows, lanes):
+        with su.plan(-1, lanes):
+            return ss.ss1d_scan_forward(u[rows], dt[rows], par[0], Bs[rows], Cs[rows], par[1], par[2], final_state=True)
+
+    y, end = run(slice(0, B), 0)
+    for rows in (slice(0, 3), slice(B - 3, B), slice(B // 2, B // 2 + 3)):
+        want, state = run(rows, 4)
+        assert torch.equal(y[rows], want) and torch.equal(end[rows], state)

@@ -35,3 +35,22 @@ def test_strides_of_one_token_or_group_are_free(lib):  # noqa: F811
     assert calls(lib, L=1, G=1, strides=strides(1, 1, token=1 << 61, group=1 << 61)) == alias
     assert calls(lib, L=1, strides=strides(1, 2, token=-64)) == shape
     assert calls(lib, L=3, G=1, strides=strides(3, 1, group=-16)) == shape
+
+
+def test_launches_are_limited_by_the_threads_that_they_take(lib):  # noqa: F811
+    ALIAS, SHAPE = bnd.SS2D_ERR_ALIAS, bnd.SS2D_ERR_SHAPE
+
+    def both(packed=False, **kw):
+        cu = () if packed else (9,)
+        return scan(lib, overlapping(14, 10, 0, cu), **kw), scan_bwd(lib, overlapping(23, 13, 0, cu), **kw)
+
+    # S D N past 2^32 where nothing is joined, and up to 2^24 blocks of 64 channels
+    assert both(B=70000, S=70000, L=2, D=4096, G=1) == (ALIAS, ALIAS)
+    assert both(B=1 << 17, S=1 << 17, L=2, D=8128, G=1) == (ALIAS, ALIAS)  # 127 blocks each
+    assert both(B=1 << 17, S=1 << 17, L=2, D=8192, G=1) == (SHAPE, SHAPE)
+    # 2^29 tokens; their sums of dB and dC take 2^25 blocks
+    assert both(True, B=1, S=4, L=1 << 29, D=64, G=1) == (ALIAS, SHAPE)
+    assert both(True, B=1, S=4, L=1 << 27, D=64, G=1) == (ALIAS, ALIAS)
+    # columns of the parameters' sums
+    assert both(B=1, S=1, L=1, D=1 << 23, N=32) == (ALIAS, SHAPE)
+    assert both(B=1, S=1, L=1, D=7 << 20, N=32) == (ALIAS, ALIAS)
