@@ -82,16 +82,16 @@ int overlap(const Span* outs, int n_out, const Span* ins, int n_in) {
   return SS2D_OK;
 }
 
-// The states of dense rows without tokens are those before them.
-__global__ __launch_bounds__(256) void k_copy(const char* from, char* to, int64_t bytes) {
-  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 2;
-  if (i >= bytes) return;
-  *reinterpret_cast<uint16_t*>(to + i) = from ? *reinterpret_cast<const uint16_t*>(from + i) : uint16_t(0);
+// The states of dense rows without tokens are those before them, in units of the smaller data type.
+__global__ __launch_bounds__(256) void k_copy(const uint16_t* from, uint16_t* to, int64_t count) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < count; i += int64_t(gridDim.x) * 256)
+    to[i] = from ? from[i] : uint16_t(0);
 }
 int copy_states(const void* from, void* to, int64_t bytes, hipStream_t st) {
   if (!to || from == to || bytes == 0) return 0;
-  hipLaunchKernelGGL(k_copy, dim3(static_cast<unsigned>((bytes + 511) / 512)), dim3(256), 0, st,
-                     static_cast<const char*>(from), static_cast<char*>(to), bytes);
+  const int64_t blocks = std::min<int64_t>((bytes + 511) / 512, 1 << 16);  // a launch's threads stay countable in 32 bits
+  hipLaunchKernelGGL(k_copy, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, static_cast<const uint16_t*>(from),
+                     static_cast<uint16_t*>(to), bytes / 2);
   return static_cast<int>(hipGetLastError());
 }
 

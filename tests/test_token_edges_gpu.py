@@ -4,7 +4,6 @@ import pytest
 import torch
 
 import selective_scan_ss2d_amd as ss
-from selective_scan_ss2d_amd import _binding as bnd
 from tests import scan_util as su
 from tests import token_util as tu
 from tests.test_scan_gpu import args, gpu
@@ -137,3 +136,17 @@ def test_scan_of_more_states_than_threads_of_a_launch():
     for rows in (slice(0, 3), slice(B - 3, B), slice(B // 2, B // 2 + 3)):
         want, state = run(rows, 4)
         assert torch.equal(y[rows], want) and torch.equal(end[rows], state)
+
+
+@pytest.mark.parametrize("B, D, KW, dtype", [(3, 5, 4, F32), (2, 7, 2, BF16), (80000, 8192, 8, BF16)])
+def test_conv_states_of_rows_without_tokens(B, D, KW, dtype):
+    """The states, and back their gradients, pass through, more than 2^33 bytes of them as well."""
+    state = torch.randn(B, KW - 1, D, device="cuda", dtype=dtype)
+    x, w = torch.zeros(B, 0, D, device="cuda", dtype=dtype), torch.ones(D, KW, device="cuda")
+    y, end = ss.ss1d_conv_forward(x, w, initial_state=state, final_state=True)
+    assert y.shape == x.shape and torch.equal(end, state)
+    del end
+    d = ss.ss1d_conv_backward(x, w, x, initial_state=state, dstate=state)
+    assert torch.equal(d["initial_state"], state) and not d["conv_w"].any()
+    del d
+    assert not ss.ss1d_conv_forward(x, w, final_state=True)[1].any()
