@@ -39,6 +39,18 @@ def test_packed_scan(case):
     scan_both(su.make_inputs(1, T, D, G, N, dtype, seed=T + N, gate=gate, h0=len(cu) - 1), seg, cu)
 
 
+@pytest.mark.parametrize("seg", [-1, 0, 64])
+@pytest.mark.parametrize("first", [True, False])
+def test_a_prompt_among_single_tokens(first, seg):
+    """Continuous batching: one prompt of 700 tokens and 150 sequences of one token or none."""
+    singles = [n % 5 != 3 for n in range(150)]
+    lengths = [700] + singles if first else singles + [700]
+    cu = [0]
+    for n in lengths:
+        cu.append(cu[-1] + int(n))
+    scan_both(su.make_inputs(1, cu[-1], 24, 1, 16, F32, seed=11, h0=len(lengths)), seg, cu)
+
+
 # B, L, D, N, segment, offsets: 69, 130 and 75 or so units, whose sums go four at a time and some alone
 @pytest.mark.parametrize("B, L, D, N, seg, cu", [
     (1, 1100, 20, 16, 16, None), (65, 20, 9, 4, 16, None), (1, 1000, 12, 16, 16, [0, 3, 400, 400, 401, 993]),
@@ -159,6 +171,28 @@ DEEP = [((64, 28, 28, 384), 32, BF16, True, True), ((64, 1500, 96), 16, BF16, Tr
 def test_group_norm_of_deep_rows(case):
     gn.test_both_directions(case, 0.5)
     group_gradients(case)
+
+
+def test_group_norm_by_chunks_off_16_bytes():
+    """Rows that start off 16 bytes, of groups too large for registers: by single values."""
+    x, dy, w, b = (v.cuda() for v in gn.make((2, 20000, 64), BF16, True))
+    off = torch.zeros(x.numel() + 1, dtype=BF16, device="cuda")[1:].view(x.shape)
+    off.copy_(x)
+    assert off.data_ptr() % 16 and off.is_contiguous()
+    kw = dict(weight=w, bias=b)
+    y, stats = ss.ss2d_group_norm_forward(off, 2, stats=True, **kw)
+    want, same = ss.ss2d_group_norm_forward(x, 2, stats=True, **kw)
+    d, dwant = ss.ss2d_group_norm_backward(off, dy, 2, **kw), ss.ss2d_group_norm_backward(x, dy, 2, **kw)
+    # sums of 640,000 values in another order: their roundings in quadrature
+    e = (8 + gn.summed(640000) ** 0.5) * su.F32_HALF
+    assert float((stats / same - 1).abs()[..., 1].max()) <= 2 * e
+    for got, ref, rel in [(y, want, su.BF16_HALF), (d["x"], dwant["x"], su.BF16_HALF)] + [
+            (d[n], dwant[n], 0.0) for n in ("weight", "bias")]:
+        got, ref = got.double(), ref.double()
+        # both are rounded to bfloat16; the parameters' sums go over 40,000 positions, whose terms
+        # of both signs leave 1 / 200 of their magnitudes
+        bound = (2 * rel + 8 * e) * float(ref.norm()) if rel else 200 * 2 * e * float(ref.norm())
+        assert float((got - ref).norm()) <= bound
 
 
 def conv_parameters(t, silu):
