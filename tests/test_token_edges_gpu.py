@@ -136,6 +136,20 @@ def test_scan_of_more_states_than_threads_of_a_launch():
     for rows in (slice(0, 3), slice(B - 3, B), slice(B // 2, B // 2 + 3)):
         want, state = run(rows, 4)
         assert torch.equal(y[rows], want) and torch.equal(end[rows], state)
+    del end
+
+    def back(rows):
+        return ss.ss1d_scan_backward(u[rows], dt[rows], par[0], Bs[rows], Cs[rows], par[1], par[2], y[rows])
+
+    got = back(slice(0, B))
+    for rows in (slice(0, 3), slice(B - 3, B)):
+        want = back(rows)
+        for n in ("u", "dt_raw", "Bs", "Cs"):
+            assert torch.equal(got[n][rows], want[n]), n
+    # dDs in 64 bits, by parts; sums of 140,000 terms of both signs in fp32
+    ref = sum((y[i:i + 1000].double() * u[i:i + 1000].double()).sum((0, 1)) for i in range(0, B, 1000))
+    mag = sum((y[i:i + 1000].double() * u[i:i + 1000].double()).abs().sum((0, 1)) for i in range(0, B, 1000))
+    assert float((got["Ds"] - ref).norm()) <= 16 * su.F32_HALF * float(mag.norm()) <= 1e-3 * float(ref.norm())
 
 
 @pytest.mark.parametrize("B, D, KW, dtype", [(3, 5, 4, F32), (2, 7, 2, BF16), (80000, 8192, 8, BF16)])
@@ -150,3 +164,31 @@ def test_conv_states_of_rows_without_tokens(B, D, KW, dtype):
     assert torch.equal(d["initial_state"], state) and not d["conv_w"].any()
     del d
     assert not ss.ss1d_conv_forward(x, w, final_state=True)[1].any()
+
+
+@pytest.mark.parametrize("channel", [3, 69])
+@pytest.mark.parametrize("seg", [0, 16])
+def test_nan_in_u_reaches_no_other_gradient(channel, seg):
+    """What does not read u of that token and channel, or the states behind it, is as without the NaN: the
+    last channel's too, whose values idle lanes copy."""
+    t = gpu(su.make_inputs(2, 60, 70, 1, 16, F32, seed=4))
+
+    def both():
+        with su.plan(seg):
+            _, saved = ss.ss1d_scan_forward_save(*args(t), z=t["z"])
+            return ss.ss1d_scan_backward(*args(t), t["dy"], z=t["z"], saved=saved)
+
+    clean = both()
+    t["u"][1, 30, channel] = float("nan")
+    got = both()
+    rest = [i for i in range(70) if i != channel]
+    for n in ("u", "dt_raw", "z"):
+        assert torch.equal(got[n][0], clean[n][0]) and torch.equal(got[n][1][:, rest], clean[n][1][:, rest]), n
+        assert torch.equal(got[n][1, :30], clean[n][1, :30]), n
+    assert torch.equal(got["u"], clean["u"])  # the adjoint does not read the states
+    for n in ("A_log", "Ds", "dt_bias"):
+        assert torch.equal(got[n][rest], clean[n][rest]), n
+    for n in ("Bs", "Cs"):
+        assert torch.equal(got[n][0], clean[n][0]) and torch.equal(got[n][1, :30], clean[n][1, :30]), n
+    assert torch.equal(got["Bs"][1, 31:], clean["Bs"][1, 31:])
+    assert got["Bs"][1, 30].isnan().all() and got["Cs"][1, 30:].isnan().all() and got["z"][1, 30:, channel].isnan().all()
