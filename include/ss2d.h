@@ -640,11 +640,12 @@ int64_t ss2d_norm_scratch_bytes(int64_t B, int64_t L, int64_t D, int64_t G, int 
  *
  * Arithmetic: delta, the state, every sum and the gate are fp32; outputs are rounded once.  A rate
  * exp(A_log) log2(e) above the largest fp32 (A_log of 88.4 or more) is taken as that: the state is
- * forgotten at every token whose delta is not 0.  Few
- * sequences are cut into segments that run at once from a zero start and are joined by
- * h <- exp(A sum delta) h + end.  NaN and infinities reach what the definition says, and nothing
- * before their token, of another sequence or, if they are u's, dt_raw's or z's, another channel
- * (an infinity may come out as NaN); dB and dC of their token and group are sums over channels.
+ * forgotten at every token whose delta is not 0.  Few sequences are cut into segments that run at
+ * once from a zero start and are joined by h <- exp(A sum delta) h + end.  NaN and infinities reach
+ * what the definition says, and nothing before their token, of another sequence or, if they are u's,
+ * dt_raw's or z's, another channel (an infinity may come out as NaN); dB and dC of their token and
+ * group are sums over channels, and a channel's dA_log, dDs and ddt_bias, sums over tokens, may be
+ * NaN with any of its states.
  *
  * ss1d_scan_forward writes y and, if ht is not NULL, the end states; ht may be h0 itself (in place).
  * saved (NULL, or ss1d_scan_saved_bytes bytes of device memory, aligned to 256) keeps what
@@ -734,8 +735,7 @@ int ss1d_conv_step(const void *x, const float *conv_w, const float *conv_b, void
                    const int64_t *strides, int silu, int dtype, void *stream);
 
 /* ---- group norm ---------------------------------------------------------------------------------
- * The norm of the backbone's convolution stages, over positions and groups of channels, with its
- * activation:
+ * A norm of channels-last maps over positions and groups of channels, with its activation:
  *   y = act((x - mean) / sqrt(var + eps) * weight + bias),   act = SiLU (silu 1) or none (0)
  * with mean and var (of the values themselves, about their mean) over the L positions and C / G
  * channels of an image's group.
@@ -743,8 +743,7 @@ int ss1d_conv_step(const void *x, const float *conv_w, const float *conv_b, void
  *   stats (B, G, 2) fp32, or NULL: mean and 1 / sqrt(var + eps), written by the forward for the
  *     backward, which computes them again without (no positions: 0 and 1 / sqrt(eps)).
  * All contiguous.  C a multiple of G, at most 2^20; L below 2^31; B G at most 2^25, B C about 2^28
- * (SS2D_ERR_SHAPE above).  Statistics are fp32, by the mean
- * first and then the squares about it.
+ * (SS2D_ERR_SHAPE above).  Statistics are fp32, by the mean first and then the squares about it.
  *
  * ss2d_group_norm_backward: the gradients of sum(dy * y): dx in dtype, dweight and dbias (given with
  * weight, with bias) in fp32, summed in a fixed order; without positions they are 0.

@@ -7,7 +7,7 @@
 // values with each sum, and two rotations of a row; over the waves in LDS; over the blocks of 64
 // channels by a second kernel.  No atomics: every sum has a fixed order.
 // It is bound by the vector pipes: 99.5 instructions per step of 16 channels of 16 states, of which the
-// states again take a quarter and the sums over channels a fifth; at 128 registers two waves per SIMD
+// states again take a quarter and the sums over channels a fifth; at 254 registers two waves per SIMD
 // keep them 77% busy.  8 x 2048 tokens of 2048 channels, bf16 with gate, in two segments per sequence:
 // 100 us (what segments send on) + 5 (join) + 502 + 13 (dB, dC) + 5 (vectors); whole, at one wave per
 // SIMD, 758 in all.  Tiles of 32 steps or of more registers spill, and a reload waits for the

@@ -2,12 +2,13 @@
 //
 // A block holds whole groups of an image in registers: x is read once, its mean and then the squares
 // about it are summed over the block, and y is written.  Where a group is too large for that, chunks
-// of positions give every channel's mean and sum of squares about it, one wave per group joins
+// of positions give every channel's mean and sum of squares about it, one block per group joins
 // them, and another pass normalises.
 // What bounds it is HBM where a block's loads of a few hundred KB are in flight at once: bf16, 64 maps of
-// 56 x 56 x 192, 154 MB, 40 us (3.8 TB/s: two blocks of a CU load and write in turn); fp32, 64 of 28 x 28 x
-// 384, 154 MB forward 31 us, 231 MB backward 60 to 76 (its registers hold x and dy of 10 rows, which
-// leaves two blocks of 512 threads per CU).
+// 56 x 56 x 192, 154 MB, 40 us (3.8 TB/s: one block of 1024 threads per CU loads, sums and writes in
+// turn); fp32, 64 of 28 x 28 x 384, 154 MB forward 28 us, 231 MB backward 62 to 68 (its registers hold x
+// and dy of 10 rows: 125, two blocks of 512 threads per CU).  In bfloat16 the backward's pieces of eight
+// channels take 169 registers there, one block per CU.
 #include <algorithm>
 #include <numeric>
 
@@ -158,7 +159,9 @@ __device__ __forceinline__ void statistics(const Args& a, const Tile& t, Piece<T
 }
 
 constexpr int kMaxGroups = 256;  // of a set
-// Rows of a thread that there are kernels for; at most registers for two blocks of 512 threads per CU.
+// Rows of a thread that there are kernels for.  Two blocks of 512 threads fit a CU at 128 registers: the
+// forward keeps to that at 20 rows (126), the backward at 10 in fp32 (125), but at 4 in bfloat16 (121; 6, 8
+// and 10 take 137, 153 and 169).
 constexpr int kDeepestBack = 10;
 template <int... kRows> struct RowCounts {
   static int least(int64_t rows, int deepest) {  // 0: none holds as many

@@ -30,7 +30,8 @@ int check(int64_t B, int64_t L, int64_t C, int64_t G, float eps, int dtype) {
   if (!ss2d::host_mul_ok(B, L, &rows) || !ss2d::host_mul_ok(std::max(rows, B), C, &n) ||
       n > ss2d::kHostMaxElems / 64)
     return SS2D_ERR_SHAPE;
-  // threads of one launch: a wave per group of an image, a block per image and 32 channels
+  // threads of one launch: a join's 64 per group of an image (more only where a thread then has four
+  // channels of a chunk or more: below 2^26 in all), a block of 256 per image and 32 channels
   if (B > (int64_t(1) << 25) / G || B > (int64_t(1) << 23) / ((C + 31) / 32)) return SS2D_ERR_SHAPE;
   return SS2D_OK;
 }
